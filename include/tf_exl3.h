@@ -43,7 +43,8 @@ typedef enum {
   TF_ERR_CUDA = 6,     /* a CUDA runtime call or launch failed (tf_last_error) */
   TF_ERR_TIMEOUT = 7,  /* a kernel's bounded wait expired (tf_device_error)    */
   TF_ERR_POINTER = 8,  /* a pointer is not device memory of the current device */
-  TF_ERR_SCRATCH = 9   /* the problem needs more scratch than the given workspace or the no-allocation array holds */
+  TF_ERR_SCRATCH = 9,  /* the problem needs more scratch than the given workspace or the no-allocation array holds */
+  TF_ERR_INDEX = 10    /* a kernel met an index outside its array and skipped it (tf_spec.h, tf_device_error) */
 } tf_status;
 
 typedef enum { TF_F16 = 0, TF_F32 = 1, TF_BF16 = 2 } tf_dtype;
@@ -281,8 +282,9 @@ const char* tf_last_error(void);
 /*
  * tf_device_error -- synchronises `stream`, then returns TF_ERR_TIMEOUT if a
  * kernel of this library on the current device gave up a bounded wait since
- * the last call (and clears that record), TF_ERR_CUDA if the synchronisation
- * failed, else TF_OK. The pages have no counterpart (their kernels have no
+ * the last call (and clears that record), else TF_ERR_INDEX if one skipped an
+ * index outside its array (tf_spec.h; cleared too), TF_ERR_CUDA if the
+ * synchronisation failed, else TF_OK. The pages have no counterpart (their kernels have no
  * waits that can give up).
  */
 tf_status tf_device_error(void* stream);

@@ -13,12 +13,16 @@ import ctypes
 import os
 
 from . import build as _build
+from . import spec as _spec
+from .spec import (TF_MAX_NODES, tf_kv_keep, tf_kv_write, tf_tree_attention,  # noqa: F401
+                   tf_tree_attention_workspace, tf_verify_draft, tf_verify_draft_workspace)
 
 TF_OK, TF_ERR_NULL, TF_ERR_SHAPE, TF_ERR_BITS, TF_ERR_DTYPE = 0, 1, 2, 3, 4
 TF_ERR_ALIGN, TF_ERR_CUDA, TF_ERR_TIMEOUT, TF_ERR_POINTER, TF_ERR_SCRATCH = 5, 6, 7, 8, 9
+TF_ERR_INDEX = 10
 TF_F16, TF_F32, TF_BF16 = 0, 1, 2
 
-# Every entry point include/tf_exl3.h declares, with its ctypes signature.
+# Every entry point the headers under include/ declare, with its ctypes signature.
 _VP, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 SIGNATURES = {
     "tf_abi_version": (_I, []),
@@ -37,6 +41,7 @@ SIGNATURES = {
     "tf_last_error": (ctypes.c_char_p, []),
     "tf_device_error": (_I, [_VP]),
     "tf_selftest_stranded_wait": (_I, [_VP]),
+    **_spec.SIGNATURES,
 }
 
 _lib = None
@@ -247,8 +252,12 @@ def tf_selftest_stranded_wait(stream=None):
 
 
 def tf_device_error(stream=None):
-    """Synchronises the stream; raises TFError if a kernel gave up a bounded wait."""
-    _check(lib().tf_device_error(_stream(stream)), "tf_device_error")
+    """Synchronises the stream; raises TFError if a kernel gave up a bounded wait
+    or skipped an index outside its array."""
+    status = lib().tf_device_error(_stream(stream))
+    if status == TF_ERR_TIMEOUT:
+        _spec.forget_workspaces()
+    _check(status, "tf_device_error")
 
 
 def project(x, suh, trellis, svh, bits, out_features, out_dtype=None, stream=None):

@@ -14,7 +14,9 @@
 
 namespace tfx {
 
-__device__ int g_device_error;  // OR of error bits set by kernels (1 = a bounded wait gave up)
+// OR of error bits set by kernels (1 = a bounded wait gave up, 2 = an index
+// outside its array was skipped).
+__device__ int g_device_error;
 
 namespace {
 
@@ -158,6 +160,7 @@ const char* tf_status_string(int status) {
     case TF_ERR_TIMEOUT: return "a kernel gave up a bounded wait";
     case TF_ERR_POINTER: return "a pointer is not device memory of the current device";
     case TF_ERR_SCRATCH: return "the problem needs more scratch than the given workspace or the fixed no-allocation array holds";
+    case TF_ERR_INDEX: return "a kernel met an index outside its array and skipped it";
     default: return "unknown status";
   }
 }
@@ -435,11 +438,11 @@ tf_status tf_device_error(void* stream) {
   if (flag != 0) {
     const int zero = 0;
     e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
-    if (e == cudaSuccess && ctx->counters != nullptr)
+    if (e == cudaSuccess && (flag & 1) != 0 && ctx->counters != nullptr)
       e = cudaMemset(ctx->counters, 0, ctx->counter_len * sizeof(int));  // an aborted launch may leave counts
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "resetting the error record");
-    return TF_ERR_TIMEOUT;
+    return (flag & 1) != 0 ? TF_ERR_TIMEOUT : TF_ERR_INDEX;
   }
   return TF_OK;
 }

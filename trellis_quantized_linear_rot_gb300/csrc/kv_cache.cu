@@ -1,0 +1,109 @@
+// Copies in the paged cache (tf_kv_write, tf_kv_keep).
+//
+// Both move rows of head_dim elements of 16 bits, as 16-byte chunks, one
+// chunk of one head a thread; the arithmetic is all addressing, and what
+// bounds them is the launch for a few tokens and memory for full batches.
+#include "spec.cuh"
+
+namespace tfx {
+namespace {
+
+constexpr int kThreads = 256;
+
+__global__ void __launch_bounds__(kThreads)
+kv_write_kernel(CacheView c, uint16_t* k, uint16_t* v, const uint16_t* k_new, const uint16_t* v_new, int64_t seq,
+                int64_t node, int64_t head, int nodes) {
+  const int chunks = c.kv_heads * (c.head_dim / 8);
+  const int64_t total = static_cast<int64_t>(c.batch) * nodes * chunks;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t id = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; id < total; id += stride) {
+    const int row = static_cast<int>(id / chunks);
+    const int rest = static_cast<int>(id - static_cast<int64_t>(row) * chunks);
+    const int h = rest / (c.head_dim / 8);
+    const int e = (rest - h * (c.head_dim / 8)) * 8;
+    const int b = row / nodes, i = row - b * nodes;
+    const int len = c.lengths[b];
+    if (len < 0) continue;
+    const int64_t at = slot_offset(c, b, static_cast<int64_t>(len) + i);
+    if (at < 0) continue;
+    const int64_t src = b * seq + i * node + h * head + e;
+    const int64_t dst = at + h * c.stride_head + e;
+    const uint4 x = *reinterpret_cast<const uint4*>(k_new + src);
+    const uint4 y = *reinterpret_cast<const uint4*>(v_new + src);
+    *reinterpret_cast<uint4*>(k + dst) = x;
+    *reinterpret_cast<uint4*>(v + dst) = y;
+  }
+}
+
+// One thread moves one chunk of one head of one layer along the whole path.
+// The path rises, so a slot is read before it is written: entry k comes from
+// slot path[k] >= k, and every later source is above k.
+__global__ void __launch_bounds__(kThreads)
+kv_keep_kernel(CacheView c, uint16_t* k, uint16_t* v, const int32_t* path, const int32_t* counts, int nodes,
+               int32_t* new_lengths) {
+  __shared__ int64_t from[TF_MAX_NODES], to[TF_MAX_NODES];
+  __shared__ int kept;
+  const int b = blockIdx.y, layer = blockIdx.z;
+  const int len = c.lengths[b];
+  if (len < 0) {
+    if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) new_lengths[b] = len;
+    return;
+  }
+  if (threadIdx.x == 0) {
+    int n = counts[b];
+    if (n < 0 || n > nodes) {
+      record_index_error(c.err);
+      n = n < 0 ? 0 : nodes;
+    }
+    int last = -1, i = 0;
+    for (; i < n; ++i) {
+      const int p = path[b * nodes + i];
+      if (p <= last || p >= nodes) {
+        record_index_error(c.err);
+        break;
+      }
+      last = p;
+    }
+    kept = i;
+    if (blockIdx.x == 0 && layer == 0) new_lengths[b] = len + i;
+  }
+  __syncthreads();
+  const int n = kept;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int p = path[b * nodes + i];
+    from[i] = p == i ? -1 : slot_offset(c, b, static_cast<int64_t>(len) + p);
+    to[i] = from[i] < 0 ? -1 : slot_offset(c, b, static_cast<int64_t>(len) + i);
+  }
+  __syncthreads();
+  const int chunks = c.kv_heads * (c.head_dim / 8);
+  for (int id = blockIdx.x * kThreads + threadIdx.x; id < 2 * chunks; id += gridDim.x * kThreads) {
+    const int part = id / chunks, rest = id - part * chunks;
+    const int h = rest / (c.head_dim / 8);
+    uint16_t* base = (part ? v : k) + layer * c.stride_layer + h * c.stride_head + (rest - h * (c.head_dim / 8)) * 8;
+    for (int i = 0; i < n; ++i)
+      if (to[i] >= 0) *reinterpret_cast<uint4*>(base + to[i]) = *reinterpret_cast<const uint4*>(base + from[i]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const CacheView& c, void* k, void* v, const void* k_new, const void* v_new, int64_t seq,
+                            int64_t node, int64_t head, int nodes, cudaStream_t s) {
+  const int64_t total = static_cast<int64_t>(c.batch) * nodes * c.kv_heads * (c.head_dim / 8);
+  const int64_t blocks = (total + kThreads - 1) / kThreads;
+  kv_write_kernel<<<static_cast<unsigned>(blocks < 65536 ? blocks : 65536), kThreads, 0, s>>>(
+      c, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), static_cast<const uint16_t*>(k_new),
+      static_cast<const uint16_t*>(v_new), seq, node, head, nodes);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_keep(const CacheView& c, void* k, void* v, const int32_t* path, const int32_t* counts,
+                           int nodes, int32_t* new_lengths, cudaStream_t s) {
+  const int chunks = 2 * c.kv_heads * (c.head_dim / 8);
+  const dim3 grid((chunks + kThreads - 1) / kThreads, c.batch, c.layers);
+  kv_keep_kernel<<<grid, kThreads, 0, s>>>(c, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), path, counts,
+                                           nodes, new_lengths);
+  return cudaGetLastError();
+}
+
+}  // namespace tfx

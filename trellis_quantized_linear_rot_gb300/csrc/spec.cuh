@@ -1,0 +1,100 @@
+// Device helpers shared by the cache, attention and verification kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "spec.h"
+
+namespace tfx {
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ void record_index_error(int* err) { atomicOr(err, kErrIndex); }
+
+// Slots a sequence's page table can name (below 2^31 by the host's check).
+__device__ __forceinline__ int slot_capacity(const CacheView& c) { return c.table_width * c.page_size; }
+
+// What exists of a sequence: its context slots and the slots up to its last
+// node. A length the table cannot hold is cut to what it can (recorded).
+struct Span {
+  int context, slots;  // -1, 0 for an idle sequence
+};
+__device__ __forceinline__ Span sequence_span(const CacheView& c, int b, int nodes) {
+  const int len = c.lengths[b], cap = slot_capacity(c);
+  if (len < 0) return {-1, 0};
+  if (len <= cap - nodes) return {len, len + nodes};
+  record_index_error(c.err);
+  return {min(len, cap), cap};
+}
+
+// Offset of slot `slot` of sequence `b` (layer 0, head 0), or -1 where the
+// slot lies past the table or its page outside the pool (recorded).
+__device__ __forceinline__ int64_t slot_offset(const CacheView& c, int b, int64_t slot) {
+  if (slot < 0 || slot >= slot_capacity(c)) {
+    record_index_error(c.err);
+    return -1;
+  }
+  const int p = static_cast<int>(slot) / c.page_size;
+  const int page = c.page_table[b * c.stride_table + p];
+  if (page < 0 || page >= c.pages) {
+    record_index_error(c.err);
+    return -1;
+  }
+  return page * c.stride_page + (static_cast<int>(slot) - p * c.page_size) * c.stride_token;
+}
+
+// The ancestors of up to TF_MAX_NODES nodes as bit masks: bit j of anc[i] is
+// set when row i sees node j (itself or an ancestor, none absent). Seven
+// rounds of pointer doubling, since a path has at most 128 nodes. Every
+// thread of a block of at least TF_MAX_NODES threads calls it.
+struct TreeMasks {
+  uint32_t anc[TF_MAX_NODES][4];
+  int16_t up[TF_MAX_NODES];
+};
+
+__device__ __forceinline__ void build_tree_masks(TreeMasks& t, const int32_t* parents, int nodes, int* err) {
+  const int j = threadIdx.x;
+  if (j < nodes) {
+    int p = parents[j];
+    if (p >= j) {
+      record_index_error(err);
+      p = -2;
+    }
+    for (int w = 0; w < 4; ++w) t.anc[j][w] = 0;
+    if (p >= -1) t.anc[j][j >> 5] = 1u << (j & 31);
+    t.up[j] = p >= 0 ? p : -1;
+  }
+  __syncthreads();
+  for (int span = 1; span < nodes; span *= 2) {
+    uint32_t m[4] = {0, 0, 0, 0};
+    int up = -1;
+    if (j < nodes && t.up[j] >= 0) {
+      const int p = t.up[j];
+      for (int w = 0; w < 4; ++w) m[w] = t.anc[p][w];
+      up = t.up[p];
+    }
+    __syncthreads();
+    if (j < nodes) {
+      for (int w = 0; w < 4; ++w) t.anc[j][w] |= m[w];
+      t.up[j] = up;
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace tfx

@@ -1,0 +1,69 @@
+// Internal types and launchers of the operators declared in tf_spec.h.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "tf_spec.h"
+
+namespace tfx {
+
+constexpr int kErrWait = 1;   // device error bits: a bounded wait gave up,
+constexpr int kErrIndex = 2;  // an index outside its array was skipped
+
+// The fields of tf_kv_cache the kernels read, without the array pointers.
+struct CacheView {
+  int64_t stride_layer, stride_page, stride_token, stride_head;
+  const int32_t* page_table;
+  const int32_t* lengths;
+  int64_t stride_table;
+  int layers, pages, page_size, kv_heads, head_dim, batch, table_width;
+  int* err;
+};
+
+struct AttendArgs {
+  CacheView c;
+  const void* k;
+  const void* v;
+  const void* q;
+  int64_t q_seq, q_node, q_head;
+  const int32_t* parents;
+  int64_t stride_parents;
+  void* out;
+  float* lse;
+  int nodes, heads, group;
+  float scale;
+  float* partials;
+  int* counters;
+  int num_sms;
+};
+
+struct VerifyArgs {
+  const void* logits;
+  const void* draft;
+  int64_t seq, node, draft_seq, draft_node;
+  const int32_t* tokens;
+  const int32_t* parents;
+  int64_t stride_parents;
+  const float* u_accept;
+  const float* u_sample;
+  float inv_temp;
+  int greedy;
+  int batch, nodes, vocab;
+  int32_t* counts;
+  int32_t* path;
+  int32_t* out_tokens;
+  float* logprobs;
+  int* err;
+  int num_sms;
+};
+
+cudaError_t launch_kv_write(const CacheView& c, void* k, void* v, const void* k_new, const void* v_new,
+                            int64_t seq, int64_t node, int64_t head, int nodes, cudaStream_t s);
+cudaError_t launch_kv_keep(const CacheView& c, void* k, void* v, const int32_t* path, const int32_t* counts,
+                           int nodes, int32_t* new_lengths, cudaStream_t s);
+cudaError_t launch_tree_attention(const AttendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_verify_draft(const VerifyArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace tfx
