@@ -291,6 +291,26 @@ def test_attention_workspace_serves_other_sizes_and_a_graph(n):
     tf.tf_device_error()
 
 
+def test_attention_one_workspace_for_many_sizes_in_turn():
+    """Counters and parts of calls of different sizes must not lie over one
+    another: one workspace, calls of many sizes in turn, twice."""
+    rng = np.random.default_rng(12)
+    ws = tf.tf_tree_attention_workspace(64, 40, 40, 8, 128)
+    cases = [Case("bf16", [200, 0, 77], 40, 8, 5, 128, 16, seed=1), Case("bf16", [3000], 1, 1, 1, 64, 64, seed=2),
+             Case("bf16", [30] * 64, 3, 4, 4, 64, 16, seed=3), Case("bf16", [900, 800], 20, 4, 2, 128, 32, seed=4),
+             Case("bf16", [5000], 16, 2, 8, 128, 64, seed=5)]
+    trees = [i32([tree("tree", c.n, rng) for _ in c.lens]) for c in cases]
+    fresh = [tf.tf_tree_attention(c.q, c.k, c.v, c.table, c.lengths, t,
+                                  workspace=tf.tf_tree_attention_workspace(64, 40, 40, 8, 128))
+             for c, t in zip(cases, trees)]
+    for _ in range(2):
+        for c, t, (o, l) in zip(cases, trees, fresh):
+            o2, l2 = tf.tf_tree_attention(c.q, c.k, c.v, c.table, c.lengths, t, workspace=ws)
+            assert torch.equal(o, o2) and torch.equal(l, l2)
+    for c, t in zip(cases, trees):
+        c.check(t.tolist())
+
+
 def test_attention_bad_indices_are_skipped_and_recorded():
     c = Case("fp16", [100, 100], 4, 1, 2, 64, 16, seed=13)
     par = i32([[-1, 0, 1, 2]] * 2)

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "per_device.h"
 #include "tf_spec.h"
 
 namespace tfx {
@@ -39,6 +40,14 @@ struct AttendArgs {
   int num_sms;
 };
 
+// Blocks of an attention launch for each SM.
+constexpr int kBlocksPerSm = 2;
+
+struct AttendWorkspace {
+  size_t partials_at, bytes;
+};
+AttendWorkspace attend_workspace(int nodes, int heads, int kv_heads, int head_dim, int num_sms);
+
 struct VerifyArgs {
   const void* logits;
   const void* draft;
@@ -63,7 +72,7 @@ cudaError_t launch_kv_write(const CacheView& c, void* k, void* v, const void* k_
                             int64_t seq, int64_t node, int64_t head, int nodes, cudaStream_t s);
 cudaError_t launch_kv_keep(const CacheView& c, void* k, void* v, const int32_t* path, const int32_t* counts,
                            int nodes, int32_t* new_lengths, cudaStream_t s);
-cudaError_t launch_tree_attention(const AttendArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_tree_attention(const AttendArgs& a, int dtype, int device, cudaStream_t s);
 cudaError_t launch_verify_draft(const VerifyArgs& a, int dtype, cudaStream_t s);
 
 }  // namespace tfx

@@ -109,7 +109,9 @@ size_t tf_tree_attention_workspace_bytes(int batch, int nodes, int heads, int kv
   if (batch < 0 || batch > 65535 || nodes < 0 || nodes > TF_MAX_NODES || heads < 1 || kv_heads < 1 ||
       heads % kv_heads || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
-  return 256;
+  int device, sms, *err;
+  if (current_device_state(&device, &sms, &err) != TF_OK) return 0;
+  return attend_workspace(nodes, heads, kv_heads, head_dim, sms).bytes;
 }
 
 tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_stride_seq, int64_t q_stride_node,
@@ -135,8 +137,8 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
   if (s == TF_OK) s = check_pointers_on_device(device, q, parents, out, lse);
   if (s == TF_OK) s = check_pointers_on_device(device, workspace, workspace, workspace, workspace);
   if (s != TF_OK) return s;
-  if (workspace_bytes < tf_tree_attention_workspace_bytes(cache->batch, nodes, heads, cache->kv_heads, d))
-    return TF_ERR_SCRATCH;
+  const AttendWorkspace ws = attend_workspace(nodes, heads, cache->kv_heads, d, sms);
+  if (workspace_bytes < ws.bytes) return TF_ERR_SCRATCH;
   AttendArgs a;
   a.c = view_of(cache, err);
   a.k = cache->k;
@@ -153,10 +155,10 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
   a.heads = heads;
   a.group = heads / cache->kv_heads;
   a.scale = static_cast<float>(scale);
-  a.partials = nullptr;
-  a.counters = nullptr;
+  a.counters = static_cast<int*>(workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.partials_at);
   a.num_sms = sms;
-  return launched(launch_tree_attention(a, cache->dtype, static_cast<cudaStream_t>(stream)), "tree attention launch");
+  return launched(launch_tree_attention(a, cache->dtype, device, static_cast<cudaStream_t>(stream)), "tree attention launch");
 }
 
 size_t tf_verify_draft_workspace_bytes(int batch, int nodes) {
