@@ -151,6 +151,15 @@ def test_attention_long_context_is_split_and_joined(n):
     Case("fp16", [7000, 3], n, 1, 5, 64, 16, seed=6).check([tree("tree", n, rng), tree("star", n, rng)])
 
 
+@pytest.mark.parametrize("b,n", [(300, 1), (129, 6), (700, 2)])
+def test_attention_large_batches(b, n):
+    """More sequences than a block scans at once, lengths of all kinds."""
+    rng = np.random.default_rng(b)
+    lens = [int(x) for x in rng.integers(-1, 90, b)]
+    lens[7] = 400
+    Case("bf16", lens, n, 1, 2, 64, 16, seed=b).check(tree("chain", n, rng))
+
+
 @pytest.mark.parametrize("kind", ["star", "roots", "holes", "padded", "chain"])
 @pytest.mark.parametrize("n", [2, 33, 128])
 def test_attention_tree_shapes(kind, n):

@@ -42,16 +42,20 @@ BAD_CACHES = [
     (dict(lengths=0x10002), tf.TF_ERR_ALIGN)]
 
 
+def byref(c):
+    return None if c is None else ctypes.byref(c)
+
+
 def write(lib, c, k=P, v=P, st=(1024, 1024, 128), n=3):
-    return lib.tf_kv_write(c, k, v, *st, n, S)
+    return lib.tf_kv_write(byref(c), k, v, *st, n, S)
 
 
 def attend(lib, c, q=P, st=(40960, 5120, 128), par=P, sp=3, out=P, lse=P, n=3, h=40, scale=0.1, ws=P, nb=1 << 40):
-    return lib.tf_tree_attention(c, q, *st, par, sp, out, lse, n, h, scale, ws, nb, S)
+    return lib.tf_tree_attention(byref(c), q, *st, par, sp, out, lse, n, h, scale, ws, nb, S)
 
 
 def keep(lib, c, path=P, counts=P, n=3, new=0x20000):
-    return lib.tf_kv_keep(c, path, counts, n, new, S)
+    return lib.tf_kv_keep(byref(c), path, counts, n, new, S)
 
 
 @pytest.mark.parametrize("bad,status", BAD_CACHES)
@@ -83,6 +87,7 @@ def test_attention_refusals(lib):
     assert attend(lib, cache(), st=(-8, 0, 0)) == attend(lib, cache(), sp=-1) == tf.TF_ERR_SHAPE
     assert attend(lib, cache(), scale=float("inf")) == attend(lib, cache(), scale=float("nan")) == tf.TF_ERR_SHAPE
     assert attend(lib, cache(batch=65535), n=128, h=40) == tf.TF_ERR_SHAPE       # too many rows
+    assert attend(lib, cache(batch=1000, table_width=1 << 20), n=1) == tf.TF_ERR_SHAPE   # too many tiles to number
     for k in ("q", "par", "out", "lse", "ws"):
         assert attend(lib, cache(), **{k: NUL}) == tf.TF_ERR_NULL, k
     for k in ("q", "out", "ws"):
@@ -134,3 +139,9 @@ def test_without_gpu_valid_calls_fail_cleanly(lib):
 def test_status_text(lib):
     assert lib.tf_status_string(tf.TF_ERR_INDEX).decode() not in ("", "unknown status")
     assert ctypes.sizeof(KVCache) == 104
+
+
+def test_the_bindings_bytes_are_the_structure():
+    from trellis_quantized_linear_rot_gb300 import spec
+    values = [0x1000, 0x2000, 3, 4, 5, 6, 0x7000, 0x8000, 9, 10, 11, 12, 13, 14, 15, 16, 17]
+    assert spec._pack_cache(*values) == bytes(KVCache(*values))

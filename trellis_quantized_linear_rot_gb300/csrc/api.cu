@@ -6,6 +6,7 @@
 #include <array>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -136,6 +137,14 @@ tf_status current_device_state(int* device, int* num_sms, int** err_flag) {
 
 tf_status check_pointers_on_device(int device, const void* a, const void* b, const void* c, const void* d) {
   return check_device_ptrs(device, a, b, c, d);
+}
+
+tf_status check_pointers_on_device(int device, std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs) {
+    tf_status s = check_device_ptr(p, device);
+    if (s != TF_OK) return s;
+  }
+  return TF_OK;
 }
 
 tf_status record_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }

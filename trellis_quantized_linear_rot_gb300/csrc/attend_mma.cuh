@@ -76,6 +76,18 @@ __device__ __forceinline__ bool bad16(uint16_t x) {
   return (x & m) == m;
 }
 
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Whether either half of a word is not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t bad_pair(uint32_t x) {
+  constexpr uint32_t m = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+  const uint32_t y = ~x & m;   // a half is bad when none of its exponent bits is clear
+  return (y & 0xFFFFu) == 0 || (y >> 16) == 0;
+}
+
 template <int D, int kRowWarps>
 struct MmaShape {
   static constexpr int kThreads = 128;
@@ -83,11 +95,20 @@ struct MmaShape {
   static constexpr int kKeyWarps = 4 / kRowWarps;
   static constexpr int kTile = D == 256 ? 32 : 64;
   static constexpr int kRowBytes = D * 2;
-  static constexpr int kHalf = kTile * kRowBytes;                       // keys or values of a tile
+  static constexpr int kHalf = kTile * kRowBytes;   // keys or values of a tile
   static constexpr int kStages = kRowWarps == 1 ? (D == 64 ? 5 : 3) : (D == 64 ? 3 : 2);
-  static constexpr int kJoinBytes = kKeyWarps > 1 ? kRows * D * 4 : 0;  // shared with the rows of q
-  static constexpr int kQBytes = kRows * kRowBytes > kJoinBytes ? kRows * kRowBytes : kJoinBytes;
-  static constexpr int kSmem = kStages * 2 * kHalf + kQBytes;
+  static constexpr int kQBytes = kRows * kRowBytes;
+  // A row block has at least a row a node, and more than 16 rows may have any
+  // number of nodes.
+  static constexpr int kNodes = kRowWarps == 1 ? 16 : TF_MAX_NODES;
+  // A row block's q and parents come with the copies of its first tile, into
+  // the places of that tile's stage, and go to registers when the item begins;
+  // with D = 256 q stays in shared memory, in a place of its own.
+  static constexpr int kQPlaces = kStages + (D == 256 ? 1 : 0);
+  static constexpr int kSmem = kStages * 2 * kHalf + kQPlaces * kQBytes + kStages * kNodes * 4;
+  // The warps' sums are joined in a stage whose tile is done with, kJoinCols
+  // columns at a time.
+  static constexpr int kJoinCols = 2 * kHalf / (kKeyWarps * kRows * 4) < D ? 2 * kHalf / (kKeyWarps * kRows * 4) : D;
 };
 
 template <typename T, int D, int kRowWarps>
@@ -97,14 +118,14 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   constexpr int kKeys = kTile / S::kKeyWarps;   // keys of a tile a warp takes
   constexpr int kN = kKeys / 8;                 // its 8-key blocks
   constexpr int kChunks = D / 8;
-  static_assert(kKeys % 16 == 0 || kN == 1, "a warp takes whole 16-key steps");
+  constexpr int kRing = kStages + 1;            // tiles whose offsets are known
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ TreeMasks masks;
-  __shared__ long long scratch[kThreads / 32 + 3];
-  __shared__ int64_t at[2][kTile];
+  __shared__ TreeMasks<S::kNodes> masks;
+  __shared__ int scratch[kThreads / 32 + 2];
+  __shared__ int64_t at[kRing][kTile];
   __shared__ float wm[4][16], wl[4][16];
-  __shared__ uint32_t bad[kTile / 32];               // keys of this tile with values that are not finite
-  __shared__ uint32_t gone[kStages + 1][kTile / 32];  // keys whose page is outside the pool
+  __shared__ uint32_t bad[kTile / 32];          // keys of this tile with values that are not finite
+  __shared__ uint32_t gone[kRing][kTile / 32];  // keys whose page is outside the pool
   __shared__ int last_here;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int row_warp = warp % kRowWarps, key_warp = warp / kRowWarps;
@@ -114,51 +135,85 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
 
   Line line;
   Cursor look;   // next tile whose offsets are looked up
-  if (!find_run<kTile, kThreads>(a, items, gridDim.x, scratch, &line, &look)) return;
-  Cursor cur = look;
+  if (!find_run<kTile, kThreads>(a, items, scratch, &line, &look)) return;
+  Cursor cur = look, load = look;   // tiles computed and copied next
   const uint32_t ring = smem_u32(smem);
-  unsigned char* qs = smem + kStages * 2 * S::kHalf;
-  const uint32_t q_at = ring + kStages * 2 * S::kHalf;
-  const int n_tiles = static_cast<int>(line.end - line.begin);
-
-  // Offset of this thread's key of tile i of the run (the cursor's), -1 for a
-  // slot that is not there. Whole warps call it.
-  auto offset_of = [&](const Cursor& c, int i) -> int64_t {
-    const int slot = c.t * kTile + tid;
-    const bool exists = slot < c.span.slots;
-    const int64_t o = exists ? slot_offset(a.c, c.b, slot) : -1;
-    const uint32_t none = __ballot_sync(~0u, exists && o < 0);
-    if (lane == 0) gone[i % (kStages + 1)][warp] = none;
-    return o < 0 ? -1 : o + static_cast<int64_t>(c.item / row_blocks) * a.c.stride_head;
-  };
+  const uint32_t q_ring = ring + kStages * 2 * S::kHalf;
+  const uint32_t p_ring = q_ring + S::kQPlaces * S::kQBytes;
+  const int* parents_ring = reinterpret_cast<const int*>(smem + kStages * 2 * S::kHalf + S::kQPlaces * S::kQBytes);
+  const int n_tiles = line.end - line.begin;
   const T* kp = static_cast<const T*>(a.k);
   const T* vp = static_cast<const T*>(a.v);
-  auto issue = [&](int i) {   // copies of tile i of the run
+
+  // The page of this thread's key of the tile at cursor c is asked for early
+  // (look_up), and its offset put in the ring for tile i later (settle; whole
+  // warps call it): -1 for a slot that is not there.
+  struct Pending {
+    int page, row, kvh;
+    bool exists;
+  };
+  auto look_up = [&](const Cursor& c) -> Pending {
+    const int slot = c.t * kTile + tid, p = slot / a.c.page_size;
+    const bool exists = slot < c.span.slots;
+    return {exists ? a.c.page_table[c.b * a.c.stride_table + p] : 0, slot - p * a.c.page_size, c.item / row_blocks, exists};
+  };
+  auto settle = [&](const Pending& x, int i) {
+    const bool outside = x.exists && static_cast<unsigned>(x.page) >= static_cast<unsigned>(a.c.pages);
+    const uint32_t none = __ballot_sync(~0u, outside);
+    if (lane == 0) gone[i % kRing][warp] = none;
+    if (none && outside) record_index_error(a.c.err);
+    at[i % kRing][tid] = x.exists && !outside ? x.page * a.c.stride_page + x.row * a.c.stride_token +
+                                                    x.kvh * a.c.stride_head
+                                              : -1;
+  };
+  // Copies of q and of the parents for the item of tile i (at cursor c).
+  auto issue_rows = [&](const Cursor& c, int i) {
+    const int h = c.item / row_blocks, first_row = (c.item - h * row_blocks) * kRows;
+    const uint32_t dst = q_ring + (i % kStages) * S::kQBytes;
+    for (int id = tid; id < kRows * kChunks; id += kThreads) {
+      const int r = id / kChunks, ch = id % kChunks;
+      const bool real = first_row + r < rows_all;
+      const RowOf ro = row_of(a, h, real ? first_row + r : 0);
+      copy16(dst + r * S::kRowBytes + ((ch ^ (r & 7)) << 4),
+             static_cast<const T*>(a.q) + c.b * a.q_seq + ro.node * a.q_node + ro.head * a.q_head + ch * 8, real);
+    }
+    if (tid < a.nodes) copy4(p_ring + ((i % kStages) * S::kNodes + tid) * 4, a.parents + c.b * a.stride_parents + tid);
+  };
+  // Copies of tile i of the run.
+  auto issue = [&](int i) {
     const uint32_t dst = ring + (i % kStages) * 2 * S::kHalf;
-    for (int id = tid; id < kTile * kChunks; id += kThreads) {
-      const int key = id / kChunks, ch = id % kChunks;
-      const int64_t o = at[i & 1][key];
+#pragma unroll
+    for (int n = 0; n < kTile * kChunks / kThreads; ++n) {
+      const int id = n * kThreads + tid, key = id / kChunks, ch = id % kChunks;
+      const int64_t o = at[i % kRing][key];
       const uint32_t d = dst + key * S::kRowBytes + ((ch ^ (key & 7)) << 4);
       copy16(d, kp + (o < 0 ? 0 : o + ch * 8), o >= 0);
       copy16(d + S::kHalf, vp + (o < 0 ? 0 : o + ch * 8), o >= 0);
     }
   };
 
-  // Fill the ring: offsets of a tile, then its copies.
+  // Fill the ring: q of the first item, the offsets of the first kStages
+  // tiles, the copies of all but the last of them.
+  issue_rows(cur, 0);
+  Pending first[kStages];
+#pragma unroll
+  for (int i = 0; i < kStages; ++i)
+    if (i < n_tiles) {
+      if (tid < kTile) first[i] = look_up(look);
+      advance<kTile>(a, items, &look);
+    }
+#pragma unroll
+  for (int i = 0; i < kStages; ++i)
+    if (i < n_tiles && tid < kTile) settle(first[i], i);
+  __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) {
     if (i < n_tiles) {
-      if (tid < kTile) at[i & 1][tid] = offset_of(look, i);
-      __syncthreads();
+      if (i > 0 && load.t == 0) issue_rows(load, i);
       issue(i);
-      advance<kTile>(a, items, &look);
+      advance<kTile>(a, items, &load);
     }
     copies_commit();
-  }
-  if (kStages - 1 < n_tiles) {
-    __syncthreads();
-    if (tid < kTile) at[(kStages - 1) & 1][tid] = offset_of(look, kStages - 1);
-    advance<kTile>(a, items, &look);
   }
 
   uint32_t qf[D == 256 ? 1 : D / 16][4];
@@ -166,33 +221,43 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   float m[2], l[2];
   int kvh = 0, row0 = 0;
   int node[2];
+  const uint32_t q_at = q_ring + kStages * S::kQBytes;   // D = 256 only
   bool fresh = true;
   const float sc = a.scale * kLog2e;
 
 #pragma unroll 1
   for (int i = 0; i < n_tiles; ++i) {
+    copies_wait<kStages - 2>();
+    __syncthreads();   // tile i has landed; everyone is done with tile i - 1
+    if (i + kStages - 1 < n_tiles) {
+      if (load.t == 0) issue_rows(load, i + kStages - 1);
+      issue(i + kStages - 1);
+      advance<kTile>(a, items, &load);
+    }
+    copies_commit();
+    const bool more = i + kStages < n_tiles;
+    Pending next = {};
+    if (more && tid < kTile) next = look_up(look);   // settled after this tile
+    if (more) advance<kTile>(a, items, &look);
+
     if (fresh) {   // a new item: its rows of q, its masks
       kvh = cur.item / row_blocks;
       row0 = (cur.item - kvh * row_blocks) * kRows;
-      __syncthreads();
-      for (int id = tid; id < kRows * kChunks; id += kThreads) {
-        const int r = id / kChunks, ch = id % kChunks;
-        uint4 x = {0, 0, 0, 0};
-        if (row0 + r < rows_all) {
-          const RowOf ro = row_of(a, kvh, row0 + r);
-          x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + cur.b * a.q_seq + ro.node * a.q_node +
-                                              ro.head * a.q_head + ch * 8);
-        }
-        *reinterpret_cast<uint4*>(qs + r * S::kRowBytes + ((ch ^ (r & 7)) << 4)) = x;
-      }
-      build_tree_masks(masks, a.parents + cur.b * a.stride_parents, a.nodes, a.c.err);
-      if constexpr (D != 256) {
+      const uint32_t q_new = q_ring + (i % kStages) * S::kQBytes;
+      if constexpr (D == 256) {
+        unsigned char* q8 = smem + kStages * 2 * S::kHalf;
+        for (int id = tid; id < S::kQBytes / 16; id += kThreads)
+          reinterpret_cast<uint4*>(q8 + kStages * S::kQBytes)[id] =
+              reinterpret_cast<const uint4*>(q8 + (i % kStages) * S::kQBytes)[id];
+      } else {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const int r = row_warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-          ldsm4(qf[ks], q_at + r * S::kRowBytes + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4));
+          ldsm4(qf[ks], q_new + r * S::kRowBytes + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4));
         }
       }
+      masks.build(parents_ring + (i % kStages) * S::kNodes, a.nodes, a.c.err);
+#pragma unroll
       for (int e = 0; e < D / 8; ++e)
         for (int x = 0; x < 4; ++x) o[e][x] = 0.f;
       for (int x = 0; x < 2; ++x) {
@@ -202,36 +267,31 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
       }
       fresh = false;
     }
-    copies_wait<kStages - 2>();
-    __syncthreads();   // tile i has landed; everyone is done with tile i - 1
-    if (i + kStages - 1 < n_tiles) issue(i + kStages - 1);
-    copies_commit();
-    const bool more = i + kStages < n_tiles;
-    int64_t next_at = -1;
-    if (more && tid < kTile) next_at = offset_of(look, i + kStages);   // stored after this tile
 
     const uint32_t kt = ring + (i % kStages) * 2 * S::kHalf, vt = kt + S::kHalf;
     const int slot0 = cur.t * kTile;
     uint32_t missing = 0;
-    for (int x = 0; x < kTile / 32; ++x) missing |= gone[i % (kStages + 1)][x];
+    for (int x = 0; x < kTile / 32; ++x) missing |= gone[i % kRing][x];
     const bool tail = slot0 + kTile > cur.span.context || missing;
     bool any_bad = false;
-    if (tail) {
-      // Values of tree nodes that are not finite must not reach the rows that
-      // do not see them (0 times infinity): they are set to 0 here and added
-      // after the product to the rows that do.
+    // Values of tree nodes that are not finite must not reach the rows that do
+    // not see them (0 times infinity): they are set to 0 here and added after
+    // the product to the rows that do. The only node is seen by every row.
+    if (tail && a.nodes > 1) {
       if (tid < kTile / 32) bad[tid] = 0;
       __syncthreads();
       unsigned char* v8 = smem + (i % kStages) * 2 * S::kHalf + S::kHalf;
-      const int j0 = max(0, cur.span.context - slot0);
-      for (int id = tid; id < (kTile - j0) * kChunks; id += kThreads) {
-        const int key = j0 + id / kChunks, ch = id % kChunks;
-        uint16_t* w = reinterpret_cast<uint16_t*>(v8 + key * S::kRowBytes + ((ch ^ (key & 7)) << 4));
-        for (int x = 0; x < 8; ++x)
-          if (bad16<T>(w[x])) {
-            w[x] = 0;
-            atomicOr(&bad[key / 32], 1u << (key % 32));
-          }
+      const int j0 = max(0, cur.span.context - slot0), j1 = min(kTile, cur.span.slots - slot0);
+      for (int id = j0 * kChunks + tid; id < j1 * kChunks; id += kThreads) {
+        const int key = id / kChunks, ch = id % kChunks;
+        uint4* w = reinterpret_cast<uint4*>(v8 + key * S::kRowBytes + ((ch ^ (key & 7)) << 4));
+        const uint4 x = *w;
+        if (bad_pair<T>(x.x) | bad_pair<T>(x.y) | bad_pair<T>(x.z) | bad_pair<T>(x.w)) {
+          uint16_t* h = reinterpret_cast<uint16_t*>(w);
+          for (int y = 0; y < 8; ++y)
+            if (bad16<T>(h[y])) h[y] = 0;
+          atomicOr(&bad[key / 32], 1u << (key % 32));
+        }
       }
       __syncthreads();
       for (int x = 0; x < kTile / 32; ++x) any_bad |= bad[x] != 0;
@@ -268,8 +328,8 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
           const int key = key_warp * kKeys + n * 8 + (lane % 4) * 2 + (x & 1), slot = slot0 + key;
           const int i_row = node[x >> 1], j = slot - cur.span.context;
           bool sees = slot < cur.span.slots && i_row >= 0;
-          if (sees && j >= 0) sees = masks.anc[i_row][j >> 5] >> (j & 31) & 1;
-          if (!sees || (gone[i % (kStages + 1)][key / 32] >> (key % 32) & 1)) s[n][x] = -INFINITY;
+          if (sees && j >= 0) sees = masks.sees(i_row, j);
+          if (!sees || (gone[i % kRing][key / 32] >> (key % 32) & 1)) s[n][x] = -INFINITY;
         }
       }
     uint32_t p[kN][2];
@@ -314,7 +374,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
         const T* row = vp + off + static_cast<int64_t>(kvh) * a.c.stride_head;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (node[x] < 0 || !(masks.anc[node[x]][j >> 5] >> (j & 31) & 1)) continue;
+          if (node[x] < 0 || !masks.sees(node[x], j)) continue;
 #pragma unroll
           for (int e = 0; e < D / 8; ++e)
             for (int y = 0; y < 2; ++y) {
@@ -327,83 +387,101 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
 
     const bool item_ends = cur.t + 1 == cur.nt;
     if (item_ends || i + 1 == n_tiles) {
+      const bool whole = item_ends && cur.first >= line.begin;
+      const int rows = min(kRows, rows_all - row0);
+      const bool idle = cur.span.context < 0;
+      float* part = a.partials + part_index(line, blockIdx.x, cur.first) * kPartFloats<kRows, D>;
       // Sums over the four lanes of a row, then over the warps with other keys.
+#pragma unroll
       for (int x = 0; x < 2; ++x) {
         l[x] += __shfl_xor_sync(~0u, l[x], 1);
         l[x] += __shfl_xor_sync(~0u, l[x], 2);
       }
-      float* sum = reinterpret_cast<float*>(qs);
+      // Where a row's result goes: out and lse, or this block's part.
+      auto finish = [&](int rl, float top, float sum, bool first, float* inv, T** out) {
+        const RowOf ro = row_of(a, kvh, row0 + rl);
+        const bool present = !idle && masks.sees(ro.node, ro.node);
+        const bool empty = !present || sum == 0.f;
+        *inv = empty ? 0.f : 1.f / sum;
+        const size_t out_at = (static_cast<size_t>(cur.b) * a.nodes + ro.node) * a.heads + ro.head;
+        *out = static_cast<T*>(a.out) + out_at * D;
+        if (first) a.lse[out_at] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+      };
       if constexpr (S::kKeyWarps > 1) {
+#pragma unroll
         for (int x = 0; x < 2; ++x)
           if (lane % 4 == 0) wm[warp][lane / 4 + x * 8] = m[x], wl[warp][lane / 4 + x * 8] = l[x];
-        __syncthreads();
+        __syncthreads();   // and everyone is done with tile i
+        float* sums = reinterpret_cast<float*>(smem + (i % kStages) * 2 * S::kHalf);
         float f[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int r = lane / 4 + x * 8;
-          float top = -INFINITY;
-          for (int w = 0; w < 4; ++w) top = fmaxf(top, wm[w][r]);
-          const float base = top == -INFINITY ? 0.f : top;
-          f[x] = exp2_approx(m[x] - base);
-          l[x] = 0.f;
-          for (int w = 0; w < 4; ++w) l[x] += wl[w][r] * exp2_approx(wm[w][r] - base);
-          m[x] = top;
+          const float top = fmaxf(fmaxf(wm[0][r], wm[1][r]), fmaxf(wm[2][r], wm[3][r]));
+          f[x] = exp2_approx(m[x] - (top == -INFINITY ? 0.f : top));
         }
-        for (int w = 0; w < 4; ++w) {
-          if (warp == w)
 #pragma unroll
-            for (int e = 0; e < D / 8; ++e)
+        for (int c0 = 0; c0 < D; c0 += S::kJoinCols) {
+          if (c0) __syncthreads();
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                float2* to = reinterpret_cast<float2*>(sum + (lane / 4 + x * 8) * D + e * 8 + (lane % 4) * 2);
-                float2 y = w ? *to : float2{0.f, 0.f};
-                y.x += f[x] * o[e][2 * x];
-                y.y += f[x] * o[e][2 * x + 1];
-                *to = y;
-              }
+          for (int e = c0 / 8; e < (c0 + S::kJoinCols) / 8; ++e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int r = lane / 4 + x * 8;
+              // columns rotated by the row, so that a warp's rows lie in different banks
+              const int col = (e * 8 - c0 + (lane % 4) * 2 + r * 8) % S::kJoinCols;
+              *reinterpret_cast<float2*>(sums + (warp * 16 + r) * S::kJoinCols + col) =
+                  float2{f[x] * o[e][2 * x], f[x] * o[e][2 * x + 1]};
+            }
           __syncthreads();
-        }
-      }
-      const bool whole = item_ends && cur.first >= line.begin;
-      const int rows = min(kRows, rows_all - row0);
-      const bool idle = cur.span.context < 0;
-      if (whole) {
+          for (int id = tid; id < rows * (S::kJoinCols / 4); id += kThreads) {
+            const int r = id / (S::kJoinCols / 4), e = (id - r * (S::kJoinCols / 4)) * 4;
+            float4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int rl = row_warp * 16 + lane / 4 + x * 8;
-          if (node[x] < 0) continue;
-          const RowOf ro = row_of(a, kvh, row0 + rl);
-          const bool present = !idle && (masks.anc[ro.node][ro.node >> 5] >> (ro.node & 31) & 1);
-          const bool empty = !present || l[x] == 0.f;
-          const float inv = empty ? 0.f : 1.f / l[x];
-          const size_t out_at = (static_cast<size_t>(cur.b) * a.nodes + ro.node) * a.heads + ro.head;
-          T* out = static_cast<T*>(a.out) + out_at * D;
+            for (int w = 0; w < 4; ++w) {
+              const float4 z = *reinterpret_cast<const float4*>(sums + (w * 16 + r) * S::kJoinCols +
+                                                                (e + r * 8) % S::kJoinCols);
+              y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            }
+            const float top = fmaxf(fmaxf(wm[0][r], wm[1][r]), fmaxf(wm[2][r], wm[3][r]));
+            const float base = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
 #pragma unroll
-          for (int e = 0; e < D / 8; ++e) {
-            if (S::kKeyWarps > 1 && e % S::kKeyWarps != key_warp) continue;
-            const int col = e * 8 + (lane % 4) * 2;
-            float y0 = o[e][2 * x], y1 = o[e][2 * x + 1];
-            if (S::kKeyWarps > 1) y0 = sum[rl * D + col], y1 = sum[rl * D + col + 1];
-            *reinterpret_cast<uint32_t*>(out + col) = empty ? 0u : pack2(T(), y0 * inv, y1 * inv);
+            for (int w = 0; w < 4; ++w) sum += wl[w][r] * exp2_approx(wm[w][r] - base);
+            if (whole) {
+              float inv;
+              T* out;
+              finish(r, top, sum, c0 + e == 0, &inv, &out);
+              const bool empty = inv == 0.f;
+              const uint2 z = {empty ? 0u : pack2(T(), y.x * inv, y.y * inv),
+                               empty ? 0u : pack2(T(), y.z * inv, y.w * inv)};
+              *reinterpret_cast<uint2*>(out + c0 + e) = z;
+            } else {
+              *reinterpret_cast<float4*>(part + r * D + c0 + e) = y;
+              if (c0 + e == 0) part[kRows * D + r] = top, part[kRows * D + kRows + r] = sum;
+            }
           }
-          if (lane % 4 == 0 && key_warp == 0) a.lse[out_at] = empty ? -INFINITY : (m[x] + log2f(l[x])) * kLn2;
         }
       } else {
-        float* part = Part<kRows, D>::at(a, line, blockIdx.x, cur.first);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int rl = row_warp * 16 + lane / 4 + x * 8;
           if (rl >= rows) continue;
+          float inv = 1.f;
+          T* out = nullptr;
+          if (whole) finish(rl, m[x], l[x], lane % 4 == 0, &inv, &out);
 #pragma unroll
           for (int e = 0; e < D / 8; ++e) {
-            if (S::kKeyWarps > 1 && e % S::kKeyWarps != key_warp) continue;
             const int col = e * 8 + (lane % 4) * 2;
-            float2 y = {o[e][2 * x], o[e][2 * x + 1]};
-            if (S::kKeyWarps > 1) y = *reinterpret_cast<const float2*>(sum + rl * D + col);
-            *reinterpret_cast<float2*>(part + rl * D + col) = y;
+            if (whole)
+              *reinterpret_cast<uint32_t*>(out + col) = inv == 0.f ? 0u : pack2(T(), o[e][2 * x] * inv, o[e][2 * x + 1] * inv);
+            else
+              *reinterpret_cast<float2*>(part + rl * D + col) = float2{o[e][2 * x], o[e][2 * x + 1]};
           }
-          if (lane % 4 == 0 && key_warp == 0) part[kRows * D + rl] = m[x], part[kRows * D + kRows + rl] = l[x];
+          if (!whole && lane % 4 == 0) part[kRows * D + rl] = m[x], part[kRows * D + kRows + rl] = l[x];
         }
+      }
+      if (!whole) {
         __threadfence();
         __syncthreads();
         if (tid == 0) {
@@ -415,9 +493,9 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
           join_parts<T, kRows, D, kThreads>(a, line, masks, cur.b, kvh, row0, rows, cur.first, cur.nt, idle);
       }
       fresh = true;
+      __syncthreads();   // the masks and the stage may be written again
     }
-    if (more && tid < kTile) at[(i + kStages) & 1][tid] = next_at;
-    if (more) advance<kTile>(a, items, &look);
+    if (more && tid < kTile) settle(next, i + kStages);
     advance<kTile>(a, items, &cur);
   }
 }

@@ -25,18 +25,33 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// The line of tiles and this block's run of it.
+// The line of tiles (below 2^31: checked on the host) and this block's run of
+// it: the first `longer` runs have per + 1 tiles, the others per. No more
+// runs than tiles, so that no run between two others is empty.
 struct Line {
-  long long total;   // tiles of all items
-  long long begin, end;
-  int blocks;        // runs: blocks of the launch, at most one a tile
+  int blocks, per, longer;
+  int begin, end;
+  __device__ __forceinline__ void cut(int total, int launched) {
+    blocks = min(total, launched);
+    per = total / blocks;
+    longer = total - per * blocks;
+    const int i = min(static_cast<int>(blockIdx.x), blocks);
+    begin = begin_of(i);
+    end = i < blocks ? begin_of(i + 1) : begin;
+  }
+  __device__ __forceinline__ int begin_of(int block) const { return block * per + min(block, longer); }
+  // The block whose run holds tile f.
+  __device__ __forceinline__ int block_of(int f) const {
+    const int border = longer * (per + 1);
+    return f < border ? f / (per + 1) : longer + (f - border) / per;
+  }
 };
 
 // Position of a tile: item `item` (kv head, row block) of sequence b, tile t
 // of its nt. first = place of the item's tile 0 in the line.
 struct Cursor {
   int b, item, t, nt;
-  long long first;
+  int first;
   Span span;
 };
 
@@ -45,62 +60,50 @@ __device__ __forceinline__ int tiles_of(const Span& s) {
   return s.slots <= kTile ? 1 : (s.slots + kTile - 1) / kTile;
 }
 
-// Block-wide: the line's length, this block's run and the cursor at its
-// begin. `scratch` has room for kThreads / 32 + 3 long longs. False where the
-// run is empty. Batches of up to kThreads sequences are scanned once, larger
-// ones twice (length, then place).
+// Block-wide: the line, this block's run and the cursor at its begin.
+// `scratch` has room for kThreads / 32 + 2 ints. False where the run is
+// empty. Batches of up to kThreads sequences are scanned once, larger ones
+// twice (length, then place).
 template <int kTile, int kThreads>
-__device__ bool find_run(const AttendArgs& a, int items, int blocks, long long* scratch, Line* line, Cursor* cur) {
+__device__ bool find_run(const AttendArgs& a, int items, int* scratch, Line* line, Cursor* cur) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int batch = a.c.batch;
-  long long* found = scratch + kWarps + 1;   // [0] first tile of the sequence, [1] sequence
-  long long before = 0;
-  // No more runs than tiles, so that no run between two others is empty.
-  auto cut = [&](long long all) {
-    line->total = all;
-    line->blocks = all < blocks ? static_cast<int>(all) : blocks;
-    const int i = min(static_cast<int>(blockIdx.x), line->blocks);
-    line->begin = all * i / line->blocks;
-    line->end = i < line->blocks ? all * (i + 1) / line->blocks : all;
-  };
-  for (int pass = 0; pass < 2; ++pass) {
-    before = 0;
+  int* found = scratch + kWarps;   // [0] first tile of the sequence, [1] sequence
+  for (int pass = batch <= kThreads ? 1 : 0; pass < 2; ++pass) {
+    int before = 0;
     for (int b0 = 0; b0 < batch; b0 += kThreads) {
       const int b = b0 + tid;
-      long long n = 0;
-      if (b < batch) n = static_cast<long long>(tiles_of<kTile>(sequence_span(a.c, b, a.nodes))) * items;
-      long long run = n;
+      const int n = b < batch ? tiles_of<kTile>(sequence_span(a.c, b, a.nodes)) * items : 0;
+      int run = n;
       for (int o = 1; o < 32; o *= 2) {
-        const long long y = __shfl_up_sync(~0u, run, o);
+        const int y = __shfl_up_sync(~0u, run, o);
         if (lane >= o) run += y;
       }
       if (lane == 31) scratch[warp] = run;
       __syncthreads();
-      long long prior = before, all = before;
+      int prior = before, all = before;
       for (int w = 0; w < kWarps; ++w) {
         if (w < warp) prior += scratch[w];
         all += scratch[w];
       }
       run += prior;
-      const bool last = b0 + kThreads >= batch;
-      if (pass == 0 && last) cut(all);
-      if ((pass == 1 || batch <= kThreads) && line->begin >= run - n && line->begin < run) {
+      if (b0 + kThreads >= batch && (pass == 0 || batch <= kThreads)) line->cut(all, gridDim.x);
+      if (pass == 1 && line->begin >= run - n && line->begin < run) {
         found[0] = run - n;
         found[1] = b;
       }
       before = all;
       __syncthreads();
     }
-    if (batch <= kThreads) break;
   }
   if (line->begin >= line->end) return false;
-  cur->b = static_cast<int>(found[1]);
+  cur->b = found[1];
   cur->span = sequence_span(a.c, cur->b, a.nodes);
   cur->nt = tiles_of<kTile>(cur->span);
-  const long long in = line->begin - found[0];
-  cur->item = static_cast<int>(in / cur->nt);
-  cur->t = static_cast<int>(in - static_cast<long long>(cur->item) * cur->nt);
+  const int in = line->begin - found[0];
+  cur->item = in / cur->nt;
+  cur->t = in - cur->item * cur->nt;
   cur->first = line->begin - cur->t;
   return true;
 }
@@ -117,34 +120,22 @@ __device__ __forceinline__ void advance(const AttendArgs& a, int items, Cursor* 
   c->nt = tiles_of<kTile>(c->span);
 }
 
-// The block whose run holds tile f of the line, and where its run begins.
-__device__ __forceinline__ int block_of(const Line& l, long long f) {
-  return static_cast<int>(((f + 1) * l.blocks - 1) / l.total);
+// Place of a block's part of the item at `first`. A block has two parts in
+// the workspace: of the item its run begins in, and of a later item it ends
+// in. A part is kRows rows of D sums, kRows maxima (in units of log 2) and
+// kRows sums of weights.
+__device__ __forceinline__ int part_index(const Line& l, int block, int first) {
+  return 2 * block + (l.begin_of(block) < first ? 1 : 0);
 }
-__device__ __forceinline__ long long begin_of(const Line& l, int block) { return l.total * block / l.blocks; }
-
-// Place of a block's part of the item at `first`.
-__device__ __forceinline__ size_t part_index(const Line& l, int block, long long first) {
-  return 2 * static_cast<size_t>(block) + (begin_of(l, block) < first ? 1 : 0);
-}
-
-// A block has two parts in the workspace: of the item its run begins in, and
-// of a later item it ends in. A part is kRows rows of D sums, kRows maxima
-// (in units of log 2) and kRows sums of weights.
 template <int kRows, int D>
-struct Part {
-  static constexpr size_t kFloats = static_cast<size_t>(kRows) * (D + 2);
-  static __device__ __forceinline__ float* at(const AttendArgs& a, const Line& l, int block, long long first) {
-    return a.partials + part_index(l, block, first) * kFloats;
-  }
-};
+constexpr size_t kPartFloats = static_cast<size_t>(kRows) * (D + 2);
 
 // Counts this block's part of the item (nt tiles from `first`); true in the
 // block that arrives last. An item cut between blocks is counted at the place
 // of its first part, so that the counters' number does not depend on the
 // call's sizes and a workspace serves any of them.
-__device__ __forceinline__ bool arrives_last(const AttendArgs& a, const Line& l, long long first, int nt) {
-  const int b0 = block_of(l, first), parts = block_of(l, first + nt - 1) - b0 + 1;
+__device__ __forceinline__ bool arrives_last(const AttendArgs& a, const Line& l, int first, int nt) {
+  const int b0 = l.block_of(first), parts = l.block_of(first + nt - 1) - b0 + 1;
   int* counter = a.counters + part_index(l, b0, first);
   const bool last = atomicAdd(counter, 1) + 1 == parts;
   if (last) *counter = 0;   // ready for the next call
@@ -162,27 +153,47 @@ __device__ __forceinline__ RowOf row_of(const AttendArgs& a, int kvh, int r) {
 
 // Whole block: joins the parts of the item at `first` (nt tiles) and writes
 // rows row0 .. row0 + rows - 1 of its kv head. Parts are added in run order.
-template <typename T, int kRows, int D, int kThreads>
-__device__ void join_parts(const AttendArgs& a, const Line& line, const TreeMasks& masks, int b, int kvh, int row0,
-                           int rows, long long first, int nt, bool idle) {
-  const int b0 = block_of(line, first), b1 = block_of(line, first + nt - 1);
+template <typename T, int kRows, int D, int kThreads, typename Masks>
+__device__ void join_parts(const AttendArgs& a, const Line& line, const Masks& masks, int b, int kvh, int row0,
+                           int rows, int first, int nt, bool idle) {
+  constexpr size_t kPart = kPartFloats<kRows, D>;
+  const int b0 = line.block_of(first), n = line.block_of(first + nt - 1) - b0 + 1;
+  // Every part but the first is the one its block begins with.
+  const float* part0 = a.partials + part_index(line, b0, first) * kPart;
+  const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart;
   for (int id = threadIdx.x; id < rows * (D / 4); id += kThreads) {
     const int r = id / (D / 4), e = (id - r * (D / 4)) * 4;
-    float top = -INFINITY;
-    for (int p = b0; p <= b1; ++p) top = fmaxf(top, __ldcg(Part<kRows, D>::at(a, line, p, first) + kRows * D + r));
-    const float base = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
+    float top = -INFINITY, l = 0.f;
     float4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = b0; p <= b1; ++p) {
-      const float* part = Part<kRows, D>::at(a, line, p, first);
-      const float w = exp2_approx(__ldcg(part + kRows * D + r) - base);
-      l += w * __ldcg(part + kRows * D + kRows + r);
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(part + r * D + e));
-      o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
+    // Groups of parts, all of a group's loads in flight at once.
+    constexpr int kGroup = 6;
+    for (int p0 = 0; p0 < n; p0 += kGroup) {
+      float m[kGroup], w[kGroup];
+      float4 x[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const float* part = p0 + i == 0 ? part0 : part1 + (p0 + i - 1) * 2 * kPart;
+        const bool real = p0 + i < n;
+        m[i] = real ? __ldcg(part + kRows * D + r) : -INFINITY;
+        w[i] = real ? __ldcg(part + kRows * D + kRows + r) : 0.f;
+        x[i] = real ? __ldcg(reinterpret_cast<const float4*>(part + r * D + e)) : float4{0.f, 0.f, 0.f, 0.f};
+      }
+      float high = top;
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) high = fmaxf(high, m[i]);
+      const float base = high == -INFINITY ? 0.f : high;
+      const float keep = exp2_approx(top - base);
+      top = high;
+      l *= keep, o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const float f = exp2_approx(m[i] - base);
+        l += f * w[i];
+        o.x += f * x[i].x, o.y += f * x[i].y, o.z += f * x[i].z, o.w += f * x[i].w;
+      }
     }
     const RowOf ro = row_of(a, kvh, row0 + r);
-    const bool present = !idle && (masks.anc[ro.node][ro.node >> 5] >> (ro.node & 31) & 1);
+    const bool present = !idle && masks.sees(ro.node, ro.node);
     const bool empty = !present || l == 0.f;
     const float inv = empty ? 0.f : 1.f / l;
     const size_t at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;

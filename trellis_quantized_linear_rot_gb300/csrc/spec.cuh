@@ -58,43 +58,46 @@ __device__ __forceinline__ int64_t slot_offset(const CacheView& c, int b, int64_
   return page * c.stride_page + (static_cast<int>(slot) - p * c.page_size) * c.stride_token;
 }
 
-// The ancestors of up to TF_MAX_NODES nodes as bit masks: bit j of anc[i] is
-// set when row i sees node j (itself or an ancestor, none absent). Seven
-// rounds of pointer doubling, since a path has at most 128 nodes. Every
-// thread of a block of at least TF_MAX_NODES threads calls it.
+// The ancestors of up to kNodes nodes as bit masks: sees(i, j) when row i sees
+// node j (itself or an ancestor, none absent). Built in log2(nodes) rounds of
+// pointer doubling, by all threads of a block of at least kNodes.
+template <int kNodes>
 struct TreeMasks {
-  uint32_t anc[TF_MAX_NODES][4];
-  int16_t up[TF_MAX_NODES];
-};
+  static constexpr int kWords = (kNodes + 31) / 32;
+  uint32_t anc[kNodes][kWords];
+  int16_t up[kNodes];
 
-__device__ __forceinline__ void build_tree_masks(TreeMasks& t, const int32_t* parents, int nodes, int* err) {
-  const int j = threadIdx.x;
-  if (j < nodes) {
-    int p = parents[j];
-    if (p >= j) {
-      record_index_error(err);
-      p = -2;
-    }
-    for (int w = 0; w < 4; ++w) t.anc[j][w] = 0;
-    if (p >= -1) t.anc[j][j >> 5] = 1u << (j & 31);
-    t.up[j] = p >= 0 ? p : -1;
-  }
-  __syncthreads();
-  for (int span = 1; span < nodes; span *= 2) {
-    uint32_t m[4] = {0, 0, 0, 0};
-    int up = -1;
-    if (j < nodes && t.up[j] >= 0) {
-      const int p = t.up[j];
-      for (int w = 0; w < 4; ++w) m[w] = t.anc[p][w];
-      up = t.up[p];
-    }
-    __syncthreads();
+  __device__ __forceinline__ bool sees(int i, int j) const { return anc[i][j >> 5] >> (j & 31) & 1; }
+
+  __device__ __forceinline__ void build(const int32_t* parents, int nodes, int* err) {
+    const int j = threadIdx.x;
     if (j < nodes) {
-      for (int w = 0; w < 4; ++w) t.anc[j][w] |= m[w];
-      t.up[j] = up;
+      int p = parents[j];
+      if (p >= j) {
+        record_index_error(err);
+        p = -2;
+      }
+      for (int w = 0; w < kWords; ++w) anc[j][w] = 0;
+      if (p >= -1) anc[j][j >> 5] = 1u << (j & 31);
+      up[j] = p >= 0 ? p : -1;
     }
     __syncthreads();
+    for (int span = 1; span < nodes; span *= 2) {
+      uint32_t m[kWords] = {};
+      int next = -1;
+      if (j < nodes && up[j] >= 0) {
+        const int p = up[j];
+        for (int w = 0; w < kWords; ++w) m[w] = anc[p][w];
+        next = up[p];
+      }
+      __syncthreads();
+      if (j < nodes) {
+        for (int w = 0; w < kWords; ++w) anc[j][w] |= m[w];
+        up[j] = next;
+      }
+      __syncthreads();
+    }
   }
-}
+};
 
 }  // namespace tfx

@@ -76,8 +76,8 @@ tf_status tf_kv_write(const tf_kv_cache* cache, const void* k_new, const void* v
     return TF_ERR_ALIGN;
   int device, sms, *err;
   s = current_device_state(&device, &sms, &err);
-  if (s == TF_OK) s = check_pointers_on_device(device, cache->k, cache->v, k_new, v_new);
-  if (s == TF_OK) s = check_pointers_on_device(device, cache->page_table, cache->lengths, k_new, v_new);
+  if (s == TF_OK)
+    s = check_pointers_on_device(device, {cache->k, cache->v, cache->page_table, cache->lengths, k_new, v_new});
   if (s != TF_OK) return s;
   return launched(launch_kv_write(view_of(cache, err), cache->k, cache->v, k_new, v_new, stride_seq, stride_node,
                                   stride_head, nodes, static_cast<cudaStream_t>(stream)),
@@ -97,8 +97,9 @@ tf_status tf_kv_keep(const tf_kv_cache* cache, const int32_t* path, const int32_
   if (std::llabs(apart) < static_cast<int64_t>(cache->batch) * 4) return TF_ERR_POINTER;
   int device, sms, *err;
   s = current_device_state(&device, &sms, &err);
-  if (s == TF_OK) s = check_pointers_on_device(device, cache->k, cache->v, cache->page_table, cache->lengths);
-  if (s == TF_OK) s = check_pointers_on_device(device, path, counts, new_lengths, new_lengths);
+  if (s == TF_OK)
+    s = check_pointers_on_device(
+        device, {cache->k, cache->v, cache->page_table, cache->lengths, path, counts, new_lengths});
   if (s != TF_OK) return s;
   return launched(launch_kv_keep(view_of(cache, err), cache->k, cache->v, path, counts, nodes, new_lengths,
                                  static_cast<cudaStream_t>(stream)),
@@ -125,6 +126,11 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
       q_stride_seq < 0 || q_stride_node < 0 || q_stride_head < 0 || stride_parents < 0 || !std::isfinite(scale) ||
       static_cast<int64_t>(cache->batch) * nodes * heads > kMaxRows)
     return TF_ERR_SHAPE;
+  // The kernels number the tiles (of at least 32 slots) of all items in 31 bits.
+  const int64_t row_blocks = (static_cast<int64_t>(nodes) * (heads / cache->kv_heads) + 63) / 64;
+  const int64_t tiles = (static_cast<int64_t>(cache->table_width) * cache->page_size + 31) / 32;
+  if (static_cast<double>(tiles) * static_cast<double>(row_blocks * cache->kv_heads) * cache->batch > 2147483647.0)
+    return TF_ERR_SHAPE;
   if (cache->batch == 0 || nodes == 0) return TF_OK;
   s = check_cache_pointers(cache);
   if (s == TF_ERR_NULL || !q || !parents || !out || !lse || !workspace) return TF_ERR_NULL;
@@ -133,9 +139,9 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
     return TF_ERR_ALIGN;
   int device, sms, *err;
   s = current_device_state(&device, &sms, &err);
-  if (s == TF_OK) s = check_pointers_on_device(device, cache->k, cache->v, cache->page_table, cache->lengths);
-  if (s == TF_OK) s = check_pointers_on_device(device, q, parents, out, lse);
-  if (s == TF_OK) s = check_pointers_on_device(device, workspace, workspace, workspace, workspace);
+  if (s == TF_OK)
+    s = check_pointers_on_device(
+        device, {cache->k, cache->v, cache->page_table, cache->lengths, q, parents, out, lse, workspace});
   if (s != TF_OK) return s;
   const AttendWorkspace ws = attend_workspace(nodes, heads, cache->kv_heads, d, sms);
   if (workspace_bytes < ws.bytes) return TF_ERR_SCRATCH;
@@ -191,10 +197,11 @@ tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int
     return TF_ERR_ALIGN;
   int device, sms, *err;
   tf_status s = current_device_state(&device, &sms, &err);
-  if (s == TF_OK) s = check_pointers_on_device(device, logits, tokens, parents, workspace);
-  if (s == TF_OK) s = check_pointers_on_device(device, counts, path, out_tokens, logprobs);
-  if (s == TF_OK && !greedy)
-    s = check_pointers_on_device(device, u_sample, draft ? u_accept : u_sample, draft ? draft_logits : u_sample, u_sample);
+  if (s == TF_OK)
+    s = check_pointers_on_device(device,
+                                 {logits, tokens, parents, workspace, counts, path, out_tokens, logprobs});
+  if (s == TF_OK && !greedy) s = check_pointers_on_device(device, {u_sample});
+  if (s == TF_OK && draft) s = check_pointers_on_device(device, {u_accept, draft_logits});
   if (s != TF_OK) return s;
   if (workspace_bytes < tf_verify_draft_workspace_bytes(batch, nodes)) return TF_ERR_SCRATCH;
   VerifyArgs a;
