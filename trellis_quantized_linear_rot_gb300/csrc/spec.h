@@ -64,9 +64,11 @@ struct VerifyArgs {
   int32_t* path;
   int32_t* out_tokens;
   float* logprobs;
+  int* work;   // [3][batch * nodes] decisions, [batch] counters, all zero between calls
   int* err;
   int num_sms;
 };
+size_t verify_workspace_bytes(int batch, int nodes);
 
 cudaError_t launch_kv_write(const CacheView& c, void* k, void* v, const void* k_new, const void* v_new,
                             int64_t seq, int64_t node, int64_t head, int nodes, cudaStream_t s);

@@ -169,7 +169,7 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
 
 size_t tf_verify_draft_workspace_bytes(int batch, int nodes) {
   if (batch < 0 || batch > 65535 || nodes < 1 || nodes > TF_MAX_NODES) return 0;
-  return 256;
+  return verify_workspace_bytes(batch, nodes);
 }
 
 tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int64_t stride_node,
@@ -225,6 +225,7 @@ tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int
   a.path = path;
   a.out_tokens = out_tokens;
   a.logprobs = logprobs;
+  a.work = static_cast<int*>(workspace);
   a.err = err;
   a.num_sms = sms;
   return launched(launch_verify_draft(a, dtype, static_cast<cudaStream_t>(stream)), "draft verification launch");

@@ -2,94 +2,143 @@
 // (tf_verify_draft).
 //
 // Probabilities are whole numbers: w = round(2^30 exp(z - max z)), and their
-// sums are exact in 64 bits, so a token never depends on the order of a sum.
-// One block takes one sequence and walks down its tree, reading the rows of
-// the nodes it reaches.
+// sums are exact in 64 bits, so a token never depends on the order of a sum
+// nor on how a row is split.
+//
+// What a node decides (the child it goes on to, or the token sampled) depends
+// on its own rows of logits only, so the nodes can be taken in any order, and
+// the answer is the chain of decisions from node 0. A cluster of blocks takes
+// a node: each block a part of the vocabulary, with one exchange through
+// distributed shared memory for the maximum, one for the sum and one for each
+// refusal's rest; the row is read from memory once and again from the L1
+// cache. The clusters go through the rows node by node (all sequences' node
+// 0, then their node 1, ..), and before a cluster takes a row it looks
+// whether the parent has been decided against it: then the row is passed over
+// unread, and so are its descendants. Nothing waits for a decision: few rows
+// are all taken at once, in the time of one, and of many only little more
+// than those on the accepted paths are read. The block that completes a
+// sequence's last row follows the decisions and writes the outputs.
+#include <cooperative_groups.h>
+
 #include "spec.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace tfx {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr float kOne = 1073741824.f;                 // 2^30: the largest weight
+constexpr double kUnit = 2305843009213693952.0;      // 2^61
+constexpr double kHalfUnit = 2147483648.0;           // 2^31: the normalised rows' unit
 
-__device__ __forceinline__ float clean(float x) { return isnan(x) ? -INFINITY : x; }
+__device__ __forceinline__ uint32_t whole(float x) { return __float2uint_rn(x); }   // a NaN becomes 0
 
-// One row of logits: z = x / T and the weights against the row's maximum.
+// A row of logits: z = x / T, and e = exp(z - max z). The row's vectors of 16
+// bytes are numbered from the aligned address at or before its first element;
+// element k of vector v is number v * kVec + k - shift.
 template <typename T>
 struct Row {
+  static constexpr int kVec = 16 / sizeof(T);
   const T* x;
   float inv, top;
-  __device__ __forceinline__ float z(int i) const { return __fmul_rn(clean(to_f32(x[i])), inv); }
+
+  __device__ __forceinline__ int shift() const {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  }
+  __device__ __forceinline__ float z(T v) const { return __fmul_rn(to_f32(v), inv); }
   __device__ __forceinline__ float e(float z) const {
-    if (z == top) return z > -INFINITY ? 1.f : 0.f;
+    if (fabsf(top) == INFINITY) return z == top && top > 0.f ? 1.f : 0.f;
     return expf(__fsub_rn(z, top));
   }
-};
-
-__device__ __forceinline__ uint32_t whole(float x) { return __float2uint_rn(x); }
-
-struct Shared {
-  unsigned long long sums[kWarps + 1];
-  float tops[kWarps];
-  int at[kWarps];
-  int token;
-};
-
-__device__ float block_max(Shared& s, float x, int i, int* where) {
-  for (int o = 16; o; o >>= 1) {
-    const float y = __shfl_xor_sync(~0u, x, o);
-    const int j = __shfl_xor_sync(~0u, i, o);
-    if (y > x || (y == x && j < i)) x = y, i = j;
-  }
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) s.tops[threadIdx.x / 32] = x, s.at[threadIdx.x / 32] = i;
-  __syncthreads();
-  x = s.tops[0], i = s.at[0];
-  for (int w = 1; w < kWarps; ++w)
-    if (s.tops[w] > x || (s.tops[w] == x && s.at[w] < i)) x = s.tops[w], i = s.at[w];
-  *where = i;
-  return x;
-}
-
-// Sum over the block of each warp's sum; s.sums[w] keeps what lies before
-// warp w and s.sums[kWarps] the total.
-__device__ unsigned long long block_sum(Shared& s, unsigned long long x) {
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) s.sums[threadIdx.x / 32 + 1] = x;
-  if (threadIdx.x == 0) s.sums[0] = 0;
-  __syncthreads();
-  if (threadIdx.x == 0)
-    for (int w = 1; w <= kWarps; ++w) s.sums[w] += s.sums[w - 1];
-  __syncthreads();
-  return s.sums[kWarps];
-}
-
-// The least i with weight(0) + .. + weight(i) > t, for a t below the total;
-// the warps' parts are contiguous and s.sums is block_sum's.
-template <typename F>
-__device__ int block_pick(Shared& s, unsigned long long t, int lo, int hi, F weight) {
-  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (t >= s.sums[w] && t < s.sums[w + 1]) {
-    unsigned long long before = s.sums[w];
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const unsigned long long x = i0 + lane < hi ? weight(i0 + lane) : 0;
-      unsigned long long run = x;
-      for (int o = 1; o < 32; o *= 2) {
-        const unsigned long long y = __shfl_up_sync(~0u, run, o);
-        if (lane >= o) run += y;
-      }
-      const unsigned hit = __ballot_sync(~0u, before + run > t);
-      if (hit) {
-        if (lane == 0) s.token = i0 + __ffs(hit) - 1;
-        break;
-      }
-      before += __shfl_sync(~0u, run, 31);
+  __device__ __forceinline__ int vectors(int vocab) const { return (vocab + shift() + kVec - 1) / kVec; }
+  // kVec elements from number i on, those outside [0, vocab) as -inf.
+  __device__ __forceinline__ void load(int i, int vocab, float (&z_out)[kVec]) const {
+    T v[kVec];
+    if (i >= 0 && i + kVec <= vocab && (reinterpret_cast<uintptr_t>(x + i) & 15) == 0) {
+      *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(x + i);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) z_out[k] = z(v[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) z_out[k] = i + k >= 0 && i + k < vocab ? z(x[i + k]) : -INFINITY;
     }
   }
-  __syncthreads();
-  return s.token;
+};
+
+// A warp's part [v0, v1) of a row's vectors: f(number of the first element, z)
+// for each. Whole vectors come kAhead a lane at a time, so that their loads
+// are in flight together; the row's first and last vector may be cut.
+template <int kAhead, typename T, typename F>
+__device__ __forceinline__ void sweep(const Row<T>& r, int vocab, int v0, int v1, F f) {
+  constexpr int kVec = Row<T>::kVec;
+  const int lane = threadIdx.x % 32, shift = r.shift();
+  const int f0 = max(v0, shift ? 1 : 0), f1 = min(v1, (vocab + shift) / kVec);   // whole ones
+  const uint4* base = reinterpret_cast<const uint4*>(r.x - shift);
+  int v = f0 + lane;
+  for (; v + 32 * (kAhead - 1) < f1; v += 32 * kAhead) {
+    uint4 raw[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) raw[u] = base[v + 32 * u];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const T* x = reinterpret_cast<const T*>(&raw[u]);
+      float z[kVec];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) z[k] = r.z(x[k]);
+      f((v + 32 * u) * kVec - shift, z);
+    }
+  }
+  for (; v < f1; v += 32) {
+    const uint4 raw = base[v];
+    const T* x = reinterpret_cast<const T*>(&raw);
+    float z[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) z[k] = r.z(x[k]);
+    f(v * kVec - shift, z);
+  }
+  if (lane == 0) {
+    float z[kVec];
+    if (v0 < f0 && v0 < v1) {
+      r.load(v0 * kVec - shift, vocab, z);
+      f(v0 * kVec - shift, z);
+    }
+    if (f1 < v1 && v1 - 1 >= f0) {
+      r.load((v1 - 1) * kVec - shift, vocab, z);
+      f((v1 - 1) * kVec - shift, z);
+    }
+  }
 }
+
+// What the blocks of a cluster tell one another, twice so that an exchange
+// can begin while the one before is still being read.
+struct Exchange {
+  unsigned long long sum[2][kMaxCluster];
+  float top[2][kMaxCluster], qtop[2][kMaxCluster];
+  int at[2][kMaxCluster];
+};
+
+struct Shared {
+  Exchange x;
+  unsigned long long sums[kWarps + 1];   // weight before each warp of this block, and all of it
+  float tops[kWarps], qtops[kWarps];
+  int ats[kWarps];
+  int par[TF_MAX_NODES], tok[TF_MAX_NODES];
+  float zp[TF_MAX_NODES], zq[TF_MAX_NODES];   // logits of the node's children's tokens
+  float u[TF_MAX_NODES];
+  int next_row;
+  int state[TF_MAX_NODES], out_tok[TF_MAX_NODES];
+  float out_lp[TF_MAX_NODES];
+};
+
+// Decisions in the workspace: 0 while open, -1 for a row that cannot be on
+// the path, else the child gone on to + 2 (1: none). A call leaves all zero.
+struct Results {
+  int* state;
+  int* token;
+  float* logprob;
+  int* arrived;
+};
 
 __device__ __forceinline__ unsigned long long threshold(float u, unsigned long long total) {
   const double x = floor(static_cast<double>(u) * static_cast<double>(total));
@@ -98,120 +147,391 @@ __device__ __forceinline__ unsigned long long threshold(float u, unsigned long l
   return t < total ? t : total - 1;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_draft_kernel(VerifyArgs a) {
-  __shared__ Shared s;
-  __shared__ int par[TF_MAX_NODES], tok[TF_MAX_NODES];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  for (int j = tid; j < a.nodes; j += kThreads) {
-    int p = a.parents[b * a.stride_parents + j];
-    if (p >= j) {
-      record_index_error(a.err);
-      p = -2;
-    }
-    par[j] = p;
-    tok[j] = a.tokens[b * a.nodes + j];
+// One warp: counts a finished row of sequence b, and where it is the last
+// one, follows the decisions and writes the sequence's outputs.
+__device__ void arrive(const VerifyArgs& a, const Results& r, Shared& s, int b) {
+  const int lane = threadIdx.x % 32;
+  int last = 0;
+  if (lane == 0) {
+    __threadfence();
+    last = atomicAdd(r.arrived + b, 1) + 1 == a.nodes;
+    __threadfence();
   }
-  const int part = (a.vocab + kWarps - 1) / kWarps;
-  const int lo = min(a.vocab, tid / 32 * part), hi = min(a.vocab, lo + part), lane = tid % 32;
-  __syncthreads();
-  int count = 0, node = par[0] >= -1 ? 0 : -1;
+  if (!__shfl_sync(~0u, last, 0)) return;
   const int64_t row0 = static_cast<int64_t>(b) * a.nodes;
-  while (node >= 0) {
-    Row<T> p{static_cast<const T*>(a.logits) + b * a.seq + node * a.node, a.inv_temp, 0.f};
-    Row<T> q{static_cast<const T*>(a.draft) + b * a.draft_seq + node * a.draft_node, a.inv_temp, 0.f};
-    const bool draft = a.draft != nullptr && !a.greedy;
-    float top = -INFINITY;
-    int best = a.vocab;
-    for (int i = lo + lane; i < hi; i += 32) {
-      const float z = p.z(i);
-      if (z > top) top = z, best = i;
-    }
-    p.top = block_max(s, top, best, &best);
-    unsigned long long sum = 0;
-    for (int i = lo + lane; i < hi; i += 32) sum += whole(p.e(p.z(i)) * 1073741824.f);
-    const unsigned long long mass = block_sum(s, sum);
-    int next = -1, token = -1;
-    if (mass > 0 && draft) {
-      float qtop = -INFINITY;
-      int unused = 0;
-      for (int i = lo + lane; i < hi; i += 32) qtop = fmaxf(qtop, q.z(i));
-      q.top = block_max(s, qtop, 0, &unused);
-      sum = 0;
-      for (int i = lo + lane; i < hi; i += 32) sum += whole(q.e(q.z(i)) * 1073741824.f);
-      const unsigned long long qmass = block_sum(s, sum);
-      const float cp = static_cast<float>(2305843009213693952.0 / static_cast<double>(mass));
-      const double q1 = qmass ? 2305843009213693952.0 / static_cast<double>(qmass) : 0.0;
-      double level = 0.0, left = 2147483648.0;
-      float cq = 0.f;
-      auto rest = [&](int i) -> unsigned long long {
-        const uint32_t x = whole(__fmul_rn(p.e(p.z(i)), cp)), y = whole(__fmul_rn(q.e(q.z(i)), cq));
-        return x > y ? x - y : 0;
-      };
-      for (int c = node + 1; c < a.nodes && next < 0; ++c) {
-        const int t = tok[c];
-        if (par[c] != node || t < 0 || t >= a.vocab) continue;
-        const float qt = __fmul_rn(q.e(q.z(t)), static_cast<float>(q1));
-        const double rt = level > 0.0 ? static_cast<double>(rest(t)) : static_cast<double>(__fmul_rn(p.e(p.z(t)), cp));
-        if (static_cast<double>(a.u_accept[row0 + c]) * static_cast<double>(qt) * left < rt * 2147483648.0) {
-          next = c;
-          break;
-        }
-        level += left / 2147483648.0;
-        cq = static_cast<float>(level * q1);
-        sum = 0;
-        for (int i = lo + lane; i < hi; i += 32) sum += rest(i);
-        const unsigned long long all = block_sum(s, sum);
-        left = static_cast<double>(all);
-        if (all == 0) {
-          level = 0.0;
-          break;
-        }
-      }
-      if (next >= 0) {
-        token = tok[next];
-      } else if (level > 0.0) {
-        token = block_pick(s, threshold(a.u_sample[row0 + node], s.sums[kWarps]), lo, hi, rest);
-      } else {
-        sum = 0;
-        for (int i = lo + lane; i < hi; i += 32) sum += whole(p.e(p.z(i)) * 1073741824.f);
-        block_sum(s, sum);
-        token = block_pick(s, threshold(a.u_sample[row0 + node], mass), lo, hi,
-                           [&](int i) -> unsigned long long { return whole(p.e(p.z(i)) * 1073741824.f); });
-      }
-    } else if (mass > 0) {
-      token = a.greedy ? best
-                       : block_pick(s, threshold(a.u_sample[row0 + node], mass), lo, hi,
-                                    [&](int i) -> unsigned long long { return whole(p.e(p.z(i)) * 1073741824.f); });
-      for (int c = a.nodes - 1; c > node; --c)
-        if (par[c] == node && tok[c] == token) next = c;
-    }
-    if (tid == 0) {
+  for (int j = lane; j < a.nodes; j += 32) {
+    s.state[j] = __ldcg(r.state + row0 + j);
+    s.out_tok[j] = __ldcg(r.token + row0 + j);
+    s.out_lp[j] = __ldcg(r.logprob + row0 + j);
+    r.state[row0 + j] = 0;
+    r.token[row0 + j] = 0;
+    r.logprob[row0 + j] = 0.f;
+  }
+  if (lane == 0) r.arrived[b] = 0;
+  __syncwarp();
+  int count = 0;
+  for (int node = s.state[0] > 0 ? 0 : -1; node >= 0; node = s.state[node] - 2) {
+    if (lane == 0) {
       a.path[row0 + count] = node;
-      a.out_tokens[row0 + count] = token;
-      a.logprobs[row0 + count] =
-          token < 0 ? 0.f
-                    : __fsub_rn(p.z(token), p.top) - logf(static_cast<float>(mass) * 9.31322574615478515625e-10f);
+      a.out_tokens[row0 + count] = s.out_tok[node];
+      a.logprobs[row0 + count] = s.out_lp[node];
     }
     ++count;
-    node = next;
-    __syncthreads();
   }
-  if (tid == 0) a.counts[b] = count;
-  for (int k = count + tid; k < a.nodes; k += kThreads) {
+  if (lane == 0) a.counts[b] = count;
+  for (int k = count + lane; k < a.nodes; k += 32) {
     a.path[row0 + k] = -1;
     a.out_tokens[row0 + k] = -1;
     a.logprobs[row0 + k] = 0.f;
   }
 }
 
+// One warp: writes a row's decision.
+__device__ void decide(const VerifyArgs& a, const Results& r, Shared& s, int b, int node, int next, int token,
+                       float logprob) {
+  if (threadIdx.x % 32 == 0) {
+    const int64_t row = static_cast<int64_t>(b) * a.nodes + node;
+    __stcg(r.token + row, token);
+    __stcg(r.logprob + row, logprob);
+    __stcg(r.state + row, next + 2);
+  }
+  arrive(a, r, s, b);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_constant__ VerifyArgs a) {
+  __shared__ Shared s;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int clusters = gridDim.x / ranks, cluster_id = blockIdx.x / ranks;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rows = a.batch * a.nodes;   // row i: node i / batch of sequence i % batch
+  const Results res{a.work, a.work + rows, reinterpret_cast<float*>(a.work + 2 * static_cast<size_t>(rows)),
+                    a.work + 3 * static_cast<size_t>(rows)};
+  int side = 0;   // which half of the exchange is next
+  constexpr int kVec = Row<T>::kVec;
+
+  // Sum of x over the cluster; s.sums holds what lies before each warp of
+  // this block, *before what lies before this block.
+  auto total = [&](unsigned long long x, unsigned long long* before) {
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    __syncthreads();   // the sums before are no longer read
+    if (lane == 0) s.sums[warp + 1] = x;
+    if (tid == 0) s.sums[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+      unsigned long long y = lane < kWarps ? s.sums[lane + 1] : 0;
+      for (int o = 1; o < kWarps; o *= 2) {
+        const unsigned long long z = __shfl_up_sync(~0u, y, o);
+        if (lane >= o) y += z;
+      }
+      if (lane < kWarps) s.sums[lane + 1] = y;
+      const unsigned long long all = __shfl_sync(~0u, y, kWarps - 1);
+      if (lane < ranks) cluster.map_shared_rank(&s.x.sum[side][0], lane)[rank] = all;
+    }
+    cluster.sync();
+    unsigned long long sum = 0;
+    *before = 0;
+    for (int k = 0; k < ranks; ++k) {
+      if (k == rank) *before = sum;
+      sum += s.x.sum[side][k];
+    }
+    side ^= 1;
+    return sum;
+  };
+
+  auto part_of = [&](int vecs, int* lo, int* hi) {
+    const int per_block = (vecs + ranks - 1) / ranks, b0 = min(vecs, rank * per_block), b1 = min(vecs, b0 + per_block);
+    const int per_warp = (b1 - b0 + kWarps - 1) / kWarps;
+    *lo = min(b1, b0 + warp * per_warp);
+    *hi = min(b1, *lo + per_warp);
+  };
+
+#pragma unroll 1
+  for (int i = cluster_id; i < rows;) {
+    // Before any row but the first: the next one that is not decided against.
+    if (i != cluster_id) {
+      if (rank == 0 && warp == 0) {
+        int found = rows;
+        for (int base = i; base < rows && found == rows; base += 32 * clusters) {
+          const int64_t k = base + static_cast<int64_t>(lane) * clusters;
+          bool dead = false;
+          int node = 0, b = 0;
+          if (k < rows) {
+            node = static_cast<int>(k) / a.batch, b = static_cast<int>(k) % a.batch;
+            if (node > 0) {
+              const int p = a.parents[b * a.stride_parents + node];
+              if (p < 0) {
+                dead = true;
+              } else if (p < node) {
+                const int st = __ldcg(res.state + static_cast<int64_t>(b) * a.nodes + p);
+                dead = st != 0 && st != node + 2;
+              }
+            }
+          }
+          const unsigned live = __ballot_sync(~0u, k < rows && !dead);
+          const int first = live ? __ffs(live) - 1 : 32;
+          if (dead && lane < first) __stcg(res.state + static_cast<int64_t>(b) * a.nodes + node, -1);
+          for (unsigned gone = __ballot_sync(~0u, dead && lane < first); gone; gone &= gone - 1)
+            arrive(a, res, s, __shfl_sync(~0u, b, __ffs(gone) - 1));
+          if (live) found = base + first * clusters;
+        }
+        if (lane < ranks) cluster.map_shared_rank(&s.next_row, lane)[0] = found;
+      }
+      cluster.sync();
+      i = s.next_row;
+      if (i >= rows) break;
+    }
+    const int node = i / a.batch, b = i - node * a.batch;
+    const int64_t row0 = static_cast<int64_t>(b) * a.nodes;
+    const bool draft = a.draft != nullptr;
+    Row<T> p{static_cast<const T*>(a.logits) + b * a.seq + node * a.node, a.inv_temp, 0.f};
+    Row<T> q{draft ? static_cast<const T*>(a.draft) + b * a.draft_seq + node * a.draft_node : p.x, a.inv_temp, 0.f};
+    const float u_node = a.greedy ? 0.f : a.u_sample[row0 + node];
+    if (tid < a.nodes) {
+      int up = a.parents[b * a.stride_parents + tid];
+      const int t = a.tokens[row0 + tid];
+      if (up >= tid) {
+        if (tid == node) record_index_error(a.err);
+        up = -2;
+      }
+      const bool child = up == node && tid > node && t >= 0 && t < a.vocab;
+      s.par[tid] = tid == node ? up : (child ? node : -2);   // children that may be asked, and the row's own
+      s.tok[tid] = t;
+      if (draft) s.u[tid] = a.u_accept[row0 + tid];
+      if (child) {
+        s.zp[tid] = p.z(p.x[t]);
+        s.zq[tid] = q.z(q.x[t]);
+      }
+    }
+
+    // This warp's vectors of each row.
+    int v0, v1, q0, q1v;
+    part_of(p.vectors(a.vocab), &v0, &v1);
+    part_of(q.vectors(a.vocab), &q0, &q1v);
+
+    // Maxima.
+    float top = -INFINITY, qtop = -INFINITY;
+    sweep<8>(p, a.vocab, v0, v1, [&](int, const float(&z)[kVec]) {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) top = fmaxf(top, z[k]);
+    });
+    if (draft)
+      sweep<8>(q, a.vocab, q0, q1v, [&](int, const float(&z)[kVec]) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) qtop = fmaxf(qtop, z[k]);
+      });
+    for (int o = 16; o; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      qtop = fmaxf(qtop, __shfl_xor_sync(~0u, qtop, o));
+    }
+    if (lane == 0) s.tops[warp] = top, s.qtops[warp] = qtop;
+    __syncthreads();
+    if (warp == 0) {
+      top = lane < kWarps ? s.tops[lane] : -INFINITY;
+      qtop = lane < kWarps ? s.qtops[lane] : -INFINITY;
+      for (int o = 16; o; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        qtop = fmaxf(qtop, __shfl_xor_sync(~0u, qtop, o));
+      }
+      if (lane < ranks) {
+        Exchange* to = cluster.map_shared_rank(&s.x, lane);
+        to->top[side][rank] = top;
+        to->qtop[side][rank] = qtop;
+      }
+    }
+    cluster.sync();
+    for (int k = 0; k < ranks; ++k) {
+      p.top = k ? fmaxf(p.top, s.x.top[side][k]) : s.x.top[side][k];
+      q.top = k ? fmaxf(q.top, s.x.qtop[side][k]) : s.x.qtop[side][k];
+    }
+    side ^= 1;
+
+    const int up = s.par[node];
+    const bool dead = node == 0 ? up < -1 : up < 0;
+    int next = -1, token = -1;
+    unsigned long long mass = 0, before = 0;
+    bool pick = false;   // the token is still to be found by its cumulative weight
+    float cp = 0.f, cq = 0.f;
+    double level = 0.0;
+    auto weight = [&](float z) -> uint32_t { return whole(p.e(z) * kOne); };
+    auto rest = [&](float zp, float zq) -> uint32_t {
+      const uint32_t x = whole(__fmul_rn(p.e(zp), cp)), y = whole(__fmul_rn(q.e(zq), cq));
+      return x > y ? x - y : 0;
+    };
+    unsigned long long goal = 0, goal_total = 0;
+    if (!dead && p.top > -INFINITY) {
+      unsigned long long sum = 0;
+      int best = INT32_MAX;
+      sweep<2>(p, a.vocab, v0, v1, [&](int e0, const float(&z)[kVec]) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+          sum += weight(z[k]);
+          if (a.greedy && z[k] == p.top) best = min(best, e0 + k);
+        }
+      });
+      if (a.greedy) {
+        best = __reduce_min_sync(~0u, best);
+        if (lane == 0) s.ats[warp] = best;
+        __syncthreads();
+        if (warp == 0) {
+          best = __reduce_min_sync(~0u, lane < kWarps ? s.ats[lane] : INT32_MAX);
+          if (lane < ranks) cluster.map_shared_rank(&s.x.at[side][0], lane)[rank] = best;
+        }
+        const int half = side;
+        mass = total(sum, &before);
+        token = INT32_MAX;
+        for (int k = 0; k < ranks; ++k) token = min(token, s.x.at[half][k]);
+      } else {
+        mass = total(sum, &before);
+        pick = true;
+        goal_total = mass;
+      }
+      if (draft) {
+        unsigned long long qmass = 0, unused;
+        sum = 0;
+        if (q.top > -INFINITY)
+          sweep<2>(q, a.vocab, q0, q1v, [&](int, const float(&z)[kVec]) {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum += whole(q.e(z[k]) * kOne);
+          });
+        // p's sums, for a node whose token comes from p itself.
+        const unsigned long long p_warp = s.sums[warp], p_end = s.sums[warp + 1], p_before = before;
+        qmass = total(sum, &unused);
+        cp = static_cast<float>(kUnit / static_cast<double>(mass));
+        const double q1 = qmass ? kUnit / static_cast<double>(qmass) : 0.0;
+        double left = kHalfUnit;
+        for (int c = node + 1; c < a.nodes; ++c) {
+          if (s.par[c] != node) continue;
+          const float pt = __fmul_rn(p.e(s.zp[c]), cp), qt = __fmul_rn(q.e(s.zq[c]), static_cast<float>(q1));
+          const double rt = level > 0.0 ? static_cast<double>(rest(s.zp[c], s.zq[c])) : static_cast<double>(pt);
+          if (static_cast<double>(s.u[c]) * static_cast<double>(qt) * left < rt * kHalfUnit) {
+            next = c;
+            token = s.tok[c];
+            pick = false;
+            break;
+          }
+          level += left / kHalfUnit;
+          cq = static_cast<float>(level * q1);
+          sum = 0;
+          sweep<2>(p, a.vocab, v0, v1, [&](int e0, const float(&zp)[kVec]) {
+            float zq[kVec];
+            q.load(e0, a.vocab, zq);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum += rest(zp[k], zq[k]);
+          });
+          unsigned long long rest_before;
+          goal_total = total(sum, &rest_before);
+          left = static_cast<double>(goal_total);
+          if (goal_total == 0) {
+            level = 0.0;
+            goal_total = mass;
+            break;
+          }
+          before = rest_before;
+        }
+        if (pick && level == 0.0) {   // p itself: its sums again
+          __syncthreads();
+          s.sums[warp] = p_warp;
+          if (warp == kWarps - 1) s.sums[kWarps] = p_end;
+          before = p_before;
+          __syncthreads();
+        }
+      }
+      if (pick) goal = threshold(u_node, goal_total);
+    }
+
+    // The warp that holds the token finds it; else the first one decides.
+    const bool mine = pick ? goal >= before + s.sums[warp] && goal < before + s.sums[warp + 1] : rank == 0 && warp == 0;
+    if (mine) {
+      float z_token = 0.f;
+      if (pick) {
+        unsigned long long run = before + s.sums[warp];
+        for (int v = v0; v < v1; v += 32) {
+          float zp[kVec], zq[kVec];
+          uint32_t w[kVec];
+          const bool real = v + lane < v1;
+          const int e0 = (v + lane) * kVec - p.shift();
+          unsigned long long x = 0;
+          if (real) p.load(e0, a.vocab, zp);
+          if (real && level > 0.0) q.load(e0, a.vocab, zq);
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) {
+            w[k] = !real ? 0 : level > 0.0 ? rest(zp[k], zq[k]) : weight(zp[k]);
+            x += w[k];
+          }
+          unsigned long long upto = x;
+          for (int o = 1; o < 32; o *= 2) {
+            const unsigned long long y = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const unsigned hit = __ballot_sync(~0u, run + upto > goal);
+          if (hit) {
+            const int who = __ffs(hit) - 1;
+            if (lane == who) {
+              unsigned long long at = run + upto - x;
+              bool open = true;
+#pragma unroll
+              for (int k = 0; k < kVec; ++k) {
+                at += w[k];
+                if (open && at > goal) token = e0 + k, z_token = zp[k], open = false;
+              }
+            }
+            token = __shfl_sync(~0u, token, who);
+            z_token = __shfl_sync(~0u, z_token, who);
+            break;
+          }
+          run += __shfl_sync(~0u, upto, 31);
+        }
+      } else if (token >= 0) {
+        z_token = p.z(p.x[token]);
+      }
+      if (!draft && token >= 0)
+        for (int c = a.nodes - 1; c > node; --c)
+          if (s.par[c] == node && s.tok[c] == token) next = c;
+      if (dead) {
+        if (lane == 0) __stcg(res.state + row0 + node, -1);
+        arrive(a, res, s, b);
+      } else {
+        const float lp = token < 0 ? 0.f : __fsub_rn(z_token, p.top) - logf(static_cast<float>(mass) * 9.31322574615478515625e-10f);
+        decide(a, res, s, b, node, next, token, lp);
+      }
+    }
+    __syncthreads();   // the row's lists may be written again
+    i += clusters;
+  }
+  cluster.sync();      // no block leaves while another may still write to its shared memory
+}
+
+template <typename T>
+cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t s) {
+  // Few rows: more blocks for each; never more than the SMs hold at once.
+  const int64_t rows = static_cast<int64_t>(a.batch) * a.nodes;
+  int ranks = kMaxCluster;
+  while (ranks > 2 && rows * ranks > a.num_sms) ranks /= 2;
+  const int64_t most = a.num_sms / ranks;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows < most ? rows : most) * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T>, a);
+}
+
 }  // namespace
 
+size_t verify_workspace_bytes(int batch, int nodes) {
+  return (3 * static_cast<size_t>(batch) * nodes + batch + 1) * sizeof(int);
+}
+
 cudaError_t launch_verify_draft(const VerifyArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == TF_F32) verify_draft_kernel<float><<<a.batch, kThreads, 0, s>>>(a);
-  if (dtype == TF_F16) verify_draft_kernel<__half><<<a.batch, kThreads, 0, s>>>(a);
-  if (dtype == TF_BF16) verify_draft_kernel<__nv_bfloat16><<<a.batch, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (dtype == TF_F32) return launch_typed<float>(a, s);
+  return dtype == TF_F16 ? launch_typed<__half>(a, s) : launch_typed<__nv_bfloat16>(a, s);
 }
 
 }  // namespace tfx
