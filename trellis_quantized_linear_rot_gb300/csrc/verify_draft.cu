@@ -20,6 +20,8 @@
 // sequence's last row follows the decisions and writes the outputs.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "spec.cuh"
 
 namespace cg = cooperative_groups;
@@ -34,6 +36,15 @@ constexpr double kHalfUnit = 2147483648.0;           // 2^31: the normalised row
 
 __device__ __forceinline__ uint32_t whole(float x) { return __float2uint_rn(x); }   // a NaN becomes 0
 
+template <typename T>
+__device__ __forceinline__ T lowest();   // -inf
+template <>
+__device__ __forceinline__ float lowest<float>() { return -INFINITY; }
+template <>
+__device__ __forceinline__ __half lowest<__half>() { return __ushort_as_half(0xFC00); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 lowest<__nv_bfloat16>() { return __ushort_as_bfloat16(0xFF80); }
+
 // A row of logits: z = x / T, and e = exp(z - max z). The row's vectors of 16
 // bytes are numbered from the aligned address at or before its first element;
 // element k of vector v is number v * kVec + k - shift.
@@ -47,28 +58,28 @@ struct Row {
     return static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   }
   __device__ __forceinline__ float z(T v) const { return __fmul_rn(to_f32(v), inv); }
+  // kFinite: the maximum is (else it is +inf, and its own places alone count).
+  template <bool kFinite>
   __device__ __forceinline__ float e(float z) const {
-    if (fabsf(top) == INFINITY) return z == top && top > 0.f ? 1.f : 0.f;
+    if (!kFinite) return z == top ? 1.f : 0.f;
     return expf(__fsub_rn(z, top));
   }
+  __device__ __forceinline__ float e(float z) const { return top < INFINITY ? e<true>(z) : e<false>(z); }
   __device__ __forceinline__ int vectors(int vocab) const { return (vocab + shift() + kVec - 1) / kVec; }
   // kVec elements from number i on, those outside [0, vocab) as -inf.
-  __device__ __forceinline__ void load(int i, int vocab, float (&z_out)[kVec]) const {
-    T v[kVec];
+  __device__ __forceinline__ void load(int i, int vocab, T (&v)[kVec]) const {
     if (i >= 0 && i + kVec <= vocab && (reinterpret_cast<uintptr_t>(x + i) & 15) == 0) {
       *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(x + i);
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) z_out[k] = z(v[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) z_out[k] = i + k >= 0 && i + k < vocab ? z(x[i + k]) : -INFINITY;
+      for (int k = 0; k < kVec; ++k) v[k] = i + k >= 0 && i + k < vocab ? x[i + k] : lowest<T>();
     }
   }
 };
 
-// A warp's part [v0, v1) of a row's vectors: f(number of the first element, z)
-// for each. Whole vectors come kAhead a lane at a time, so that their loads
-// are in flight together; the row's first and last vector may be cut.
+// A warp's part [v0, v1) of a row's vectors: f(number of the first element,
+// the elements) for each. Whole vectors come kAhead a lane at a time, so that
+// their loads are in flight together; the row's first and last may be cut.
 template <int kAhead, typename T, typename F>
 __device__ __forceinline__ void sweep(const Row<T>& r, int vocab, int v0, int v1, F f) {
   constexpr int kVec = Row<T>::kVec;
@@ -76,38 +87,93 @@ __device__ __forceinline__ void sweep(const Row<T>& r, int vocab, int v0, int v1
   const int f0 = max(v0, shift ? 1 : 0), f1 = min(v1, (vocab + shift) / kVec);   // whole ones
   const uint4* base = reinterpret_cast<const uint4*>(r.x - shift);
   int v = f0 + lane;
+  alignas(16) T x[kVec];
   for (; v + 32 * (kAhead - 1) < f1; v += 32 * kAhead) {
     uint4 raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) raw[u] = base[v + 32 * u];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const T* x = reinterpret_cast<const T*>(&raw[u]);
-      float z[kVec];
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) z[k] = r.z(x[k]);
-      f((v + 32 * u) * kVec - shift, z);
+      *reinterpret_cast<uint4*>(x) = raw[u];
+      f((v + 32 * u) * kVec - shift, x);
     }
   }
   for (; v < f1; v += 32) {
-    const uint4 raw = base[v];
-    const T* x = reinterpret_cast<const T*>(&raw);
-    float z[kVec];
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) z[k] = r.z(x[k]);
-    f(v * kVec - shift, z);
+    *reinterpret_cast<uint4*>(x) = base[v];
+    f(v * kVec - shift, x);
   }
-  if (lane == 0) {
-    float z[kVec];
-    if (v0 < f0 && v0 < v1) {
-      r.load(v0 * kVec - shift, vocab, z);
-      f(v0 * kVec - shift, z);
+  if (lane == 0 && v0 < v1) {
+    if (v0 < f0) {
+      r.load(v0 * kVec - shift, vocab, x);
+      f(v0 * kVec - shift, x);
     }
     if (f1 < v1 && v1 - 1 >= f0) {
-      r.load((v1 - 1) * kVec - shift, vocab, z);
-      f((v1 - 1) * kVec - shift, z);
+      r.load((v1 - 1) * kVec - shift, vocab, x);
+      f((v1 - 1) * kVec - shift, x);
     }
   }
+}
+
+// The largest element so far, NaNs left out. z grows with x, so the largest z
+// is that of the largest x, and 16-bit types are compared two at a time.
+struct Largest32 {
+  float top = -INFINITY;
+  __device__ __forceinline__ void add(const float (&x)[4]) {
+    top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+  }
+  __device__ __forceinline__ float get() const { return top; }
+};
+template <typename T, typename T2>
+struct Largest16 {
+  T2 top;
+  __device__ Largest16() { top.x = top.y = lowest<T>(); }
+  __device__ __forceinline__ void add(const T (&x)[8]) {
+    const T2* y = reinterpret_cast<const T2*>(x);
+    top = __hmax2(top, __hmax2(__hmax2(y[0], y[1]), __hmax2(y[2], y[3])));
+  }
+  __device__ __forceinline__ float get() const { return fmaxf(to_f32(top.x), to_f32(top.y)); }
+};
+template <typename T>
+struct Largest;
+template <>
+struct Largest<float> : Largest32 {};
+template <>
+struct Largest<__half> : Largest16<__half, __half2> {};
+template <>
+struct Largest<__nv_bfloat16> : Largest16<__nv_bfloat16, __nv_bfloat162> {};
+
+// A warp's sum of the weights of its part of a row.
+template <typename T, bool kFinite>
+__device__ __forceinline__ unsigned long long sum_weights(const Row<T>& r, int vocab, int lo, int hi) {
+  unsigned long long sum = 0;
+  sweep<kFinite ? 2 : 1>(r, vocab, lo, hi, [&](int, const T(&x)[Row<T>::kVec]) {
+#pragma unroll
+    for (int k = 0; k < Row<T>::kVec; ++k) sum += whole(r.template e<kFinite>(r.z(x[k])) * kOne);
+  });
+  return sum;
+}
+
+// What is left of p over a draft distribution q, in units of 2^-31.
+struct Rest {
+  float cp, cq;
+  __device__ __forceinline__ uint32_t operator()(float ep, float eq) const {
+    const uint32_t x = whole(__fmul_rn(ep, cp)), y = whole(__fmul_rn(eq, cq));
+    return x > y ? x - y : 0;
+  }
+};
+template <typename T, bool kFinite>
+__device__ __forceinline__ unsigned long long sum_rest(const Row<T>& p, const Row<T>& q, const Rest& rest, int vocab,
+                                                       int lo, int hi) {
+  unsigned long long sum = 0;
+  sweep<kFinite ? 2 : 1>(p, vocab, lo, hi, [&](int e0, const T(&x)[Row<T>::kVec]) {
+    alignas(16) T y[Row<T>::kVec];
+    q.load(e0, vocab, y);
+#pragma unroll
+    for (int k = 0; k < Row<T>::kVec; ++k)
+      sum += kFinite ? rest(p.template e<true>(p.z(x[k])), q.template e<true>(q.z(y[k])))
+                     : rest(p.e(p.z(x[k])), q.top > -INFINITY ? q.e(q.z(y[k])) : 0.f);
+  });
+  return sum;
 }
 
 // What the blocks of a cluster tell one another, twice so that an exchange
@@ -121,6 +187,7 @@ struct Exchange {
 struct Shared {
   Exchange x;
   unsigned long long sums[kWarps + 1];   // weight before each warp of this block, and all of it
+  unsigned long long fine[kWarps];
   float tops[kWarps], qtops[kWarps];
   int ats[kWarps];
   int par[TF_MAX_NODES], tok[TF_MAX_NODES];
@@ -240,10 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     return sum;
   };
 
-  auto part_of = [&](int vecs, int* lo, int* hi) {
+  auto part_of = [&](int vecs, int* lo, int* hi, int w) {
     const int per_block = (vecs + ranks - 1) / ranks, b0 = min(vecs, rank * per_block), b1 = min(vecs, b0 + per_block);
     const int per_warp = (b1 - b0 + kWarps - 1) / kWarps;
-    *lo = min(b1, b0 + warp * per_warp);
+    *lo = min(b1, b0 + w * per_warp);
     *hi = min(b1, *lo + per_warp);
   };
 
@@ -307,20 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
 
     // This warp's vectors of each row.
     int v0, v1, q0, q1v;
-    part_of(p.vectors(a.vocab), &v0, &v1);
-    part_of(q.vectors(a.vocab), &q0, &q1v);
+    part_of(p.vectors(a.vocab), &v0, &v1, warp);
+    part_of(q.vectors(a.vocab), &q0, &q1v, warp);
 
     // Maxima.
-    float top = -INFINITY, qtop = -INFINITY;
-    sweep<8>(p, a.vocab, v0, v1, [&](int, const float(&z)[kVec]) {
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) top = fmaxf(top, z[k]);
-    });
-    if (draft)
-      sweep<8>(q, a.vocab, q0, q1v, [&](int, const float(&z)[kVec]) {
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) qtop = fmaxf(qtop, z[k]);
-      });
+    Largest<T> most, qmost;
+    sweep<8>(p, a.vocab, v0, v1, [&](int, const T(&x)[kVec]) { most.add(x); });
+    if (draft) sweep<8>(q, a.vocab, q0, q1v, [&](int, const T(&x)[kVec]) { qmost.add(x); });
+    float top = __fmul_rn(most.get(), a.inv_temp), qtop = __fmul_rn(qmost.get(), a.inv_temp);
     for (int o = 16; o; o >>= 1) {
       top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
       qtop = fmaxf(qtop, __shfl_xor_sync(~0u, qtop, o));
@@ -352,25 +413,19 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     int next = -1, token = -1;
     unsigned long long mass = 0, before = 0;
     bool pick = false;   // the token is still to be found by its cumulative weight
-    float cp = 0.f, cq = 0.f;
+    Rest rest{0.f, 0.f};
     double level = 0.0;
-    auto weight = [&](float z) -> uint32_t { return whole(p.e(z) * kOne); };
-    auto rest = [&](float zp, float zq) -> uint32_t {
-      const uint32_t x = whole(__fmul_rn(p.e(zp), cp)), y = whole(__fmul_rn(q.e(zq), cq));
-      return x > y ? x - y : 0;
-    };
     unsigned long long goal = 0, goal_total = 0;
     if (!dead && p.top > -INFINITY) {
-      unsigned long long sum = 0;
-      int best = INT32_MAX;
-      sweep<2>(p, a.vocab, v0, v1, [&](int e0, const float(&z)[kVec]) {
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-          sum += weight(z[k]);
-          if (a.greedy && z[k] == p.top) best = min(best, e0 + k);
-        }
-      });
+      const unsigned long long sum = p.top < INFINITY ? sum_weights<T, true>(p, a.vocab, v0, v1)
+                                                      : sum_weights<T, false>(p, a.vocab, v0, v1);
       if (a.greedy) {
+        int best = INT32_MAX;
+        sweep<2>(p, a.vocab, v0, v1, [&](int e0, const T(&x)[kVec]) {
+#pragma unroll
+          for (int k = kVec - 1; k >= 0; --k)
+            if (p.z(x[k]) == p.top) best = min(best, e0 + k);
+        });
         best = __reduce_min_sync(~0u, best);
         if (lane == 0) s.ats[warp] = best;
         __syncthreads();
@@ -388,23 +443,22 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
         goal_total = mass;
       }
       if (draft) {
-        unsigned long long qmass = 0, unused;
-        sum = 0;
-        if (q.top > -INFINITY)
-          sweep<2>(q, a.vocab, q0, q1v, [&](int, const float(&z)[kVec]) {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) sum += whole(q.e(z[k]) * kOne);
-          });
+        unsigned long long unused;
+        const unsigned long long q_sum = q.top == -INFINITY ? 0
+                                         : q.top < INFINITY ? sum_weights<T, true>(q, a.vocab, q0, q1v)
+                                                            : sum_weights<T, false>(q, a.vocab, q0, q1v);
         // p's sums, for a node whose token comes from p itself.
         const unsigned long long p_warp = s.sums[warp], p_end = s.sums[warp + 1], p_before = before;
-        qmass = total(sum, &unused);
-        cp = static_cast<float>(kUnit / static_cast<double>(mass));
+        const unsigned long long qmass = total(q_sum, &unused);
+        rest.cp = static_cast<float>(kUnit / static_cast<double>(mass));
         const double q1 = qmass ? kUnit / static_cast<double>(qmass) : 0.0;
         double left = kHalfUnit;
         for (int c = node + 1; c < a.nodes; ++c) {
           if (s.par[c] != node) continue;
-          const float pt = __fmul_rn(p.e(s.zp[c]), cp), qt = __fmul_rn(q.e(s.zq[c]), static_cast<float>(q1));
-          const double rt = level > 0.0 ? static_cast<double>(rest(s.zp[c], s.zq[c])) : static_cast<double>(pt);
+          const float ep = isnan(s.zp[c]) ? 0.f : p.e(s.zp[c]);
+          const float eq = isnan(s.zq[c]) || q.top == -INFINITY ? 0.f : q.e(s.zq[c]);
+          const float pt = __fmul_rn(ep, rest.cp), qt = __fmul_rn(eq, static_cast<float>(q1));
+          const double rt = level > 0.0 ? static_cast<double>(rest(ep, eq)) : static_cast<double>(pt);
           if (static_cast<double>(s.u[c]) * static_cast<double>(qt) * left < rt * kHalfUnit) {
             next = c;
             token = s.tok[c];
@@ -412,16 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
             break;
           }
           level += left / kHalfUnit;
-          cq = static_cast<float>(level * q1);
-          sum = 0;
-          sweep<2>(p, a.vocab, v0, v1, [&](int e0, const float(&zp)[kVec]) {
-            float zq[kVec];
-            q.load(e0, a.vocab, zq);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) sum += rest(zp[k], zq[k]);
-          });
+          rest.cq = static_cast<float>(level * q1);
           unsigned long long rest_before;
-          goal_total = total(sum, &rest_before);
+          const bool finite = p.top < INFINITY && fabsf(q.top) < INFINITY;
+          goal_total = total(finite ? sum_rest<T, true>(p, q, rest, a.vocab, v0, v1)
+                                    : sum_rest<T, false>(p, q, rest, a.vocab, v0, v1), &rest_before);
           left = static_cast<double>(goal_total);
           if (goal_total == 0) {
             level = 0.0;
@@ -441,51 +490,77 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
       if (pick) goal = threshold(u_node, goal_total);
     }
 
-    // The warp that holds the token finds it; else the first one decides.
-    const bool mine = pick ? goal >= before + s.sums[warp] && goal < before + s.sums[warp + 1] : rank == 0 && warp == 0;
-    if (mine) {
-      float z_token = 0.f;
-      if (pick) {
-        unsigned long long run = before + s.sums[warp];
-        for (int v = v0; v < v1; v += 32) {
-          float zp[kVec], zq[kVec];
-          uint32_t w[kVec];
-          const bool real = v + lane < v1;
-          const int e0 = (v + lane) * kVec - p.shift();
-          unsigned long long x = 0;
-          if (real) p.load(e0, a.vocab, zp);
-          if (real && level > 0.0) q.load(e0, a.vocab, zq);
+    // The block that holds the token finds it: the part of one warp is shared
+    // out among all its warps, then the part of one of those is looked through.
+    bool mine = rank == 0 && warp == 0;   // the warp that writes the decision
+    float z_token = 0.f;
+    if (pick) {
+      mine = false;
+      const bool here = goal >= before && goal < before + s.sums[kWarps];
+      if (here) {
+        int w = 0;
+        while (goal >= before + s.sums[w + 1]) ++w;
+        unsigned long long run = before + s.sums[w];
+        int lo, hi;
+        part_of(p.vectors(a.vocab), &lo, &hi, w);
+        const int per = (hi - lo + kWarps - 1) / kWarps;
+        lo = min(hi, lo + warp * per);
+        hi = min(hi, lo + per);
+        uint32_t weights[kVec];
+        alignas(16) T x[kVec];
+        alignas(16) T y[kVec];
+        auto weigh = [&](int v) {   // weights of vector v, and their sum
+          unsigned long long sum = 0;
+          const int e0 = v * kVec - p.shift();
+          p.load(e0, a.vocab, x);
+          if (level > 0.0) q.load(e0, a.vocab, y);
 #pragma unroll
           for (int k = 0; k < kVec; ++k) {
-            w[k] = !real ? 0 : level > 0.0 ? rest(zp[k], zq[k]) : weight(zp[k]);
-            x += w[k];
+            const float ep = p.e(p.z(x[k]));
+            weights[k] = level > 0.0 ? rest(ep, q.top > -INFINITY ? q.e(q.z(y[k])) : 0.f) : whole(ep * kOne);
+            sum += weights[k];
           }
-          unsigned long long upto = x;
-          for (int o = 1; o < 32; o *= 2) {
-            const unsigned long long y = __shfl_up_sync(~0u, upto, o);
-            if (lane >= o) upto += y;
-          }
-          const unsigned hit = __ballot_sync(~0u, run + upto > goal);
-          if (hit) {
-            const int who = __ffs(hit) - 1;
-            if (lane == who) {
-              unsigned long long at = run + upto - x;
-              bool open = true;
-#pragma unroll
-              for (int k = 0; k < kVec; ++k) {
-                at += w[k];
-                if (open && at > goal) token = e0 + k, z_token = zp[k], open = false;
-              }
+          return sum;
+        };
+        unsigned long long sum = 0;
+        for (int v = lo + lane; v < hi; v += 32) sum += weigh(v);
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) s.fine[warp] = sum;
+        __syncthreads();
+        for (int k = 0; k < warp; ++k) run += s.fine[k];
+        mine = goal >= run && goal < run + s.fine[warp];
+        if (mine) {
+          for (int v = lo; v < hi; v += 32) {
+            const unsigned long long own = v + lane < hi ? weigh(v + lane) : 0;
+            unsigned long long upto = own;
+            for (int o = 1; o < 32; o *= 2) {
+              const unsigned long long z = __shfl_up_sync(~0u, upto, o);
+              if (lane >= o) upto += z;
             }
-            token = __shfl_sync(~0u, token, who);
-            z_token = __shfl_sync(~0u, z_token, who);
-            break;
+            const unsigned hit = __ballot_sync(~0u, run + upto > goal);
+            if (hit) {
+              const int who = __ffs(hit) - 1;
+              if (lane == who) {
+                unsigned long long at = run + upto - own;
+                bool open = true;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                  at += weights[k];
+                  if (open && at > goal) token = (v + lane) * kVec - p.shift() + k, z_token = p.z(x[k]), open = false;
+                }
+              }
+              token = __shfl_sync(~0u, token, who);
+              z_token = __shfl_sync(~0u, z_token, who);
+              break;
+            }
+            run += __shfl_sync(~0u, upto, 31);
           }
-          run += __shfl_sync(~0u, upto, 31);
         }
-      } else if (token >= 0) {
-        z_token = p.z(p.x[token]);
       }
+    } else if (mine && token >= 0) {
+      z_token = p.z(p.x[token]);
+    }
+    if (mine) {
       if (!draft && token >= 0)
         for (int c = a.nodes - 1; c > node; --c)
           if (s.par[c] == node && s.tok[c] == token) next = c;
