@@ -6,18 +6,18 @@
 // nor on how a row is split.
 //
 // What a node decides (the child it goes on to, or the token sampled) depends
-// on its own rows of logits only, so the nodes can be taken in any order, and
-// the answer is the chain of decisions from node 0. A cluster of blocks takes
-// a node: each block a part of the vocabulary, with one exchange through
-// distributed shared memory for the maximum, one for the sum and one for each
-// refusal's rest; the row is read from memory once and again from the L1
-// cache. The clusters go through the rows node by node (all sequences' node
-// 0, then their node 1, ..), and before a cluster takes a row it looks
-// whether the parent has been decided against it: then the row is passed over
-// unread, and so are its descendants. Nothing waits for a decision: few rows
-// are all taken at once, in the time of one, and of many only little more
-// than those on the accepted paths are read. The block that completes a
-// sequence's last row follows the decisions and writes the outputs.
+// on its own rows of logits only. A cluster of blocks takes a node: each block
+// a part of the vocabulary, with one exchange through distributed shared
+// memory for the maximum, one for the sum and one for each refusal's rest; the
+// row is read from memory once and again from the L1 cache or L2. What bounds
+// a row is the arithmetic of exp (about 15 instructions an element and pass)
+// and the latency of the exchanges.
+//
+// With no more rows than SMs, every row is taken at once by a cluster of its
+// own, in the time of one row, and the block that completes a sequence's last
+// row follows the decisions from node 0 and writes the outputs. With more, a
+// cluster takes a sequence and walks down its tree, so that only the rows on
+// the accepted path are read.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -193,13 +193,14 @@ struct Shared {
   int par[TF_MAX_NODES], tok[TF_MAX_NODES];
   float zp[TF_MAX_NODES], zq[TF_MAX_NODES];   // logits of the node's children's tokens
   float u[TF_MAX_NODES];
-  int next_row;
+  int next_node;
   int state[TF_MAX_NODES], out_tok[TF_MAX_NODES];
   float out_lp[TF_MAX_NODES];
 };
 
-// Decisions in the workspace: 0 while open, -1 for a row that cannot be on
-// the path, else the child gone on to + 2 (1: none). A call leaves all zero.
+// Decisions in the workspace, one for each row: the child gone on to + 2 (1:
+// none, -1: the row's node is absent), the token and its log-probability; and
+// the rows arrived of each sequence. A call leaves all zero.
 struct Results {
   int* state;
   int* token;
@@ -253,28 +254,14 @@ __device__ void arrive(const VerifyArgs& a, const Results& r, Shared& s, int b) 
   }
 }
 
-// One warp: writes a row's decision.
-__device__ void decide(const VerifyArgs& a, const Results& r, Shared& s, int b, int node, int next, int token,
-                       float logprob) {
-  if (threadIdx.x % 32 == 0) {
-    const int64_t row = static_cast<int64_t>(b) * a.nodes + node;
-    __stcg(r.token + row, token);
-    __stcg(r.logprob + row, logprob);
-    __stcg(r.state + row, next + 2);
-  }
-  arrive(a, r, s, b);
-}
-
-template <typename T>
+template <typename T, bool kWalk>
 __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
-  const int clusters = gridDim.x / ranks, cluster_id = blockIdx.x / ranks;
+  const int ranks = cluster.num_blocks(), rank = cluster.block_rank(), id = blockIdx.x / ranks;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int rows = a.batch * a.nodes;   // row i: node i / batch of sequence i % batch
-  const Results res{a.work, a.work + rows, reinterpret_cast<float*>(a.work + 2 * static_cast<size_t>(rows)),
-                    a.work + 3 * static_cast<size_t>(rows)};
+  const int b = kWalk ? id : id / a.nodes;
+  const int64_t row0 = static_cast<int64_t>(b) * a.nodes;
   int side = 0;   // which half of the exchange is next
   constexpr int kVec = Row<T>::kVec;
 
@@ -314,46 +301,13 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     *hi = min(b1, *lo + per_warp);
   };
 
+  const bool draft = a.draft != nullptr;
+  int count = 0;   // nodes gone through (a walk)
 #pragma unroll 1
-  for (int i = cluster_id; i < rows;) {
-    // Before any row but the first: the next one that is not decided against.
-    if (i != cluster_id) {
-      if (rank == 0 && warp == 0) {
-        int found = rows;
-        for (int base = i; base < rows && found == rows; base += 32 * clusters) {
-          const int64_t k = base + static_cast<int64_t>(lane) * clusters;
-          bool dead = false;
-          int node = 0, b = 0;
-          if (k < rows) {
-            node = static_cast<int>(k) / a.batch, b = static_cast<int>(k) % a.batch;
-            if (node > 0) {
-              const int p = a.parents[b * a.stride_parents + node];
-              if (p < 0) {
-                dead = true;
-              } else if (p < node) {
-                const int st = __ldcg(res.state + static_cast<int64_t>(b) * a.nodes + p);
-                dead = st != 0 && st != node + 2;
-              }
-            }
-          }
-          const unsigned live = __ballot_sync(~0u, k < rows && !dead);
-          const int first = live ? __ffs(live) - 1 : 32;
-          if (dead && lane < first) __stcg(res.state + static_cast<int64_t>(b) * a.nodes + node, -1);
-          for (unsigned gone = __ballot_sync(~0u, dead && lane < first); gone; gone &= gone - 1)
-            arrive(a, res, s, __shfl_sync(~0u, b, __ffs(gone) - 1));
-          if (live) found = base + first * clusters;
-        }
-        if (lane < ranks) cluster.map_shared_rank(&s.next_row, lane)[0] = found;
-      }
-      cluster.sync();
-      i = s.next_row;
-      if (i >= rows) break;
-    }
-    const int node = i / a.batch, b = i - node * a.batch;
-    const int64_t row0 = static_cast<int64_t>(b) * a.nodes;
-    const bool draft = a.draft != nullptr;
+  for (int node = kWalk ? 0 : id - b * a.nodes; node >= 0;) {
     Row<T> p{static_cast<const T*>(a.logits) + b * a.seq + node * a.node, a.inv_temp, 0.f};
     Row<T> q{draft ? static_cast<const T*>(a.draft) + b * a.draft_seq + node * a.draft_node : p.x, a.inv_temp, 0.f};
+    bool child = false;
     const float u_node = a.greedy ? 0.f : a.u_sample[row0 + node];
     if (tid < a.nodes) {
       int up = a.parents[b * a.stride_parents + tid];
@@ -362,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
         if (tid == node) record_index_error(a.err);
         up = -2;
       }
-      const bool child = up == node && tid > node && t >= 0 && t < a.vocab;
+      child = up == node && tid > node && t >= 0 && t < a.vocab;
       s.par[tid] = tid == node ? up : (child ? node : -2);   // children that may be asked, and the row's own
       s.tok[tid] = t;
       if (draft) s.u[tid] = a.u_accept[row0 + tid];
@@ -380,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     // Maxima.
     Largest<T> most, qmost;
     sweep<8>(p, a.vocab, v0, v1, [&](int, const T(&x)[kVec]) { most.add(x); });
-    if (draft) sweep<8>(q, a.vocab, q0, q1v, [&](int, const T(&x)[kVec]) { qmost.add(x); });
+    const bool ask = __syncthreads_or(child) && draft;   // a leaf has no use for the draft's row
+    if (ask) sweep<8>(q, a.vocab, q0, q1v, [&](int, const T(&x)[kVec]) { qmost.add(x); });
     float top = __fmul_rn(most.get(), a.inv_temp), qtop = __fmul_rn(qmost.get(), a.inv_temp);
     for (int o = 16; o; o >>= 1) {
       top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -442,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
         pick = true;
         goal_total = mass;
       }
-      if (draft) {
+      if (ask) {
         unsigned long long unused;
         const unsigned long long q_sum = q.top == -INFINITY ? 0
                                          : q.top < INFINITY ? sum_weights<T, true>(q, a.vocab, q0, q1v)
@@ -564,29 +519,57 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
       if (!draft && token >= 0)
         for (int c = a.nodes - 1; c > node; --c)
           if (s.par[c] == node && s.tok[c] == token) next = c;
-      if (dead) {
-        if (lane == 0) __stcg(res.state + row0 + node, -1);
+      if (lane == 0) {
+        const float logprob = token < 0 ? 0.f
+                                        : __fsub_rn(z_token, p.top) -
+                                              logf(static_cast<float>(mass) * 9.31322574615478515625e-10f);
+        if (kWalk) {
+          if (!dead) {
+            a.path[row0 + count] = node;
+            a.out_tokens[row0 + count] = token;
+            a.logprobs[row0 + count] = logprob;
+          }
+        } else {
+          const size_t rows = static_cast<size_t>(a.batch) * a.nodes;
+          __stcg(a.work + row0 + node, dead ? -1 : next + 2);
+          __stcg(a.work + rows + row0 + node, token);
+          __stcg(reinterpret_cast<float*>(a.work + 2 * rows) + row0 + node, logprob);
+        }
+      }
+      if (!kWalk) {
+        const size_t rows = static_cast<size_t>(a.batch) * a.nodes;
+        const Results res{a.work, a.work + rows, reinterpret_cast<float*>(a.work + 2 * rows), a.work + 3 * rows};
         arrive(a, res, s, b);
-      } else {
-        const float lp = token < 0 ? 0.f : __fsub_rn(z_token, p.top) - logf(static_cast<float>(mass) * 9.31322574615478515625e-10f);
-        decide(a, res, s, b, node, next, token, lp);
+      } else if (lane < ranks) {
+        cluster.map_shared_rank(&s.next_node, lane)[0] = next;
       }
     }
-    __syncthreads();   // the row's lists may be written again
-    i += clusters;
+    if (!kWalk) break;
+    if (!dead) ++count;
+    cluster.sync();   // the next node is known; the row's lists may be written again
+    node = s.next_node;
   }
-  cluster.sync();      // no block leaves while another may still write to its shared memory
+  if (kWalk && rank == 0) {
+    if (tid == 0) a.counts[b] = count;
+    for (int k = count + tid; k < a.nodes; k += kThreads) {
+      a.path[row0 + k] = -1;
+      a.out_tokens[row0 + k] = -1;
+      a.logprobs[row0 + k] = 0.f;
+    }
+  }
+  cluster.sync();     // no block leaves while another may still write to its shared memory
 }
 
 template <typename T>
 cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t s) {
-  // Few rows: more blocks for each; never more than the SMs hold at once.
+  // One block an SM: as many blocks for a cluster as leave every cluster its place.
   const int64_t rows = static_cast<int64_t>(a.batch) * a.nodes;
+  const bool walk = rows > a.num_sms;
+  const int64_t clusters = walk ? a.batch : rows;
   int ranks = kMaxCluster;
-  while (ranks > 2 && rows * ranks > a.num_sms) ranks /= 2;
-  const int64_t most = a.num_sms / ranks;
+  while (ranks > 1 && clusters * ranks > a.num_sms) ranks /= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows < most ? rows : most) * ranks));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -595,7 +578,8 @@ cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T>, a);
+  return walk ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, true>, a)
+              : cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, false>, a);
 }
 
 }  // namespace
