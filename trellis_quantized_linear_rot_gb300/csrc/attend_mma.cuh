@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
         }
         __syncthreads();
         if (last_here)
-          join_parts<T, kRows, D, kThreads>(a, line, masks, cur.b, kvh, row0, rows, cur.first, cur.nt, idle);
+          join_parts<T, kRows, D, kThreads>(a, line, masks, cur.b, kvh, row0, rows, cur.first, cur.nt, idle, tid);
       }
       fresh = true;
       __syncthreads();   // the masks and the stage may be written again

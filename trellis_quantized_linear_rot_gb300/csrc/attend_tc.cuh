@@ -1,0 +1,620 @@
+// Tree attention with tcgen05: more than 16 rows a kv head.
+//
+// With R rows a kv head the call does R operations a byte of the cache. A tile
+// of 128 rows costs the tensor cores about 1,000 cycles for 128 keys (two
+// products of 128 x 128 x 128) whether its rows are used or not, and memory
+// about 2,800 cycles (64 KB at this SM's share), so up to one full tile of
+// rows the cache's bytes bound it, and with several the tensor cores and the
+// exponentials (128 x 128 a tile, 16 a cycle: as long as the products).
+//
+// One block an SM, a run of tiles each (attend_work.cuh). An item is a
+// (sequence, kv head, block of whole nodes with at most 128 rows). Its key
+// tiles go alternately to two streams, each with its own scores, weights,
+// sums and running maximum in Tensor Memory and registers, so that one
+// stream's products run while the other's exponentials do:
+//   warp 0        copies: q of an item; keys and values of a tile, a box for
+//                 each page or part of one, three tiles in flight
+//   warps 1, 2    products of stream 0 and 1: S = Q K^T into Tensor Memory;
+//                 O += P V with P from Tensor Memory
+//   warps 4-7, 8-11  weights of stream 0 and 1, one thread a row: maximum,
+//                 exponentials, P over S in Tensor Memory. A row's sums are
+//                 rescaled only when its maximum has risen by more than 2^8
+//                 (weights of up to 2^8 lose nothing in either dtype), which
+//                 after the first tiles is rare
+// At an item's end the two streams are joined, each group of warps taking
+// half of the columns. All waits are bounded.
+#pragma once
+
+#include "attend_mma.cuh"
+
+namespace tfx {
+
+// D[tmem] (+)= A B: A and B in shared memory, or A in Tensor Memory. One
+// issuing thread.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+// Instruction descriptor: idesc_f16_f32 with the operands' type and, for the
+// second product, a B whose rows (keys) run along the other axis.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_by_keys) {
+  const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+  return idesc_f16_f32(128, n) | (type << 7) | (type << 10) | (b_by_keys ? 1u << 16 : 0u);
+}
+// Shared-memory descriptor of values as B: 128-byte rows (64 columns) a key
+// with the 128-byte swizzle, groups of 8 keys 1,024 bytes apart, the next 64
+// columns `next` bytes on.
+__device__ __forceinline__ uint64_t desc_by_keys(uint32_t at, uint32_t next) {
+  return (smem_desc_sw128(at, 1024) & ~(0xFFFFull << 16)) | (static_cast<uint64_t>(next >> 4) << 16);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// 32 columns of this thread's Tensor Memory lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+enum TcBarrier { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 3, kVFull = kKEmpty + 3, kVEmpty = kVFull + 3,
+                 kSFull = kVEmpty + 3, kPFull = kSFull + 2, kPvDone = kPFull + 2, kBarriers = kPvDone + 2 };
+
+struct TcShared {
+  unsigned long long bars[kBarriers];
+  float row_max[2][128], row_sum[2][128];   // of the streams, at an item's end
+  uint32_t gone[3][4];                      // keys of a stage whose page is outside the pool
+  uint32_t bad[2][4];                       // keys of a stream's tile with values that are not finite
+  int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
+  int scratch[384 / 32 + 2];
+  uint32_t tmem;
+  int abort, last_here;
+};
+
+template <int D>
+struct TcShape {
+  static constexpr int kThreads = 384;
+  static constexpr int kTile = 128;
+  static constexpr int kParts = D / 64;                  // 64-column parts of a tile
+  static constexpr int kPartBytes = kTile * 128;         // one part of q, keys or values
+  static constexpr int kTileBytes = kParts * kPartBytes;
+  static constexpr int kStages = 3;
+  static constexpr int kShared = (1 + 2 * kStages) * kTileBytes;   // where TcShared begins
+  static constexpr int kSmem = kShared + static_cast<int>(sizeof(TcShared));
+  static_assert(kSmem <= 232448, "a block has 227 KB");
+  // Tensor Memory columns: scores of the streams (weights over them), sums.
+  static constexpr int kScores = 0, kSums = 256, kColumns = 512;
+};
+
+// Node i's row of the tree: the nodes it sees, walked up from the parents.
+struct Seen {
+  uint32_t w[4];
+};
+__device__ __forceinline__ Seen seen_by(const int16_t* up, int node) {
+  Seen s = {{0, 0, 0, 0}};
+  for (int i = node; i >= 0 && up[i] >= -1; i = up[i])
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i >> 5 == x) s.w[x] |= 1u << (i & 31);
+  return s;
+}
+// What join_parts asks: whether a node is present.
+struct Presence {
+  const int16_t* up;
+  __device__ __forceinline__ bool sees(int i, int) const { return up[i] >= -1; }
+};
+
+struct TcMaps {
+  CUtensorMap q, k, v;
+};
+struct TcArgs {
+  AttendArgs a;
+  int block_nodes;   // whole nodes of a row block
+  int box;           // rows of a copy of keys or values: divides the tile and the page
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(384, 1)
+tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs args) {
+  using S = TcShape<D>;
+  constexpr int kTile = S::kTile, kStages = S::kStages;
+  const AttendArgs& a = args.a;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  TcShared& sh = *reinterpret_cast<TcShared*>(smem + S::kShared);
+  volatile int* abort_flag = &sh.abort;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
+  const int items = a.c.kv_heads * row_blocks;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t q_at = base, k_at = base + S::kTileBytes, v_at = k_at + kStages * S::kTileBytes;
+  auto bar = [&](int i) { return smem_u32(&sh.bars[i]); };
+  if (base & 1023) {   // the swizzled tiles need it; there is no static shared memory before them
+    if (tid == 0) atomicOr(a.c.err, kErrWait);
+    return;
+  }
+
+  Line line;
+  Cursor cur;
+  if (!find_run<kTile, S::kThreads>(a, items, sh.scratch, &line, &cur)) return;
+  const int n_tiles = line.end - line.begin;
+
+  if (tid == 0) {
+    sh.abort = 0;
+    mbar_init(bar(kQFull), 1);
+    mbar_init(bar(kQEmpty), 2);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(kKFull + i), 1);
+      mbar_init(bar(kKEmpty + i), 1);
+      mbar_init(bar(kVFull + i), 1);
+      mbar_init(bar(kVEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kSFull + i), 1);
+      mbar_init(bar(kPFull + i), 128);
+      mbar_init(bar(kPvDone + i), 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), S::kColumns);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copies
+    const int box = args.box, boxes = kTile / box;   // at most 16
+    const uint32_t box_bytes = static_cast<uint32_t>(box) * 128;
+    bool ok = true;
+    int tiles_out = 0;   // tiles whose copies were issued
+    // Page of this lane's box of the tile at a cursor: asked for a tile ahead.
+    auto look_up = [&](const Cursor& c) {
+      const int slot = c.t * kTile + lane * box;
+      return lane < boxes && slot < c.span.slots ? a.c.page_table[c.b * a.c.stride_table + slot / a.c.page_size] : -1;
+    };
+    Cursor next = cur;
+    int page = look_up(next);
+#pragma unroll 1
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      const int st = j % kStages, use = j / kStages;
+      const int kvh = cur.item / row_blocks;
+      const int slot = cur.t * kTile + lane * box;
+      const bool exists = lane < boxes && slot < cur.span.slots;
+      const bool outside = exists && static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages);
+      const bool copy = exists && !outside;
+      const int this_page = page;
+      if (j + 1 < n_tiles) {
+        advance<kTile>(a, items, &next);
+        page = look_up(next);
+      }
+      if (outside) record_index_error(a.c.err);
+      const int row = slot % a.c.page_size;
+      const uint32_t wanted = __popc(__ballot_sync(~0u, copy)) * box_bytes * S::kParts;
+      const uint32_t missing = __ballot_sync(~0u, outside);
+      if (use > 0) ok = mbar_wait(bar(kKEmpty + st), (use - 1) & 1, abort_flag);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + st), wanted);
+      __syncwarp();
+      if (copy)
+        for (int h = 0; h < S::kParts; ++h)
+          tma_load_4d(k_at + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, &maps.k, h * 64, row, kvh,
+                      this_page, bar(kKFull + st));
+      if (use > 0) ok = mbar_wait(bar(kVEmpty + st), (use - 1) & 1, abort_flag);
+      if (lane < 4) {
+        uint32_t word = 0;
+        if (missing)
+          for (int i = 0; i < 32; ++i) word |= (missing >> ((lane * 32 + i) / box) & 1u) << i;
+        sh.gone[st][lane] = word;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + st), ok ? wanted : 0);
+      __syncwarp();
+      if (copy && ok)
+        for (int h = 0; h < S::kParts; ++h)
+          tma_load_4d(v_at + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, &maps.v, h * 64, row, kvh,
+                      this_page, bar(kVFull + st));
+      tiles_out = j + 1;
+      advance<kTile>(a, items, &cur);
+    }
+    if (!ok) {   // given up: the copies in flight still have to land
+      volatile int never = 0;
+      for (int j = tiles_out > kStages ? tiles_out - kStages : 0; j < tiles_out; ++j) {
+        mbar_wait(bar(kKFull + j % kStages), (j / kStages) & 1, &never);
+        mbar_wait(bar(kVFull + j % kStages), (j / kStages) & 1, &never);
+      }
+    }
+  } else if (warp == 3) {
+    // ----------------------------------------------------------- copies of q
+    int n_items = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      if (j == 0 || cur.t == 0) {
+        if (n_items > 0) ok = mbar_wait_sleepy(bar(kQEmpty), (n_items - 1) & 1, abort_flag, 100);
+        if (!ok) break;
+        const int kvh = cur.item / row_blocks;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kQFull), static_cast<uint32_t>(args.block_nodes * a.group) * 128 * S::kParts);
+          for (int h = 0; h < S::kParts; ++h)
+            tma_load_4d(q_at + h * S::kPartBytes, &maps.q, h * 64, kvh * a.group,
+                        (cur.item - kvh * row_blocks) * args.block_nodes, cur.b, bar(kQFull));
+        }
+        __syncwarp();
+        ++n_items;
+      }
+      advance<kTile>(a, items, &cur);
+    }
+    if (!ok) {
+      volatile int never = 0;
+      mbar_wait(bar(kQFull), (n_items - 1) & 1, &never);
+    }
+  } else if (warp == 1 || warp == 2) {
+    // -------------------------------------------------------------- products
+    const int s = warp - 1;
+    const uint32_t scores = tmem + S::kScores + s * 128, sums = tmem + S::kSums + s * D;
+    constexpr uint32_t kScoreDesc = idesc_of<T>(128, false), kSumDesc = idesc_of<T>(D, true);
+    int n = 0, n_items = 0;
+    bool fresh = true, first = true, done = false, ok = true;
+#pragma unroll 1
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      const int st = j % kStages, phase = (j / kStages) & 1;
+      const int item_end = j + cur.nt - 1 - cur.t;   // the item's last tile
+      if (fresh) {
+        ok = mbar_wait(bar(kQFull), n_items & 1, abort_flag);
+        fresh = false, first = true, done = false;
+      }
+      if ((j & 1) == s && ok) {
+        ok = mbar_wait(bar(kKFull + st), phase, abort_flag);
+        // the weights lie over the scores until their product is done
+        if (ok && n > 0) ok = mbar_wait(bar(kPvDone + s), (n - 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * S::kPartBytes + (k % 4) * 32;
+            mma_ss(scores, smem_desc_sw128(q_at + off, 1024),
+                   smem_desc_sw128(k_at + st * S::kTileBytes + off, 1024), kScoreDesc, k > 0);
+          }
+          // only what someone will wait for, so that nothing arrives after the end
+          if (j + kStages < n_tiles) mma_commit(bar(kKEmpty + st));
+          mma_commit(bar(kSFull + s));
+          if (j + 2 > item_end && item_end + 1 < n_tiles) mma_commit(bar(kQEmpty));
+        }
+        __syncwarp();
+        done = j + 2 > item_end;
+        ok = mbar_wait(bar(kVFull + st), phase, abort_flag) && mbar_wait(bar(kPFull + s), n & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(sums, scores + k * 8, desc_by_keys(v_at + st * S::kTileBytes + k * 2048, S::kPartBytes), kSumDesc,
+                   !first || k > 0);
+          if (j + kStages < n_tiles) mma_commit(bar(kVEmpty + st));
+          mma_commit(bar(kPvDone + s));
+        }
+        __syncwarp();
+        first = false;
+        ++n;
+      }
+      if (j == item_end) {
+        // a stream without a tile of the item does not hold q up
+        if (!done && j + 1 < n_tiles && elect_one()) mbar_arrive(bar(kQEmpty));
+        __syncwarp();
+        fresh = true;
+        ++n_items;
+      }
+      advance<kTile>(a, items, &cur);
+    }
+    if (!ok && n > 0) {   // given up: the products in flight still have to end
+      volatile int never = 0;
+      mbar_wait(bar(kPvDone + s), (n - 1) & 1, &never);
+    }
+  } else if (warp >= 4) {
+    // --------------------------------------------------------------- weights
+    const int s = (warp - 4) / 4, row = (warp % 4) * 32 + lane, both = tid - 128;
+    const uint32_t mine = static_cast<uint32_t>((warp % 4) * 32) << 16;   // this warp's Tensor Memory lanes
+    const uint32_t scores = tmem + mine + S::kScores + s * 128, sums = tmem + mine + S::kSums + s * D;
+    const float sc = a.scale * kLog2e;
+    const int row_node = row / a.group;
+    int n = 0;
+    bool fresh = true, used = false;
+    int kvh = 0, node0 = 0, node = -1;
+    Seen seen = {};
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < n_tiles; ++j) {
+      const int st = j % kStages, phase = (j / kStages) & 1;
+      if (fresh) {
+        kvh = cur.item / row_blocks;
+        node0 = (cur.item - kvh * row_blocks) * args.block_nodes;
+        node = row_node < args.block_nodes && node0 + row_node < a.nodes ? node0 + row_node : -1;
+        m = -INFINITY, l = 0.f, used = false;
+        if (both < a.nodes) {
+          int p = a.parents[cur.b * a.stride_parents + both];
+          if (p >= both) {
+            record_index_error(a.c.err);
+            p = -2;
+          }
+          sh.up[both] = p < -2 ? -2 : p;
+        }
+        if (!group_all(3, 256, !*abort_flag)) break;
+        seen = node >= 0 && a.nodes > 1 ? seen_by(sh.up, node) : Seen{{node >= 0 && sh.up[0] >= -1 ? 1u : 0u, 0, 0, 0}};
+        fresh = false;
+      }
+      const int slot0 = cur.t * kTile;
+      if ((j & 1) == s) {
+        mbar_wait(bar(kSFull + s), n & 1, abort_flag);
+        mbar_wait(bar(kVFull + st), phase, abort_flag);   // makes gone[] visible; held until this tile's product
+        tc_fence_after();
+        uint32_t missing = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) missing |= sh.gone[st][w];
+        // The group agrees on what it does next, whatever a thread that gave up has read.
+        const bool plain = group_all(1 + s, 128, !missing && !*abort_flag);
+        const bool alive = plain || group_all(1 + s, 128, !*abort_flag);
+        if (alive) {
+          const bool tail = slot0 + kTile > cur.span.context || !plain;
+          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};   // keys this row sees
+          if (tail) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int off = slot0 + w * 32 - cur.span.context;   // tree node of the word's first key
+              uint32_t word = ~0u;
+              if (off > -32) {
+                auto tree = [&](int i) {
+                  return i == 0 ? seen.w[0] : i == 1 ? seen.w[1] : i == 2 ? seen.w[2] : i == 3 ? seen.w[3] : 0u;
+                };
+                word = off >= 0 ? __funnelshift_r(tree(off >> 5), tree((off >> 5) + 1), off & 31)
+                                : (tree(0) << -off) | ((1u << -off) - 1);
+              }
+              const int left = cur.span.slots - slot0 - w * 32;
+              if (left < 32) word &= left > 0 ? (1u << left) - 1 : 0u;
+              vis[w] = node >= 0 ? word & ~sh.gone[st][w] : 0u;
+            }
+          }
+          float v[32];
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(scores + c * 32, v);
+            if (tail) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = vis[c] >> i & 1 ? v[i] * sc : -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+            } else {
+              float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int i = 0; i < 32; ++i) hi[i % 4] = fmaxf(hi[i % 4], v[i] * sc);
+              top = fmaxf(top, fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])));
+            }
+          }
+          const bool rise = top > m + 8.f || m == -INFINITY;
+          if (__any_sync(~0u, rise && used && m > -INFINITY)) {
+            const float f = rise && m > -INFINITY ? exp2_approx(m - fmaxf(m, top)) : 1.f;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              uint32_t w[16];
+              tmem_ld16(sums + c * 16, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+              tmem_st16(sums + c * 16, w);
+            }
+          }
+          if (rise) m = fmaxf(m, top);
+          const float low = m == -INFINITY ? 0.f : -m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(scores + c * 32, v);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[i] = exp2_approx(fmaf(v[i], sc, low));
+              if (tail && !(vis[c] >> i & 1)) v[i] = 0.f;
+              sum[i % 4] += v[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack2(T(), v[2 * i], v[2 * i + 1]);
+            tmem_st16(scores + c * 16, w);   // over scores already read
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          bool any_bad = false;
+          if (tail) {
+            // Values that must not be multiplied, even by 0: of slots that do
+            // not exist, and of tree nodes where they are not finite (added
+            // below to the rows that see them). They become 0.
+            if (row < 4) sh.bad[s][row] = 0;
+            group_all(1 + s, 128, true);
+            const int j0 = !plain ? 0 : max(0, cur.span.context - slot0), j1 = cur.span.slots - slot0;
+            for (int id = j0 * (D / 8) + row; id < kTile * (D / 8); id += 128) {
+              const int key = id / (D / 8), ch = id % (D / 8);
+              uint4* at = reinterpret_cast<uint4*>(smem + (v_at - base) + st * S::kTileBytes + (ch / 8) * S::kPartBytes +
+                                                   key * 128 + (((ch % 8) ^ (key & 7)) << 4));
+              if (key >= j1 || (sh.gone[st][key / 32] >> (key % 32) & 1)) {
+                *at = uint4{0, 0, 0, 0};
+              } else if (a.nodes > 1 && slot0 + key >= cur.span.context) {
+                const uint4 x = *at;
+                if (bad_pair<T>(x.x) | bad_pair<T>(x.y) | bad_pair<T>(x.z) | bad_pair<T>(x.w)) {
+                  uint16_t* h = reinterpret_cast<uint16_t*>(at);
+                  for (int y = 0; y < 8; ++y)
+                    if (bad16<T>(h[y])) h[y] = 0;
+                  atomicOr(&sh.bad[s][key / 32], 1u << (key % 32));
+                }
+              }
+            }
+            fence_proxy_async_shared();
+            group_all(1 + s, 128, true);
+            for (int w = 0; w < 4; ++w) any_bad |= sh.bad[s][w] != 0;
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kPFull + s));
+          if (any_bad) {
+            mbar_wait(bar(kPvDone + s), n & 1, abort_flag);
+            tc_fence_after();
+            for (int key = 0; key < kTile; ++key) {
+              if (!(sh.bad[s][key / 32] >> (key % 32) & 1)) continue;
+              const int64_t off = slot_offset(a.c, cur.b, slot0 + key);
+              const uint32_t word = key < 64 ? (key < 32 ? vis[0] : vis[1]) : (key < 96 ? vis[2] : vis[3]);
+              const bool add = word >> (key % 32) & 1;
+              const T* src = static_cast<const T*>(a.v) + (off < 0 ? 0 : off) + kvh * a.c.stride_head;
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                float o[16];
+                uint32_t w[16];
+                tmem_ld16(sums + c * 16, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const T x = src[c * 16 + i];
+                  if (add && off >= 0 && bad16<T>(*reinterpret_cast<const uint16_t*>(&x))) o[i] += to_f32(x);
+                  w[i] = __float_as_uint(o[i]);
+                }
+                tmem_st16(sums + c * 16, w);
+                tmem_wait_st();
+              }
+            }
+            tc_fence_before();
+          }
+        }
+        used = true;
+        ++n;
+      }
+      const bool item_ends = cur.t + 1 == cur.nt;
+      if (item_ends || j + 1 == n_tiles) {
+        // The streams' sums together; each group takes half of the columns.
+        if (used) mbar_wait(bar(kPvDone + s), (n - 1) & 1, abort_flag);
+        sh.row_max[s][row] = used ? m : -INFINITY;
+        sh.row_sum[s][row] = used ? l : 0.f;
+        tc_fence_before();
+        if (!group_all(3, 256, !*abort_flag)) break;
+        tc_fence_after();
+        const float m0 = sh.row_max[0][row], m1 = sh.row_max[1][row], top = fmaxf(m0, m1);
+        const float low = top == -INFINITY ? 0.f : top;
+        const float f0 = exp2_approx(m0 - low), f1 = exp2_approx(m1 - low);
+        const float sum = f0 * sh.row_sum[0][row] + f1 * sh.row_sum[1][row];
+        // A stream without a tile of this item has nothing in its columns (its
+        // maximum is -inf, but so is that of one that saw nothing).
+        const int here = j + 1 - max(0, j - cur.t);   // the item's tiles in this run
+        const bool has0 = here > 1 || (j & 1) == 0, has1 = here > 1 || (j & 1) == 1;
+        const bool whole = item_ends && cur.first >= line.begin;
+        const bool idle = cur.span.context < 0;
+        const int rows = min(args.block_nodes, a.nodes - node0) * a.group;
+        const bool present = node >= 0 && !idle && sh.up[node] >= -1;
+        const bool empty = !present || sum == 0.f;
+        const float inv = whole ? (empty ? 0.f : 1.f / sum) : 1.f;
+        const size_t out_at = node >= 0 ? (static_cast<size_t>(cur.b) * a.nodes + node) * a.heads + kvh * a.group +
+                                              row - row_node * a.group : 0;
+        T* out = static_cast<T*>(a.out) + out_at * D;
+        float* part = a.partials + part_index(line, blockIdx.x, cur.first) * kPartFloats<128, D>;
+#pragma unroll 1
+        for (int c = s * (D / 32); c < (s + 1) * (D / 32); ++c) {
+          float x[16] = {}, y[16] = {};
+          if (has0) tmem_ld16(tmem + mine + S::kSums + c * 16, x);
+          if (has1) tmem_ld16(tmem + mine + S::kSums + D + c * 16, y);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            // a stream in which the row saw nothing holds zeros there
+            x[i] = (f0 * x[i] + f1 * y[i]) * inv;
+          }
+          if (node >= 0) {
+            if (whole) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = empty ? 0u : pack2(T(), x[2 * i], x[2 * i + 1]);
+              *reinterpret_cast<uint4*>(out + c * 16) = uint4{w[0], w[1], w[2], w[3]};
+              *reinterpret_cast<uint4*>(out + c * 16 + 8) = uint4{w[4], w[5], w[6], w[7]};
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(part + row * D + c * 16 + i) = float4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+            }
+          }
+        }
+        tc_fence_before();
+        if (node >= 0 && s == 0) {
+          if (whole) {
+            a.lse[out_at] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+          } else {
+            part[128 * D + row] = top;
+            part[128 * D + 128 + row] = sum;
+          }
+        }
+        if (!whole) {
+          __threadfence();
+          group_all(3, 256, true);
+          if (both == 0) {
+            sh.last_here = arrives_last(a, line, cur.first, cur.nt);
+            __threadfence();
+          }
+          group_all(3, 256, true);
+          if (sh.last_here)
+            join_parts<T, 128, D, 256>(a, line, Presence{sh.up}, cur.b, kvh, node0 * a.group, rows, cur.first, cur.nt, idle, both);
+        }
+        // Sums, masks and row_max have been read.
+        if (!group_all(3, 256, true)) break;
+        fresh = true;
+      }
+      advance<kTile>(a, items, &cur);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, S::kColumns);
+  if (tid == 0 && sh.abort) atomicOr(a.c.err, kErrWait);
+}
+
+}  // namespace tfx

@@ -151,17 +151,17 @@ __device__ __forceinline__ RowOf row_of(const AttendArgs& a, int kvh, int r) {
   return {node, kvh * a.group + r - node * a.group};
 }
 
-// Whole block: joins the parts of the item at `first` (nt tiles) and writes
+// kThreads threads (this one is number tid): joins the parts of the item at `first` (nt tiles) and writes
 // rows row0 .. row0 + rows - 1 of its kv head. Parts are added in run order.
 template <typename T, int kRows, int D, int kThreads, typename Masks>
 __device__ void join_parts(const AttendArgs& a, const Line& line, const Masks& masks, int b, int kvh, int row0,
-                           int rows, int first, int nt, bool idle) {
+                           int rows, int first, int nt, bool idle, int tid) {
   constexpr size_t kPart = kPartFloats<kRows, D>;
   const int b0 = line.block_of(first), n = line.block_of(first + nt - 1) - b0 + 1;
   // Every part but the first is the one its block begins with.
   const float* part0 = a.partials + part_index(line, b0, first) * kPart;
   const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart;
-  for (int id = threadIdx.x; id < rows * (D / 4); id += kThreads) {
+  for (int id = tid; id < rows * (D / 4); id += kThreads) {
     const int r = id / (D / 4), e = (id - r * (D / 4)) * 4;
     float top = -INFINITY, l = 0.f;
     float4 o = {0.f, 0.f, 0.f, 0.f};

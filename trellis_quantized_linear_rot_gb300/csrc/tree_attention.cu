@@ -1,6 +1,12 @@
 // Launch of the attention of a drafted token tree over a paged cache
 // (tf_tree_attention).
-#include "attend_mma.cuh"
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+#include <numeric>
+
+#include "attend_tc.cuh"
 
 namespace tfx {
 namespace {
@@ -23,12 +29,87 @@ cudaError_t launch_mma(const AttendArgs& a, int device, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A map of 16-bit elements over (n0, n1, n2, n3) with strides of the last
+// three in elements, boxes of (64, b1, b2, 1) with the 128-byte swizzle.
+bool make_map(CUtensorMap* map, bool half, const void* at, const int64_t (&n)[4], const int64_t (&stride)[3], int b1,
+              int b2) {
+  cuuint64_t dims[4], strides[3];
+  for (int i = 0; i < 4; ++i) dims[i] = static_cast<cuuint64_t>(n[i]);
+  // A dimension of one element has any stride.
+  for (int i = 0; i < 3; ++i) strides[i] = n[i + 1] == 1 ? 16 : static_cast<cuuint64_t>(stride[i]) * 2;
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2), 1}, ones[4] = {1, 1, 1, 1};
+  auto encode = map_encoder();
+  return encode && encode(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                          const_cast<void*>(at), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t launch_tc(const AttendArgs& a, int box, int device, cudaStream_t s) {
+  using S = TcShape<D>;
+  static PerDeviceOnce<kMaxDevices> once;
+  const int e = once.run(device, cudaErrorInvalidDevice, [] {
+    return static_cast<int>(cudaFuncSetAttribute(tree_attention_tc_kernel<T, D>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+  });
+  if (e != cudaSuccess) return static_cast<cudaError_t>(e);
+  const bool half = std::is_same<T, __half>::value;
+  TcArgs args;
+  args.a = a;
+  args.block_nodes = std::min(S::kTile / a.group, a.nodes);
+  args.box = box;
+  TcMaps maps;
+  const CacheView& c = a.c;
+  if (!make_map(&maps.q, half, a.q, {D, a.heads, a.nodes, c.batch}, {a.q_head, a.q_node, a.q_seq}, a.group,
+                args.block_nodes) ||
+      !make_map(&maps.k, half, a.k, {D, c.page_size, c.kv_heads, c.pages},
+                {c.stride_token, c.stride_head, c.stride_page}, box, 1) ||
+      !make_map(&maps.v, half, a.v, {D, c.page_size, c.kv_heads, c.pages},
+                {c.stride_token, c.stride_head, c.stride_page}, box, 1))
+    return cudaErrorInvalidValue;
+  tree_attention_tc_kernel<T, D><<<a.num_sms, S::kThreads, S::kSmem, s>>>(maps, args);
+  return cudaGetLastError();
+}
+
+// Rows of a copy for the tcgen05 kernel: the largest that divides both the
+// tile and the page, 0 where the call does not suit the kernel (pages that
+// are no multiple of 8 rows, more heads a kv head than a tile has rows, a
+// stride of 0 that repeats an element).
+int tc_box(const AttendArgs& a) {
+  const CacheView& c = a.c;
+  if (c.head_dim == 256 || a.group > 128) return 0;
+  const int box = std::gcd(c.page_size, 128);
+  const bool repeats = (c.page_size > 1 && !c.stride_token) || (c.kv_heads > 1 && !c.stride_head) ||
+                       (c.pages > 1 && !c.stride_page) || (a.heads > 1 && !a.q_head) || (a.nodes > 1 && !a.q_node) ||
+                       (c.batch > 1 && !a.q_seq);
+  return box >= 8 && !repeats ? box : 0;
+}
+
 template <typename T>
 cudaError_t launch_typed(const AttendArgs& a, int device, cudaStream_t s) {
   const bool few = a.nodes * a.group <= kFewRows;
+  const int box = few ? 0 : tc_box(a);
   switch (a.c.head_dim) {
-    case 64: return few ? launch_mma<T, 64, 1>(a, device, s) : launch_mma<T, 64, 4>(a, device, s);
-    case 128: return few ? launch_mma<T, 128, 1>(a, device, s) : launch_mma<T, 128, 4>(a, device, s);
+    case 64:
+      return few ? launch_mma<T, 64, 1>(a, device, s)
+                 : box ? launch_tc<T, 64>(a, box, device, s) : launch_mma<T, 64, 4>(a, device, s);
+    case 128:
+      return few ? launch_mma<T, 128, 1>(a, device, s)
+                 : box ? launch_tc<T, 128>(a, box, device, s) : launch_mma<T, 128, 4>(a, device, s);
     default: return few ? launch_mma<T, 256, 1>(a, device, s) : launch_mma<T, 256, 4>(a, device, s);
   }
 }
