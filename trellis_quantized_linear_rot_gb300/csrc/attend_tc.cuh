@@ -71,19 +71,19 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// 32 columns of this thread's Tensor Memory lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
+// Columns of this thread's Tensor Memory lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t column, float (&v)[32]) {
   uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at)
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(column)
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
@@ -97,14 +97,109 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) 
       : "memory");
 }
 
-enum TcBarrier { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + 3, kVFull = kKEmpty + 3, kVEmpty = kVFull + 3,
-                 kSFull = kVEmpty + 3, kPFull = kSFull + 2, kPvDone = kPFull + 2, kBarriers = kPvDone + 2 };
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// One row of a tile, by its thread: from the scores (128 columns at `scores`)
+// to the weights over them, with the running maximum m and sum l. The sums
+// (D columns at `sums`) are rescaled where the maximum has risen by more than
+// 2^8 since they were begun. kCut: only the keys in vis are seen. sc >= 0.
+template <typename T, int D, bool kCut>
+__device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, const uint32_t (&vis)[4], bool begun,
+                                      float* m_row, float* l_row) {
+  // The scores are read twice, in parts: all 128 of them and what is made of
+  // them do not fit a thread's registers.
+  float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  auto word_of = [&](int c) { return c < 2 ? (c == 0 ? vis[0] : vis[1]) : (c == 2 ? vis[2] : vis[3]); };
+#pragma unroll(kCut ? 1 : 4)
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    tmem_ld32(scores + c * 32, v);
+    const uint32_t word = kCut ? word_of(c) : 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      if (kCut) {
+        if (!(word >> i & 1)) v[i] = -INFINITY;
+        if (!(word >> (i + 1) & 1)) v[i + 1] = -INFINITY;
+      }
+      hi[i / 2 % 4] = fmaxf(hi[i / 2 % 4], fmaxf(v[i], v[i + 1]));
+    }
+  }
+  float top = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+  top = top == -INFINITY ? -INFINITY : top * sc;
+  float m = *m_row, l = *l_row;
+  const bool rise = top > m + 8.f || m == -INFINITY;
+  if (__any_sync(~0u, rise && begun && m > -INFINITY)) {
+    const float f = rise && m > -INFINITY ? exp2_approx(m - fmaxf(m, top)) : 1.f;
+    l *= f;
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      float o[16];
+      uint32_t w[16];
+      tmem_ld16(sums + c * 16, o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+      tmem_st16(sums + c * 16, w);
+    }
+  }
+  if (rise) m = fmaxf(m, top);
+  const float low = m == -INFINITY ? 0.f : -m;
+  float2 sum[4] = {};
+#pragma unroll(kCut ? 1 : 4)
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    tmem_ld32(scores + c * 32, v);
+    const uint32_t word = kCut ? word_of(c) : 0;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float2 x = fma2(float2{v[2 * i], v[2 * i + 1]}, float2{sc, sc}, float2{low, low});
+      x.x = exp2_approx(x.x);
+      x.y = exp2_approx(x.y);
+      if (kCut) {
+        if (!(word >> (2 * i) & 1)) x.x = 0.f;
+        if (!(word >> (2 * i + 1) & 1)) x.y = 0.f;
+      }
+      sum[i % 4] = add2(sum[i % 4], x);
+      w[i] = pack2(T(), x.x, x.y);
+    }
+    tmem_st16(scores + c * 16, w);   // over scores already read
+  }
+  const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+  *m_row = m;
+  *l_row = l + (both.x + both.y);
+}
+
+// A tile j lies in stage j % 3 and belongs to stream j % 2. Its barriers are
+// number j % 6, so that whoever waits on one waits for each of its phases in
+// turn (a barrier of a stage would be waited for by the streams by turns, and
+// a wait that passes over a phase cannot tell it from the next but one).
+constexpr int kTcSlots = 6;
+enum TcBarrier { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + kTcSlots, kVFull = kKEmpty + kTcSlots,
+                 kVEmpty = kVFull + kTcSlots, kSFull = kVEmpty + kTcSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+                 kBarriers = kPvDone + 2 };
 
 struct TcShared {
   unsigned long long bars[kBarriers];
   float row_max[2][128], row_sum[2][128];   // of the streams, at an item's end
   uint32_t gone[3][4];                      // keys of a stage whose page is outside the pool
-  uint32_t bad[2][4];                       // keys of a stream's tile with values that are not finite
+  uint32_t bad[4];                          // tree nodes with values that are not finite
+  int any_gone;
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
   int scratch[384 / 32 + 2];
   uint32_t tmem;
@@ -180,9 +275,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
 
   if (tid == 0) {
     sh.abort = 0;
+    sh.any_gone = 0;
     mbar_init(bar(kQFull), 1);
     mbar_init(bar(kQEmpty), 2);
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kTcSlots; ++i) {
       mbar_init(bar(kKFull + i), 1);
       mbar_init(bar(kKEmpty + i), 1);
       mbar_init(bar(kVFull + i), 1);
@@ -224,7 +320,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     int page = look_up(next);
 #pragma unroll 1
     for (int j = 0; j < n_tiles && ok; ++j) {
-      const int st = j % kStages, use = j / kStages;
+      const int st = j % kStages, slot_j = j % kTcSlots;
+      const int before = j - kStages, slot_b = before % kTcSlots, phase_b = (before / kTcSlots) & 1;   // the stage's last tile
       const int kvh = cur.item / row_blocks;
       const int slot = cur.t * kTile + lane * box;
       const bool exists = lane < boxes && slot < cur.span.slots;
@@ -239,36 +336,37 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
       const int row = slot % a.c.page_size;
       const uint32_t wanted = __popc(__ballot_sync(~0u, copy)) * box_bytes * S::kParts;
       const uint32_t missing = __ballot_sync(~0u, outside);
-      if (use > 0) ok = mbar_wait(bar(kKEmpty + st), (use - 1) & 1, abort_flag);
+      if (before >= 0) ok = mbar_wait(bar(kKEmpty + slot_b), phase_b, abort_flag);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + st), wanted);
+      if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + slot_j), wanted);
       __syncwarp();
       if (copy)
         for (int h = 0; h < S::kParts; ++h)
           tma_load_4d(k_at + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, &maps.k, h * 64, row, kvh,
-                      this_page, bar(kKFull + st));
-      if (use > 0) ok = mbar_wait(bar(kVEmpty + st), (use - 1) & 1, abort_flag);
+                      this_page, bar(kKFull + slot_j));
+      if (before >= 0) ok = mbar_wait(bar(kVEmpty + slot_b), phase_b, abort_flag);
       if (lane < 4) {
         uint32_t word = 0;
         if (missing)
           for (int i = 0; i < 32; ++i) word |= (missing >> ((lane * 32 + i) / box) & 1u) << i;
         sh.gone[st][lane] = word;
+        if (missing) sh.any_gone = 1;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + st), ok ? wanted : 0);
+      if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + slot_j), ok ? wanted : 0);
       __syncwarp();
       if (copy && ok)
         for (int h = 0; h < S::kParts; ++h)
           tma_load_4d(v_at + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, &maps.v, h * 64, row, kvh,
-                      this_page, bar(kVFull + st));
+                      this_page, bar(kVFull + slot_j));
       tiles_out = j + 1;
       advance<kTile>(a, items, &cur);
     }
     if (!ok) {   // given up: the copies in flight still have to land
       volatile int never = 0;
       for (int j = tiles_out > kStages ? tiles_out - kStages : 0; j < tiles_out; ++j) {
-        mbar_wait(bar(kKFull + j % kStages), (j / kStages) & 1, &never);
-        mbar_wait(bar(kVFull + j % kStages), (j / kStages) & 1, &never);
+        mbar_wait(bar(kKFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
+        mbar_wait(bar(kVFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
       }
     }
   } else if (warp == 3) {
@@ -305,14 +403,14 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     bool fresh = true, first = true, done = false, ok = true;
 #pragma unroll 1
     for (int j = 0; j < n_tiles && ok; ++j) {
-      const int st = j % kStages, phase = (j / kStages) & 1;
+      const int st = j % kStages, slot_j = j % kTcSlots, phase = (j / kTcSlots) & 1;
       const int item_end = j + cur.nt - 1 - cur.t;   // the item's last tile
       if (fresh) {
         ok = mbar_wait(bar(kQFull), n_items & 1, abort_flag);
         fresh = false, first = true, done = false;
       }
       if ((j & 1) == s && ok) {
-        ok = mbar_wait(bar(kKFull + st), phase, abort_flag);
+        ok = mbar_wait(bar(kKFull + slot_j), phase, abort_flag);
         // the weights lie over the scores until their product is done
         if (ok && n > 0) ok = mbar_wait(bar(kPvDone + s), (n - 1) & 1, abort_flag);
         if (!ok) break;
@@ -325,13 +423,13 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
                    smem_desc_sw128(k_at + st * S::kTileBytes + off, 1024), kScoreDesc, k > 0);
           }
           // only what someone will wait for, so that nothing arrives after the end
-          if (j + kStages < n_tiles) mma_commit(bar(kKEmpty + st));
+          if (j + kStages < n_tiles) mma_commit(bar(kKEmpty + slot_j));
           mma_commit(bar(kSFull + s));
           if (j + 2 > item_end && item_end + 1 < n_tiles) mma_commit(bar(kQEmpty));
         }
         __syncwarp();
         done = j + 2 > item_end;
-        ok = mbar_wait(bar(kVFull + st), phase, abort_flag) && mbar_wait(bar(kPFull + s), n & 1, abort_flag);
+        ok = mbar_wait(bar(kVFull + slot_j), phase, abort_flag) && mbar_wait(bar(kPFull + s), n & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -339,7 +437,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
           for (int k = 0; k < kTile / 16; ++k)
             mma_ts(sums, scores + k * 8, desc_by_keys(v_at + st * S::kTileBytes + k * 2048, S::kPartBytes), kSumDesc,
                    !first || k > 0);
-          if (j + kStages < n_tiles) mma_commit(bar(kVEmpty + st));
+          if (j + kStages < n_tiles) mma_commit(bar(kVEmpty + slot_j));
           mma_commit(bar(kPvDone + s));
         }
         __syncwarp();
@@ -366,176 +464,88 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     const uint32_t scores = tmem + mine + S::kScores + s * 128, sums = tmem + mine + S::kSums + s * D;
     const float sc = a.scale * kLog2e;
     const int row_node = row / a.group;
+    const T* values = static_cast<const T*>(a.v);
     int n = 0;
-    bool fresh = true, used = false;
-    int kvh = 0, node0 = 0, node = -1;
-    Seen seen = {};
-    float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-    for (int j = 0; j < n_tiles; ++j) {
-      const int st = j % kStages, phase = (j / kStages) & 1;
-      if (fresh) {
-        kvh = cur.item / row_blocks;
-        node0 = (cur.item - kvh * row_blocks) * args.block_nodes;
-        node = row_node < args.block_nodes && node0 + row_node < a.nodes ? node0 + row_node : -1;
-        m = -INFINITY, l = 0.f, used = false;
-        if (both < a.nodes) {
-          int p = a.parents[cur.b * a.stride_parents + both];
-          if (p >= both) {
-            record_index_error(a.c.err);
-            p = -2;
-          }
-          sh.up[both] = p < -2 ? -2 : p;
+    for (int ja = 0; ja < n_tiles;) {   // the items of the run, tiles ja .. jb - 1 of it
+      const int jb = ja + min(n_tiles - ja, cur.nt - cur.t);
+      const int kvh = cur.item / row_blocks, node0 = (cur.item - kvh * row_blocks) * args.block_nodes;
+      const int node = row_node < args.block_nodes && node0 + row_node < a.nodes ? node0 + row_node : -1;
+      if (both < a.nodes) {
+        int p = a.parents[cur.b * a.stride_parents + both];
+        if (p >= both) {
+          record_index_error(a.c.err);
+          p = -2;
         }
-        if (!group_all(3, 256, !*abort_flag)) break;
-        seen = node >= 0 && a.nodes > 1 ? seen_by(sh.up, node) : Seen{{node >= 0 && sh.up[0] >= -1 ? 1u : 0u, 0, 0, 0}};
-        fresh = false;
+        sh.up[both] = p < -2 ? -2 : p;
       }
-      const int slot0 = cur.t * kTile;
-      if ((j & 1) == s) {
+      if (both < 4) sh.bad[both] = 0;
+      if (!group_all(3, 256, !*abort_flag)) break;
+      Seen seen = {};
+      if (node >= 0) seen = seen_by(sh.up, node);
+      float m = -INFINITY, l = 0.f;
+      bool used = false;
+#pragma unroll 1
+      for (int j = ja + ((ja ^ s) & 1); j < jb; j += 2) {
+        const int st = j % kStages;
+        const int slot0 = (cur.t + j - ja) * kTile;
         mbar_wait(bar(kSFull + s), n & 1, abort_flag);
-        mbar_wait(bar(kVFull + st), phase, abort_flag);   // makes gone[] visible; held until this tile's product
+        // (held until this tile's product; makes gone[] visible)
+        mbar_wait(bar(kVFull + j % kTcSlots), (j / kTcSlots) & 1, abort_flag);
+        __syncwarp();
         tc_fence_after();
-        uint32_t missing = 0;
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};   // keys this row sees
+        if (slot0 + kTile <= cur.span.context && !*static_cast<volatile int*>(&sh.any_gone)) {
+          weigh<T, D, false>(scores, sums, sc, vis, used, &m, &l);
+        } else {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) missing |= sh.gone[st][w];
-        // The group agrees on what it does next, whatever a thread that gave up has read.
-        const bool plain = group_all(1 + s, 128, !missing && !*abort_flag);
-        const bool alive = plain || group_all(1 + s, 128, !*abort_flag);
-        if (alive) {
-          const bool tail = slot0 + kTile > cur.span.context || !plain;
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};   // keys this row sees
-          if (tail) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int off = slot0 + w * 32 - cur.span.context;   // tree node of the word's first key
-              uint32_t word = ~0u;
-              if (off > -32) {
-                auto tree = [&](int i) {
-                  return i == 0 ? seen.w[0] : i == 1 ? seen.w[1] : i == 2 ? seen.w[2] : i == 3 ? seen.w[3] : 0u;
-                };
-                word = off >= 0 ? __funnelshift_r(tree(off >> 5), tree((off >> 5) + 1), off & 31)
-                                : (tree(0) << -off) | ((1u << -off) - 1);
-              }
-              const int left = cur.span.slots - slot0 - w * 32;
-              if (left < 32) word &= left > 0 ? (1u << left) - 1 : 0u;
-              vis[w] = node >= 0 ? word & ~sh.gone[st][w] : 0u;
+          for (int w = 0; w < 4; ++w) {
+            const int off = slot0 + w * 32 - cur.span.context;   // tree node of the word's first key
+            uint32_t word = ~0u;
+            if (off > -32) {
+              auto tree = [&](int i) {
+                return i == 0 ? seen.w[0] : i == 1 ? seen.w[1] : i == 2 ? seen.w[2] : i == 3 ? seen.w[3] : 0u;
+              };
+              word = off >= 0 ? __funnelshift_r(tree(off >> 5), tree((off >> 5) + 1), off & 31)
+                              : (tree(0) << -off) | ((1u << -off) - 1);
             }
+            const int left = cur.span.slots - slot0 - w * 32;
+            if (left < 32) word &= left > 0 ? (1u << left) - 1 : 0u;
+            vis[w] = node >= 0 ? word & ~sh.gone[st][w] : 0u;
           }
-          float v[32];
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(scores + c * 32, v);
-            if (tail) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = vis[c] >> i & 1 ? v[i] * sc : -INFINITY;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
-            } else {
-              float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-              for (int i = 0; i < 32; ++i) hi[i % 4] = fmaxf(hi[i % 4], v[i] * sc);
-              top = fmaxf(top, fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])));
-            }
-          }
-          const bool rise = top > m + 8.f || m == -INFINITY;
-          if (__any_sync(~0u, rise && used && m > -INFINITY)) {
-            const float f = rise && m > -INFINITY ? exp2_approx(m - fmaxf(m, top)) : 1.f;
-            l *= f;
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              float o[16];
-              uint32_t w[16];
-              tmem_ld16(sums + c * 16, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
-              tmem_st16(sums + c * 16, w);
-            }
-          }
-          if (rise) m = fmaxf(m, top);
-          const float low = m == -INFINITY ? 0.f : -m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(scores + c * 32, v);
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] = exp2_approx(fmaf(v[i], sc, low));
-              if (tail && !(vis[c] >> i & 1)) v[i] = 0.f;
-              sum[i % 4] += v[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack2(T(), v[2 * i], v[2 * i + 1]);
-            tmem_st16(scores + c * 16, w);   // over scores already read
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          bool any_bad = false;
-          if (tail) {
-            // Values that must not be multiplied, even by 0: of slots that do
-            // not exist, and of tree nodes where they are not finite (added
-            // below to the rows that see them). They become 0.
-            if (row < 4) sh.bad[s][row] = 0;
-            group_all(1 + s, 128, true);
-            const int j0 = !plain ? 0 : max(0, cur.span.context - slot0), j1 = cur.span.slots - slot0;
-            for (int id = j0 * (D / 8) + row; id < kTile * (D / 8); id += 128) {
-              const int key = id / (D / 8), ch = id % (D / 8);
-              uint4* at = reinterpret_cast<uint4*>(smem + (v_at - base) + st * S::kTileBytes + (ch / 8) * S::kPartBytes +
-                                                   key * 128 + (((ch % 8) ^ (key & 7)) << 4));
-              if (key >= j1 || (sh.gone[st][key / 32] >> (key % 32) & 1)) {
-                *at = uint4{0, 0, 0, 0};
-              } else if (a.nodes > 1 && slot0 + key >= cur.span.context) {
-                const uint4 x = *at;
-                if (bad_pair<T>(x.x) | bad_pair<T>(x.y) | bad_pair<T>(x.z) | bad_pair<T>(x.w)) {
-                  uint16_t* h = reinterpret_cast<uint16_t*>(at);
-                  for (int y = 0; y < 8; ++y)
-                    if (bad16<T>(h[y])) h[y] = 0;
-                  atomicOr(&sh.bad[s][key / 32], 1u << (key % 32));
-                }
+          // Values that must not be multiplied, even by 0: of slots that do
+          // not exist, and of tree nodes where they are not finite (added at
+          // the item's end to the rows that see them). They become 0.
+          const int j1 = cur.span.slots - slot0;
+          for (int id = row; id < kTile * (D / 8); id += 128) {
+            const int key = id / (D / 8), ch = id % (D / 8), nd = slot0 + key - cur.span.context;
+            uint4* at = reinterpret_cast<uint4*>(smem + (v_at - base) + st * S::kTileBytes + (ch / 8) * S::kPartBytes +
+                                                 key * 128 + (((ch % 8) ^ (key & 7)) << 4));
+            if (key >= j1 || (sh.gone[st][key / 32] >> (key % 32) & 1)) {
+              *at = uint4{0, 0, 0, 0};
+            } else if (a.nodes > 1 && nd >= 0) {
+              const uint4 x = *at;
+              if (bad_pair<T>(x.x) | bad_pair<T>(x.y) | bad_pair<T>(x.z) | bad_pair<T>(x.w)) {
+                uint16_t* h = reinterpret_cast<uint16_t*>(at);
+                for (int y = 0; y < 8; ++y)
+                  if (bad16<T>(h[y])) h[y] = 0;
+                atomicOr(&sh.bad[nd / 32], 1u << (nd % 32));
               }
             }
-            fence_proxy_async_shared();
-            group_all(1 + s, 128, true);
-            for (int w = 0; w < 4; ++w) any_bad |= sh.bad[s][w] != 0;
           }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(kPFull + s));
-          if (any_bad) {
-            mbar_wait(bar(kPvDone + s), n & 1, abort_flag);
-            tc_fence_after();
-            for (int key = 0; key < kTile; ++key) {
-              if (!(sh.bad[s][key / 32] >> (key % 32) & 1)) continue;
-              const int64_t off = slot_offset(a.c, cur.b, slot0 + key);
-              const uint32_t word = key < 64 ? (key < 32 ? vis[0] : vis[1]) : (key < 96 ? vis[2] : vis[3]);
-              const bool add = word >> (key % 32) & 1;
-              const T* src = static_cast<const T*>(a.v) + (off < 0 ? 0 : off) + kvh * a.c.stride_head;
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                float o[16];
-                uint32_t w[16];
-                tmem_ld16(sums + c * 16, o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const T x = src[c * 16 + i];
-                  if (add && off >= 0 && bad16<T>(*reinterpret_cast<const uint16_t*>(&x))) o[i] += to_f32(x);
-                  w[i] = __float_as_uint(o[i]);
-                }
-                tmem_st16(sums + c * 16, w);
-                tmem_wait_st();
-              }
-            }
-            tc_fence_before();
-          }
+          fence_proxy_async_shared();
+          weigh<T, D, true>(scores, sums, sc, vis, used, &m, &l);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull + s));
         used = true;
         ++n;
       }
-      const bool item_ends = cur.t + 1 == cur.nt;
-      if (item_ends || j + 1 == n_tiles) {
+      {
         // The streams' sums together; each group takes half of the columns.
         if (used) mbar_wait(bar(kPvDone + s), (n - 1) & 1, abort_flag);
+        __syncwarp();
         sh.row_max[s][row] = used ? m : -INFINITY;
         sh.row_sum[s][row] = used ? l : 0.f;
         tc_fence_before();
@@ -547,10 +557,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         const float sum = f0 * sh.row_sum[0][row] + f1 * sh.row_sum[1][row];
         // A stream without a tile of this item has nothing in its columns (its
         // maximum is -inf, but so is that of one that saw nothing).
-        const int here = j + 1 - max(0, j - cur.t);   // the item's tiles in this run
-        const bool has0 = here > 1 || (j & 1) == 0, has1 = here > 1 || (j & 1) == 1;
-        const bool whole = item_ends && cur.first >= line.begin;
+        const bool has0 = jb - ja > 1 || (ja & 1) == 0, has1 = jb - ja > 1 || (ja & 1) == 1;
+        const bool whole = cur.t == 0 && cur.nt == jb - ja;
         const bool idle = cur.span.context < 0;
+        const bool any_bad = (sh.bad[0] | sh.bad[1] | sh.bad[2] | sh.bad[3]) != 0;
         const int rows = min(args.block_nodes, a.nodes - node0) * a.group;
         const bool present = node >= 0 && !idle && sh.up[node] >= -1;
         const bool empty = !present || sum == 0.f;
@@ -565,10 +575,19 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
           if (has0) tmem_ld16(tmem + mine + S::kSums + c * 16, x);
           if (has1) tmem_ld16(tmem + mine + S::kSums + D + c * 16, y);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            // a stream in which the row saw nothing holds zeros there
-            x[i] = (f0 * x[i] + f1 * y[i]) * inv;
-          }
+          for (int i = 0; i < 16; ++i) x[i] = (f0 * x[i] + f1 * y[i]) * inv;
+          if (any_bad)
+            for (int w = 0; w < 4; ++w)
+              for (uint32_t left = sh.bad[w] & (w == 0 ? seen.w[0] : w == 1 ? seen.w[1] : w == 2 ? seen.w[2] : seen.w[3]);
+                   left; left &= left - 1) {
+                const int64_t off = slot_offset(a.c, cur.b, cur.span.context + w * 32 + __ffs(left) - 1);
+                if (off < 0) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const T z = values[off + kvh * a.c.stride_head + c * 16 + i];
+                  if (bad16<T>(*reinterpret_cast<const uint16_t*>(&z))) x[i] += to_f32(z);
+                }
+              }
           if (node >= 0) {
             if (whole) {
               uint32_t w[8];
@@ -603,11 +622,12 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
           if (sh.last_here)
             join_parts<T, 128, D, 256>(a, line, Presence{sh.up}, cur.b, kvh, node0 * a.group, rows, cur.first, cur.nt, idle, both);
         }
-        // Sums, masks and row_max have been read.
+        // Sums, parents and maxima have been read.
         if (!group_all(3, 256, true)) break;
-        fresh = true;
       }
+      cur.t += jb - ja - 1;
       advance<kTile>(a, items, &cur);
+      ja = jb;
     }
   }
   tc_fence_before();

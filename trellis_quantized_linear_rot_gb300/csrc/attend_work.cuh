@@ -161,48 +161,63 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, const Masks& m
   // Every part but the first is the one its block begins with.
   const float* part0 = a.partials + part_index(line, b0, first) * kPart;
   const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart;
-  for (int id = tid; id < rows * (D / 4); id += kThreads) {
-    const int r = id / (D / 4), e = (id - r * (D / 4)) * 4;
-    float top = -INFINITY, l = 0.f;
-    float4 o = {0.f, 0.f, 0.f, 0.f};
-    // Groups of parts, all of a group's loads in flight at once.
-    constexpr int kGroup = 6;
+  // A thread takes four columns of kBatch rows at a time, kGroup parts of each
+  // at once, so that many loads are in flight; few rows have many parts and
+  // many rows few.
+  constexpr int kBatch = kRows > 16 ? 4 : 1, kGroup = kRows > 16 ? 2 : 6, kStep = kThreads / (D / 4);
+  const int e = tid % (D / 4) * 4;
+  for (int r0 = tid / (D / 4); r0 < rows; r0 += kBatch * kStep) {
+    float top[kBatch], l[kBatch];
+    float4 o[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top[k] = -INFINITY, l[k] = 0.f, o[k] = float4{0.f, 0.f, 0.f, 0.f};
     for (int p0 = 0; p0 < n; p0 += kGroup) {
-      float m[kGroup], w[kGroup];
-      float4 x[kGroup];
+      float m[kBatch][kGroup], w[kBatch][kGroup];
+      float4 x[kBatch][kGroup];
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        const float* part = p0 + i == 0 ? part0 : part1 + (p0 + i - 1) * 2 * kPart;
-        const bool real = p0 + i < n;
-        m[i] = real ? __ldcg(part + kRows * D + r) : -INFINITY;
-        w[i] = real ? __ldcg(part + kRows * D + kRows + r) : 0.f;
-        x[i] = real ? __ldcg(reinterpret_cast<const float4*>(part + r * D + e)) : float4{0.f, 0.f, 0.f, 0.f};
-      }
-      float high = top;
+      for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) high = fmaxf(high, m[i]);
-      const float base = high == -INFINITY ? 0.f : high;
-      const float keep = exp2_approx(top - base);
-      top = high;
-      l *= keep, o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+        for (int i = 0; i < kGroup; ++i) {
+          const float* part = p0 + i == 0 ? part0 : part1 + (p0 + i - 1) * 2 * kPart;
+          const int r = r0 + k * kStep;
+          const bool real = p0 + i < n && r < rows;
+          m[k][i] = real ? __ldcg(part + kRows * D + r) : -INFINITY;
+          w[k][i] = real ? __ldcg(part + kRows * D + kRows + r) : 0.f;
+          x[k][i] = real ? __ldcg(reinterpret_cast<const float4*>(part + r * D + e)) : float4{0.f, 0.f, 0.f, 0.f};
+        }
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        const float f = exp2_approx(m[i] - base);
-        l += f * w[i];
-        o.x += f * x[i].x, o.y += f * x[i].y, o.z += f * x[i].z, o.w += f * x[i].w;
+      for (int k = 0; k < kBatch; ++k) {
+        float high = top[k];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) high = fmaxf(high, m[k][i]);
+        const float base = high == -INFINITY ? 0.f : high;
+        const float keep = exp2_approx(top[k] - base);
+        top[k] = high;
+        l[k] *= keep, o[k].x *= keep, o[k].y *= keep, o[k].z *= keep, o[k].w *= keep;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          const float f = exp2_approx(m[k][i] - base);
+          l[k] += f * w[k][i];
+          o[k].x += f * x[k][i].x, o[k].y += f * x[k][i].y, o[k].z += f * x[k][i].z, o[k].w += f * x[k][i].w;
+        }
       }
     }
-    const RowOf ro = row_of(a, kvh, row0 + r);
-    const bool present = !idle && masks.sees(ro.node, ro.node);
-    const bool empty = !present || l == 0.f;
-    const float inv = empty ? 0.f : 1.f / l;
-    const size_t at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;
-    T* out = static_cast<T*>(a.out) + at * D + e;
-    const float y[4] = {o.x, o.y, o.z, o.w};
-    T t[4];
-    for (int i = 0; i < 4; ++i) t[i] = from_f32<T>(empty ? 0.f : y[i] * inv);
-    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(t);
-    if (e == 0) a.lse[at] = empty ? -INFINITY : (top + log2f(l)) * kLn2;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * kStep;
+      if (r >= rows) continue;
+      const RowOf ro = row_of(a, kvh, row0 + r);
+      const bool present = !idle && masks.sees(ro.node, ro.node);
+      const bool empty = !present || l[k] == 0.f;
+      const float inv = empty ? 0.f : 1.f / l[k];
+      const size_t at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;
+      const float y[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+      alignas(8) T t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = from_f32<T>(empty ? 0.f : y[i] * inv);
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + e) = *reinterpret_cast<const uint2*>(t);
+      if (e == 0) a.lse[at] = empty ? -INFINITY : (top[k] + log2f(l[k])) * kLn2;
+    }
   }
 }
 

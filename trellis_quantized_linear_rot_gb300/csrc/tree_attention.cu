@@ -88,10 +88,10 @@ cudaError_t launch_tc(const AttendArgs& a, int box, int device, cudaStream_t s) 
 // Rows of a copy for the tcgen05 kernel: the largest that divides both the
 // tile and the page, 0 where the call does not suit the kernel (pages that
 // are no multiple of 8 rows, more heads a kv head than a tile has rows, a
-// stride of 0 that repeats an element).
+// stride of 0 that repeats an element, a negative scale).
 int tc_box(const AttendArgs& a) {
   const CacheView& c = a.c;
-  if (c.head_dim == 256 || a.group > 128) return 0;
+  if (c.head_dim == 256 || a.group > 128 || a.scale < 0.f) return 0;
   const int box = std::gcd(c.page_size, 128);
   const bool repeats = (c.page_size > 1 && !c.stride_token) || (c.kv_heads > 1 && !c.stride_head) ||
                        (c.pages > 1 && !c.stride_page) || (a.heads > 1 && !a.q_head) || (a.nodes > 1 && !a.q_node) ||
