@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   const int row_blocks = (rows_all + kRows - 1) / kRows;
   const int items = a.c.kv_heads * row_blocks;
 
+  if (a.join_later) pdl_launch_dependents();
   Line line;
   Cursor look;   // next tile whose offsets are looked up
   if (!find_run<kTile, kThreads>(a, items, scratch, &line, &look)) return;
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
           if (!whole && lane % 4 == 0) part[kRows * D + rl] = m[x], part[kRows * D + kRows + rl] = l[x];
         }
       }
-      if (!whole) {
+      if (!whole && !a.join_later) {
         __threadfence();
         __syncthreads();
         if (tid == 0) {
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
         }
         __syncthreads();
         if (last_here)
-          join_parts<T, kRows, D, kThreads>(a, line, masks, cur.b, kvh, row0, rows, cur.first, cur.nt, idle, tid);
+          join_parts<T, kRows, D, kThreads>(a, line, cur.b, kvh, row0, rows, cur.first, cur.nt, idle, tid);
       }
       fresh = true;
       __syncthreads();   // the masks and the stage may be written again

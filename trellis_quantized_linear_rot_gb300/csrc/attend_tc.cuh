@@ -22,7 +22,8 @@
 //                 (weights of up to 2^8 lose nothing in either dtype), which
 //                 after the first tiles is rare
 // At an item's end the two streams are joined, each group of warps taking
-// half of the columns. All waits are bounded.
+// half of the columns; items cut between blocks are joined by a launch of its
+// own. All waits are bounded.
 #pragma once
 
 #include "attend_mma.cuh"
@@ -203,7 +204,7 @@ struct TcShared {
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
   int scratch[384 / 32 + 2];
   uint32_t tmem;
-  int abort, last_here;
+  int abort;
 };
 
 template <int D>
@@ -233,12 +234,6 @@ __device__ __forceinline__ Seen seen_by(const int16_t* up, int node) {
       if (i >> 5 == x) s.w[x] |= 1u << (i & 31);
   return s;
 }
-// What join_parts asks: whether a node is present.
-struct Presence {
-  const int16_t* up;
-  __device__ __forceinline__ bool sees(int i, int) const { return up[i] >= -1; }
-};
-
 struct TcMaps {
   CUtensorMap q, k, v;
 };
@@ -268,6 +263,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     return;
   }
 
+  pdl_launch_dependents();   // the join may get ready
   Line line;
   Cursor cur;
   if (!find_run<kTile, S::kThreads>(a, items, sh.scratch, &line, &cur)) return;
@@ -516,8 +512,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
           // Values that must not be multiplied, even by 0: of slots that do
           // not exist, and of tree nodes where they are not finite (added at
           // the item's end to the rows that see them). They become 0.
-          const int j1 = cur.span.slots - slot0;
-          for (int id = row; id < kTile * (D / 8); id += 128) {
+          const int j0 = sh.any_gone ? 0 : max(0, cur.span.context - slot0), j1 = cur.span.slots - slot0;
+          for (int id = j0 * (D / 8) + row; id < kTile * (D / 8); id += 128) {
             const int key = id / (D / 8), ch = id % (D / 8), nd = slot0 + key - cur.span.context;
             uint4* at = reinterpret_cast<uint4*>(smem + (v_at - base) + st * S::kTileBytes + (ch / 8) * S::kPartBytes +
                                                  key * 128 + (((ch % 8) ^ (key & 7)) << 4));
@@ -597,8 +593,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
               *reinterpret_cast<uint4*>(out + c * 16 + 8) = uint4{w[4], w[5], w[6], w[7]};
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(part + row * D + c * 16 + i) = float4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+              for (int i = 0; i < 16; ++i) __stcg(part + (c * 16 + i) * 128 + row, x[i]);
             }
           }
         }
@@ -610,17 +605,6 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
             part[128 * D + row] = top;
             part[128 * D + 128 + row] = sum;
           }
-        }
-        if (!whole) {
-          __threadfence();
-          group_all(3, 256, true);
-          if (both == 0) {
-            sh.last_here = arrives_last(a, line, cur.first, cur.nt);
-            __threadfence();
-          }
-          group_all(3, 256, true);
-          if (sh.last_here)
-            join_parts<T, 128, D, 256>(a, line, Presence{sh.up}, cur.b, kvh, node0 * a.group, rows, cur.first, cur.nt, idle, both);
         }
         // Sums, parents and maxima have been read.
         if (!group_all(3, 256, true)) break;

@@ -12,6 +12,8 @@
 // waits for another.
 #pragma once
 
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "spec.cuh"
 
@@ -31,11 +33,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
 struct Line {
   int blocks, per, longer;
   int begin, end;
-  __device__ __forceinline__ void cut(int total, int launched) {
+  __device__ __forceinline__ void cut(int total, int launched, int block) {
     blocks = min(total, launched);
     per = total / blocks;
     longer = total - per * blocks;
-    const int i = min(static_cast<int>(blockIdx.x), blocks);
+    const int i = min(block, blocks);
     begin = begin_of(i);
     end = i < blocks ? begin_of(i + 1) : begin;
   }
@@ -88,7 +90,7 @@ __device__ bool find_run(const AttendArgs& a, int items, int* scratch, Line* lin
         all += scratch[w];
       }
       run += prior;
-      if (b0 + kThreads >= batch && (pass == 0 || batch <= kThreads)) line->cut(all, gridDim.x);
+      if (b0 + kThreads >= batch && (pass == 0 || batch <= kThreads)) line->cut(all, gridDim.x, blockIdx.x);
       if (pass == 1 && line->begin >= run - n && line->begin < run) {
         found[0] = run - n;
         found[1] = b;
@@ -151,11 +153,12 @@ __device__ __forceinline__ RowOf row_of(const AttendArgs& a, int kvh, int r) {
   return {node, kvh * a.group + r - node * a.group};
 }
 
-// kThreads threads (this one is number tid): joins the parts of the item at `first` (nt tiles) and writes
-// rows row0 .. row0 + rows - 1 of its kv head. Parts are added in run order.
-template <typename T, int kRows, int D, int kThreads, typename Masks>
-__device__ void join_parts(const AttendArgs& a, const Line& line, const Masks& masks, int b, int kvh, int row0,
-                           int rows, int first, int nt, bool idle, int tid) {
+// kThreads threads (this one is number tid): joins the parts of the item at
+// `first` (nt tiles) and writes its rows, which start at row0 of its kv head.
+// Parts are added in run order.
+template <typename T, int kRows, int D, int kThreads>
+__device__ void join_parts(const AttendArgs& a, const Line& line, int b, int kvh, int row0, int rows, int first,
+                           int nt, bool idle, int tid) {
   constexpr size_t kPart = kPartFloats<kRows, D>;
   const int b0 = line.block_of(first), n = line.block_of(first + nt - 1) - b0 + 1;
   // Every part but the first is the one its block begins with.
@@ -207,7 +210,8 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, const Masks& m
       const int r = r0 + k * kStep;
       if (r >= rows) continue;
       const RowOf ro = row_of(a, kvh, row0 + r);
-      const bool present = !idle && masks.sees(ro.node, ro.node);
+      const int up = a.parents[b * a.stride_parents + ro.node];
+      const bool present = !idle && up >= -1 && up < ro.node;
       const bool empty = !present || l[k] == 0.f;
       const float inv = empty ? 0.f : 1.f / l[k];
       const size_t at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;
@@ -219,6 +223,194 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, const Masks& m
       if (e == 0) a.lse[at] = empty ? -INFINITY : (top[k] + log2f(l[k])) * kLn2;
     }
   }
+}
+
+// The same for parts of 128 rows, which are stored by column (column c of row
+// r at c * 128 + r: there a thread has a row, and a warp's writes lie
+// together): this thread joins kColumns columns from c0 on of row r, kGroup
+// parts at once.
+template <typename T, int D, int kColumns, int kGroup>
+__device__ void join_row(const AttendArgs& a, const Line& line, int b, int kvh, int row0, int r, int c0, int first,
+                         int nt, bool idle) {
+  constexpr size_t kPart = kPartFloats<128, D>;
+  const int b0 = line.block_of(first), n = line.block_of(first + nt - 1) - b0 + 1;
+  const float* part0 = a.partials + part_index(line, b0, first) * kPart + r;
+  const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart + r;
+  float top = -INFINITY, l = 0.f, o[kColumns] = {};
+#pragma unroll 1
+  for (int p0 = 0; p0 < n; p0 += kGroup) {
+    float m[kGroup], w[kGroup], x[kGroup][kColumns];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const bool real = p0 + i < n;
+      const float* from = p0 + i == 0 || !real ? part0 : part1 + (p0 + i - 1) * 2 * kPart;
+      m[i] = real ? __ldcg(from + 128 * D) : -INFINITY;
+      w[i] = real ? __ldcg(from + 128 * D + 128) : 0.f;
+#pragma unroll
+      for (int c = 0; c < kColumns; ++c) x[i][c] = real ? __ldcg(from + (c0 + c) * 128) : 0.f;
+    }
+    float high = top;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) high = fmaxf(high, m[i]);
+    const float base = high == -INFINITY ? 0.f : high, keep = exp2_approx(top - base);
+    top = high;
+    l *= keep;
+#pragma unroll
+    for (int c = 0; c < kColumns; ++c) o[c] *= keep;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const float f = exp2_approx(m[i] - base);
+      l += f * w[i];
+#pragma unroll
+      for (int c = 0; c < kColumns; ++c) o[c] += f * x[i][c];
+    }
+  }
+  const RowOf ro = row_of(a, kvh, row0 + r);
+  const int up = a.parents[b * a.stride_parents + ro.node];
+  const bool empty = idle || up < -1 || up >= ro.node || l == 0.f;
+  const float inv = empty ? 0.f : 1.f / l;
+  const size_t at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;
+  T* out = static_cast<T*>(a.out) + at * D;
+#pragma unroll
+  for (int c = 0; c < kColumns; c += 8) {
+    alignas(16) T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(empty ? 0.f : o[c + i] * inv);
+    *reinterpret_cast<uint4*>(out + c0 + c) = *reinterpret_cast<const uint4*>(t);
+  }
+  if (c0 == 0) a.lse[at] = empty ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+// The join as a launch of its own: in the main launch one block reads all
+// parts of an item after everybody else has left, here the whole GPU does.
+// Block (x, y): item x, or, where there are more items than the main launch
+// had blocks (runs), the item that run x begins inside of, if x is the first
+// run to do so. It starts early (programmatic dependent launch) and waits for
+// the parts. y is a row, whose parts the block's groups of D / 4 threads share
+// out (kRows of 16 or 64), or kColumns columns of all 128 rows.
+template <typename T, int kRows, int D, int kTile, int kColumns, int kGroup>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs a, int row_blocks,
+                                                   int block_rows, int runs) {
+  __shared__ int scratch[6];
+  __shared__ int sums[2][4];
+  const int tid = threadIdx.x, items = a.c.kv_heads * row_blocks;
+  Line line;
+  Cursor cur;
+  int b0 = 0, n = 1;
+  if (gridDim.x == runs) {
+    if (find_run<kTile, 128>(a, items, scratch, &line, &cur) && cur.t > 0) {
+      b0 = line.block_of(cur.first);
+      if (static_cast<int>(blockIdx.x) == b0 + 1) n = line.block_of(cur.first + cur.nt - 1) - b0 + 1;
+    }
+  } else {
+    cur.b = blockIdx.x / items;
+    cur.item = blockIdx.x - cur.b * items;
+    int before = 0, all = 0;   // tiles of the sequences before b, and of all
+    for (int i = tid; i < a.c.batch; i += 128) {
+      const int tiles = tiles_of<kTile>(sequence_span(a.c, i, a.nodes)) * items;
+      all += tiles;
+      if (i < cur.b) before += tiles;
+    }
+    before = __reduce_add_sync(~0u, before);
+    all = __reduce_add_sync(~0u, all);
+    if (tid % 32 == 0) sums[0][tid / 32] = before, sums[1][tid / 32] = all;
+    __syncthreads();
+    cur.span = sequence_span(a.c, cur.b, a.nodes);
+    cur.nt = tiles_of<kTile>(cur.span);
+    cur.first = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3] + cur.item * cur.nt;
+    line.cut(sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3], runs, 0);
+    b0 = line.block_of(cur.first);
+    n = line.block_of(cur.first + cur.nt - 1) - b0 + 1;
+  }
+  pdl_wait_prerequisites();
+  if (n == 1) return;   // whole, or another block's
+  const int first = cur.first, nt = cur.nt, b = cur.b;
+  const int kvh = cur.item / row_blocks, row0 = (cur.item - kvh * row_blocks) * block_rows;
+  const int rows = min(block_rows, a.nodes * a.group - row0);
+  const Span span = cur.span;
+  if constexpr (kRows == 128) {
+    if (tid < rows)
+      join_row<T, D, kColumns, kGroup>(a, line, b, kvh, row0, tid, blockIdx.y * kColumns, first, nt, span.context < 0);
+  } else {
+    constexpr int kLanes = D / 4, kGroups = 128 / kLanes, kAhead = 6;
+    constexpr size_t kPart = kPartFloats<kRows, D>;
+    __shared__ float4 others[kGroups][kLanes];
+    __shared__ float tops[kGroups], ls[kGroups];
+    const int r = blockIdx.y, g = tid / kLanes, e = tid % kLanes * 4;
+    if (r >= rows) return;
+    const float* part0 = a.partials + part_index(line, b0, first) * kPart;
+    const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart;
+    float top = -INFINITY, l = 0.f;
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int p0 = g; p0 < n; p0 += kGroups * kAhead) {
+      float m[kAhead], w[kAhead];
+      float4 x[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int p = p0 + i * kGroups;
+        const float* part = p == 0 ? part0 : part1 + (p - 1) * 2 * kPart;
+        m[i] = p < n ? __ldcg(part + kRows * D + r) : -INFINITY;
+        w[i] = p < n ? __ldcg(part + kRows * D + kRows + r) : 0.f;
+        x[i] = p < n ? __ldcg(reinterpret_cast<const float4*>(part + r * D + e)) : float4{0.f, 0.f, 0.f, 0.f};
+      }
+      float high = top;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) high = fmaxf(high, m[i]);
+      const float base = high == -INFINITY ? 0.f : high, keep = exp2_approx(top - base);
+      top = high;
+      l *= keep, o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float f = exp2_approx(m[i] - base);
+        l += f * w[i], o.x += f * x[i].x, o.y += f * x[i].y, o.z += f * x[i].z, o.w += f * x[i].w;
+      }
+    }
+    others[g][tid % kLanes] = o;
+    if (e == 0) tops[g] = top, ls[g] = l;
+    __syncthreads();
+    if (g > 0) return;
+    for (int k = 1; k < kGroups; ++k) top = fmaxf(top, tops[k]);
+    const float base = top == -INFINITY ? 0.f : top;
+    l = 0.f, o = float4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < kGroups; ++k) {
+      const float f = exp2_approx(tops[k] - base);
+      const float4 x = others[k][tid % kLanes];
+      l += f * ls[k], o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+    }
+    const RowOf ro = row_of(a, kvh, row0 + r);
+    const int up = a.parents[b * a.stride_parents + ro.node];
+    const bool empty = span.context < 0 || up < -1 || up >= ro.node || l == 0.f;
+    const float inv = empty ? 0.f : 1.f / l;
+    const size_t out_at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;
+    const float y[4] = {o.x, o.y, o.z, o.w};
+    alignas(8) T t[4];
+    for (int i = 0; i < 4; ++i) t[i] = from_f32<T>(empty ? 0.f : y[i] * inv);
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + out_at * D + e) = *reinterpret_cast<const uint2*>(t);
+    if (e == 0) a.lse[out_at] = empty ? -INFINITY : (top + log2f(l)) * kLn2;
+  }
+}
+
+template <typename T, int kRows, int D, int kTile, int kColumns, int kGroup>
+cudaError_t launch_join_as(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int items = a.c.batch * a.c.kv_heads * row_blocks;
+  cfg.gridDim = dim3(std::min(items, runs), kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, kRows, D, kTile, kColumns, kGroup>, a, row_blocks, block_rows, runs);
+}
+
+// Few items have many parts each: few columns a block, many parts at once.
+template <typename T, int kRows, int D, int kTile>
+cudaError_t launch_join(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
+  if (runs >= 4 * a.c.batch * a.c.kv_heads * row_blocks || kRows < 128)
+    return launch_join_as<T, kRows, D, kTile, 8, 8>(a, runs, row_blocks, block_rows, s);
+  return launch_join_as<T, kRows, D, kTile, kRows < 128 ? 8 : 32, kRows < 128 ? 8 : 2>(a, runs, row_blocks, block_rows, s);
 }
 
 }  // namespace tfx

@@ -38,6 +38,7 @@ struct AttendArgs {
   float* partials;
   int* counters;
   int num_sms;
+  int join_later;   // the parts are joined by a launch of their own
 };
 
 // Blocks of an attention launch for each SM.

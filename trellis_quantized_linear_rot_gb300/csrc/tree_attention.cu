@@ -16,8 +16,17 @@ constexpr int kMaxDevices = 64;
 // Rows a kv head up to which the 16-row kernel takes them in one block.
 constexpr int kFewRows = 16;
 
+// Whether an item is cut into so many parts that a launch of its own joins
+// them: its share of the blocks, or of the tiles it can have if those are
+// fewer, is over kManyParts.
+constexpr int kManyParts = 6;
+bool many_parts(const AttendArgs& a, int blocks, int items, int tile) {
+  const int64_t tiles = (static_cast<int64_t>(a.c.table_width) * a.c.page_size + tile - 1) / tile;
+  return std::min<int64_t>(blocks / items, tiles) > kManyParts;
+}
+
 template <typename T, int D, int kRowWarps>
-cudaError_t launch_mma(const AttendArgs& a, int device, cudaStream_t s) {
+cudaError_t launch_mma(AttendArgs a, int device, cudaStream_t s) {
   using S = MmaShape<D, kRowWarps>;
   static PerDeviceOnce<kMaxDevices> once;
   const int e = once.run(device, cudaErrorInvalidDevice, [] {
@@ -25,8 +34,12 @@ cudaError_t launch_mma(const AttendArgs& a, int device, cudaStream_t s) {
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
   });
   if (e != cudaSuccess) return static_cast<cudaError_t>(e);
-  tree_attention_mma_kernel<T, D, kRowWarps><<<kBlocksPerSm * a.num_sms, S::kThreads, S::kSmem, s>>>(a);
-  return cudaGetLastError();
+  const int blocks = kBlocksPerSm * a.num_sms, row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
+  a.join_later = many_parts(a, blocks, a.c.batch * a.c.kv_heads * row_blocks, S::kTile);
+  tree_attention_mma_kernel<T, D, kRowWarps><<<blocks, S::kThreads, S::kSmem, s>>>(a);
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess || !a.join_later) return launched;
+  return launch_join<T, S::kRows, D, S::kTile>(a, blocks, row_blocks, S::kRows, s);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -81,8 +94,12 @@ cudaError_t launch_tc(const AttendArgs& a, int box, int device, cudaStream_t s) 
       !make_map(&maps.v, half, a.v, {D, c.page_size, c.kv_heads, c.pages},
                 {c.stride_token, c.stride_head, c.stride_page}, box, 1))
     return cudaErrorInvalidValue;
+  const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
   tree_attention_tc_kernel<T, D><<<a.num_sms, S::kThreads, S::kSmem, s>>>(maps, args);
-  return cudaGetLastError();
+  const cudaError_t launched = cudaGetLastError();
+  // No item has a second tile to be cut off.
+  if (launched != cudaSuccess || static_cast<int64_t>(c.table_width) * c.page_size <= S::kTile) return launched;
+  return launch_join<T, 128, D, S::kTile>(a, a.num_sms, row_blocks, args.block_nodes * a.group, s);
 }
 
 // Rows of a copy for the tcgen05 kernel: the largest that divides both the
