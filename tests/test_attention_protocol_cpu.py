@@ -52,7 +52,7 @@ class Sim:
         self.q_full, self.q_empty = Barrier(1), Barrier(2)
         self.s_full, self.p_full, self.pv_done = ([Barrier(1), Barrier(1)] for _ in range(3))
         self.k, self.v = [None] * STAGES, [None] * STAGES   # tile whose data a stage holds
-        self.q = None
+        self.q, self.k_issued = None, 0
         self.scores = [None, None]
         self.summed = []
         self.events = []          # things that happen later, in any order (or in order, per queue)
@@ -62,17 +62,18 @@ class Sim:
         return (j // self.slots) & 1
 
     # --- the warps, as generators: `yield (barrier, parity)` waits
-    def copies(self):
+    def copies(self, data, empty, what):
+        """Keys, and values: one warp, but each side goes on whenever it can."""
         for j in range(len(self.tiles)):
             b = j - STAGES
             if b >= 0:
-                yield self.k_empty[self.number(b)], self.phase(b)
-            self.k[j % STAGES] = None
-            self.events.append(("k", j))
-            if b >= 0:
-                yield self.v_empty[self.number(b)], self.phase(b)
-            self.v[j % STAGES] = None
-            self.events.append(("v", j))
+                yield empty[self.number(b)], self.phase(b)
+            if what == "v" and self.k_issued <= j:
+                yield lambda j=j: self.k_issued > j
+            if what == "k":
+                self.k_issued = j + 1
+            data[j % STAGES] = None
+            self.events.append((what, j))
 
     def q_copies(self):
         n = 0
@@ -85,14 +86,14 @@ class Sim:
                 n += 1
 
     def products(self, s):
-        n = item = 0
-        fresh = True
-        for j, (i, t) in enumerate(self.tiles):
-            end = self.last[i]
-            if fresh:
-                yield self.q_full, item & 1
-                fresh, done = False, False
-            if j % 2 == s:
+        n = 0
+        for item, i in enumerate(sorted(self.last)):
+            jb = self.last[i] + 1
+            mine = [j for j, (k, _) in enumerate(self.tiles) if k == i and j % 2 == s]
+            yield self.q_full, item & 1
+            if not mine and jb < len(self.tiles):
+                self.q_empty.arrive()
+            for j in mine:
                 yield self.k_full[self.number(j)], self.phase(j)
                 if n:
                     yield self.pv_done[s], (n - 1) & 1
@@ -101,10 +102,9 @@ class Sim:
                 todo = [("scores", s, j), ("arrive", self.s_full[s])]
                 if j + STAGES < len(self.tiles):
                     todo.append(("arrive", self.k_empty[self.number(j)]))
-                if j + 2 > end and end + 1 < len(self.tiles):
+                if j + 2 >= jb and jb < len(self.tiles):
                     todo.append(("arrive", self.q_empty))
                 self.queues[s] += todo
-                done = j + 2 > end
                 yield self.v_full[self.number(j)], self.phase(j)
                 yield self.p_full[s], n & 1
                 if self.v[j % STAGES] != j:
@@ -114,10 +114,6 @@ class Sim:
                     todo.append(("arrive", self.v_empty[self.number(j)]))
                 self.queues[s] += todo
                 n += 1
-            if j == end:
-                if not done and j + 1 < len(self.tiles):
-                    self.q_empty.arrive()
-                fresh, item = True, item + 1
 
     def weights(self, s):
         n = 0
@@ -161,13 +157,15 @@ class Sim:
         return True
 
     def run(self):
-        warps = [self.copies(), self.q_copies(), self.products(0), self.products(1), self.weights(0), self.weights(1)]
-        waits = [None] * 6
-        live = set(range(6))
+        warps = [self.copies(self.k, self.k_empty, "k"), self.q_copies(), self.products(0), self.products(1),
+                 self.weights(0), self.weights(1), self.copies(self.v, self.v_empty, "v")]
+        waits = [None] * 7
+        live = set(range(7))
         met = set()
-        slow = self.rng.choice([None, 0, 1, 2, 3, 4, 5])    # a warp that gets few turns
+        slow = self.rng.choice([None, 0, 1, 2, 3, 4, 5, 6])    # a warp that gets few turns
         while live:
-            ready = [w for w in live if waits[w] is None or (waits[w] != "meet" and waits[w][0].passes(waits[w][1]))]
+            ready = [w for w in live if waits[w] is None or (callable(waits[w]) and waits[w]()) or
+                     (isinstance(waits[w], tuple) and waits[w][0].passes(waits[w][1]))]
             if slow in ready and len(ready) > 1 and self.rng.random() < 0.9:
                 ready.remove(slow)
             if (not ready or self.rng.random() < 0.4) and self.happen():

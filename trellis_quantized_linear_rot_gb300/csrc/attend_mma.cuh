@@ -130,13 +130,13 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int row_warp = warp % kRowWarps, key_warp = warp / kRowWarps;
   const int rows_all = a.nodes * a.group;
-  const int row_blocks = (rows_all + kRows - 1) / kRows;
-  const int items = a.c.kv_heads * row_blocks;
+  const int row_blocks = (rows_all + kRows - 1) / kRows, team = blockIdx.x / row_blocks;
+  const Rows mine{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
 
   if (a.join_later) pdl_launch_dependents();
   Line line;
   Cursor look;   // next tile whose offsets are looked up
-  if (!find_run<kTile, kThreads>(a, items, scratch, &line, &look)) return;
+  if (!find_run<kTile, kThreads>(a, gridDim.x / row_blocks, team, scratch, &line, &look)) return;
   Cursor cur = look, load = look;   // tiles computed and copied next
   const uint32_t ring = smem_u32(smem);
   const uint32_t q_ring = ring + kStages * 2 * S::kHalf;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   auto look_up = [&](const Cursor& c) -> Pending {
     const int slot = c.t * kTile + tid, p = slot / a.c.page_size;
     const bool exists = slot < c.span.slots;
-    return {exists ? a.c.page_table[c.b * a.c.stride_table + p] : 0, slot - p * a.c.page_size, c.item / row_blocks, exists};
+    return {exists ? a.c.page_table[c.b * a.c.stride_table + p] : 0, slot - p * a.c.page_size, c.item, exists};
   };
   auto settle = [&](const Pending& x, int i) {
     const bool outside = x.exists && static_cast<unsigned>(x.page) >= static_cast<unsigned>(a.c.pages);
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   };
   // Copies of q and of the parents for the item of tile i (at cursor c).
   auto issue_rows = [&](const Cursor& c, int i) {
-    const int h = c.item / row_blocks, first_row = (c.item - h * row_blocks) * kRows;
+    const int h = c.item, first_row = mine.rb * kRows;
     const uint32_t dst = q_ring + (i % kStages) * S::kQBytes;
     for (int id = tid; id < kRows * kChunks; id += kThreads) {
       const int r = id / kChunks, ch = id % kChunks;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   for (int i = 0; i < kStages; ++i)
     if (i < n_tiles) {
       if (tid < kTile) first[i] = look_up(look);
-      advance<kTile>(a, items, &look);
+      advance<kTile>(a, &look);
     }
 #pragma unroll
   for (int i = 0; i < kStages; ++i)
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
     if (i < n_tiles) {
       if (i > 0 && load.t == 0) issue_rows(load, i);
       issue(i);
-      advance<kTile>(a, items, &load);
+      advance<kTile>(a, &load);
     }
     copies_commit();
   }
@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   uint32_t qf[D == 256 ? 1 : D / 16][4];
   float o[D / 8][4];
   float m[2], l[2];
-  int kvh = 0, row0 = 0;
+  const int row0 = mine.rb * kRows;
+  int kvh = 0;
   int node[2];
   const uint32_t q_at = q_ring + kStages * S::kQBytes;   // D = 256 only
   bool fresh = true;
@@ -233,17 +234,16 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
     if (i + kStages - 1 < n_tiles) {
       if (load.t == 0) issue_rows(load, i + kStages - 1);
       issue(i + kStages - 1);
-      advance<kTile>(a, items, &load);
+      advance<kTile>(a, &load);
     }
     copies_commit();
     const bool more = i + kStages < n_tiles;
     Pending next = {};
     if (more && tid < kTile) next = look_up(look);   // settled after this tile
-    if (more) advance<kTile>(a, items, &look);
+    if (more) advance<kTile>(a, &look);
 
     if (fresh) {   // a new item: its rows of q, its masks
-      kvh = cur.item / row_blocks;
-      row0 = (cur.item - kvh * row_blocks) * kRows;
+      kvh = cur.item;
       const uint32_t q_new = q_ring + (i % kStages) * S::kQBytes;
       if constexpr (D == 256) {
         unsigned char* q8 = smem + kStages * 2 * S::kHalf;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
       const bool whole = item_ends && cur.first >= line.begin;
       const int rows = min(kRows, rows_all - row0);
       const bool idle = cur.span.context < 0;
-      float* part = a.partials + part_index(line, blockIdx.x, cur.first) * kPartFloats<kRows, D>;
+      float* part = a.partials + part_index(line, mine, team, cur.first) * kPartFloats<kRows, D>;
       // Sums over the four lanes of a row, then over the warps with other keys.
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -486,18 +486,18 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
         __threadfence();
         __syncthreads();
         if (tid == 0) {
-          last_here = arrives_last(a, line, cur.first, cur.nt);
+          last_here = arrives_last(a, line, mine, cur.first, cur.nt);
           __threadfence();
         }
         __syncthreads();
         if (last_here)
-          join_parts<T, kRows, D, kThreads>(a, line, cur.b, kvh, row0, rows, cur.first, cur.nt, idle, tid);
+          join_parts<T, kRows, D, kThreads>(a, line, mine, cur.b, kvh, row0, rows, cur.first, cur.nt, idle, tid);
       }
       fresh = true;
       __syncthreads();   // the masks and the stage may be written again
     }
     if (more && tid < kTile) settle(next, i + kStages);
-    advance<kTile>(a, items, &cur);
+    advance<kTile>(a, &cur);
   }
 }
 

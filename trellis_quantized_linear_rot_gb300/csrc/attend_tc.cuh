@@ -7,9 +7,9 @@
 // rows the cache's bytes bound it, and with several the tensor cores and the
 // exponentials (128 x 128 a tile, 16 a cycle: as long as the products).
 //
-// One block an SM, a run of tiles each (attend_work.cuh). An item is a
-// (sequence, kv head, block of whole nodes with at most 128 rows). Its key
-// tiles go alternately to two streams, each with its own scores, weights,
+// One block an SM, a run of tiles for each team of blocks, one block for each
+// block of rows: whole nodes with at most 128 rows (attend_work.cuh). An
+// item's key tiles go alternately to two streams, each with its own scores, weights,
 // sums and running maximum in Tensor Memory and registers, so that one
 // stream's products run while the other's exponentials do:
 //   warp 0        copies: q of an item; keys and values of a tile, a box for
@@ -67,6 +67,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
+}
+// Whether the phase of that parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -254,7 +266,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
   volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
-  const int items = a.c.kv_heads * row_blocks;
+  const int team = blockIdx.x / row_blocks;
+  const Rows own{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
+  const int node0 = own.rb * args.block_nodes;
   const uint32_t base = smem_u32(smem);
   const uint32_t q_at = base, k_at = base + S::kTileBytes, v_at = k_at + kStages * S::kTileBytes;
   auto bar = [&](int i) { return smem_u32(&sh.bars[i]); };
@@ -266,7 +280,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
   pdl_launch_dependents();   // the join may get ready
   Line line;
   Cursor cur;
-  if (!find_run<kTile, S::kThreads>(a, items, sh.scratch, &line, &cur)) return;
+  if (!find_run<kTile, S::kThreads>(a, gridDim.x / row_blocks, team, sh.scratch, &line, &cur)) return;
   const int n_tiles = line.end - line.begin;
 
   if (tid == 0) {
@@ -305,65 +319,75 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     // ---------------------------------------------------------------- copies
     const int box = args.box, boxes = kTile / box;   // at most 16
     const uint32_t box_bytes = static_cast<uint32_t>(box) * 128;
-    bool ok = true;
-    int tiles_out = 0;   // tiles whose copies were issued
-    // Page of this lane's box of the tile at a cursor: asked for a tile ahead.
+    // Keys and values go at their own pace, whichever has a free stage: keys
+    // are done with earlier. Each side asks for its pages a tile ahead.
+    struct Side {
+      Cursor cur, next;
+      int page, j;
+    };
     auto look_up = [&](const Cursor& c) {
       const int slot = c.t * kTile + lane * box;
       return lane < boxes && slot < c.span.slots ? a.c.page_table[c.b * a.c.stride_table + slot / a.c.page_size] : -1;
     };
-    Cursor next = cur;
-    int page = look_up(next);
-#pragma unroll 1
-    for (int j = 0; j < n_tiles && ok; ++j) {
-      const int st = j % kStages, slot_j = j % kTcSlots;
-      const int before = j - kStages, slot_b = before % kTcSlots, phase_b = (before / kTcSlots) & 1;   // the stage's last tile
-      const int kvh = cur.item / row_blocks;
-      const int slot = cur.t * kTile + lane * box;
-      const bool exists = lane < boxes && slot < cur.span.slots;
-      const bool outside = exists && static_cast<unsigned>(page) >= static_cast<unsigned>(a.c.pages);
+    Side ks = {cur, cur, look_up(cur), 0}, vs = ks;
+    auto free_stage = [&](const Side& x, int empty) {
+      const int b = x.j - kStages;   // the tile before in its stage
+      return x.j < n_tiles && (b < 0 || mbar_test(bar(empty + b % kTcSlots), (b / kTcSlots) & 1));
+    };
+    auto issue = [&](Side* x, const CUtensorMap* map, uint32_t ring, int full, bool values) {
+      const int st = x->j % kStages, slot = x->cur.t * kTile + lane * box;
+      const bool exists = lane < boxes && slot < x->cur.span.slots;
+      const bool outside = exists && static_cast<unsigned>(x->page) >= static_cast<unsigned>(a.c.pages);
       const bool copy = exists && !outside;
-      const int this_page = page;
-      if (j + 1 < n_tiles) {
-        advance<kTile>(a, items, &next);
-        page = look_up(next);
+      const int page = x->page, kvh = x->cur.item, row = slot % a.c.page_size;
+      if (x->j + 1 < n_tiles) {
+        advance<kTile>(a, &x->next);
+        x->page = look_up(x->next);
       }
-      if (outside) record_index_error(a.c.err);
-      const int row = slot % a.c.page_size;
       const uint32_t wanted = __popc(__ballot_sync(~0u, copy)) * box_bytes * S::kParts;
       const uint32_t missing = __ballot_sync(~0u, outside);
-      if (before >= 0) ok = mbar_wait(bar(kKEmpty + slot_b), phase_b, abort_flag);
-      if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + slot_j), wanted);
+      if (values) {
+        if (outside) record_index_error(a.c.err);
+        if (lane < 4) {
+          uint32_t word = 0;
+          if (missing)
+            for (int i = 0; i < 32; ++i) word |= (missing >> ((lane * 32 + i) / box) & 1u) << i;
+          sh.gone[st][lane] = word;
+          if (missing) sh.any_gone = 1;
+        }
+        __syncwarp();
+      }
+      const uint32_t b = bar(full + x->j % kTcSlots);
+      if (lane == 0) mbar_arrive_expect_tx(b, wanted);
       __syncwarp();
       if (copy)
         for (int h = 0; h < S::kParts; ++h)
-          tma_load_4d(k_at + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, &maps.k, h * 64, row, kvh,
-                      this_page, bar(kKFull + slot_j));
-      if (before >= 0) ok = mbar_wait(bar(kVEmpty + slot_b), phase_b, abort_flag);
-      if (lane < 4) {
-        uint32_t word = 0;
-        if (missing)
-          for (int i = 0; i < 32; ++i) word |= (missing >> ((lane * 32 + i) / box) & 1u) << i;
-        sh.gone[st][lane] = word;
-        if (missing) sh.any_gone = 1;
+          tma_load_4d(ring + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, map, h * 64, row, kvh, page, b);
+      __syncwarp();
+      x->cur = x->next;
+      ++x->j;
+    };
+    unsigned long long since = global_ns();
+#pragma unroll 1
+    for (uint32_t it = 1; vs.j < n_tiles; ++it) {
+      const bool k_now = __all_sync(~0u, free_stage(ks, kKEmpty));
+      if (k_now) issue(&ks, &maps.k, k_at, kKFull, false);
+      const bool v_now = vs.j < ks.j && __all_sync(~0u, free_stage(vs, kVEmpty));
+      if (v_now) issue(&vs, &maps.v, v_at, kVFull, true);
+      if (k_now || v_now) {
+        since = global_ns();
+      } else {
+        __nanosleep(20);
+        if ((it & 63) == 0) {
+          if (global_ns() - since > kWaitLimitNs) *abort_flag = 1;
+          if (__any_sync(~0u, *abort_flag)) break;
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + slot_j), ok ? wanted : 0);
-      __syncwarp();
-      if (copy && ok)
-        for (int h = 0; h < S::kParts; ++h)
-          tma_load_4d(v_at + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, &maps.v, h * 64, row, kvh,
-                      this_page, bar(kVFull + slot_j));
-      tiles_out = j + 1;
-      advance<kTile>(a, items, &cur);
     }
-    if (!ok) {   // given up: the copies in flight still have to land
+    if (vs.j < n_tiles) {   // given up: the copies in flight still have to land
       volatile int never = 0;
-      for (int j = tiles_out > kStages ? tiles_out - kStages : 0; j < tiles_out; ++j) {
-        mbar_wait(bar(kKFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
-        mbar_wait(bar(kVFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
-      }
+      for (int j = max(0, ks.j - kStages); j < ks.j; ++j) mbar_wait(bar(kKFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
+      for (int j = max(0, vs.j - kStages); j < vs.j; ++j) mbar_wait(bar(kVFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
     }
   } else if (warp == 3) {
     // ----------------------------------------------------------- copies of q
@@ -372,19 +396,19 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
 #pragma unroll 1
     for (int j = 0; j < n_tiles && ok; ++j) {
       if (j == 0 || cur.t == 0) {
-        if (n_items > 0) ok = mbar_wait_sleepy(bar(kQEmpty), (n_items - 1) & 1, abort_flag, 100);
+        if (n_items > 0) ok = __all_sync(~0u, mbar_wait_sleepy(bar(kQEmpty), (n_items - 1) & 1, abort_flag, 100));
         if (!ok) break;
-        const int kvh = cur.item / row_blocks;
+        const int kvh = cur.item;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(kQFull), static_cast<uint32_t>(args.block_nodes * a.group) * 128 * S::kParts);
           for (int h = 0; h < S::kParts; ++h)
             tma_load_4d(q_at + h * S::kPartBytes, &maps.q, h * 64, kvh * a.group,
-                        (cur.item - kvh * row_blocks) * args.block_nodes, cur.b, bar(kQFull));
+                        node0, cur.b, bar(kQFull));
         }
         __syncwarp();
         ++n_items;
       }
-      advance<kTile>(a, items, &cur);
+      advance<kTile>(a, &cur);
     }
     if (!ok) {
       volatile int never = 0;
@@ -395,21 +419,25 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     const int s = warp - 1;
     const uint32_t scores = tmem + S::kScores + s * 128, sums = tmem + S::kSums + s * D;
     constexpr uint32_t kScoreDesc = idesc_of<T>(128, false), kSumDesc = idesc_of<T>(D, true);
-    int n = 0, n_items = 0;
-    bool fresh = true, first = true, done = false, ok = true;
+    int n = 0;
+    bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < n_tiles && ok; ++j) {
-      const int st = j % kStages, slot_j = j % kTcSlots, phase = (j / kTcSlots) & 1;
-      const int item_end = j + cur.nt - 1 - cur.t;   // the item's last tile
-      if (fresh) {
-        ok = mbar_wait(bar(kQFull), n_items & 1, abort_flag);
-        fresh = false, first = true, done = false;
-      }
-      if ((j & 1) == s && ok) {
+    for (int ja = 0, n_items = 0; ja < n_tiles && ok; ++n_items) {   // the items of the run, tiles ja .. jb - 1
+      const int jb = ja + min(n_tiles - ja, cur.nt - cur.t), j0 = ja + ((ja ^ s) & 1);
+      ok = __all_sync(~0u, mbar_wait(bar(kQFull), n_items & 1, abort_flag));
+      // a stream without a tile of the item does not hold q up
+      if (ok && j0 >= jb && jb < n_tiles && elect_one()) mbar_arrive(bar(kQEmpty));
+      __syncwarp();
+#pragma unroll 1
+      for (int j = j0; j < jb && ok; j += 2) {
+        const int st = j % kStages, slot_j = j % kTcSlots, phase = (j / kTcSlots) & 1;
         ok = mbar_wait(bar(kKFull + slot_j), phase, abort_flag);
         // the weights lie over the scores until their product is done
         if (ok && n > 0) ok = mbar_wait(bar(kPvDone + s), (n - 1) & 1, abort_flag);
-        if (!ok) break;
+        if (!__all_sync(~0u, ok)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -418,36 +446,32 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
             mma_ss(scores, smem_desc_sw128(q_at + off, 1024),
                    smem_desc_sw128(k_at + st * S::kTileBytes + off, 1024), kScoreDesc, k > 0);
           }
+          mma_commit(bar(kSFull + s));
           // only what someone will wait for, so that nothing arrives after the end
           if (j + kStages < n_tiles) mma_commit(bar(kKEmpty + slot_j));
-          mma_commit(bar(kSFull + s));
-          if (j + 2 > item_end && item_end + 1 < n_tiles) mma_commit(bar(kQEmpty));
+          if (j + 2 >= jb && jb < n_tiles) mma_commit(bar(kQEmpty));
         }
         __syncwarp();
-        done = j + 2 > item_end;
         ok = mbar_wait(bar(kVFull + slot_j), phase, abort_flag) && mbar_wait(bar(kPFull + s), n & 1, abort_flag);
-        if (!ok) break;
+        if (!__all_sync(~0u, ok)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
             mma_ts(sums, scores + k * 8, desc_by_keys(v_at + st * S::kTileBytes + k * 2048, S::kPartBytes), kSumDesc,
-                   !first || k > 0);
-          if (j + kStages < n_tiles) mma_commit(bar(kVEmpty + slot_j));
+                   j > j0 || k > 0);
           mma_commit(bar(kPvDone + s));
+          if (j + kStages < n_tiles) mma_commit(bar(kVEmpty + slot_j));
         }
         __syncwarp();
-        first = false;
         ++n;
       }
-      if (j == item_end) {
-        // a stream without a tile of the item does not hold q up
-        if (!done && j + 1 < n_tiles && elect_one()) mbar_arrive(bar(kQEmpty));
-        __syncwarp();
-        fresh = true;
-        ++n_items;
-      }
-      advance<kTile>(a, items, &cur);
+      cur.t += jb - ja - 1;
+      advance<kTile>(a, &cur);
+      ja = jb;
     }
     if (!ok && n > 0) {   // given up: the products in flight still have to end
       volatile int never = 0;
@@ -465,7 +489,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
 #pragma unroll 1
     for (int ja = 0; ja < n_tiles;) {   // the items of the run, tiles ja .. jb - 1 of it
       const int jb = ja + min(n_tiles - ja, cur.nt - cur.t);
-      const int kvh = cur.item / row_blocks, node0 = (cur.item - kvh * row_blocks) * args.block_nodes;
+      const int kvh = cur.item;
       const int node = row_node < args.block_nodes && node0 + row_node < a.nodes ? node0 + row_node : -1;
       if (both < a.nodes) {
         int p = a.parents[cur.b * a.stride_parents + both];
@@ -564,7 +588,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         const size_t out_at = node >= 0 ? (static_cast<size_t>(cur.b) * a.nodes + node) * a.heads + kvh * a.group +
                                               row - row_node * a.group : 0;
         T* out = static_cast<T*>(a.out) + out_at * D;
-        float* part = a.partials + part_index(line, blockIdx.x, cur.first) * kPartFloats<128, D>;
+        float* part = a.partials + part_index(line, own, team, cur.first) * kPartFloats<128, D>;
 #pragma unroll 1
         for (int c = s * (D / 32); c < (s + 1) * (D / 32); ++c) {
           float x[16] = {}, y[16] = {};
@@ -610,7 +634,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         if (!group_all(3, 256, true)) break;
       }
       cur.t += jb - ja - 1;
-      advance<kTile>(a, items, &cur);
+      advance<kTile>(a, &cur);
       ja = jb;
     }
   }

@@ -1,15 +1,16 @@
 // How the attention kernels divide their work, and how the parts of a row are
 // joined.
 //
-// An item is one (sequence, kv head, block of rows): its rows all read the
-// same keys. The tiles of all items, sequence by sequence, form one line that
-// is cut into equal runs, one for each block of the launch, so that ragged
-// lengths and few long sequences fill the GPU alike. Lengths are on the
-// device, so every block finds its run itself. A run holds whole items but
-// for its first and its last, which other blocks may share: those leave
-// (max, sum, weighted sum) of their part in the workspace, and the block that
-// arrives last at the item joins the parts in the order of the runs. No block
-// waits for another.
+// An item is one (sequence, kv head). The tiles of all items, sequence by
+// sequence, form one line that is cut into equal runs, so that ragged lengths
+// and few long sequences fill the GPU alike. A run has a team of blocks, one
+// for each block of rows (one if the rows of a kv head fit one): they read the
+// same keys at about the same time, so that memory gives them once and L2 the
+// other times. Lengths are on the device, so every block finds its run itself.
+// A run holds whole items but for its first and its last, which other runs may
+// share: those leave (max, sum, weighted sum) of their part in the workspace,
+// and the parts are joined in the order of the runs, by the block that arrives
+// last at the item or by a launch of its own. No block waits for another.
 #pragma once
 
 #include <algorithm>
@@ -27,30 +28,28 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// The line of tiles (below 2^31: checked on the host) and this block's run of
-// it: the first `longer` runs have per + 1 tiles, the others per. No more
+// The line of tiles (below 2^31: checked on the host) and one run of it: the first `longer` runs have per + 1 tiles, the others per. No more
 // runs than tiles, so that no run between two others is empty.
 struct Line {
-  int blocks, per, longer;
+  int runs, per, longer;
   int begin, end;
-  __device__ __forceinline__ void cut(int total, int launched, int block) {
-    blocks = min(total, launched);
-    per = total / blocks;
-    longer = total - per * blocks;
-    const int i = min(block, blocks);
+  __device__ __forceinline__ void cut(int total, int most, int run) {
+    runs = min(total, most);
+    per = total / runs;
+    longer = total - per * runs;
+    const int i = min(run, runs);
     begin = begin_of(i);
-    end = i < blocks ? begin_of(i + 1) : begin;
+    end = i < runs ? begin_of(i + 1) : begin;
   }
-  __device__ __forceinline__ int begin_of(int block) const { return block * per + min(block, longer); }
-  // The block whose run holds tile f.
-  __device__ __forceinline__ int block_of(int f) const {
+  __device__ __forceinline__ int begin_of(int run) const { return run * per + min(run, longer); }
+  // The run that holds tile f.
+  __device__ __forceinline__ int run_of(int f) const {
     const int border = longer * (per + 1);
     return f < border ? f / (per + 1) : longer + (f - border) / per;
   }
 };
 
-// Position of a tile: item `item` (kv head, row block) of sequence b, tile t
-// of its nt. first = place of the item's tile 0 in the line.
+// Position of a tile: item `item` (kv head) of sequence b, tile t of its nt. first = place of the item's tile 0 in the line.
 struct Cursor {
   int b, item, t, nt;
   int first;
@@ -62,12 +61,13 @@ __device__ __forceinline__ int tiles_of(const Span& s) {
   return s.slots <= kTile ? 1 : (s.slots + kTile - 1) / kTile;
 }
 
-// Block-wide: the line, this block's run and the cursor at its begin.
+// Block-wide: the line, run number `run` of at most `most`, and the cursor at its begin.
 // `scratch` has room for kThreads / 32 + 2 ints. False where the run is
 // empty. Batches of up to kThreads sequences are scanned once, larger ones
 // twice (length, then place).
 template <int kTile, int kThreads>
-__device__ bool find_run(const AttendArgs& a, int items, int* scratch, Line* line, Cursor* cur) {
+__device__ bool find_run(const AttendArgs& a, int most, int run, int* scratch, Line* line, Cursor* cur) {
+  const int items = a.c.kv_heads;
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int batch = a.c.batch;
@@ -77,22 +77,22 @@ __device__ bool find_run(const AttendArgs& a, int items, int* scratch, Line* lin
     for (int b0 = 0; b0 < batch; b0 += kThreads) {
       const int b = b0 + tid;
       const int n = b < batch ? tiles_of<kTile>(sequence_span(a.c, b, a.nodes)) * items : 0;
-      int run = n;
+      int upto = n;
       for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(~0u, run, o);
-        if (lane >= o) run += y;
+        const int y = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += y;
       }
-      if (lane == 31) scratch[warp] = run;
+      if (lane == 31) scratch[warp] = upto;
       __syncthreads();
       int prior = before, all = before;
       for (int w = 0; w < kWarps; ++w) {
         if (w < warp) prior += scratch[w];
         all += scratch[w];
       }
-      run += prior;
-      if (b0 + kThreads >= batch && (pass == 0 || batch <= kThreads)) line->cut(all, gridDim.x, blockIdx.x);
-      if (pass == 1 && line->begin >= run - n && line->begin < run) {
-        found[0] = run - n;
+      upto += prior;
+      if (b0 + kThreads >= batch && (pass == 0 || batch <= kThreads)) line->cut(all, most, run);
+      if (pass == 1 && line->begin >= upto - n && line->begin < upto) {
+        found[0] = upto - n;
         found[1] = b;
       }
       before = all;
@@ -111,34 +111,37 @@ __device__ bool find_run(const AttendArgs& a, int items, int* scratch, Line* lin
 }
 
 template <int kTile>
-__device__ __forceinline__ void advance(const AttendArgs& a, int items, Cursor* c) {
+__device__ __forceinline__ void advance(const AttendArgs& a, Cursor* c) {
   if (++c->t < c->nt) return;
   c->t = 0;
   c->first += c->nt;
-  if (++c->item < items) return;
+  if (++c->item < a.c.kv_heads) return;
   c->item = 0;
   if (++c->b >= a.c.batch) return;
   c->span = sequence_span(a.c, c->b, a.nodes);
   c->nt = tiles_of<kTile>(c->span);
 }
 
-// Place of a block's part of the item at `first`. A block has two parts in
-// the workspace: of the item its run begins in, and of a later item it ends
-// in. A part is kRows rows of D sums, kRows maxima (in units of log 2) and
-// kRows sums of weights.
-__device__ __forceinline__ int part_index(const Line& l, int block, int first) {
-  return 2 * block + (l.begin_of(block) < first ? 1 : 0);
+// Place of run `run`'s part of the item at `first`, for row block rb of
+// row_blocks. A run has two parts for each row block in the workspace: of the
+// item it begins in, and of a later item it ends in. A part is kRows rows of D
+// sums, kRows maxima (in units of log 2) and kRows sums of weights.
+struct Rows {
+  int rb, row_blocks;
+};
+__device__ __forceinline__ int part_index(const Line& l, const Rows& w, int run, int first) {
+  return 2 * (run * w.row_blocks + w.rb) + (l.begin_of(run) < first ? 1 : 0);
 }
 template <int kRows, int D>
 constexpr size_t kPartFloats = static_cast<size_t>(kRows) * (D + 2);
 
 // Counts this block's part of the item (nt tiles from `first`); true in the
-// block that arrives last. An item cut between blocks is counted at the place
-// of its first part, so that the counters' number does not depend on the
-// call's sizes and a workspace serves any of them.
-__device__ __forceinline__ bool arrives_last(const AttendArgs& a, const Line& l, int first, int nt) {
-  const int b0 = l.block_of(first), parts = l.block_of(first + nt - 1) - b0 + 1;
-  int* counter = a.counters + part_index(l, b0, first);
+// block that arrives last. An item cut between runs is counted at the place of
+// its first part, so that the counters' number does not depend on the call's
+// sizes and a workspace serves any of them.
+__device__ __forceinline__ bool arrives_last(const AttendArgs& a, const Line& l, const Rows& w, int first, int nt) {
+  const int p0 = l.run_of(first), parts = l.run_of(first + nt - 1) - p0 + 1;
+  int* counter = a.counters + part_index(l, w, p0, first);
   const bool last = atomicAdd(counter, 1) + 1 == parts;
   if (last) *counter = 0;   // ready for the next call
   return last;
@@ -157,13 +160,14 @@ __device__ __forceinline__ RowOf row_of(const AttendArgs& a, int kvh, int r) {
 // `first` (nt tiles) and writes its rows, which start at row0 of its kv head.
 // Parts are added in run order.
 template <typename T, int kRows, int D, int kThreads>
-__device__ void join_parts(const AttendArgs& a, const Line& line, int b, int kvh, int row0, int rows, int first,
+__device__ void join_parts(const AttendArgs& a, const Line& line, const Rows& w, int b, int kvh, int row0, int rows, int first,
                            int nt, bool idle, int tid) {
   constexpr size_t kPart = kPartFloats<kRows, D>;
-  const int b0 = line.block_of(first), n = line.block_of(first + nt - 1) - b0 + 1;
-  // Every part but the first is the one its block begins with.
-  const float* part0 = a.partials + part_index(line, b0, first) * kPart;
-  const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart;
+  const int p0 = line.run_of(first), n = line.run_of(first + nt - 1) - p0 + 1;
+  // Every part but the first is the one its run begins with.
+  const float* part0 = a.partials + part_index(line, w, p0, first) * kPart;
+  const float* part1 = a.partials + 2 * (static_cast<size_t>(p0 + 1) * w.row_blocks + w.rb) * kPart;
+  const size_t step = 2 * static_cast<size_t>(w.row_blocks) * kPart;
   // A thread takes four columns of kBatch rows at a time, kGroup parts of each
   // at once, so that many loads are in flight; few rows have many parts and
   // many rows few.
@@ -174,18 +178,18 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, int b, int kvh
     float4 o[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) top[k] = -INFINITY, l[k] = 0.f, o[k] = float4{0.f, 0.f, 0.f, 0.f};
-    for (int p0 = 0; p0 < n; p0 += kGroup) {
-      float m[kBatch][kGroup], w[kBatch][kGroup];
+    for (int q0 = 0; q0 < n; q0 += kGroup) {
+      float m[kBatch][kGroup], u[kBatch][kGroup];
       float4 x[kBatch][kGroup];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-          const float* part = p0 + i == 0 ? part0 : part1 + (p0 + i - 1) * 2 * kPart;
+          const float* part = q0 + i == 0 ? part0 : part1 + (q0 + i - 1) * step;
           const int r = r0 + k * kStep;
-          const bool real = p0 + i < n && r < rows;
+          const bool real = q0 + i < n && r < rows;
           m[k][i] = real ? __ldcg(part + kRows * D + r) : -INFINITY;
-          w[k][i] = real ? __ldcg(part + kRows * D + kRows + r) : 0.f;
+          u[k][i] = real ? __ldcg(part + kRows * D + kRows + r) : 0.f;
           x[k][i] = real ? __ldcg(reinterpret_cast<const float4*>(part + r * D + e)) : float4{0.f, 0.f, 0.f, 0.f};
         }
 #pragma unroll
@@ -200,7 +204,7 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, int b, int kvh
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
           const float f = exp2_approx(m[k][i] - base);
-          l[k] += f * w[k][i];
+          l[k] += f * u[k][i];
           o[k].x += f * x[k][i].x, o[k].y += f * x[k][i].y, o[k].z += f * x[k][i].z, o[k].w += f * x[k][i].w;
         }
       }
@@ -230,22 +234,23 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, int b, int kvh
 // together): this thread joins kColumns columns from c0 on of row r, kGroup
 // parts at once.
 template <typename T, int D, int kColumns, int kGroup>
-__device__ void join_row(const AttendArgs& a, const Line& line, int b, int kvh, int row0, int r, int c0, int first,
-                         int nt, bool idle) {
+__device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, int b, int kvh, int row0, int r, int c0,
+                         int first, int nt, bool idle) {
   constexpr size_t kPart = kPartFloats<128, D>;
-  const int b0 = line.block_of(first), n = line.block_of(first + nt - 1) - b0 + 1;
-  const float* part0 = a.partials + part_index(line, b0, first) * kPart + r;
-  const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart + r;
+  const int p0 = line.run_of(first), n = line.run_of(first + nt - 1) - p0 + 1;
+  const float* part0 = a.partials + part_index(line, w, p0, first) * kPart + r;
+  const float* part1 = a.partials + 2 * (static_cast<size_t>(p0 + 1) * w.row_blocks + w.rb) * kPart + r;
+  const size_t step = 2 * static_cast<size_t>(w.row_blocks) * kPart;
   float top = -INFINITY, l = 0.f, o[kColumns] = {};
 #pragma unroll 1
-  for (int p0 = 0; p0 < n; p0 += kGroup) {
-    float m[kGroup], w[kGroup], x[kGroup][kColumns];
+  for (int q0 = 0; q0 < n; q0 += kGroup) {
+    float m[kGroup], u[kGroup], x[kGroup][kColumns];
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
-      const bool real = p0 + i < n;
-      const float* from = p0 + i == 0 || !real ? part0 : part1 + (p0 + i - 1) * 2 * kPart;
+      const bool real = q0 + i < n;
+      const float* from = q0 + i == 0 || !real ? part0 : part1 + (q0 + i - 1) * step;
       m[i] = real ? __ldcg(from + 128 * D) : -INFINITY;
-      w[i] = real ? __ldcg(from + 128 * D + 128) : 0.f;
+      u[i] = real ? __ldcg(from + 128 * D + 128) : 0.f;
 #pragma unroll
       for (int c = 0; c < kColumns; ++c) x[i][c] = real ? __ldcg(from + (c0 + c) * 128) : 0.f;
     }
@@ -260,7 +265,7 @@ __device__ void join_row(const AttendArgs& a, const Line& line, int b, int kvh, 
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
       const float f = exp2_approx(m[i] - base);
-      l += f * w[i];
+      l += f * u[i];
 #pragma unroll
       for (int c = 0; c < kColumns; ++c) o[c] += f * x[i][c];
     }
@@ -283,31 +288,32 @@ __device__ void join_row(const AttendArgs& a, const Line& line, int b, int kvh, 
 
 // The join as a launch of its own: in the main launch one block reads all
 // parts of an item after everybody else has left, here the whole GPU does.
-// Block (x, y): item x, or, where there are more items than the main launch
-// had blocks (runs), the item that run x begins inside of, if x is the first
-// run to do so. It starts early (programmatic dependent launch) and waits for
-// the parts. y is a row, whose parts the block's groups of D / 4 threads share
-// out (kRows of 16 or 64), or kColumns columns of all 128 rows.
+// Block (x, y): an item and row block, or, where there are more of those than
+// the main launch had blocks, the item that a run begins inside of, if it is
+// the first run to do so. It starts early (programmatic dependent launch) and
+// waits for the parts. y is a row, whose parts the block's groups of D / 4
+// threads share out (kRows of 16 or 64), or kColumns columns of all 128 rows.
 template <typename T, int kRows, int D, int kTile, int kColumns, int kGroup>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs a, int row_blocks,
                                                    int block_rows, int runs) {
   __shared__ int scratch[6];
   __shared__ int sums[2][4];
-  const int tid = threadIdx.x, items = a.c.kv_heads * row_blocks;
+  const int tid = threadIdx.x, team = blockIdx.x / row_blocks;
+  const Rows w{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
   Line line;
   Cursor cur;
-  int b0 = 0, n = 1;
-  if (gridDim.x == runs) {
-    if (find_run<kTile, 128>(a, items, scratch, &line, &cur) && cur.t > 0) {
-      b0 = line.block_of(cur.first);
-      if (static_cast<int>(blockIdx.x) == b0 + 1) n = line.block_of(cur.first + cur.nt - 1) - b0 + 1;
+  int p0 = 0, n = 1;
+  if (gridDim.x == runs * row_blocks) {
+    if (find_run<kTile, 128>(a, runs, team, scratch, &line, &cur) && cur.t > 0) {
+      p0 = line.run_of(cur.first);
+      if (team == p0 + 1) n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
     }
   } else {
-    cur.b = blockIdx.x / items;
-    cur.item = blockIdx.x - cur.b * items;
+    cur.b = team / a.c.kv_heads;
+    cur.item = team - cur.b * a.c.kv_heads;
     int before = 0, all = 0;   // tiles of the sequences before b, and of all
     for (int i = tid; i < a.c.batch; i += 128) {
-      const int tiles = tiles_of<kTile>(sequence_span(a.c, i, a.nodes)) * items;
+      const int tiles = tiles_of<kTile>(sequence_span(a.c, i, a.nodes)) * a.c.kv_heads;
       all += tiles;
       if (i < cur.b) before += tiles;
     }
@@ -319,18 +325,17 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     cur.nt = tiles_of<kTile>(cur.span);
     cur.first = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3] + cur.item * cur.nt;
     line.cut(sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3], runs, 0);
-    b0 = line.block_of(cur.first);
-    n = line.block_of(cur.first + cur.nt - 1) - b0 + 1;
+    p0 = line.run_of(cur.first);
+    n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
   }
   pdl_wait_prerequisites();
   if (n == 1) return;   // whole, or another block's
-  const int first = cur.first, nt = cur.nt, b = cur.b;
-  const int kvh = cur.item / row_blocks, row0 = (cur.item - kvh * row_blocks) * block_rows;
+  const int first = cur.first, nt = cur.nt, b = cur.b, kvh = cur.item, row0 = w.rb * block_rows;
   const int rows = min(block_rows, a.nodes * a.group - row0);
   const Span span = cur.span;
   if constexpr (kRows == 128) {
     if (tid < rows)
-      join_row<T, D, kColumns, kGroup>(a, line, b, kvh, row0, tid, blockIdx.y * kColumns, first, nt, span.context < 0);
+      join_row<T, D, kColumns, kGroup>(a, line, w, b, kvh, row0, tid, blockIdx.y * kColumns, first, nt, span.context < 0);
   } else {
     constexpr int kLanes = D / 4, kGroups = 128 / kLanes, kAhead = 6;
     constexpr size_t kPart = kPartFloats<kRows, D>;
@@ -338,19 +343,20 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     __shared__ float tops[kGroups], ls[kGroups];
     const int r = blockIdx.y, g = tid / kLanes, e = tid % kLanes * 4;
     if (r >= rows) return;
-    const float* part0 = a.partials + part_index(line, b0, first) * kPart;
-    const float* part1 = a.partials + 2 * static_cast<size_t>(b0 + 1) * kPart;
+    const float* part0 = a.partials + part_index(line, w, p0, first) * kPart;
+    const float* part1 = a.partials + 2 * (static_cast<size_t>(p0 + 1) * row_blocks + w.rb) * kPart;
+    const size_t step = 2 * static_cast<size_t>(row_blocks) * kPart;
     float top = -INFINITY, l = 0.f;
     float4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int p0 = g; p0 < n; p0 += kGroups * kAhead) {
-      float m[kAhead], w[kAhead];
+    for (int q0 = g; q0 < n; q0 += kGroups * kAhead) {
+      float m[kAhead], u[kAhead];
       float4 x[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int p = p0 + i * kGroups;
-        const float* part = p == 0 ? part0 : part1 + (p - 1) * 2 * kPart;
+        const int p = q0 + i * kGroups;
+        const float* part = p == 0 ? part0 : part1 + (p - 1) * step;
         m[i] = p < n ? __ldcg(part + kRows * D + r) : -INFINITY;
-        w[i] = p < n ? __ldcg(part + kRows * D + kRows + r) : 0.f;
+        u[i] = p < n ? __ldcg(part + kRows * D + kRows + r) : 0.f;
         x[i] = p < n ? __ldcg(reinterpret_cast<const float4*>(part + r * D + e)) : float4{0.f, 0.f, 0.f, 0.f};
       }
       float high = top;
@@ -362,7 +368,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const float f = exp2_approx(m[i] - base);
-        l += f * w[i], o.x += f * x[i].x, o.y += f * x[i].y, o.z += f * x[i].z, o.w += f * x[i].w;
+        l += f * u[i], o.x += f * x[i].x, o.y += f * x[i].y, o.z += f * x[i].z, o.w += f * x[i].w;
       }
     }
     others[g][tid % kLanes] = o;
@@ -396,8 +402,7 @@ cudaError_t launch_join_as(const AttendArgs& a, int runs, int row_blocks, int bl
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int items = a.c.batch * a.c.kv_heads * row_blocks;
-  cfg.gridDim = dim3(std::min(items, runs), kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
+  cfg.gridDim = dim3(std::min(a.c.batch * a.c.kv_heads, runs) * row_blocks, kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -408,7 +413,7 @@ cudaError_t launch_join_as(const AttendArgs& a, int runs, int row_blocks, int bl
 // Few items have many parts each: few columns a block, many parts at once.
 template <typename T, int kRows, int D, int kTile>
 cudaError_t launch_join(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
-  if (runs >= 4 * a.c.batch * a.c.kv_heads * row_blocks || kRows < 128)
+  if (runs >= 4 * a.c.batch * a.c.kv_heads || kRows < 128)
     return launch_join_as<T, kRows, D, kTile, 8, 8>(a, runs, row_blocks, block_rows, s);
   return launch_join_as<T, kRows, D, kTile, kRows < 128 ? 8 : 32, kRows < 128 ? 8 : 2>(a, runs, row_blocks, block_rows, s);
 }

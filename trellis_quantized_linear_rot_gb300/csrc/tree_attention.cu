@@ -16,13 +16,16 @@ constexpr int kMaxDevices = 64;
 // Rows a kv head up to which the 16-row kernel takes them in one block.
 constexpr int kFewRows = 16;
 
+// Blocks of a launch with `blocks` places: whole teams of row_blocks, one at least.
+int team_blocks(int blocks, int row_blocks) { return std::max(1, blocks / row_blocks) * row_blocks; }
+
 // Whether an item is cut into so many parts that a launch of its own joins
-// them: its share of the blocks, or of the tiles it can have if those are
+// them: its share of the runs, or of the tiles it can have if those are
 // fewer, is over kManyParts.
 constexpr int kManyParts = 6;
-bool many_parts(const AttendArgs& a, int blocks, int items, int tile) {
+bool many_parts(const AttendArgs& a, int runs, int tile) {
   const int64_t tiles = (static_cast<int64_t>(a.c.table_width) * a.c.page_size + tile - 1) / tile;
-  return std::min<int64_t>(blocks / items, tiles) > kManyParts;
+  return std::min<int64_t>(runs / (a.c.batch * a.c.kv_heads), tiles) > kManyParts;
 }
 
 template <typename T, int D, int kRowWarps>
@@ -34,12 +37,13 @@ cudaError_t launch_mma(AttendArgs a, int device, cudaStream_t s) {
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
   });
   if (e != cudaSuccess) return static_cast<cudaError_t>(e);
-  const int blocks = kBlocksPerSm * a.num_sms, row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
-  a.join_later = many_parts(a, blocks, a.c.batch * a.c.kv_heads * row_blocks, S::kTile);
+  const int row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
+  const int blocks = team_blocks(kBlocksPerSm * a.num_sms, row_blocks);
+  a.join_later = many_parts(a, blocks / row_blocks, S::kTile);
   tree_attention_mma_kernel<T, D, kRowWarps><<<blocks, S::kThreads, S::kSmem, s>>>(a);
   const cudaError_t launched = cudaGetLastError();
   if (launched != cudaSuccess || !a.join_later) return launched;
-  return launch_join<T, S::kRows, D, S::kTile>(a, blocks, row_blocks, S::kRows, s);
+  return launch_join<T, S::kRows, D, S::kTile>(a, blocks / row_blocks, row_blocks, S::kRows, s);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -95,11 +99,12 @@ cudaError_t launch_tc(const AttendArgs& a, int box, int device, cudaStream_t s) 
                 {c.stride_token, c.stride_head, c.stride_page}, box, 1))
     return cudaErrorInvalidValue;
   const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
-  tree_attention_tc_kernel<T, D><<<a.num_sms, S::kThreads, S::kSmem, s>>>(maps, args);
+  const int blocks = team_blocks(a.num_sms, row_blocks);
+  tree_attention_tc_kernel<T, D><<<blocks, S::kThreads, S::kSmem, s>>>(maps, args);
   const cudaError_t launched = cudaGetLastError();
   // No item has a second tile to be cut off.
   if (launched != cudaSuccess || static_cast<int64_t>(c.table_width) * c.page_size <= S::kTile) return launched;
-  return launch_join<T, 128, D, S::kTile>(a, a.num_sms, row_blocks, args.block_nodes * a.group, s);
+  return launch_join<T, 128, D, S::kTile>(a, blocks / row_blocks, row_blocks, args.block_nodes * a.group, s);
 }
 
 // Rows of a copy for the tcgen05 kernel: the largest that divides both the
@@ -133,15 +138,19 @@ cudaError_t launch_typed(const AttendArgs& a, int device, cudaStream_t s) {
 
 }  // namespace
 
-// A counter for each part (their number and place depend on the device
-// alone), then two parts for each block of the launch: 16 rows, or 64 (the
+// A counter for each part (their number and place depend on the device alone;
+// a launch with more blocks of rows than places has one run, and nothing to
+// join), then two parts for each block of the launch: 16 rows, or 64 (the
 // tcgen05 kernel has half the blocks and twice the rows).
 AttendWorkspace attend_workspace(int nodes, int heads, int kv_heads, int head_dim, int num_sms) {
   const int64_t rows = static_cast<int64_t>(nodes) * (heads / kv_heads);
-  const size_t parts = static_cast<size_t>(kBlocksPerSm) * num_sms * 2;
+  const size_t places = static_cast<size_t>(kBlocksPerSm) * num_sms;
+  const size_t blocks = std::max<size_t>(places, (rows + 63) / 64);
+  // Blocks of rows of the tcgen05 kernel hold whole nodes, half of 128 rows at least.
+  const size_t wide = std::max<size_t>(num_sms, nodes) * 2;
   AttendWorkspace w;
-  w.partials_at = (parts * sizeof(int) + 255) & ~static_cast<size_t>(255);
-  w.bytes = w.partials_at + parts * (rows <= kFewRows ? 16 : 64) * (head_dim + 2) * sizeof(float);
+  w.partials_at = (2 * places * sizeof(int) + 255) & ~static_cast<size_t>(255);
+  w.bytes = w.partials_at + 2 * (rows <= kFewRows ? places * 16 : std::max(blocks, wide) * 64) * (head_dim + 2) * sizeof(float);
   return w;
 }
 
