@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   const int row_blocks = (rows_all + kRows - 1) / kRows, team = blockIdx.x / row_blocks;
   const Rows mine{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
 
-  if (a.join_later) pdl_launch_dependents();
+  chain();
   Line line;
   Cursor look;   // next tile whose offsets are looked up
   if (!find_run<kTile, kThreads>(a, gridDim.x / row_blocks, team, scratch, &line, &look)) return;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
     bool exists;
   };
   auto look_up = [&](const Cursor& c) -> Pending {
-    const int slot = c.t * kTile + tid, p = slot / a.c.page_size;
+    const int slot = c.t * kTile + tid, p = a.c.by_page(slot);
     const bool exists = slot < c.span.slots;
     return {exists ? a.c.page_table[c.b * a.c.stride_table + p] : 0, slot - p * a.c.page_size, c.item, exists};
   };

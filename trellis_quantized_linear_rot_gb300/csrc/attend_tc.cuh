@@ -277,7 +277,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     return;
   }
 
-  pdl_launch_dependents();   // the join may get ready
+  chain();
   Line line;
   Cursor cur;
   if (!find_run<kTile, S::kThreads>(a, gridDim.x / row_blocks, team, sh.scratch, &line, &cur)) return;
@@ -327,7 +327,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     };
     auto look_up = [&](const Cursor& c) {
       const int slot = c.t * kTile + lane * box;
-      return lane < boxes && slot < c.span.slots ? a.c.page_table[c.b * a.c.stride_table + slot / a.c.page_size] : -1;
+      return lane < boxes && slot < c.span.slots ? a.c.page_table[c.b * a.c.stride_table + a.c.by_page(slot)] : -1;
     };
     Side ks = {cur, cur, look_up(cur), 0}, vs = ks;
     auto free_stage = [&](const Side& x, int empty) {
@@ -339,7 +339,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
       const bool exists = lane < boxes && slot < x->cur.span.slots;
       const bool outside = exists && static_cast<unsigned>(x->page) >= static_cast<unsigned>(a.c.pages);
       const bool copy = exists && !outside;
-      const int page = x->page, kvh = x->cur.item, row = slot % a.c.page_size;
+      const int page = x->page, kvh = x->cur.item, row = slot - a.c.by_page(slot) * a.c.page_size;
       if (x->j + 1 < n_tiles) {
         advance<kTile>(a, &x->next);
         x->page = look_up(x->next);

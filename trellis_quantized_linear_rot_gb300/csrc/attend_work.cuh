@@ -290,14 +290,14 @@ __device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, i
 // parts of an item after everybody else has left, here the whole GPU does.
 // Block (x, y): an item and row block, or, where there are more of those than
 // the main launch had blocks, the item that a run begins inside of, if it is
-// the first run to do so. It starts early (programmatic dependent launch) and
-// waits for the parts. y is a row, whose parts the block's groups of D / 4
+// the first run to do so. y is a row, whose parts the block's groups of D / 4
 // threads share out (kRows of 16 or 64), or kColumns columns of all 128 rows.
 template <typename T, int kRows, int D, int kTile, int kColumns, int kGroup>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs a, int row_blocks,
                                                    int block_rows, int runs) {
   __shared__ int scratch[6];
   __shared__ int sums[2][4];
+  chain();
   const int tid = threadIdx.x, team = blockIdx.x / row_blocks;
   const Rows w{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
   Line line;
@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     p0 = line.run_of(cur.first);
     n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
   }
-  pdl_wait_prerequisites();
   if (n == 1) return;   // whole, or another block's
   const int first = cur.first, nt = cur.nt, b = cur.b, kvh = cur.item, row0 = w.rb * block_rows;
   const int rows = min(block_rows, a.nodes * a.group - row0);
@@ -398,16 +397,10 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
 
 template <typename T, int kRows, int D, int kTile, int kColumns, int kGroup>
 cudaError_t launch_join_as(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(a.c.batch * a.c.kv_heads, runs) * row_blocks, kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, kRows, D, kTile, kColumns, kGroup>, a, row_blocks, block_rows, runs);
+  const dim3 grid(std::min(a.c.batch * a.c.kv_heads, runs) * row_blocks,
+                  kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
+  return launch_chained(join_kernel<T, kRows, D, kTile, kColumns, kGroup>, grid, dim3(128), 0, 1, s, a, row_blocks,
+                        block_rows, runs);
 }
 
 // Few items have many parts each: few columns a block, many parts at once.

@@ -13,6 +13,7 @@ constexpr int kThreads = 256;
 __global__ void __launch_bounds__(kThreads)
 kv_write_kernel(CacheView c, uint16_t* k, uint16_t* v, const uint16_t* k_new, const uint16_t* v_new, int64_t seq,
                 int64_t node, int64_t head, int nodes) {
+  chain();
   const int chunks = c.kv_heads * (c.head_dim / 8);
   const int64_t total = static_cast<int64_t>(c.batch) * nodes * chunks;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
@@ -43,6 +44,7 @@ kv_keep_kernel(CacheView c, uint16_t* k, uint16_t* v, const int32_t* path, const
                int32_t* new_lengths) {
   __shared__ int64_t from[TF_MAX_NODES], to[TF_MAX_NODES];
   __shared__ int kept;
+  chain();
   const int b = blockIdx.y, layer = blockIdx.z;
   const int len = c.lengths[b];
   if (len < 0) {
@@ -91,19 +93,17 @@ cudaError_t launch_kv_write(const CacheView& c, void* k, void* v, const void* k_
                             int64_t node, int64_t head, int nodes, cudaStream_t s) {
   const int64_t total = static_cast<int64_t>(c.batch) * nodes * c.kv_heads * (c.head_dim / 8);
   const int64_t blocks = (total + kThreads - 1) / kThreads;
-  kv_write_kernel<<<static_cast<unsigned>(blocks < 65536 ? blocks : 65536), kThreads, 0, s>>>(
-      c, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), static_cast<const uint16_t*>(k_new),
-      static_cast<const uint16_t*>(v_new), seq, node, head, nodes);
-  return cudaGetLastError();
+  return launch_chained(kv_write_kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0,
+                        1, s, c, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v),
+                        static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new), seq, node, head, nodes);
 }
 
 cudaError_t launch_kv_keep(const CacheView& c, void* k, void* v, const int32_t* path, const int32_t* counts,
                            int nodes, int32_t* new_lengths, cudaStream_t s) {
   const int chunks = 2 * c.kv_heads * (c.head_dim / 8);
   const dim3 grid((chunks + kThreads - 1) / kThreads, c.batch, c.layers);
-  kv_keep_kernel<<<grid, kThreads, 0, s>>>(c, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), path, counts,
-                                           nodes, new_lengths);
-  return cudaGetLastError();
+  return launch_chained(kv_keep_kernel, grid, dim3(kThreads), 0, 1, s, c, static_cast<uint16_t*>(k),
+                        static_cast<uint16_t*>(v), path, counts, nodes, new_lengths);
 }
 
 }  // namespace tfx

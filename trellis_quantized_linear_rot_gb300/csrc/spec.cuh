@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ptx.cuh"
 #include "spec.h"
 
 namespace tfx {
@@ -23,6 +24,13 @@ template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// First instructions of a kernel launched by launch_chained: wait for the
+// kernel before it, and let the next one be set up.
+__device__ __forceinline__ void chain() {
+  pdl_wait_prerequisites();
+  pdl_launch_dependents();
+}
 
 __device__ __forceinline__ void record_index_error(int* err) { atomicOr(err, kErrIndex); }
 
@@ -49,7 +57,7 @@ __device__ __forceinline__ int64_t slot_offset(const CacheView& c, int b, int64_
     record_index_error(c.err);
     return -1;
   }
-  const int p = static_cast<int>(slot) / c.page_size;
+  const int p = c.by_page(static_cast<int>(slot));
   const int page = c.page_table[b * c.stride_table + p];
   if (page < 0 || page >= c.pages) {
     record_index_error(c.err);

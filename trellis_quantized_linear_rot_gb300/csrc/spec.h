@@ -13,6 +13,22 @@ namespace tfx {
 constexpr int kErrWait = 1;   // device error bits: a bounded wait gave up,
 constexpr int kErrIndex = 2;  // an index outside its array was skipped
 
+// Division of numbers below 2^31 by a divisor known on the host: two
+// instructions on the device instead of about twenty.
+struct FastDiv {
+  uint32_t mul = 0, shift = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+#endif
+};
+
 // The fields of tf_kv_cache the kernels read, without the array pointers.
 struct CacheView {
   int64_t stride_layer, stride_page, stride_token, stride_head;
@@ -20,6 +36,7 @@ struct CacheView {
   const int32_t* lengths;
   int64_t stride_table;
   int layers, pages, page_size, kv_heads, head_dim, batch, table_width;
+  FastDiv by_page;
   int* err;
 };
 
@@ -69,7 +86,29 @@ struct VerifyArgs {
   int* err;
   int num_sms;
 };
-size_t verify_workspace_bytes(int batch, int nodes);
+size_t verify_workspace_bytes(int batch, int nodes, int num_sms);
+
+// Launches with programmatic stream serialisation: the kernel may be set up
+// while the one before it still runs, and waits for it with its first
+// instruction (every thread of every kernel launched this way does).
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream,
+                           A&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
 
 cudaError_t launch_kv_write(const CacheView& c, void* k, void* v, const void* k_new, const void* v_new,
                             int64_t seq, int64_t node, int64_t head, int nodes, cudaStream_t s);

@@ -54,6 +54,7 @@ CacheView view_of(const tf_kv_cache* c, int* err) {
   v.head_dim = c->head_dim;
   v.batch = c->batch;
   v.table_width = c->table_width;
+  v.by_page = FastDiv(static_cast<uint32_t>(c->page_size));
   v.err = err;
   return v;
 }
@@ -169,7 +170,9 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
 
 size_t tf_verify_draft_workspace_bytes(int batch, int nodes) {
   if (batch < 0 || batch > 65535 || nodes < 1 || nodes > TF_MAX_NODES) return 0;
-  return verify_workspace_bytes(batch, nodes);
+  int device, sms, *err;
+  if (current_device_state(&device, &sms, &err) != TF_OK) return 0;
+  return verify_workspace_bytes(batch, nodes, sms);
 }
 
 tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int64_t stride_node,
@@ -203,7 +206,7 @@ tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int
   if (s == TF_OK && !greedy) s = check_pointers_on_device(device, {u_sample});
   if (s == TF_OK && draft) s = check_pointers_on_device(device, {u_accept, draft_logits});
   if (s != TF_OK) return s;
-  if (workspace_bytes < tf_verify_draft_workspace_bytes(batch, nodes)) return TF_ERR_SCRATCH;
+  if (workspace_bytes < verify_workspace_bytes(batch, nodes, sms)) return TF_ERR_SCRATCH;
   VerifyArgs a;
   a.logits = logits;
   a.draft = draft ? draft_logits : nullptr;

@@ -40,8 +40,8 @@ cudaError_t launch_mma(AttendArgs a, int device, cudaStream_t s) {
   const int row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
   const int blocks = team_blocks(kBlocksPerSm * a.num_sms, row_blocks);
   a.join_later = many_parts(a, blocks / row_blocks, S::kTile);
-  tree_attention_mma_kernel<T, D, kRowWarps><<<blocks, S::kThreads, S::kSmem, s>>>(a);
-  const cudaError_t launched = cudaGetLastError();
+  const cudaError_t launched = launch_chained(tree_attention_mma_kernel<T, D, kRowWarps>, dim3(blocks),
+                                              dim3(S::kThreads), S::kSmem, 1, s, a);
   if (launched != cudaSuccess || !a.join_later) return launched;
   return launch_join<T, S::kRows, D, S::kTile>(a, blocks / row_blocks, row_blocks, S::kRows, s);
 }
@@ -100,8 +100,8 @@ cudaError_t launch_tc(const AttendArgs& a, int box, int device, cudaStream_t s) 
     return cudaErrorInvalidValue;
   const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
   const int blocks = team_blocks(a.num_sms, row_blocks);
-  tree_attention_tc_kernel<T, D><<<blocks, S::kThreads, S::kSmem, s>>>(maps, args);
-  const cudaError_t launched = cudaGetLastError();
+  const cudaError_t launched =
+      launch_chained(tree_attention_tc_kernel<T, D>, dim3(blocks), dim3(S::kThreads), S::kSmem, 1, s, maps, args);
   // No item has a second tile to be cut off.
   if (launched != cudaSuccess || static_cast<int64_t>(c.table_width) * c.page_size <= S::kTile) return launched;
   return launch_join<T, 128, D, S::kTile>(a, blocks / row_blocks, row_blocks, args.block_nodes * a.group, s);

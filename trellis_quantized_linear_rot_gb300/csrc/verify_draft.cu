@@ -257,6 +257,7 @@ __device__ void arrive(const VerifyArgs& a, const Results& r, Shared& s, int b) 
 template <typename T, bool kWalk>
 __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ Shared s;
+  chain();
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank(), id = blockIdx.x / ranks;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -560,32 +561,25 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
   cluster.sync();     // no block leaves while another may still write to its shared memory
 }
 
+bool walks(int batch, int nodes, int num_sms) { return static_cast<int64_t>(batch) * nodes > num_sms; }
+
 template <typename T>
 cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t s) {
   // One block an SM: as many blocks for a cluster as leave every cluster its place.
   const int64_t rows = static_cast<int64_t>(a.batch) * a.nodes;
-  const bool walk = rows > a.num_sms;
+  const bool walk = walks(a.batch, a.nodes, a.num_sms);
   const int64_t clusters = walk ? a.batch : rows;
   int ranks = kMaxCluster;
   while (ranks > 1 && clusters * ranks > a.num_sms) ranks /= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ranks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return walk ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, true>, a)
-              : cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, false>, a);
+  const dim3 grid(static_cast<unsigned>(clusters * ranks));
+  return walk ? launch_chained(verify_draft_kernel<T, true>, grid, dim3(kThreads), 0, ranks, s, a)
+              : launch_chained(verify_draft_kernel<T, false>, grid, dim3(kThreads), 0, ranks, s, a);
 }
 
 }  // namespace
 
-size_t verify_workspace_bytes(int batch, int nodes) {
-  return (3 * static_cast<size_t>(batch) * nodes + batch + 1) * sizeof(int);
+size_t verify_workspace_bytes(int batch, int nodes, int num_sms) {
+  return walks(batch, nodes, num_sms) ? 256 : (3 * static_cast<size_t>(batch) * nodes + batch + 1) * sizeof(int);
 }
 
 cudaError_t launch_verify_draft(const VerifyArgs& a, int dtype, cudaStream_t s) {

@@ -84,6 +84,14 @@ def _handle(stream, device):
     return stream.cuda_stream if stream is not None else _raw_stream(device.index or 0)
 
 
+def _empty(stream, shape, dtype, device):
+    """A new tensor whose memory belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _int32(t, name, shape):
     if t.dtype != torch.int32:
         raise TypeError("%s must be int32" % name)
@@ -200,11 +208,11 @@ def tf_tree_attention(q, k_cache, v_cache, page_table, lengths, parents, scale=N
     b, n, h, d = shape
     ps = _parents(parents, b, n)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = _empty(stream, shape, dtype, device)
     elif out.shape != shape or out.dtype != dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and dtype")
     if lse is None:
-        lse = torch.empty((b, n, h), dtype=torch.float32, device=device)
+        lse = _empty(stream, (b, n, h), torch.float32, device)
     elif lse.shape != (b, n, h) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [batch, nodes, heads]")
     handle = _handle(stream, device)
@@ -263,10 +271,10 @@ def tf_verify_draft(logits, tokens, parents, u_sample, temperature=1.0, draft_lo
     if code is None:
         raise TypeError("unsupported dtype %s" % dtype)
     device = logits.device
-    counts = torch.empty((b,), dtype=torch.int32, device=device)
-    path = torch.empty_like(tokens)
-    out = torch.empty_like(tokens)
-    logprobs = torch.empty(rows, dtype=torch.float32, device=device)
+    counts = _empty(stream, (b,), torch.int32, device)
+    path = _empty(stream, rows, torch.int32, device)
+    out = _empty(stream, rows, torch.int32, device)
+    logprobs = _empty(stream, rows, torch.float32, device)
     handle = _handle(stream, device)
     if workspace is not None:
         ws = _given(workspace)
@@ -292,7 +300,7 @@ def tf_kv_keep(k_cache, v_cache, page_table, lengths, path, counts, new_lengths=
         raise TypeError("path must be int32")
     _int32(counts, "counts", lengths.shape)
     if new_lengths is None:
-        new_lengths = torch.empty_like(lengths)
+        new_lengths = _empty(stream, lengths.shape, torch.int32, lengths.device)
     else:
         _int32(new_lengths, "new_lengths", lengths.shape)
     _check(lib.tf_kv_keep(c, path.data_ptr(), counts.data_ptr(), shape[1], new_lengths.data_ptr(),
