@@ -94,6 +94,7 @@ struct MmaShape {
   static constexpr int kRows = 16 * kRowWarps;
   static constexpr int kKeyWarps = 4 / kRowWarps;
   static constexpr int kTile = D == 256 ? 32 : 64;
+  static constexpr int kGap = 1;
   static constexpr int kRowBytes = D * 2;
   static constexpr int kHalf = kTile * kRowBytes;   // keys or values of a tile
   static constexpr int kStages = kRowWarps == 1 ? (D == 64 ? 5 : 3) : (D == 64 ? 3 : 2);
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   constexpr int kRing = kStages + 1;            // tiles whose offsets are known
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ TreeMasks<S::kNodes> masks;
-  __shared__ int scratch[kThreads / 32 + 2];
+  __shared__ int scratch[2 * (kThreads / 32) + 4];
   __shared__ int64_t at[kRing][kTile];
   __shared__ float wm[4][16], wl[4][16];
   __shared__ uint32_t bad[kTile / 32];          // keys of this tile with values that are not finite
@@ -136,13 +137,13 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   chain();
   Line line;
   Cursor look;   // next tile whose offsets are looked up
-  if (!find_run<kTile, kThreads>(a, gridDim.x / row_blocks, team, scratch, &line, &look)) return;
+  const int n_tiles = find_run<kTile, S::kGap, kThreads>(a, gridDim.x / row_blocks, team, scratch, &line, &look);
+  if (n_tiles == 0) return;
   Cursor cur = look, load = look;   // tiles computed and copied next
   const uint32_t ring = smem_u32(smem);
   const uint32_t q_ring = ring + kStages * 2 * S::kHalf;
   const uint32_t p_ring = q_ring + S::kQPlaces * S::kQBytes;
   const int* parents_ring = reinterpret_cast<const int*>(smem + kStages * 2 * S::kHalf + S::kQPlaces * S::kQBytes);
-  const int n_tiles = line.end - line.begin;
   const T* kp = static_cast<const T*>(a.k);
   const T* vp = static_cast<const T*>(a.v);
 
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   for (int i = 0; i < kStages; ++i)
     if (i < n_tiles) {
       if (tid < kTile) first[i] = look_up(look);
-      advance<kTile>(a, &look);
+      advance<kTile, S::kGap>(a, &look);
     }
 #pragma unroll
   for (int i = 0; i < kStages; ++i)
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
     if (i < n_tiles) {
       if (i > 0 && load.t == 0) issue_rows(load, i);
       issue(i);
-      advance<kTile>(a, &load);
+      advance<kTile, S::kGap>(a, &load);
     }
     copies_commit();
   }
@@ -234,13 +235,13 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
     if (i + kStages - 1 < n_tiles) {
       if (load.t == 0) issue_rows(load, i + kStages - 1);
       issue(i + kStages - 1);
-      advance<kTile>(a, &load);
+      advance<kTile, S::kGap>(a, &load);
     }
     copies_commit();
     const bool more = i + kStages < n_tiles;
     Pending next = {};
     if (more && tid < kTile) next = look_up(look);   // settled after this tile
-    if (more) advance<kTile>(a, &look);
+    if (more) advance<kTile, S::kGap>(a, &look);
 
     if (fresh) {   // a new item: its rows of q, its masks
       kvh = cur.item;
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
       __syncthreads();   // the masks and the stage may be written again
     }
     if (more && tid < kTile) settle(next, i + kStages);
-    advance<kTile>(a, &cur);
+    advance<kTile, S::kGap>(a, &cur);
   }
 }
 

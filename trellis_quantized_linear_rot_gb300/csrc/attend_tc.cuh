@@ -131,10 +131,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // One row of a tile, by its thread: from the scores (128 columns at `scores`)
 // to the weights over them, with the running maximum m and sum l. The sums
 // (D columns at `sums`) are rescaled where the maximum has risen by more than
-// 2^8 since they were begun. kCut: only the keys in vis are seen. sc >= 0.
+// 2^8 since they were begun. kCut: only the keys in vis are seen. sc >= 0. The
+// barrier `half` hears of the first 64 weights, so that their product can
+// begin.
 template <typename T, int D, bool kCut>
 __device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, const uint32_t (&vis)[4], bool begun,
-                                      float* m_row, float* l_row) {
+                                      uint32_t half, float* m_row, float* l_row) {
   // The scores are read twice, in parts: all 128 of them and what is made of
   // them do not fit a thread's registers.
   float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -192,6 +194,11 @@ __device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, 
       w[i] = pack2(T(), x.x, x.y);
     }
     tmem_st16(scores + c * 16, w);   // over scores already read
+    if (c == 1) {
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(half);
+    }
   }
   const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
   *m_row = m;
@@ -204,7 +211,7 @@ __device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, 
 // a wait that passes over a phase cannot tell it from the next but one).
 constexpr int kTcSlots = 6;
 enum TcBarrier { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + kTcSlots, kVFull = kKEmpty + kTcSlots,
-                 kVEmpty = kVFull + kTcSlots, kSFull = kVEmpty + kTcSlots, kPFull = kSFull + 2, kPvDone = kPFull + 2,
+                 kVEmpty = kVFull + kTcSlots, kSFull = kVEmpty + kTcSlots, kPFull = kSFull + 2, kPHalf = kPFull + 2, kPvDone = kPHalf + 2,
                  kBarriers = kPvDone + 2 };
 
 struct TcShared {
@@ -214,7 +221,7 @@ struct TcShared {
   uint32_t bad[4];                          // tree nodes with values that are not finite
   int any_gone;
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
-  int scratch[384 / 32 + 2];
+  int scratch[2 * (384 / 32) + 4];
   uint32_t tmem;
   int abort;
 };
@@ -222,7 +229,7 @@ struct TcShared {
 template <int D>
 struct TcShape {
   static constexpr int kThreads = 384;
-  static constexpr int kTile = 128;
+  static constexpr int kTile = 128, kGap = 2;
   static constexpr int kParts = D / 64;                  // 64-column parts of a tile
   static constexpr int kPartBytes = kTile * 128;         // one part of q, keys or values
   static constexpr int kTileBytes = kParts * kPartBytes;
@@ -280,8 +287,8 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
   chain();
   Line line;
   Cursor cur;
-  if (!find_run<kTile, S::kThreads>(a, gridDim.x / row_blocks, team, sh.scratch, &line, &cur)) return;
-  const int n_tiles = line.end - line.begin;
+  const int n_tiles = find_run<kTile, S::kGap, S::kThreads>(a, gridDim.x / row_blocks, team, sh.scratch, &line, &cur);
+  if (n_tiles == 0) return;
 
   if (tid == 0) {
     sh.abort = 0;
@@ -297,6 +304,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kSFull + i), 1);
       mbar_init(bar(kPFull + i), 128);
+      mbar_init(bar(kPHalf + i), 128);
       mbar_init(bar(kPvDone + i), 1);
     }
     fence_barrier_init();
@@ -341,7 +349,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
       const bool copy = exists && !outside;
       const int page = x->page, kvh = x->cur.item, row = slot - a.c.by_page(slot) * a.c.page_size;
       if (x->j + 1 < n_tiles) {
-        advance<kTile>(a, &x->next);
+        advance<kTile, S::kGap>(a, &x->next);
         x->page = look_up(x->next);
       }
       const uint32_t wanted = __popc(__ballot_sync(~0u, copy)) * box_bytes * S::kParts;
@@ -408,7 +416,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         __syncwarp();
         ++n_items;
       }
-      advance<kTile>(a, &cur);
+      advance<kTile, S::kGap>(a, &cur);
     }
     if (!ok) {
       volatile int never = 0;
@@ -452,17 +460,27 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
           if (j + 2 >= jb && jb < n_tiles) mma_commit(bar(kQEmpty));
         }
         __syncwarp();
-        ok = mbar_wait(bar(kVFull + slot_j), phase, abort_flag) && mbar_wait(bar(kPFull + s), n & 1, abort_flag);
+        ok = mbar_wait(bar(kVFull + slot_j), phase, abort_flag) && mbar_wait(bar(kPHalf + s), n & 1, abort_flag);
         if (!__all_sync(~0u, ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        auto add_up = [&](int k) {
+          mma_ts(sums, scores + k * 8, desc_by_keys(v_at + st * S::kTileBytes + k * 2048, S::kPartBytes), kSumDesc,
+                 j > j0 || k > 0);
+        };
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(sums, scores + k * 8, desc_by_keys(v_at + st * S::kTileBytes + k * 2048, S::kPartBytes), kSumDesc,
-                   j > j0 || k > 0);
+          for (int k = 0; k < kTile / 32; ++k) add_up(k);
+        }
+        __syncwarp();
+        ok = __all_sync(~0u, mbar_wait(bar(kPFull + s), n & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = kTile / 32; k < kTile / 16; ++k) add_up(k);
           mma_commit(bar(kPvDone + s));
           if (j + kStages < n_tiles) mma_commit(bar(kVEmpty + slot_j));
         }
@@ -470,7 +488,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         ++n;
       }
       cur.t += jb - ja - 1;
-      advance<kTile>(a, &cur);
+      advance<kTile, S::kGap>(a, &cur);
       ja = jb;
     }
     if (!ok && n > 0) {   // given up: the products in flight still have to end
@@ -516,7 +534,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         tc_fence_after();
         uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};   // keys this row sees
         if (slot0 + kTile <= cur.span.context && !*static_cast<volatile int*>(&sh.any_gone)) {
-          weigh<T, D, false>(scores, sums, sc, vis, used, &m, &l);
+          weigh<T, D, false>(scores, sums, sc, vis, used, bar(kPHalf + s), &m, &l);
         } else {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -554,7 +572,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
             }
           }
           fence_proxy_async_shared();
-          weigh<T, D, true>(scores, sums, sc, vis, used, &m, &l);
+          weigh<T, D, true>(scores, sums, sc, vis, used, bar(kPHalf + s), &m, &l);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -590,34 +608,34 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         T* out = static_cast<T*>(a.out) + out_at * D;
         float* part = a.partials + part_index(line, own, team, cur.first) * kPartFloats<128, D>;
 #pragma unroll 1
-        for (int c = s * (D / 32); c < (s + 1) * (D / 32); ++c) {
-          float x[16] = {}, y[16] = {};
-          if (has0) tmem_ld16(tmem + mine + S::kSums + c * 16, x);
-          if (has1) tmem_ld16(tmem + mine + S::kSums + D + c * 16, y);
+        for (int c = s * (D / 64); c < (s + 1) * (D / 64); ++c) {
+          float x[32] = {}, y[32] = {};
+          if (has0) tmem_ld32(tmem + mine + S::kSums + c * 32, x);
+          if (has1) tmem_ld32(tmem + mine + S::kSums + D + c * 32, y);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = (f0 * x[i] + f1 * y[i]) * inv;
+          for (int i = 0; i < 32; ++i) x[i] = (f0 * x[i] + f1 * y[i]) * inv;
           if (any_bad)
             for (int w = 0; w < 4; ++w)
               for (uint32_t left = sh.bad[w] & (w == 0 ? seen.w[0] : w == 1 ? seen.w[1] : w == 2 ? seen.w[2] : seen.w[3]);
                    left; left &= left - 1) {
                 const int64_t off = slot_offset(a.c, cur.b, cur.span.context + w * 32 + __ffs(left) - 1);
                 if (off < 0) continue;
+                const T* from = values + off + kvh * a.c.stride_head + c * 32;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const T z = values[off + kvh * a.c.stride_head + c * 16 + i];
-                  if (bad16<T>(*reinterpret_cast<const uint16_t*>(&z))) x[i] += to_f32(z);
-                }
+                for (int i = 0; i < 32; ++i)
+                  if (bad16<T>(reinterpret_cast<const uint16_t*>(from)[i])) x[i] += to_f32(from[i]);
               }
           if (node >= 0) {
             if (whole) {
-              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = empty ? 0u : pack2(T(), x[2 * i], x[2 * i + 1]);
-              *reinterpret_cast<uint4*>(out + c * 16) = uint4{w[0], w[1], w[2], w[3]};
-              *reinterpret_cast<uint4*>(out + c * 16 + 8) = uint4{w[4], w[5], w[6], w[7]};
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(out + c * 32 + i) =
+                    empty ? uint4{0, 0, 0, 0}
+                          : uint4{pack2(T(), x[i], x[i + 1]), pack2(T(), x[i + 2], x[i + 3]),
+                                  pack2(T(), x[i + 4], x[i + 5]), pack2(T(), x[i + 6], x[i + 7])};
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) __stcg(part + (c * 16 + i) * 128 + row, x[i]);
+              for (int i = 0; i < 32; ++i) __stcg(part + (c * 32 + i) * 128 + row, x[i]);
             }
           }
         }
@@ -634,7 +652,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         if (!group_all(3, 256, true)) break;
       }
       cur.t += jb - ja - 1;
-      advance<kTile>(a, &cur);
+      advance<kTile, S::kGap>(a, &cur);
       ja = jb;
     }
   }

@@ -28,7 +28,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// The line of tiles (below 2^31: checked on the host) and one run of it: the first `longer` runs have per + 1 tiles, the others per. No more
+// Going from one item to the next costs a block about as much as kGap tiles
+// (its sums are joined and written, another q comes), so an item has kGap
+// places in the line after those of its tiles.
+//
+// The line of places (below 2^31: checked on the host) and one run of it: the first `longer` runs have per + 1 tiles, the others per. No more
 // runs than tiles, so that no run between two others is empty.
 struct Line {
   int runs, per, longer;
@@ -42,7 +46,7 @@ struct Line {
     end = i < runs ? begin_of(i + 1) : begin;
   }
   __device__ __forceinline__ int begin_of(int run) const { return run * per + min(run, longer); }
-  // The run that holds tile f.
+  // The run that holds place f.
   __device__ __forceinline__ int run_of(int f) const {
     const int border = longer * (per + 1);
     return f < border ? f / (per + 1) : longer + (f - border) / per;
@@ -61,65 +65,81 @@ __device__ __forceinline__ int tiles_of(const Span& s) {
   return s.slots <= kTile ? 1 : (s.slots + kTile - 1) / kTile;
 }
 
-// Block-wide: the line, run number `run` of at most `most`, and the cursor at its begin.
-// `scratch` has room for kThreads / 32 + 2 ints. False where the run is
-// empty. Batches of up to kThreads sequences are scanned once, larger ones
-// twice (length, then place).
-template <int kTile, int kThreads>
-__device__ bool find_run(const AttendArgs& a, int most, int run, int* scratch, Line* line, Cursor* cur) {
-  const int items = a.c.kv_heads;
-  constexpr int kWarps = kThreads / 32;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int batch = a.c.batch;
-  int* found = scratch + kWarps;   // [0] first tile of the sequence, [1] sequence
-  for (int pass = batch <= kThreads ? 1 : 0; pass < 2; ++pass) {
-    int before = 0;
-    for (int b0 = 0; b0 < batch; b0 += kThreads) {
-      const int b = b0 + tid;
-      const int n = b < batch ? tiles_of<kTile>(sequence_span(a.c, b, a.nodes)) * items : 0;
-      int upto = n;
-      for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += y;
-      }
-      if (lane == 31) scratch[warp] = upto;
-      __syncthreads();
-      int prior = before, all = before;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) prior += scratch[w];
-        all += scratch[w];
-      }
-      upto += prior;
-      if (b0 + kThreads >= batch && (pass == 0 || batch <= kThreads)) line->cut(all, most, run);
-      if (pass == 1 && line->begin >= upto - n && line->begin < upto) {
-        found[0] = upto - n;
-        found[1] = b;
-      }
-      before = all;
-      __syncthreads();
-    }
-  }
-  if (line->begin >= line->end) return false;
-  cur->b = found[1];
-  cur->span = sequence_span(a.c, cur->b, a.nodes);
-  cur->nt = tiles_of<kTile>(cur->span);
-  const int in = line->begin - found[0];
-  cur->item = in / cur->nt;
-  cur->t = in - cur->item * cur->nt;
-  cur->first = line->begin - cur->t;
-  return true;
-}
-
-template <int kTile>
+template <int kTile, int kGap>
 __device__ __forceinline__ void advance(const AttendArgs& a, Cursor* c) {
   if (++c->t < c->nt) return;
   c->t = 0;
-  c->first += c->nt;
+  c->first += c->nt + kGap;
   if (++c->item < a.c.kv_heads) return;
   c->item = 0;
   if (++c->b >= a.c.batch) return;
   c->span = sequence_span(a.c, c->b, a.nodes);
   c->nt = tiles_of<kTile>(c->span);
+}
+
+// Block-wide: the line, run number `run` of at most `most`, the cursor at its
+// begin and its number of tiles (0: nothing to do, the cursor is not set).
+// `scratch` has room for 2 * (kThreads / 32) + 4 ints. Batches of up to
+// kThreads sequences are scanned once, larger ones twice (length, then place).
+template <int kTile, int kGap, int kThreads>
+__device__ int find_run(const AttendArgs& a, int most, int run, int* scratch, Line* line, Cursor* cur) {
+  const int items = a.c.kv_heads;
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int batch = a.c.batch;
+  // Sequence of the run's begin, its first place; tiles before begin and end.
+  int* found = scratch + 2 * kWarps;
+  for (int pass = batch <= kThreads ? 1 : 0; pass < 2; ++pass) {
+    int before = 0, tiles_before = 0;
+    for (int b0 = 0; b0 < batch; b0 += kThreads) {
+      const int b = b0 + tid;
+      const int nt = b < batch ? tiles_of<kTile>(sequence_span(a.c, b, a.nodes)) : 0;
+      const int n = b < batch ? (nt + kGap) * items : 0;
+      int upto = n, tiles = nt * items;
+      for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(~0u, upto, o), z = __shfl_up_sync(~0u, tiles, o);
+        if (lane >= o) upto += y, tiles += z;
+      }
+      if (lane == 31) scratch[warp] = upto, scratch[kWarps + warp] = tiles;
+      __syncthreads();
+      int prior = before, tiles_prior = tiles_before;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) prior += scratch[w], tiles_prior += scratch[kWarps + w];
+        before += scratch[w], tiles_before += scratch[kWarps + w];
+      }
+      upto += prior, tiles += tiles_prior;
+      if (b0 + kThreads >= batch && (pass == 0 || batch <= kThreads)) line->cut(before, most, run);
+      if (pass == 1 && n > 0) {
+        // Tiles of the line before a place of this sequence.
+        auto tiles_to = [&](int place) {
+          const int in = place - (upto - n), item = in / (nt + kGap);
+          return tiles - nt * items + item * nt + min(in - item * (nt + kGap), nt);
+        };
+        if (line->begin >= upto - n && line->begin < upto) {
+          found[0] = b;
+          found[1] = upto - n;
+          found[2] = tiles_to(line->begin);
+        }
+        if (line->end > upto - n && line->end <= upto) found[3] = tiles_to(line->end);
+      }
+      __syncthreads();
+    }
+  }
+  if (line->begin >= line->end) return 0;
+  const int n_tiles = found[3] - found[2];
+  if (n_tiles == 0) return 0;
+  cur->b = found[0];
+  cur->span = sequence_span(a.c, cur->b, a.nodes);
+  cur->nt = tiles_of<kTile>(cur->span);
+  const int in = line->begin - found[1];
+  cur->item = in / (cur->nt + kGap);
+  cur->t = in - cur->item * (cur->nt + kGap);
+  cur->first = line->begin - cur->t;
+  if (cur->t >= cur->nt) {   // in a gap: on to the next item
+    cur->t = cur->nt - 1;
+    advance<kTile, kGap>(a, cur);
+  }
+  return n_tiles;
 }
 
 // Place of run `run`'s part of the item at `first`, for row block rb of
@@ -292,10 +312,10 @@ __device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, i
 // the main launch had blocks, the item that a run begins inside of, if it is
 // the first run to do so. y is a row, whose parts the block's groups of D / 4
 // threads share out (kRows of 16 or 64), or kColumns columns of all 128 rows.
-template <typename T, int kRows, int D, int kTile, int kColumns, int kGroup>
+template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int kGroup>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs a, int row_blocks,
                                                    int block_rows, int runs) {
-  __shared__ int scratch[6];
+  __shared__ int scratch[12];
   __shared__ int sums[2][4];
   chain();
   const int tid = threadIdx.x, team = blockIdx.x / row_blocks;
@@ -304,18 +324,18 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   Cursor cur;
   int p0 = 0, n = 1;
   if (gridDim.x == runs * row_blocks) {
-    if (find_run<kTile, 128>(a, runs, team, scratch, &line, &cur) && cur.t > 0) {
+    if (find_run<kTile, kGap, 128>(a, runs, team, scratch, &line, &cur) && cur.t > 0) {
       p0 = line.run_of(cur.first);
       if (team == p0 + 1) n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
     }
   } else {
     cur.b = team / a.c.kv_heads;
     cur.item = team - cur.b * a.c.kv_heads;
-    int before = 0, all = 0;   // tiles of the sequences before b, and of all
+    int before = 0, all = 0;   // places of the sequences before b, and of all
     for (int i = tid; i < a.c.batch; i += 128) {
-      const int tiles = tiles_of<kTile>(sequence_span(a.c, i, a.nodes)) * a.c.kv_heads;
-      all += tiles;
-      if (i < cur.b) before += tiles;
+      const int places = (tiles_of<kTile>(sequence_span(a.c, i, a.nodes)) + kGap) * a.c.kv_heads;
+      all += places;
+      if (i < cur.b) before += places;
     }
     before = __reduce_add_sync(~0u, before);
     all = __reduce_add_sync(~0u, all);
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     __syncthreads();
     cur.span = sequence_span(a.c, cur.b, a.nodes);
     cur.nt = tiles_of<kTile>(cur.span);
-    cur.first = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3] + cur.item * cur.nt;
+    cur.first = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3] + cur.item * (cur.nt + kGap);
     line.cut(sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3], runs, 0);
     p0 = line.run_of(cur.first);
     n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
@@ -395,20 +415,20 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   }
 }
 
-template <typename T, int kRows, int D, int kTile, int kColumns, int kGroup>
+template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int kGroup>
 cudaError_t launch_join_as(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
   const dim3 grid(std::min(a.c.batch * a.c.kv_heads, runs) * row_blocks,
                   kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
-  return launch_chained(join_kernel<T, kRows, D, kTile, kColumns, kGroup>, grid, dim3(128), 0, 1, s, a, row_blocks,
+  return launch_chained(join_kernel<T, kRows, D, kTile, kGap, kColumns, kGroup>, grid, dim3(128), 0, 1, s, a, row_blocks,
                         block_rows, runs);
 }
 
 // Few items have many parts each: few columns a block, many parts at once.
-template <typename T, int kRows, int D, int kTile>
+template <typename T, int kRows, int D, int kTile, int kGap>
 cudaError_t launch_join(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
   if (runs >= 4 * a.c.batch * a.c.kv_heads || kRows < 128)
-    return launch_join_as<T, kRows, D, kTile, 8, 8>(a, runs, row_blocks, block_rows, s);
-  return launch_join_as<T, kRows, D, kTile, kRows < 128 ? 8 : 32, kRows < 128 ? 8 : 2>(a, runs, row_blocks, block_rows, s);
+    return launch_join_as<T, kRows, D, kTile, kGap, 8, 8>(a, runs, row_blocks, block_rows, s);
+  return launch_join_as<T, kRows, D, kTile, kGap, kRows < 128 ? 8 : 32, kRows < 128 ? 8 : 2>(a, runs, row_blocks, block_rows, s);
 }
 
 }  // namespace tfx

@@ -127,8 +127,8 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
       q_stride_seq < 0 || q_stride_node < 0 || q_stride_head < 0 || stride_parents < 0 || !std::isfinite(scale) ||
       static_cast<int64_t>(cache->batch) * nodes * heads > kMaxRows)
     return TF_ERR_SHAPE;
-  // The kernels number the tiles (of at least 32 slots) of all kv heads in 31 bits.
-  const int64_t tiles = (static_cast<int64_t>(cache->table_width) * cache->page_size + 31) / 32;
+  // The kernels number the tiles (of at least 32 slots, and up to two places more) of all kv heads in 31 bits.
+  const int64_t tiles = (static_cast<int64_t>(cache->table_width) * cache->page_size + 31) / 32 + 2;
   if (static_cast<double>(tiles) * cache->kv_heads * cache->batch > 2147483647.0)
     return TF_ERR_SHAPE;
   if (cache->batch == 0 || nodes == 0) return TF_OK;

@@ -43,7 +43,7 @@ cudaError_t launch_mma(AttendArgs a, int device, cudaStream_t s) {
   const cudaError_t launched = launch_chained(tree_attention_mma_kernel<T, D, kRowWarps>, dim3(blocks),
                                               dim3(S::kThreads), S::kSmem, 1, s, a);
   if (launched != cudaSuccess || !a.join_later) return launched;
-  return launch_join<T, S::kRows, D, S::kTile>(a, blocks / row_blocks, row_blocks, S::kRows, s);
+  return launch_join<T, S::kRows, D, S::kTile, S::kGap>(a, blocks / row_blocks, row_blocks, S::kRows, s);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
@@ -104,7 +104,7 @@ cudaError_t launch_tc(const AttendArgs& a, int box, int device, cudaStream_t s) 
       launch_chained(tree_attention_tc_kernel<T, D>, dim3(blocks), dim3(S::kThreads), S::kSmem, 1, s, maps, args);
   // No item has a second tile to be cut off.
   if (launched != cudaSuccess || static_cast<int64_t>(c.table_width) * c.page_size <= S::kTile) return launched;
-  return launch_join<T, 128, D, S::kTile>(a, blocks / row_blocks, row_blocks, args.block_nodes * a.group, s);
+  return launch_join<T, 128, D, S::kTile, S::kGap>(a, blocks / row_blocks, row_blocks, args.block_nodes * a.group, s);
 }
 
 // Rows of a copy for the tcgen05 kernel: the largest that divides both the

@@ -304,6 +304,15 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
 
   const bool draft = a.draft != nullptr;
   int count = 0;   // nodes gone through (a walk)
+  // This block's part of a row, to L2.
+  auto prefetch_part = [&](const T* row) {
+    const Row<T> r{row, 0.f, 0.f};
+    const int vecs = (a.vocab + r.shift()) / kVec, per_block = (r.vectors(a.vocab) + ranks - 1) / ranks;
+    const int v0 = max(r.shift() ? 1 : 0, rank * per_block), v1 = min(vecs, (rank + 1) * per_block);
+    if (v0 < v1)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row - r.shift() + v0 * kVec), "r"((v1 - v0) * 16)
+                   : "memory");
+  };
 #pragma unroll 1
   for (int node = kWalk ? 0 : id - b * a.nodes; node >= 0;) {
     Row<T> p{static_cast<const T*>(a.logits) + b * a.seq + node * a.node, a.inv_temp, 0.f};
@@ -364,6 +373,13 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     }
     side ^= 1;
 
+    // A walk goes on to one of the children, if to any: the first two's rows
+    // start on their way to L2 while this one is summed.
+    if (kWalk && warp == 0) {
+      const unsigned kids = __ballot_sync(~0u, child);
+      if (child && __popc(kids & ((1u << lane) - 1)) < 2)
+        prefetch_part(static_cast<const T*>(a.logits) + b * a.seq + tid * a.node);
+    }
     const int up = s.par[node];
     const bool dead = node == 0 ? up < -1 : up < 0;
     int next = -1, token = -1;
