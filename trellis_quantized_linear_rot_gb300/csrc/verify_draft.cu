@@ -33,6 +33,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
 constexpr float kOne = 1073741824.f;                 // 2^30: the largest weight
 constexpr double kUnit = 2305843009213693952.0;      // 2^61
 constexpr double kHalfUnit = 2147483648.0;           // 2^31: the normalised rows' unit
+constexpr int kNobody = -1, kRefused = -2;           // a child asked, else
 
 __device__ __forceinline__ uint32_t whole(float x) { return __float2uint_rn(x); }   // a NaN becomes 0
 
@@ -193,7 +194,9 @@ struct Shared {
   int par[TF_MAX_NODES], tok[TF_MAX_NODES];
   float zp[TF_MAX_NODES], zq[TF_MAX_NODES];   // logits of the node's children's tokens
   float u[TF_MAX_NODES];
-  int next_node;
+  int next_node, verdict;
+  unsigned long long goal;
+  Rest rest;
   int state[TF_MAX_NODES], out_tok[TF_MAX_NODES];
   float out_lp[TF_MAX_NODES];
 };
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     unsigned long long mass = 0, before = 0;
     bool pick = false;   // the token is still to be found by its cumulative weight
     Rest rest{0.f, 0.f};
-    double level = 0.0;
+    bool refused = false;   // by a child: the token comes from the rest of p
     unsigned long long goal = 0, goal_total = 0;
     if (!dead && p.top > -INFINITY) {
       const unsigned long long sum = p.top < INFINITY ? sum_weights<T, true>(p, a.vocab, v0, v1)
@@ -422,44 +425,65 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
         // p's sums, for a node whose token comes from p itself.
         const unsigned long long p_warp = s.sums[warp], p_end = s.sums[warp + 1], p_before = before;
         const unsigned long long qmass = total(q_sum, &unused);
-        rest.cp = static_cast<float>(kUnit / static_cast<double>(mass));
-        const double q1 = qmass ? kUnit / static_cast<double>(qmass) : 0.0;
-        double left = kHalfUnit;
-        for (int c = node + 1; c < a.nodes; ++c) {
-          if (s.par[c] != node) continue;
-          const float ep = isnan(s.zp[c]) ? 0.f : p.e(s.zp[c]);
-          const float eq = isnan(s.zq[c]) || q.top == -INFINITY ? 0.f : q.e(s.zq[c]);
-          const float pt = __fmul_rn(ep, rest.cp), qt = __fmul_rn(eq, static_cast<float>(q1));
-          const double rt = level > 0.0 ? static_cast<double>(rest(ep, eq)) : static_cast<double>(pt);
-          if (static_cast<double>(s.u[c]) * static_cast<double>(qt) * left < rt * kHalfUnit) {
-            next = c;
-            token = s.tok[c];
-            pick = false;
-            break;
+        // The 64-bit decisions are one thread's, in every block of the cluster
+        // alike: an SM has few fp64 units, and sixteen warps dividing at once
+        // took longer than a pass over the row.
+        double q1 = 0.0, level = 0.0, left = kHalfUnit;   // of thread 0
+        if (tid == 0) {
+          s.rest.cp = static_cast<float>(kUnit / static_cast<double>(mass));
+          q1 = qmass ? kUnit / static_cast<double>(qmass) : 0.0;
+        }
+        for (int c = node;;) {
+          if (tid == 0) {   // the next child is asked
+            s.verdict = kNobody;
+            while (++c < a.nodes && s.par[c] != node) {
+            }
+            if (c < a.nodes) {
+              const float ep = isnan(s.zp[c]) ? 0.f : p.e(s.zp[c]);
+              const float eq = isnan(s.zq[c]) || q.top == -INFINITY ? 0.f : q.e(s.zq[c]);
+              const float qt = __fmul_rn(eq, static_cast<float>(q1));
+              const double rt = refused ? static_cast<double>(s.rest(ep, eq)) : static_cast<double>(__fmul_rn(ep, s.rest.cp));
+              if (static_cast<double>(s.u[c]) * static_cast<double>(qt) * left < rt * kHalfUnit) {
+                s.verdict = c;
+              } else {
+                level += left / kHalfUnit;
+                s.rest.cq = static_cast<float>(level * q1);
+                s.verdict = kRefused;
+              }
+            }
           }
-          level += left / kHalfUnit;
-          rest.cq = static_cast<float>(level * q1);
+          __syncthreads();
+          rest = s.rest;
+          next = s.verdict;
+          if (next != kRefused) break;
           unsigned long long rest_before;
           const bool finite = p.top < INFINITY && fabsf(q.top) < INFINITY;
           goal_total = total(finite ? sum_rest<T, true>(p, q, rest, a.vocab, v0, v1)
                                     : sum_rest<T, false>(p, q, rest, a.vocab, v0, v1), &rest_before);
-          left = static_cast<double>(goal_total);
-          if (goal_total == 0) {
-            level = 0.0;
+          refused = goal_total > 0;
+          if (!refused) {   // nothing is left: the token comes from p after all
             goal_total = mass;
+            next = kNobody;
             break;
           }
           before = rest_before;
+          if (tid == 0) left = static_cast<double>(goal_total);
         }
-        if (pick && level == 0.0) {   // p itself: its sums again
+        if (next >= 0) {
+          token = s.tok[next];
+          pick = false;
+        } else if (!refused) {   // p itself: its sums again
           __syncthreads();
           s.sums[warp] = p_warp;
           if (warp == kWarps - 1) s.sums[kWarps] = p_end;
           before = p_before;
-          __syncthreads();
         }
       }
-      if (pick) goal = threshold(u_node, goal_total);
+      if (pick) {
+        if (tid == 0) s.goal = threshold(u_node, goal_total);
+        __syncthreads();
+        goal = s.goal;
+      }
     }
 
     // The block that holds the token finds it: the part of one warp is shared
@@ -485,11 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
           unsigned long long sum = 0;
           const int e0 = v * kVec - p.shift();
           p.load(e0, a.vocab, x);
-          if (level > 0.0) q.load(e0, a.vocab, y);
+          if (refused) q.load(e0, a.vocab, y);
 #pragma unroll
           for (int k = 0; k < kVec; ++k) {
             const float ep = p.e(p.z(x[k]));
-            weights[k] = level > 0.0 ? rest(ep, q.top > -INFINITY ? q.e(q.z(y[k])) : 0.f) : whole(ep * kOne);
+            weights[k] = refused ? rest(ep, q.top > -INFINITY ? q.e(q.z(y[k])) : 0.f) : whole(ep * kOne);
             sum += weights[k];
           }
           return sum;
