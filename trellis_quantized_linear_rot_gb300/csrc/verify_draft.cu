@@ -143,13 +143,29 @@ struct Largest<__half> : Largest16<__half, __half2> {};
 template <>
 struct Largest<__nv_bfloat16> : Largest16<__nv_bfloat16, __nv_bfloat162> {};
 
+// e of two elements of a row with a finite maximum, in packed instructions but
+// for exp itself; a NaN stays one (whole() makes it 0).
+template <typename T>
+__device__ __forceinline__ float2 exp_of(const Row<T>& r, T x0, T x1) {
+  const float2 z = mul2(float2{to_f32(x0), to_f32(x1)}, float2{r.inv, r.inv});
+  const float2 d = add2(z, float2{-r.top, -r.top});
+  return float2{expf(d.x), expf(d.y)};
+}
+
 // A warp's sum of the weights of its part of a row.
 template <typename T, bool kFinite>
 __device__ __forceinline__ unsigned long long sum_weights(const Row<T>& r, int vocab, int lo, int hi) {
   unsigned long long sum = 0;
-  sweep<kFinite ? 2 : 1>(r, vocab, lo, hi, [&](int, const T(&x)[Row<T>::kVec]) {
+  sweep<!kFinite ? 1 : sizeof(T) == 2 ? 2 : 4>(r, vocab, lo, hi, [&](int, const T(&x)[Row<T>::kVec]) {
 #pragma unroll
-    for (int k = 0; k < Row<T>::kVec; ++k) sum += whole(r.template e<kFinite>(r.z(x[k])) * kOne);
+    for (int k = 0; k < Row<T>::kVec; k += 2) {
+      if (kFinite) {
+        const float2 w = mul2(exp_of(r, x[k], x[k + 1]), float2{kOne, kOne});
+        sum += whole(w.x) + whole(w.y);   // at most 2^31
+      } else {
+        sum += whole(r.template e<false>(r.z(x[k])) * kOne) + whole(r.template e<false>(r.z(x[k + 1])) * kOne);
+      }
+    }
   });
   return sum;
 }
@@ -162,17 +178,57 @@ struct Rest {
     return x > y ? x - y : 0;
   }
 };
-template <typename T, bool kFinite>
-__device__ __forceinline__ unsigned long long sum_rest(const Row<T>& p, const Row<T>& q, const Rest& rest, int vocab,
-                                                       int lo, int hi) {
+template <typename T>
+__device__ unsigned long long sum_rest(const Row<T>& p, const Row<T>& q, const Rest& rest, int vocab, int lo, int hi) {
+  constexpr int kVec = Row<T>::kVec;
   unsigned long long sum = 0;
-  sweep<kFinite ? 2 : 1>(p, vocab, lo, hi, [&](int e0, const T(&x)[Row<T>::kVec]) {
-    alignas(16) T y[Row<T>::kVec];
+  const bool finite = p.top < INFINITY && fabsf(q.top) < INFINITY;
+  if (finite && p.shift() == q.shift()) {   // whole vectors of both, several in flight; the row's ends below
+    constexpr int kAhead = 2;
+    const int lane = threadIdx.x % 32, shift = p.shift();
+    const int f0 = max(lo, shift ? 1 : 0), f1 = min(hi, (vocab + shift) / kVec);
+    const uint4* pv = reinterpret_cast<const uint4*>(p.x - shift);
+    const uint4* qv = reinterpret_cast<const uint4*>(q.x - shift);
+    auto add = [&](const uint4& a, const uint4& b) {
+      alignas(16) T x[kVec];
+      alignas(16) T y[kVec];
+      *reinterpret_cast<uint4*>(x) = a;
+      *reinterpret_cast<uint4*>(y) = b;
+#pragma unroll
+      for (int k = 0; k < kVec; k += 2) {
+        const float2 u = mul2(exp_of(p, x[k], x[k + 1]), float2{rest.cp, rest.cp});
+        const float2 w = mul2(exp_of(q, y[k], y[k + 1]), float2{rest.cq, rest.cq});
+        const uint32_t u0 = whole(u.x), u1 = whole(u.y), w0 = whole(w.x), w1 = whole(w.y);
+        sum += static_cast<unsigned long long>(u0 > w0 ? u0 - w0 : 0) + (u1 > w1 ? u1 - w1 : 0);
+      }
+    };
+    int v = f0 + lane;
+    for (; v + 32 * (kAhead - 1) < f1; v += 32 * kAhead) {
+      uint4 a[kAhead], b[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) a[u] = pv[v + 32 * u], b[u] = qv[v + 32 * u];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) add(a[u], b[u]);
+    }
+    for (; v < f1; v += 32) add(pv[v], qv[v]);
+    if (lane == 0 && lo < hi) {
+      alignas(16) T x[kVec];
+      alignas(16) T y[kVec];
+      auto end = [&](int at) {
+        p.load(at * kVec - shift, vocab, x);
+        q.load(at * kVec - shift, vocab, y);
+        add(*reinterpret_cast<const uint4*>(x), *reinterpret_cast<const uint4*>(y));
+      };
+      if (lo < f0) end(lo);
+      if (f1 < hi && hi - 1 >= f0) end(hi - 1);
+    }
+    return sum;
+  }
+  sweep<1>(p, vocab, lo, hi, [&](int e0, const T(&x)[kVec]) {
+    alignas(16) T y[kVec];
     q.load(e0, vocab, y);
 #pragma unroll
-    for (int k = 0; k < Row<T>::kVec; ++k)
-      sum += kFinite ? rest(p.template e<true>(p.z(x[k])), q.template e<true>(q.z(y[k])))
-                     : rest(p.e(p.z(x[k])), q.top > -INFINITY ? q.e(q.z(y[k])) : 0.f);
+    for (int k = 0; k < kVec; ++k) sum += rest(p.e(p.z(x[k])), q.top > -INFINITY ? q.e(q.z(y[k])) : 0.f);
   });
   return sum;
 }
@@ -269,30 +325,42 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
   int side = 0;   // which half of the exchange is next
   constexpr int kVec = Row<T>::kVec;
 
-  // Sum of x over the cluster; s.sums holds what lies before each warp of
-  // this block, *before what lies before this block.
-  auto total = [&](unsigned long long x, unsigned long long* before) {
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  // Sum of x over the cluster, and the maximum of qt; s.sums holds what lies
+  // before each warp of this block, *before what lies before this block.
+  auto total = [&](unsigned long long x, float qt, unsigned long long* before, float* qt_all) {
+    for (int o = 16; o; o >>= 1) {
+      x += __shfl_xor_sync(~0u, x, o);
+      qt = fmaxf(qt, __shfl_xor_sync(~0u, qt, o));
+    }
     __syncthreads();   // the sums before are no longer read
-    if (lane == 0) s.sums[warp + 1] = x;
+    if (lane == 0) s.sums[warp + 1] = x, s.qtops[warp] = qt;
     if (tid == 0) s.sums[0] = 0;
     __syncthreads();
     if (warp == 0) {
       unsigned long long y = lane < kWarps ? s.sums[lane + 1] : 0;
+      qt = lane < kWarps ? s.qtops[lane] : -INFINITY;
       for (int o = 1; o < kWarps; o *= 2) {
         const unsigned long long z = __shfl_up_sync(~0u, y, o);
         if (lane >= o) y += z;
+        qt = fmaxf(qt, __shfl_xor_sync(~0u, qt, o));
       }
       if (lane < kWarps) s.sums[lane + 1] = y;
       const unsigned long long all = __shfl_sync(~0u, y, kWarps - 1);
-      if (lane < ranks) cluster.map_shared_rank(&s.x.sum[side][0], lane)[rank] = all;
+      qt = __shfl_sync(~0u, qt, 0);
+      if (lane < ranks) {
+        Exchange* to = cluster.map_shared_rank(&s.x, lane);
+        to->sum[side][rank] = all;
+        to->qtop[side][rank] = qt;
+      }
     }
     cluster.sync();
     unsigned long long sum = 0;
     *before = 0;
+    *qt_all = -INFINITY;
     for (int k = 0; k < ranks; ++k) {
       if (k == rank) *before = sum;
       sum += s.x.sum[side][k];
+      *qt_all = fmaxf(*qt_all, s.x.qtop[side][k]);
     }
     side ^= 1;
     return sum;
@@ -344,36 +412,23 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     part_of(p.vectors(a.vocab), &v0, &v1, warp);
     part_of(q.vectors(a.vocab), &q0, &q1v, warp);
 
-    // Maxima.
-    Largest<T> most, qmost;
+    // The maximum. (The draft's row comes after p's sum, so that p's second
+    // pass finds it in L1; it is on its way to L2 meanwhile.)
+    if (draft && tid == 0) prefetch_part(q.x);
+    Largest<T> most;
     sweep<8>(p, a.vocab, v0, v1, [&](int, const T(&x)[kVec]) { most.add(x); });
     const bool ask = __syncthreads_or(child) && draft;   // a leaf has no use for the draft's row
-    if (ask) sweep<8>(q, a.vocab, q0, q1v, [&](int, const T(&x)[kVec]) { qmost.add(x); });
-    float top = __fmul_rn(most.get(), a.inv_temp), qtop = __fmul_rn(qmost.get(), a.inv_temp);
-    for (int o = 16; o; o >>= 1) {
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      qtop = fmaxf(qtop, __shfl_xor_sync(~0u, qtop, o));
-    }
-    if (lane == 0) s.tops[warp] = top, s.qtops[warp] = qtop;
+    float top = __fmul_rn(most.get(), a.inv_temp);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) s.tops[warp] = top;
     __syncthreads();
     if (warp == 0) {
       top = lane < kWarps ? s.tops[lane] : -INFINITY;
-      qtop = lane < kWarps ? s.qtops[lane] : -INFINITY;
-      for (int o = 16; o; o >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        qtop = fmaxf(qtop, __shfl_xor_sync(~0u, qtop, o));
-      }
-      if (lane < ranks) {
-        Exchange* to = cluster.map_shared_rank(&s.x, lane);
-        to->top[side][rank] = top;
-        to->qtop[side][rank] = qtop;
-      }
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      if (lane < ranks) cluster.map_shared_rank(&s.x.top[side][0], lane)[rank] = top;
     }
     cluster.sync();
-    for (int k = 0; k < ranks; ++k) {
-      p.top = k ? fmaxf(p.top, s.x.top[side][k]) : s.x.top[side][k];
-      q.top = k ? fmaxf(q.top, s.x.qtop[side][k]) : s.x.qtop[side][k];
-    }
+    for (int k = 0; k < ranks; ++k) p.top = k ? fmaxf(p.top, s.x.top[side][k]) : s.x.top[side][k];
     side ^= 1;
 
     // A walk goes on to one of the children, if to any: the first two's rows
@@ -394,6 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     if (!dead && p.top > -INFINITY) {
       const unsigned long long sum = p.top < INFINITY ? sum_weights<T, true>(p, a.vocab, v0, v1)
                                                       : sum_weights<T, false>(p, a.vocab, v0, v1);
+      float qtop = -INFINITY, unused_top;
+      if (ask) {
+        Largest<T> qmost;
+        sweep<8>(q, a.vocab, q0, q1v, [&](int, const T(&x)[kVec]) { qmost.add(x); });
+        qtop = __fmul_rn(qmost.get(), a.inv_temp);
+      }
       if (a.greedy) {
         int best = INT32_MAX;
         sweep<2>(p, a.vocab, v0, v1, [&](int e0, const T(&x)[kVec]) {
@@ -409,11 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
           if (lane < ranks) cluster.map_shared_rank(&s.x.at[side][0], lane)[rank] = best;
         }
         const int half = side;
-        mass = total(sum, &before);
+        mass = total(sum, qtop, &before, &q.top);
         token = INT32_MAX;
         for (int k = 0; k < ranks; ++k) token = min(token, s.x.at[half][k]);
       } else {
-        mass = total(sum, &before);
+        mass = total(sum, qtop, &before, &q.top);
         pick = true;
         goal_total = mass;
       }
@@ -424,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
                                                             : sum_weights<T, false>(q, a.vocab, q0, q1v);
         // p's sums, for a node whose token comes from p itself.
         const unsigned long long p_warp = s.sums[warp], p_end = s.sums[warp + 1], p_before = before;
-        const unsigned long long qmass = total(q_sum, &unused);
+        const unsigned long long qmass = total(q_sum, -INFINITY, &unused, &unused_top);
         // The 64-bit decisions are one thread's, in every block of the cluster
         // alike: an SM has few fp64 units, and sixteen warps dividing at once
         // took longer than a pass over the row.
@@ -457,9 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
           next = s.verdict;
           if (next != kRefused) break;
           unsigned long long rest_before;
-          const bool finite = p.top < INFINITY && fabsf(q.top) < INFINITY;
-          goal_total = total(finite ? sum_rest<T, true>(p, q, rest, a.vocab, v0, v1)
-                                    : sum_rest<T, false>(p, q, rest, a.vocab, v0, v1), &rest_before);
+          goal_total = total(sum_rest(p, q, rest, a.vocab, v0, v1), -INFINITY, &rest_before, &unused_top);
           refused = goal_total > 0;
           if (!refused) {   // nothing is left: the token comes from p after all
             goal_total = mass;
