@@ -469,6 +469,53 @@ def test_verify_walks(dtype, v, temperature, with_draft):
     verify_and_check(x, tok.int(), par, us, temperature, d if with_draft else None, ua)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("temperature", [0.6, 0.8, 1.0, 1.3])
+@pytest.mark.parametrize("v", [257, 129280])
+def test_verify_one_row_is_the_definition_to_the_last_bit(dtype, temperature, v):
+    """Every step of the definition is one fp32 operation or exact, so the
+    tokens and log-probabilities are those of the same steps done one by one."""
+    x, _, g = logits_like(8, 3, v, dtype, v + 1)
+    us = torch.rand((8, 3), device="cuda", generator=g)
+    tok = torch.zeros((8, 3), dtype=torch.int32, device="cuda")
+    _, _, out, logp = tf.tf_verify_draft(x.view(24, 1, v), tok.view(24, 1), i32([[-1]] * 24), us.view(24, 1),
+                                         temperature=temperature)
+    z = x.float() * torch.tensor(1.0 / temperature, dtype=torch.float32, device="cuda")
+    top = z.amax(-1, keepdim=True)
+    w = torch.round(torch.exp(z - top) * 2.0 ** 30).long()
+    mass = w.sum(-1)
+    goal = torch.floor(us.double() * mass.double()).long()
+    want = (torch.cumsum(w, -1) <= goal[..., None]).sum(-1)
+    assert torch.equal(out.view(8, 3).long(), want)
+    lp = (torch.gather(z, 2, want[..., None])[..., 0] - top[..., 0]) - torch.log(mass.float() * 2.0 ** -30)
+    assert torch.equal(logp.view(8, 3), lp)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("v", [300, 50003])
+def test_verify_the_rest_of_a_distribution_is_the_definition_to_the_last_bit(dtype, v):
+    """A refused child (u = 1 - 2^-24 against a token the target finds
+    unlikely): the token comes from max(round(p) - round(q), 0)."""
+    x, d, g = logits_like(16, 2, v, dtype, v + 2)
+    q = torch.softmax(d[:, 0].float(), -1)
+    tok = (q / torch.softmax(x[:, 0].float(), -1)).argmax(-1).int()[:, None].expand(16, 2).contiguous()
+    us = torch.rand((16, 2), device="cuda", generator=g)
+    ua = torch.full((16, 2), 1 - 2.0 ** -24, device="cuda")
+    counts, _, out, _ = tf.tf_verify_draft(x, tok, i32([-1, 0]), us, draft_logits=d, u_accept=ua)
+    assert counts.tolist() == [1] * 16
+
+    def weights(y):
+        z = y.float()
+        return torch.exp(z - z.amax(-1, keepdim=True)), torch.round(torch.exp(z - z.amax(-1, keepdim=True)) * 2.0 ** 30).long().sum(-1)
+
+    e, mass = weights(x[:, 0])
+    f, qmass = weights(d[:, 0])
+    p = torch.round(e * (2.0 ** 61 / mass.double()).float()[:, None]).long()
+    r = (p - torch.round(f * (2.0 ** 61 / qmass.double()).float()[:, None]).long()).clamp(min=0)
+    goal = torch.floor(us[:, 0].double() * r.sum(-1).double()).long()
+    assert torch.equal(out[:, 0].long(), (torch.cumsum(r, -1) <= goal[:, None]).sum(-1))
+
+
 def test_verify_strided_rows_and_shared_tree():
     """A padded head (rows longer than the vocabulary, so that a row starts
     off a 16-byte boundary) gives what a contiguous copy gives."""

@@ -143,13 +143,13 @@ struct Largest<__half> : Largest16<__half, __half2> {};
 template <>
 struct Largest<__nv_bfloat16> : Largest16<__nv_bfloat16, __nv_bfloat162> {};
 
-// e of two elements of a row with a finite maximum, in packed instructions but
-// for exp itself; a NaN stays one (whole() makes it 0).
+// e of two elements of a row with a finite maximum; a NaN stays one (whole()
+// makes it 0). (The product and the difference are single instructions: the
+// assembler joins packed ones into a multiply-add, which rounds once where
+// the definition rounds twice.)
 template <typename T>
 __device__ __forceinline__ float2 exp_of(const Row<T>& r, T x0, T x1) {
-  const float2 z = mul2(float2{to_f32(x0), to_f32(x1)}, float2{r.inv, r.inv});
-  const float2 d = add2(z, float2{-r.top, -r.top});
-  return float2{expf(d.x), expf(d.y)};
+  return float2{r.template e<true>(r.z(x0)), r.template e<true>(r.z(x1))};
 }
 
 // A warp's sum of the weights of its part of a row.
