@@ -200,7 +200,7 @@ struct TcShared {
   unsigned long long bars[kBarriers];
   float row_max[2][128], row_sum[2][128];   // of the streams, at an item's end
   uint32_t gone[3][4];                      // keys of a stage whose page is outside the pool
-  uint32_t bad[4];                          // tree nodes with values that are not finite
+  uint32_t bad[2][4];                       // tree nodes with values that are not finite, of this item and another
   int any_gone;
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
   int scratch[2 * (384 / 32) + 4];
@@ -275,6 +275,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
   if (tid == 0) {
     sh.abort = 0;
     sh.any_gone = 0;
+    for (int i = 0; i < 4; ++i) sh.bad[0][i] = 0;
     mbar_init(bar(kQFull), 1);
     mbar_init(bar(kQEmpty), 2);
     for (int i = 0; i < kTcSlots; ++i) {
@@ -485,24 +486,30 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     const float sc = a.scale * kLog2e;
     const int row_node = row / a.group;
     const T* values = static_cast<const T*>(a.v);
-    int n = 0;
+    const int node = row_node < args.block_nodes && node0 + row_node < a.nodes ? node0 + row_node : -1;
+    int n = 0, n_items = 0, seen_b = -1;
+    Seen seen = {};
 #pragma unroll 1
     for (int ja = 0; ja < n_tiles;) {   // the items of the run, tiles ja .. jb - 1 of it
       const int jb = ja + min(n_tiles - ja, cur.nt - cur.t);
       const int kvh = cur.item;
-      const int node = row_node < args.block_nodes && node0 + row_node < a.nodes ? node0 + row_node : -1;
-      if (both < a.nodes) {
-        int p = a.parents[cur.b * a.stride_parents + both];
-        if (p >= both) {
-          record_index_error(a.c.err);
-          p = -2;
+      if (cur.b != seen_b) {   // the tree is its sequence's: another item of it has it still
+        seen_b = cur.b;
+        if (both < a.nodes) {
+          int p = a.parents[cur.b * a.stride_parents + both];
+          if (p >= both) {
+            record_index_error(a.c.err);
+            p = -2;
+          }
+          sh.up[both] = p < -2 ? -2 : p;
         }
-        sh.up[both] = p < -2 ? -2 : p;
+        if (!group_all(3, 256, !*abort_flag)) break;
+        seen = node >= 0 ? seen_by(sh.up, node) : Seen{};
       }
-      if (both < 4) sh.bad[both] = 0;
-      if (!group_all(3, 256, !*abort_flag)) break;
-      Seen seen = {};
-      if (node >= 0) seen = seen_by(sh.up, node);
+      // The other item's list of bad values is cleared: nobody reads it any more.
+      uint32_t* bad = sh.bad[n_items & 1];
+      if (both < 4) sh.bad[(n_items + 1) & 1][both] = 0;
+      ++n_items;
       float m = -INFINITY, l = 0.f;
       bool used = false;
 #pragma unroll 1
@@ -549,7 +556,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
                 uint16_t* h = reinterpret_cast<uint16_t*>(at);
                 for (int y = 0; y < 8; ++y)
                   if (bad16<T>(h[y])) h[y] = 0;
-                atomicOr(&sh.bad[nd / 32], 1u << (nd % 32));
+                atomicOr(&bad[nd / 32], 1u << (nd % 32));
               }
             }
           }
@@ -580,7 +587,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         const bool has0 = jb - ja > 1 || (ja & 1) == 0, has1 = jb - ja > 1 || (ja & 1) == 1;
         const bool whole = cur.t == 0 && cur.nt == jb - ja;
         const bool idle = cur.span.context < 0;
-        const bool any_bad = (sh.bad[0] | sh.bad[1] | sh.bad[2] | sh.bad[3]) != 0;
+        const bool any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
         const int rows = min(args.block_nodes, a.nodes - node0) * a.group;
         const bool present = node >= 0 && !idle && sh.up[node] >= -1;
         const bool empty = !present || sum == 0.f;
@@ -598,7 +605,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
           for (int i = 0; i < 32; ++i) x[i] = (f0 * x[i] + f1 * y[i]) * inv;
           if (any_bad)
             for (int w = 0; w < 4; ++w)
-              for (uint32_t left = sh.bad[w] & (w == 0 ? seen.w[0] : w == 1 ? seen.w[1] : w == 2 ? seen.w[2] : seen.w[3]);
+              for (uint32_t left = bad[w] & (w == 0 ? seen.w[0] : w == 1 ? seen.w[1] : w == 2 ? seen.w[2] : seen.w[3]);
                    left; left &= left - 1) {
                 const int64_t off = slot_offset(a.c, cur.b, cur.span.context + w * 32 + __ffs(left) - 1);
                 if (off < 0) continue;
