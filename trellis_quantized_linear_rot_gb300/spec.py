@@ -111,19 +111,23 @@ def _parents(parents, batch, nodes):
 
 def _cache(k, v, page_table, lengths, layers=False):
     """(packed tf_kv_cache, batch); k's shape and the other tensors are checked."""
-    shape, table = k.shape, page_table.shape
+    shape, st = k.shape, k.stride()
     dims = len(shape)
     if dims != 4 and not (layers and dims == 5):
         raise ValueError("a cache is [%spages, page_size, kv_heads, head_dim]" % ("layers, " if layers else ""))
-    st = _strides(k)
-    if v.shape != shape or _strides(v) != st or v.dtype != k.dtype or st[-1] != 1:
+    same = v.stride() == st
+    if 1 in shape:
+        st = _strides(k)
+        same = _strides(v) == st
+    if not same or v.shape != shape or v.dtype != k.dtype or st[-1] != 1:
         raise ValueError("k_cache and v_cache must share shape, strides and dtype, the last dimension contiguous")
-    if page_table.dtype != torch.int32 or lengths.dtype != torch.int32:
+    int32 = torch.int32
+    if page_table.dtype != int32 or lengths.dtype != int32:
         raise TypeError("page_table and lengths must be int32")
-    if lengths.dim() != 1 or not lengths.is_contiguous():
+    table, rows, batch = page_table.shape, page_table.stride(), lengths.shape
+    if len(batch) != 1 or not lengths.is_contiguous():
         raise ValueError("lengths must be [batch], contiguous")
-    batch = lengths.shape[0]
-    rows = page_table.stride()
+    batch = batch[0]
     if len(table) != 2 or table[0] != batch or (rows[1] != 1 and table[1] > 1):
         raise ValueError("page_table must be [batch, table_width], rows contiguous")
     code = _codes.get(k.dtype, -1)
