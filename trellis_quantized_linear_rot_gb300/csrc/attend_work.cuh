@@ -9,8 +9,8 @@
 // other times. Lengths are on the device, so every block finds its run itself.
 // A run holds whole items but for its first and its last, which other runs may
 // share: those leave (max, sum, weighted sum) of their part in the workspace,
-// and the parts are joined in the order of the runs, by the block that arrives
-// last at the item or by a launch of its own. No block waits for another.
+// and the parts are joined in an order that the sizes and lengths fix, by the
+// block that arrives last at the item or by a launch of its own. No block waits for another.
 #pragma once
 
 #include <algorithm>
@@ -30,10 +30,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // Going from one item to the next costs a block about as much as kGap tiles
 // (its sums are joined and written, another q comes), so an item has kGap
-// places in the line after those of its tiles.
+// places in the line after those of its tiles: 16 sequences of 16 nodes on
+// tcgen05 took 53.3 us with one, 51.4 with two, 51.2 with three.
 //
-// The line of places (below 2^31: checked on the host) and one run of it: the first `longer` runs have per + 1 tiles, the others per. No more
-// runs than tiles, so that no run between two others is empty.
+// The line of places (below 2^31: checked on the host) and one run of it: the
+// first `longer` runs have per + 1 places, the others per. No more runs than
+// places, so that no run between two others is empty.
 struct Line {
   int runs, per, longer;
   int begin, end;
@@ -53,7 +55,8 @@ struct Line {
   }
 };
 
-// Position of a tile: item `item` (kv head) of sequence b, tile t of its nt. first = place of the item's tile 0 in the line.
+// Position of a tile: item `item` (kv head) of sequence b, tile t of its nt;
+// first is the place of the item's tile 0 in the line.
 struct Cursor {
   int b, item, t, nt;
   int first;
@@ -251,11 +254,14 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, const Rows& w,
 
 // The same for parts of 128 rows, which are stored by column (column c of row
 // r at c * 128 + r: there a thread has a row, and a warp's writes lie
-// together): this thread joins kColumns columns from c0 on of row r, kGroup
-// parts at once.
-template <typename T, int D, int kColumns, int kGroup>
-__device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, int b, int kvh, int row0, int r, int c0,
-                         int first, int nt, bool idle) {
+// together): the block's kThreads / 128 groups share out the parts, kGroup at
+// once, and this thread joins kColumns columns from c0 on of row tid % 128.
+template <typename T, int D, int kColumns, int kGroup, int kThreads>
+__device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, int b, int kvh, int row0, int rows,
+                         int c0, int first, int nt, bool idle) {
+  constexpr int kGroups = kThreads / 128;
+  __shared__ float others[kGroups > 1 ? kGroups - 1 : 1][kGroups > 1 ? kColumns + 2 : 1][128];
+  const int r = threadIdx.x % 128, g = threadIdx.x / 128;
   constexpr size_t kPart = kPartFloats<128, D>;
   const int p0 = line.run_of(first), n = line.run_of(first + nt - 1) - p0 + 1;
   const float* part0 = a.partials + part_index(line, w, p0, first) * kPart + r;
@@ -263,11 +269,11 @@ __device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, i
   const size_t step = 2 * static_cast<size_t>(w.row_blocks) * kPart;
   float top = -INFINITY, l = 0.f, o[kColumns] = {};
 #pragma unroll 1
-  for (int q0 = 0; q0 < n; q0 += kGroup) {
+  for (int q0 = g * kGroup; q0 < n; q0 += kGroups * kGroup) {
     float m[kGroup], u[kGroup], x[kGroup][kColumns];
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
-      const bool real = q0 + i < n;
+      const bool real = q0 + i < n && r < rows;
       const float* from = q0 + i == 0 || !real ? part0 : part1 + (q0 + i - 1) * step;
       m[i] = real ? __ldcg(from + 128 * D) : -INFINITY;
       u[i] = real ? __ldcg(from + 128 * D + 128) : 0.f;
@@ -290,6 +296,26 @@ __device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, i
       for (int c = 0; c < kColumns; ++c) o[c] += f * x[i][c];
     }
   }
+  if constexpr (kGroups > 1) {
+    if (g > 0) {
+#pragma unroll
+      for (int c = 0; c < kColumns; ++c) others[g - 1][c][r] = o[c];
+      others[g - 1][kColumns][r] = top;
+      others[g - 1][kColumns + 1][r] = l;
+    }
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int k = 0; k < kGroups - 1; ++k) {
+      const float m = others[k][kColumns][r], high = fmaxf(top, m), base = high == -INFINITY ? 0.f : high;
+      const float keep = exp2_approx(top - base), f = exp2_approx(m - base);
+      top = high;
+      l = l * keep + f * others[k][kColumns + 1][r];
+#pragma unroll
+      for (int c = 0; c < kColumns; ++c) o[c] = o[c] * keep + f * others[k][c][r];
+    }
+  }
+  if (r >= rows) return;
   const RowOf ro = row_of(a, kvh, row0 + r);
   const int up = a.parents[b * a.stride_parents + ro.node];
   const bool empty = idle || up < -1 || up >= ro.node || l == 0.f;
@@ -312,11 +338,12 @@ __device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, i
 // the main launch had blocks, the item that a run begins inside of, if it is
 // the first run to do so. y is a row, whose parts the block's groups of D / 4
 // threads share out (kRows of 16 or 64), or kColumns columns of all 128 rows.
-template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int kGroup>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs a, int row_blocks,
-                                                   int block_rows, int runs) {
-  __shared__ int scratch[12];
-  __shared__ int sums[2][4];
+template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int kGroup, int kThreads>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttendArgs a, int row_blocks,
+                                                        int block_rows, int runs) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int scratch[2 * kWarps + 4];
+  __shared__ int sums[2][kWarps];
   chain();
   const int tid = threadIdx.x, team = blockIdx.x / row_blocks;
   const Rows w{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
@@ -324,7 +351,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   Cursor cur;
   int p0 = 0, n = 1;
   if (gridDim.x == runs * row_blocks) {
-    if (find_run<kTile, kGap, 128>(a, runs, team, scratch, &line, &cur) && cur.t > 0) {
+    if (find_run<kTile, kGap, kThreads>(a, runs, team, scratch, &line, &cur) && cur.t > 0) {
       p0 = line.run_of(cur.first);
       if (team == p0 + 1) n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
     }
@@ -332,7 +359,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     cur.b = team / a.c.kv_heads;
     cur.item = team - cur.b * a.c.kv_heads;
     int before = 0, all = 0;   // places of the sequences before b, and of all
-    for (int i = tid; i < a.c.batch; i += 128) {
+    for (int i = tid; i < a.c.batch; i += kThreads) {
       const int places = (tiles_of<kTile>(sequence_span(a.c, i, a.nodes)) + kGap) * a.c.kv_heads;
       all += places;
       if (i < cur.b) before += places;
@@ -343,8 +370,10 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
     __syncthreads();
     cur.span = sequence_span(a.c, cur.b, a.nodes);
     cur.nt = tiles_of<kTile>(cur.span);
-    cur.first = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3] + cur.item * (cur.nt + kGap);
-    line.cut(sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3], runs, 0);
+    before = all = 0;
+    for (int i = 0; i < kWarps; ++i) before += sums[0][i], all += sums[1][i];
+    cur.first = before + cur.item * (cur.nt + kGap);
+    line.cut(all, runs, 0);
     p0 = line.run_of(cur.first);
     n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
   }
@@ -353,10 +382,10 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   const int rows = min(block_rows, a.nodes * a.group - row0);
   const Span span = cur.span;
   if constexpr (kRows == 128) {
-    if (tid < rows)
-      join_row<T, D, kColumns, kGroup>(a, line, w, b, kvh, row0, tid, blockIdx.y * kColumns, first, nt, span.context < 0);
+    join_row<T, D, kColumns, kGroup, kThreads>(a, line, w, b, kvh, row0, rows, blockIdx.y * kColumns, first, nt,
+                                               span.context < 0);
   } else {
-    constexpr int kLanes = D / 4, kGroups = 128 / kLanes, kAhead = 6;
+    constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kAhead = 6;
     constexpr size_t kPart = kPartFloats<kRows, D>;
     __shared__ float4 others[kGroups][kLanes];
     __shared__ float tops[kGroups], ls[kGroups];
@@ -415,20 +444,37 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Atten
   }
 }
 
-template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int kGroup>
+template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int kGroup, int kThreads>
 cudaError_t launch_join_as(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
   const dim3 grid(std::min(a.c.batch * a.c.kv_heads, runs) * row_blocks,
                   kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
-  return launch_chained(join_kernel<T, kRows, D, kTile, kGap, kColumns, kGroup>, grid, dim3(128), 0, 1, s, a, row_blocks,
-                        block_rows, runs);
+  return launch_chained(join_kernel<T, kRows, D, kTile, kGap, kColumns, kGroup, kThreads>, grid, dim3(kThreads), 0, 1, s,
+                        a, row_blocks, block_rows, runs);
 }
 
-// Few items have many parts each: few columns a block, many parts at once.
+// Parts of an item where the lengths are alike: its share of the runs, or its
+// tiles if the page table has room for fewer.
+inline int64_t parts_of(const AttendArgs& a, int runs, int tile) {
+  const int64_t tiles = (static_cast<int64_t>(a.c.table_width) * a.c.page_size + tile - 1) / tile;
+  return std::min<int64_t>(runs / (static_cast<int64_t>(a.c.batch) * a.c.kv_heads), tiles);
+}
+
+// The more parts an item has, the more of them are read at once. Whole calls,
+// us, D = 128, rows of 16: 304 parts 15.4 with blocks of 512 threads, 17.2
+// with 256, 23.5 with 128; 38 parts 15.2, 14.9, 16.0. Rows of 128: 152 parts
+// 21.6, 28.5, 42.5; 19 parts 41.9, 43.0, 44.1; 9 parts 25.2, 22.3, 23.2; 6
+// parts 89.7, 83.0, 80.9; 3 parts 56.1 with 8 columns a block, 51.6 with 32.
 template <typename T, int kRows, int D, int kTile, int kGap>
 cudaError_t launch_join(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
-  if (runs >= 4 * a.c.batch * a.c.kv_heads || kRows < 128)
-    return launch_join_as<T, kRows, D, kTile, kGap, 8, 8>(a, runs, row_blocks, block_rows, s);
-  return launch_join_as<T, kRows, D, kTile, kGap, kRows < 128 ? 8 : 32, kRows < 128 ? 8 : 2>(a, runs, row_blocks, block_rows, s);
+  const int64_t parts = parts_of(a, runs, kTile);
+  if constexpr (kRows < 128) {
+    if (parts < 64) return launch_join_as<T, kRows, D, kTile, kGap, 8, 8, 256>(a, runs, row_blocks, block_rows, s);
+    return launch_join_as<T, kRows, D, kTile, kGap, 8, 8, 512>(a, runs, row_blocks, block_rows, s);
+  } else {
+    if (parts < 4) return launch_join_as<T, kRows, D, kTile, kGap, 32, 2, 128>(a, runs, row_blocks, block_rows, s);
+    if (parts < 16) return launch_join_as<T, kRows, D, kTile, kGap, 8, 8, 128>(a, runs, row_blocks, block_rows, s);
+    return launch_join_as<T, kRows, D, kTile, kGap, 8, 8, 512>(a, runs, row_blocks, block_rows, s);
+  }
 }
 
 }  // namespace tfx

@@ -13,20 +13,21 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-// Rows a kv head up to which the 16-row kernel takes them in one block.
+// Rows a kv head up to which the 16-row mma.sync kernel takes them in one
+// block, with two blocks an SM; above, the tcgen05 kernel, whose tiles have
+// 128 rows and whose one block an SM starts and ends slower. 8 sequences of
+// 4,096 slots, 8 kv heads of 128: 16 rows 36.3 us on mma.sync, 39.3 on
+// tcgen05; 17 rows 58.0 (blocks of 64 rows) and 39.4; 128 rows 104 and 45.
+// 1 sequence of 2,000: 16 rows 11.5 and 14.4; 24 rows 14.6 and 14.4.
 constexpr int kFewRows = 16;
 
 // Blocks of a launch with `blocks` places: whole teams of row_blocks, one at least.
 int team_blocks(int blocks, int row_blocks) { return std::max(1, blocks / row_blocks) * row_blocks; }
 
-// Whether an item is cut into so many parts that a launch of its own joins
-// them: its share of the runs, or of the tiles it can have if those are
-// fewer, is over kManyParts.
+// Parts of an item above which a launch of its own joins them. 304 parts: 22
+// us with the launch, 53 us with the last block; 38 parts 15.7 and 20.0; 9
+// parts 21.2 and 22.5; 1 to 4 parts level.
 constexpr int kManyParts = 6;
-bool many_parts(const AttendArgs& a, int runs, int tile) {
-  const int64_t tiles = (static_cast<int64_t>(a.c.table_width) * a.c.page_size + tile - 1) / tile;
-  return std::min<int64_t>(runs / (a.c.batch * a.c.kv_heads), tiles) > kManyParts;
-}
 
 template <typename T, int D, int kRowWarps>
 cudaError_t launch_mma(AttendArgs a, int device, cudaStream_t s) {
@@ -39,7 +40,7 @@ cudaError_t launch_mma(AttendArgs a, int device, cudaStream_t s) {
   if (e != cudaSuccess) return static_cast<cudaError_t>(e);
   const int row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
   const int blocks = team_blocks(kBlocksPerSm * a.num_sms, row_blocks);
-  a.join_later = many_parts(a, blocks / row_blocks, S::kTile);
+  a.join_later = parts_of(a, blocks / row_blocks, S::kTile) > kManyParts;
   const cudaError_t launched = launch_chained(tree_attention_mma_kernel<T, D, kRowWarps>, dim3(blocks),
                                               dim3(S::kThreads), S::kSmem, 1, s, a);
   if (launched != cudaSuccess || !a.join_later) return launched;
