@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
   constexpr int kRing = kStages + 1;            // tiles whose offsets are known
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ TreeMasks<S::kNodes> masks;
-  __shared__ int scratch[2 * (kThreads / 32) + 4];
+  __shared__ int scratch[2 * (kThreads / 32) + 6];
   __shared__ int64_t at[kRing][kTile];
   __shared__ float wm[4][16], wl[4][16];
   __shared__ uint32_t bad[kTile / 32];          // keys of this tile with values that are not finite

@@ -203,7 +203,7 @@ struct TcShared {
   uint32_t bad[2][4];                       // tree nodes with values that are not finite, of this item and another
   int any_gone;
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
-  int scratch[2 * (384 / 32) + 4];
+  int scratch[2 * (384 / 32) + 6];
   uint32_t tmem;
   int abort;
 };
@@ -211,7 +211,7 @@ struct TcShared {
 template <int D>
 struct TcShape {
   static constexpr int kThreads = 384;
-  static constexpr int kTile = 128, kGap = 2;
+  static constexpr int kTile = 128, kGap = 4;
   static constexpr int kParts = D / 64;                  // 64-column parts of a tile
   static constexpr int kPartBytes = kTile * 128;         // one part of q, keys or values
   static constexpr int kTileBytes = kParts * kPartBytes;
@@ -266,12 +266,6 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     return;
   }
 
-  chain();
-  Line line;
-  Cursor cur;
-  const int n_tiles = find_run<kTile, S::kGap, S::kThreads>(a, gridDim.x / row_blocks, team, sh.scratch, &line, &cur);
-  if (n_tiles == 0) return;
-
   if (tid == 0) {
     sh.abort = 0;
     sh.any_gone = 0;
@@ -301,12 +295,19 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
   }
+  // What does not depend on the kernel before is done while that still runs.
+  chain();
+  Line line;
+  Cursor cur;
+  const int n_tiles = find_run<kTile, S::kGap, S::kThreads>(a, gridDim.x / row_blocks, team, sh.scratch, &line, &cur);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp == 0) {
+  if (n_tiles == 0) {
+    // nothing to do
+  } else if (warp == 0) {
     // ---------------------------------------------------------------- copies
     const int box = args.box, boxes = kTile / box;   // at most 16
     const uint32_t box_bytes = static_cast<uint32_t>(box) * 128;

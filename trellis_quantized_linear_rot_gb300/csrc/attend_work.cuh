@@ -30,8 +30,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // Going from one item to the next costs a block about as much as kGap tiles
 // (its sums are joined and written, another q comes), so an item has kGap
-// places in the line after those of its tiles: 16 sequences of 16 nodes on
-// tcgen05 took 53.3 us with one, 51.4 with two, 51.2 with three.
+// places in the line after those of its tiles. On tcgen05, us with two, four
+// and six: a tree of 64 nodes over 50,001 slots 81.6, 80.0, 78.9; 19 trees of
+// 25 over up to 6,000 118.5, 116.0, 116.1; 19 of 53 over up to 798 29.5, 29.1,
+// 29.8. With mma.sync an item is less: 32 tokens over up to 300 slots 15.4
+// with one, 16.6 with two.
 //
 // The line of places (below 2^31: checked on the host) and one run of it: the
 // first `longer` runs have per + 1 places, the others per. No more runs than
@@ -82,7 +85,7 @@ __device__ __forceinline__ void advance(const AttendArgs& a, Cursor* c) {
 
 // Block-wide: the line, run number `run` of at most `most`, the cursor at its
 // begin and its number of tiles (0: nothing to do, the cursor is not set).
-// `scratch` has room for 2 * (kThreads / 32) + 4 ints. Batches of up to
+// `scratch` has room for 2 * (kThreads / 32) + 6 ints. Batches of up to
 // kThreads sequences are scanned once, larger ones twice (length, then place).
 template <int kTile, int kGap, int kThreads>
 __device__ int find_run(const AttendArgs& a, int most, int run, int* scratch, Line* line, Cursor* cur) {
@@ -90,13 +93,15 @@ __device__ int find_run(const AttendArgs& a, int most, int run, int* scratch, Li
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int batch = a.c.batch;
-  // Sequence of the run's begin, its first place; tiles before begin and end.
+  // Sequence of the run's begin, its first place; tiles before begin and end;
+  // the sequence's span.
   int* found = scratch + 2 * kWarps;
   for (int pass = batch <= kThreads ? 1 : 0; pass < 2; ++pass) {
     int before = 0, tiles_before = 0;
     for (int b0 = 0; b0 < batch; b0 += kThreads) {
       const int b = b0 + tid;
-      const int nt = b < batch ? tiles_of<kTile>(sequence_span(a.c, b, a.nodes)) : 0;
+      const Span span = b < batch ? sequence_span(a.c, b, a.nodes) : Span{};
+      const int nt = b < batch ? tiles_of<kTile>(span) : 0;
       const int n = b < batch ? (nt + kGap) * items : 0;
       int upto = n, tiles = nt * items;
       for (int o = 1; o < 32; o *= 2) {
@@ -122,6 +127,8 @@ __device__ int find_run(const AttendArgs& a, int most, int run, int* scratch, Li
           found[0] = b;
           found[1] = upto - n;
           found[2] = tiles_to(line->begin);
+          found[4] = span.context;
+          found[5] = span.slots;
         }
         if (line->end > upto - n && line->end <= upto) found[3] = tiles_to(line->end);
       }
@@ -132,7 +139,7 @@ __device__ int find_run(const AttendArgs& a, int most, int run, int* scratch, Li
   const int n_tiles = found[3] - found[2];
   if (n_tiles == 0) return 0;
   cur->b = found[0];
-  cur->span = sequence_span(a.c, cur->b, a.nodes);
+  cur->span = Span{found[4], found[5]};
   cur->nt = tiles_of<kTile>(cur->span);
   const int in = line->begin - found[1];
   cur->item = in / (cur->nt + kGap);
@@ -342,7 +349,7 @@ template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int k
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttendArgs a, int row_blocks,
                                                         int block_rows, int runs) {
   constexpr int kWarps = kThreads / 32;
-  __shared__ int scratch[2 * kWarps + 4];
+  __shared__ int scratch[2 * kWarps + 6];
   __shared__ int sums[2][kWarps];
   chain();
   const int tid = threadIdx.x, team = blockIdx.x / row_blocks;
