@@ -199,7 +199,7 @@ enum TcBarrier { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + kTcSlots, kVFull = 
 struct TcShared {
   unsigned long long bars[kBarriers];
   float row_max[2][128], row_sum[2][128];   // of the streams, at an item's end
-  uint32_t gone[3][4];                      // keys of a stage whose page is outside the pool
+  uint32_t gone[3][4];                      // keys of a stage whose page is outside the pool (they are 0)
   uint32_t bad[2][4];                       // tree nodes with values that are not finite, of this item and another
   int any_gone;
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
@@ -234,6 +234,9 @@ __device__ __forceinline__ Seen seen_by(const int16_t* up, int node) {
     for (int x = 0; x < 4; ++x)
       if (i >> 5 == x) s.w[x] |= 1u << (i & 31);
   return s;
+}
+__device__ __forceinline__ uint32_t seen_word(const Seen& s, int i) {
+  return i == 0 ? s.w[0] : i == 1 ? s.w[1] : i == 2 ? s.w[2] : i == 3 ? s.w[3] : 0u;
 }
 struct TcMaps {
   CUtensorMap q, k, v;
@@ -330,13 +333,14 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
       const int st = x->j % kStages, slot = x->cur.t * kTile + lane * box;
       const bool exists = lane < boxes && slot < x->cur.span.slots;
       const bool outside = exists && static_cast<unsigned>(x->page) >= static_cast<unsigned>(a.c.pages);
-      const bool copy = exists && !outside;
-      const int page = x->page, kvh = x->cur.item, row = slot - a.c.by_page(slot) * a.c.page_size;
+      // What does not exist is read past the last page: the copy writes zeros,
+      // so that nothing of an earlier tile is left to be multiplied.
+      const int page = exists && !outside ? x->page : a.c.pages;
+      const int kvh = x->cur.item, row = exists ? slot - a.c.by_page(slot) * a.c.page_size : 0;
       if (x->j + 1 < n_tiles) {
         advance<kTile, S::kGap>(a, &x->next);
         x->page = look_up(x->next);
       }
-      const uint32_t wanted = __popc(__ballot_sync(~0u, copy)) * box_bytes * S::kParts;
       const uint32_t missing = __ballot_sync(~0u, outside);
       if (values) {
         if (outside) record_index_error(a.c.err);
@@ -350,9 +354,9 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         __syncwarp();
       }
       const uint32_t b = bar(full + x->j % kTcSlots);
-      if (lane == 0) mbar_arrive_expect_tx(b, wanted);
+      if (lane == 0) mbar_arrive_expect_tx(b, S::kTileBytes);
       __syncwarp();
-      if (copy)
+      if (lane < boxes)
         for (int h = 0; h < S::kParts; ++h)
           tma_load_4d(ring + st * S::kTileBytes + h * S::kPartBytes + lane * box_bytes, map, h * 64, row, kvh, page, b);
       __syncwarp();
@@ -531,30 +535,39 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
             const int off = slot0 + w * 32 - cur.span.context;   // tree node of the word's first key
             uint32_t word = ~0u;
             if (off > -32) {
-              auto tree = [&](int i) {
-                return i == 0 ? seen.w[0] : i == 1 ? seen.w[1] : i == 2 ? seen.w[2] : i == 3 ? seen.w[3] : 0u;
-              };
-              word = off >= 0 ? __funnelshift_r(tree(off >> 5), tree((off >> 5) + 1), off & 31)
-                              : (tree(0) << -off) | ((1u << -off) - 1);
+              word = off >= 0 ? __funnelshift_r(seen_word(seen, off >> 5), seen_word(seen, (off >> 5) + 1), off & 31)
+                              : (seen.w[0] << -off) | ((1u << -off) - 1);
             }
             const int left = cur.span.slots - slot0 - w * 32;
             if (left < 32) word &= left > 0 ? (1u << left) - 1 : 0u;
             vis[w] = node >= 0 ? word & ~sh.gone[st][w] : 0u;
           }
-          // Values that must not be multiplied, even by 0: of slots that do
-          // not exist, and of tree nodes where they are not finite (added at
-          // the item's end to the rows that see them). They become 0.
-          const int j0 = sh.any_gone ? 0 : max(0, cur.span.context - slot0), j1 = cur.span.slots - slot0;
-          for (int id = j0 * (D / 8) + row; id < kTile * (D / 8); id += 128) {
-            const int key = id / (D / 8), ch = id % (D / 8), nd = slot0 + key - cur.span.context;
-            uint4* at = reinterpret_cast<uint4*>(smem + (v_at - base) + st * S::kTileBytes + (ch / 8) * S::kPartBytes +
-                                                 key * 128 + (((ch % 8) ^ (key & 7)) << 4));
-            if (key >= j1 || (sh.gone[st][key / 32] >> (key % 32) & 1)) {
-              *at = uint4{0, 0, 0, 0};
-            } else if (a.nodes > 1 && nd >= 0) {
-              const uint4 x = *at;
-              if (bad_pair<T>(x.x) | bad_pair<T>(x.y) | bad_pair<T>(x.z) | bad_pair<T>(x.w)) {
-                uint16_t* h = reinterpret_cast<uint16_t*>(at);
+          // Values that must not be multiplied, even by 0, become 0: those of
+          // rows past the last slot, and of tree nodes where they are not
+          // finite (added at the item's end to the rows that see them).
+          const int end = min(kTile, (cur.span.slots - slot0 + args.box - 1) / args.box * args.box);
+          const int j0 = max(0, cur.span.context - slot0), j1 = cur.span.slots - slot0;
+          for (int id0 = j0 * (D / 8) + row; id0 < end * (D / 8); id0 += 4 * 128) {
+            uint4 x[4];
+            auto place = [&](int id) {
+              const int key = id / (D / 8), ch = id % (D / 8);
+              return reinterpret_cast<uint4*>(smem + (v_at - base) + st * S::kTileBytes + (ch / 8) * S::kPartBytes +
+                                              key * 128 + (((ch % 8) ^ (key & 7)) << 4));
+            };
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (id0 + u * 128 < end * (D / 8)) x[u] = *place(id0 + u * 128);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int id = id0 + u * 128, key = id / (D / 8);
+              if (id >= end * (D / 8)) continue;
+              if (key >= j1) {
+                *place(id) = uint4{0, 0, 0, 0};
+              } else if (a.nodes > 1 && (bad_pair<T>(x[u].x) | bad_pair<T>(x[u].y) | bad_pair<T>(x[u].z) |
+                                         bad_pair<T>(x[u].w))) {
+                uint16_t* h = reinterpret_cast<uint16_t*>(place(id));
+                const int nd = slot0 + key - cur.span.context;
+#pragma unroll 1
                 for (int y = 0; y < 8; ++y)
                   if (bad16<T>(h[y])) h[y] = 0;
                 atomicOr(&bad[nd / 32], 1u << (nd % 32));
@@ -598,37 +611,44 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         T* out = static_cast<T*>(a.out) + out_at * D;
         float* part = a.partials + part_index(line, own, team, cur.first) * kPartFloats<128, D>;
 #pragma unroll 1
-        for (int c = s * (D / 64); c < (s + 1) * (D / 64); ++c) {
-          float x[32] = {}, y[32] = {};
-          if (has0) tmem_ld32(tmem + mine + S::kSums + c * 32, x);
-          if (has1) tmem_ld32(tmem + mine + S::kSums + D + c * 32, y);
+        for (int c = s * (D / 2); c < (s + 1) * (D / 2); c += 16) {
+          float x[16] = {}, y[16] = {};
+          if (has0) tmem_ld16(tmem + mine + S::kSums + c, x);
+          if (has1) tmem_ld16(tmem + mine + S::kSums + D + c, y);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (f0 * x[i] + f1 * y[i]) * inv;
-          if (any_bad)
-            for (int w = 0; w < 4; ++w)
-              for (uint32_t left = bad[w] & (w == 0 ? seen.w[0] : w == 1 ? seen.w[1] : w == 2 ? seen.w[2] : seen.w[3]);
-                   left; left &= left - 1) {
-                const int64_t off = slot_offset(a.c, cur.b, cur.span.context + w * 32 + __ffs(left) - 1);
-                if (off < 0) continue;
-                const T* from = values + off + kvh * a.c.stride_head + c * 32;
+          for (int i = 0; i < 16; ++i) x[i] = (f0 * x[i] + f1 * y[i]) * inv;
+          if (node < 0) continue;
+          if (whole) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (bad16<T>(reinterpret_cast<const uint16_t*>(from)[i])) x[i] += to_f32(from[i]);
-              }
-          if (node >= 0) {
-            if (whole) {
+            for (int i = 0; i < 16; i += 8)
+              *reinterpret_cast<uint4*>(out + c + i) =
+                  empty ? uint4{0, 0, 0, 0}
+                        : uint4{pack2(T(), x[i], x[i + 1]), pack2(T(), x[i + 2], x[i + 3]),
+                                pack2(T(), x[i + 4], x[i + 5]), pack2(T(), x[i + 6], x[i + 7])};
+          } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(out + c * 32 + i) =
-                    empty ? uint4{0, 0, 0, 0}
-                          : uint4{pack2(T(), x[i], x[i + 1]), pack2(T(), x[i + 2], x[i + 3]),
-                                  pack2(T(), x[i + 4], x[i + 5]), pack2(T(), x[i + 6], x[i + 7])};
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) __stcg(part + (c * 32 + i) * 128 + row, x[i]);
-            }
+            for (int i = 0; i < 16; ++i) __stcg(part + (c + i) * 128 + row, x[i]);
           }
         }
+        // Values that are not finite, where they are seen: whatever is finite
+        // adds nothing to them, so what is written already serves.
+        if (any_bad && node >= 0 && !empty)
+#pragma unroll 1
+          for (int nd = 0; nd <= node; ++nd) {
+            if (!(bad[nd / 32] >> (nd % 32) & 1) || !(seen_word(seen, nd / 32) >> (nd % 32) & 1)) continue;
+            const int64_t off = slot_offset(a.c, cur.b, cur.span.context + nd);
+            if (off < 0) continue;
+            const T* from = values + off + kvh * a.c.stride_head;
+#pragma unroll 1
+            for (int c = s * (D / 2); c < (s + 1) * (D / 2); ++c) {
+              if (!bad16<T>(reinterpret_cast<const uint16_t*>(from)[c])) continue;
+              if (whole) {
+                out[c] = from_f32<T>(to_f32(out[c]) + to_f32(from[c]));
+              } else {
+                __stcg(part + c * 128 + row, __ldcg(part + c * 128 + row) + to_f32(from[c]));
+              }
+            }
+          }
         tc_fence_before();
         if (node >= 0 && s == 0) {
           if (whole) {
