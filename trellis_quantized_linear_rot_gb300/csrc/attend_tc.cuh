@@ -300,6 +300,7 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
   auto bar = [&](int i) { return smem_u32(&sh.bars[i]); };
   if (base & 1023) {   // the swizzled tiles need it; there is no static shared memory before them
     if (tid == 0) atomicOr(a.c.err, kErrWait);
+    chain();
     return;
   }
 

@@ -265,7 +265,7 @@ __device__ void join_parts(const AttendArgs& a, const Line& line, const Rows& w,
 // once, and this thread joins kColumns columns from c0 on of row tid % 128.
 template <typename T, int D, int kColumns, int kGroup, int kThreads>
 __device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, int b, int kvh, int row0, int rows,
-                         int c0, int first, int nt, bool idle) {
+                         int c0, int first, int nt, bool idle, int up) {
   constexpr int kGroups = kThreads / 128;
   __shared__ float others[kGroups > 1 ? kGroups - 1 : 1][kGroups > 1 ? kColumns + 2 : 1][128];
   const int r = threadIdx.x % 128, g = threadIdx.x / 128;
@@ -324,7 +324,6 @@ __device__ void join_row(const AttendArgs& a, const Line& line, const Rows& w, i
   }
   if (r >= rows) return;
   const RowOf ro = row_of(a, kvh, row0 + r);
-  const int up = a.parents[b * a.stride_parents + ro.node];
   const bool empty = idle || up < -1 || up >= ro.node || l == 0.f;
   const float inv = empty ? 0.f : 1.f / l;
   const size_t at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;
@@ -351,11 +350,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
   constexpr int kWarps = kThreads / 32;
   __shared__ int scratch[2 * kWarps + 6];
   __shared__ int sums[2][kWarps];
-  chain();
   const int tid = threadIdx.x, team = blockIdx.x / row_blocks;
   const Rows w{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
   Line line;
-  Cursor cur;
+  Cursor cur = {};
   int p0 = 0, n = 1;
   if (gridDim.x == runs * row_blocks) {
     if (find_run<kTile, kGap, kThreads>(a, runs, team, scratch, &line, &cur) && cur.t > 0) {
@@ -384,13 +382,18 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     p0 = line.run_of(cur.first);
     n = line.run_of(cur.first + cur.nt - 1) - p0 + 1;
   }
-  if (n == 1) return;   // whole, or another block's
   const int first = cur.first, nt = cur.nt, b = cur.b, kvh = cur.item, row0 = w.rb * block_rows;
   const int rows = min(block_rows, a.nodes * a.group - row0);
   const Span span = cur.span;
+  const int my_row = kRows == 128 ? tid % 128 : blockIdx.y;
+  const int up = n > 1 && my_row < rows ? __ldcg(a.parents + b * a.stride_parents + (row0 + my_row) / a.group) : -2;
+  // Lengths and parents (from L2) are older than the main launch, which let
+  // this one begin only after its own wait for what came before it.
+  chain();
+  if (n == 1) return;   // whole, or another block's
   if constexpr (kRows == 128) {
     join_row<T, D, kColumns, kGroup, kThreads>(a, line, w, b, kvh, row0, rows, blockIdx.y * kColumns, first, nt,
-                                               span.context < 0);
+                                               span.context < 0, up);
   } else {
     constexpr int kLanes = D / 4, kGroups = kThreads / kLanes, kAhead = 6;
     constexpr size_t kPart = kPartFloats<kRows, D>;
@@ -439,7 +442,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
       l += f * ls[k], o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
     }
     const RowOf ro = row_of(a, kvh, row0 + r);
-    const int up = a.parents[b * a.stride_parents + ro.node];
     const bool empty = span.context < 0 || up < -1 || up >= ro.node || l == 0.f;
     const float inv = empty ? 0.f : 1.f / l;
     const size_t out_at = (static_cast<size_t>(b) * a.nodes + ro.node) * a.heads + ro.head;

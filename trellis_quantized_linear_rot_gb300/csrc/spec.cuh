@@ -25,8 +25,8 @@ __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// First instructions of a kernel launched by launch_chained: wait for the
-// kernel before it, and let the next one be set up.
+// In every thread of a kernel launched by launch_chained: waits for the kernel
+// before it, and lets the next one be set up.
 __device__ __forceinline__ void chain() {
   pdl_wait_prerequisites();
   pdl_launch_dependents();
@@ -69,7 +69,7 @@ struct Span {
   int context, slots;  // -1, 0 for an idle sequence
 };
 __device__ __forceinline__ Span sequence_span(const CacheView& c, int b, int nodes) {
-  const int len = c.lengths[b], cap = slot_capacity(c);
+  const int len = __ldcg(c.lengths + b), cap = slot_capacity(c);
   if (len < 0) return {-1, 0};
   if (len <= cap - nodes) return {len, len + nodes};
   record_index_error(c.err);

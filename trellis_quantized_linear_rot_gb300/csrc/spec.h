@@ -89,8 +89,9 @@ struct VerifyArgs {
 size_t verify_workspace_bytes(int batch, int nodes, int num_sms);
 
 // Launches with programmatic stream serialisation: the kernel may be set up
-// while the one before it still runs, and waits for it with its first
-// instruction (every thread of every kernel launched this way does).
+// while the one before it still runs. Every thread of every kernel launched
+// this way waits for that one (chain()) before it returns, and before it
+// touches anything that one may write, or writes anything that one may read.
 template <typename... P, typename... A>
 cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream,
                            A&&... args) {
