@@ -1,7 +1,8 @@
 """GB300 (sm_103a) trellis-quantized projection for decode rows.
 
-A thin Python binding over the C ABI of libtf_exl3.so (include/tf_exl3.h),
-with the same names. It only marshals arguments: every step of the
+A thin Python binding over the C ABI of libtf_exl3.so (include/tf_exl3.h;
+include/tf_spec.h for the operators on drafted tokens, in spec.py), with the
+same names. It only marshals arguments: every step of the
 computation runs in the library's CUDA kernels. PyTorch provides device
 memory and streams. There is no CPU fallback: a missing library raises.
 

@@ -18,6 +18,10 @@
 // row follows the decisions from node 0 and writes the outputs. With more, a
 // cluster takes a sequence and walks down its tree, so that only the rows on
 // the accepted path are read.
+//
+// 8 chains of 8 rows of 129,280 in bf16 with a draft: 43 us (2 blocks a row;
+// 1.3 instructions a cycle, waits for loads and for the cluster in between).
+// 32 trees of 16 rows in fp32: 70 us, 79 MB of 265 read.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -660,11 +664,18 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
   cluster.sync();     // no block leaves while another may still write to its shared memory
 }
 
+// More rows than SMs are walked through. us, all rows together and walked
+// (vocabulary 129,280): fp32 without a draft 8 x 8 rows 21 and 30, 32 x 4 34
+// and 44, 32 x 16 117 and 69; bf16 with a draft, chains 8 x 8 43 and 91, 16 x 8
+// 72 and 98, 8 x 16 73 and 181, trees 8 x 8 50 and 61, 16 x 8 128 and 66, 32 x
+// 16 179 and 104. (Trees ask more children a node and end sooner; which it is
+// only the device knows.)
 bool walks(int batch, int nodes, int num_sms) { return static_cast<int64_t>(batch) * nodes > num_sms; }
 
 template <typename T>
 cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t s) {
-  // One block an SM: as many blocks for a cluster as leave every cluster its place.
+  // One block an SM: as many blocks for a cluster as leave every cluster its
+  // place. One row of fp32: 11 us with 8 blocks, 13 with 4, 17 with 2.
   const int64_t rows = static_cast<int64_t>(a.batch) * a.nodes;
   const bool walk = walks(a.batch, a.nodes, a.num_sms);
   const int64_t clusters = walk ? a.batch : rows;
