@@ -392,23 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
   for (int node = kWalk ? 0 : id - b * a.nodes; node >= 0;) {
     Row<T> p{static_cast<const T*>(a.logits) + b * a.seq + node * a.node, a.inv_temp, 0.f};
     Row<T> q{draft ? static_cast<const T*>(a.draft) + b * a.draft_seq + node * a.draft_node : p.x, a.inv_temp, 0.f};
-    bool child = false;
     const float u_node = a.greedy ? 0.f : a.u_sample[row0 + node];
+    // Of the tree's node tid; on their way during the first pass.
+    int parent = -2, drafted = -1;
+    float u_child = 0.f;
     if (tid < a.nodes) {
-      int up = a.parents[b * a.stride_parents + tid];
-      const int t = a.tokens[row0 + tid];
-      if (up >= tid) {
-        if (tid == node) record_index_error(a.err);
-        up = -2;
-      }
-      child = up == node && tid > node && t >= 0 && t < a.vocab;
-      s.par[tid] = tid == node ? up : (child ? node : -2);   // children that may be asked, and the row's own
-      s.tok[tid] = t;
-      if (draft) s.u[tid] = a.u_accept[row0 + tid];
-      if (child) {
-        s.zp[tid] = p.z(p.x[t]);
-        s.zq[tid] = q.z(q.x[t]);
-      }
+      parent = a.parents[b * a.stride_parents + tid];
+      drafted = a.tokens[row0 + tid];
+      if (draft) u_child = a.u_accept[row0 + tid];
     }
 
     // This warp's vectors of each row.
@@ -421,6 +412,19 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     if (draft && tid == 0) prefetch_part(q.x);
     Largest<T> most;
     sweep<8>(p, a.vocab, v0, v1, [&](int, const T(&x)[kVec]) { most.add(x); });
+    bool child = false;
+    float z_child = 0.f, zq_child = 0.f;
+    if (tid < a.nodes) {
+      if (parent >= tid) {
+        if (tid == node) record_index_error(a.err);
+        parent = -2;
+      }
+      child = parent == node && tid > node && drafted >= 0 && drafted < a.vocab;
+      s.par[tid] = tid == node ? parent : (child ? node : -2);   // children that may be asked, and the row's own
+      s.tok[tid] = drafted;
+      s.u[tid] = u_child;
+      if (child && draft) z_child = p.z(p.x[drafted]), zq_child = q.z(q.x[drafted]);
+    }
     const bool ask = __syncthreads_or(child) && draft;   // a leaf has no use for the draft's row
     float top = __fmul_rn(most.get(), a.inv_temp);
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -483,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
         goal_total = mass;
       }
       if (ask) {
+        if (child) s.zp[tid] = z_child, s.zq[tid] = zq_child;
         unsigned long long unused;
         const unsigned long long q_sum = q.top == -INFINITY ? 0
                                          : q.top < INFINITY ? sum_weights<T, true>(q, a.vocab, q0, q1v)
@@ -557,8 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
       mine = false;
       const bool here = goal >= before && goal < before + s.sums[kWarps];
       if (here) {
-        int w = 0;
-        while (goal >= before + s.sums[w + 1]) ++w;
+        const int w = __ffs(__ballot_sync(~0u, lane < kWarps && goal < before + s.sums[min(lane, kWarps - 1) + 1])) - 1;
         unsigned long long run = before + s.sums[w];
         int lo, hi;
         part_of(p.vectors(a.vocab), &lo, &hi, w);
@@ -583,6 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
         };
         unsigned long long sum = 0;
         for (int v = lo + lane; v < hi; v += 32) sum += weigh(v);
+        const bool once = hi - lo <= 32;   // then this lane's weights are still there
+        const unsigned long long first = sum;
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
         if (lane == 0) s.fine[warp] = sum;
         __syncthreads();
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
         mine = goal >= run && goal < run + s.fine[warp];
         if (mine) {
           for (int v = lo; v < hi; v += 32) {
-            const unsigned long long own = v + lane < hi ? weigh(v + lane) : 0;
+            const unsigned long long own = once ? first : v + lane < hi ? weigh(v + lane) : 0;
             unsigned long long upto = own;
             for (int o = 1; o < 32; o *= 2) {
               const unsigned long long z = __shfl_up_sync(~0u, upto, o);
@@ -620,9 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
       z_token = p.z(p.x[token]);
     }
     if (mine) {
-      if (!draft && token >= 0)
-        for (int c = a.nodes - 1; c > node; --c)
-          if (s.par[c] == node && s.tok[c] == token) next = c;
+      if (!draft && token >= 0)   // the first child with that token
+        for (int c0 = 0; c0 < a.nodes && next < 0; c0 += 32) {
+          const int c = c0 + lane;
+          const unsigned hit = __ballot_sync(~0u, c > node && c < a.nodes && s.par[c] == node && s.tok[c] == token);
+          if (hit) next = c0 + __ffs(hit) - 1;
+        }
       if (lane == 0) {
         const float logprob = token < 0 ? 0.f
                                         : __fsub_rn(z_token, p.top) -
