@@ -221,6 +221,35 @@ def test_attention_a_siblings_bad_row_stays_its_own(fill, group, d):
         assert torch.isnan(got[0, hit]).all() and torch.isnan(got_l[0, hit]).all()
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,group", [(3, 2), (4, 5), (40, 4)])
+def test_attention_weights_over_the_whole_range(dtype, d, n, group):
+    """Scores from the maximum down to weights that vanish, in shuffled slots:
+    every place of a tile meets large, small and vanished weights. An infinite
+    key's score of -inf is a weight of 0, as that of -160 is in fp32."""
+    ln = 700
+    c = Case(dtype, [ln], n, 1, group, d, 16, seed=12)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    score = (torch.randint(-640, 1, (ln + n,), device="cuda", generator=g) / 4).to(c.k.dtype)
+    score[::7] = score[::7] / 8
+    score[3::50] = -160.0
+    score[0] = 0.0
+    score[ln:] = -1.0
+    s = torch.arange(ln + n, device="cuda")
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.k[c.table[0].long()[s // 16], s % 16] = 0.0
+    c.k[c.table[0].long()[s // 16], s % 16, :, 0] = score[:, None]
+    par = [tree("tree", n, np.random.default_rng(1))]
+    want, want_l = c.check(par, scale=1.0)
+    score[3::50] = -float("inf")
+    score[ln:] = -1.0
+    c.k[c.table[0].long()[s // 16], s % 16, :, 0] = score[:, None]
+    got, got_l = tf.tf_tree_attention(c.q, c.k, c.v, c.table, c.lengths, i32(par), scale=1.0)
+    assert torch.equal(got, want) and torch.equal(got_l, want_l)
+
+
 def test_attention_rising_and_falling_scores():
     """Scores that climb or fall by hundreds along the context: the running
     maximum has to move, and early or late parts vanish."""

@@ -121,20 +121,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) 
 }
 
 // 2^x for two x of at most 8 in multiply-adds: 2^n of the nearest whole n, by
-// its exponent bits, times a polynomial of degree 4 in the rest f, |f| <= 1/2
-// (fitted for the least largest relative error, 2.6e-6, far below the
-// rounding of the weights). 0 below -127, NaN for NaN.
+// its exponent bits, times a polynomial of degree 5 in the rest f, |f| <= 1/2
+// (fitted for the least largest relative error, 1.6e-7 with the coefficients
+// in fp32: as near as ex2.approx). 0 below -127, NaN for NaN.
 __device__ __forceinline__ float2 exp2_by_fma(float2 x) {
   constexpr float kWhole = 12582912.f;   // 1.5 * 2^23: added, it leaves n in the low bits
   asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));   // -127
   asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
   const float2 t = add2(x, float2{kWhole, kWhole}), n = add2(t, float2{-kWhole, -kWhole});
   const float2 f = fma2(n, float2{-1.f, -1.f}, x);
-  float2 p = fma2(f, float2{0.009570102207362652f, 0.009570102207362652f},
-                  float2{0.05591785907745361f, 0.05591785907745361f});
-  p = fma2(p, f, float2{0.240247443318367f, 0.240247443318367f});
-  p = fma2(p, f, float2{0.6931217908859253f, 0.6931217908859253f});
-  p = fma2(p, f, float2{0.9999992847442627f, 0.9999992847442627f});
+  float2 p = fma2(f, float2{0.0013276472454890609f, 0.0013276472454890609f},
+                  float2{0.009675540961325169f, 0.009675540961325169f});
+  p = fma2(p, f, float2{0.05550713092088699f, 0.05550713092088699f});
+  p = fma2(p, f, float2{0.24022120237350464f, 0.24022120237350464f});
+  p = fma2(p, f, float2{0.6931469440460205f, 0.6931469440460205f});
+  p = fma2(p, f, float2{1.0000001192092896f, 1.0000001192092896f});
   const uint32_t one = 0x3F800000u;
   return mul2(p, float2{__uint_as_float((__float_as_uint(t.x) << 23) + one),
                         __uint_as_float((__float_as_uint(t.y) << 23) + one)});
