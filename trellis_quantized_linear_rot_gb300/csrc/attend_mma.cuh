@@ -117,7 +117,8 @@ struct MmaShape {
 };
 
 template <typename T, int D, int kRowWarps>
-__global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(128, D == 256 ? 1 : 2)
+tree_attention_mma_kernel(const __grid_constant__ AttendArgs a) {
   using S = MmaShape<D, kRowWarps>;
   constexpr int kThreads = S::kThreads, kRows = S::kRows, kTile = S::kTile, kStages = S::kStages;
   constexpr int kKeys = kTile / S::kKeyWarps;   // keys of a tile a warp takes
@@ -480,7 +481,8 @@ __global__ void __launch_bounds__(128, D == 256 ? 1 : 2) tree_attention_mma_kern
           for (int e = 0; e < D / 8; ++e) {
             const int col = e * 8 + (lane % 4) * 2;
             if (whole)
-              *reinterpret_cast<uint32_t*>(out + col) = inv == 0.f ? 0u : pack2(T(), o[e][2 * x] * inv, o[e][2 * x + 1] * inv);
+              *reinterpret_cast<uint32_t*>(out + col) =
+                  inv == 0.f ? 0u : pack2(T(), o[e][2 * x] * inv, o[e][2 * x + 1] * inv);
             else
               *reinterpret_cast<float2*>(part + rl * D + col) = float2{o[e][2 * x], o[e][2 * x + 1]};
           }

@@ -238,7 +238,8 @@ __device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, 
 // a wait that passes over a phase cannot tell it from the next but one).
 constexpr int kTcSlots = 6;
 enum TcBarrier { kQFull, kQEmpty, kKFull, kKEmpty = kKFull + kTcSlots, kVFull = kKEmpty + kTcSlots,
-                 kVEmpty = kVFull + kTcSlots, kSFull = kVEmpty + kTcSlots, kPFull = kSFull + 2, kPHalf = kPFull + 2, kPvDone = kPHalf + 2,
+                 kVEmpty = kVFull + kTcSlots, kSFull = kVEmpty + kTcSlots, kPFull = kSFull + 2,
+                 kPHalf = kPFull + 2, kPvDone = kPHalf + 2,
                  kBarriers = kPvDone + 2 };
 
 struct TcShared {
@@ -428,8 +429,10 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
     }
     if (vs.j < n_tiles) {   // given up: the copies in flight still have to land
       volatile int never = 0;
-      for (int j = max(0, ks.j - kStages); j < ks.j; ++j) mbar_wait(bar(kKFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
-      for (int j = max(0, vs.j - kStages); j < vs.j; ++j) mbar_wait(bar(kVFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
+      for (int j = max(0, ks.j - kStages); j < ks.j; ++j)
+        mbar_wait(bar(kKFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
+      for (int j = max(0, vs.j - kStages); j < vs.j; ++j)
+        mbar_wait(bar(kVFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
     }
   } else if (warp == 3) {
     // ----------------------------------------------------------- copies of q

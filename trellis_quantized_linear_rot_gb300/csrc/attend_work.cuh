@@ -85,14 +85,44 @@ __device__ __forceinline__ void advance(const AttendArgs& a, Cursor* c) {
 
 // Block-wide: the line, run number `run` of at most `most`, the cursor at its
 // begin and its number of tiles (0: nothing to do, the cursor is not set).
-// `scratch` has room for 2 * (kThreads / 32) + 6 ints. Batches of up to
-// kThreads sequences are scanned once, larger ones twice (length, then place).
+// `scratch` has room for 2 * (kThreads / 32) + 6 ints. Batches of up to 32
+// sequences are scanned by every warp for itself, without meeting; of up to
+// kThreads once by the block; larger ones twice (length, then place).
 template <int kTile, int kGap, int kThreads>
 __device__ int find_run(const AttendArgs& a, int most, int run, int* scratch, Line* line, Cursor* cur) {
   const int items = a.c.kv_heads;
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int batch = a.c.batch;
+  if (batch <= 32) {
+    const Span span = lane < batch ? sequence_span(a.c, lane, a.nodes) : Span{};
+    const int nt = lane < batch ? tiles_of<kTile>(span) : 0, places = lane < batch ? nt + kGap : 0;
+    int upto = places * items, tiles = nt * items;
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(~0u, upto, o), z = __shfl_up_sync(~0u, tiles, o);
+      if (lane >= o) upto += y, tiles += z;
+    }
+    const int from = upto - places * items;
+    line->cut(__shfl_sync(~0u, upto, 31), most, run);
+    if (line->begin >= line->end) return 0;
+    // The sequences that begin and end lie in, their items and places in those.
+    const int b = __ffs(__ballot_sync(~0u, line->begin < upto)) - 1;
+    const int last = __ffs(__ballot_sync(~0u, line->end <= upto)) - 1;
+    const int nt_b = __shfl_sync(~0u, nt, b), nt_last = __shfl_sync(~0u, nt, last);
+    const int in_b = line->begin - __shfl_sync(~0u, from, b), in_last = line->end - __shfl_sync(~0u, from, last);
+    const int item = in_b / (nt_b + kGap), t = in_b - item * (nt_b + kGap);
+    const int item_last = in_last / (nt_last + kGap), t_last = in_last - item_last * (nt_last + kGap);
+    const int before = __shfl_sync(~0u, tiles - nt * items, b) + item * nt_b + min(t, nt_b);
+    const int n = __shfl_sync(~0u, tiles - nt * items, last) + item_last * nt_last + min(t_last, nt_last) - before;
+    if (n == 0) return 0;
+    const Span own{__shfl_sync(~0u, span.context, b), __shfl_sync(~0u, span.slots, b)};
+    *cur = Cursor{b, item, t, nt_b, line->begin - t, own};
+    if (t >= nt_b) {   // in a gap: on to the next item
+      cur->t = nt_b - 1;
+      advance<kTile, kGap>(a, cur);
+    }
+    return n;
+  }
   // Sequence of the run's begin, its first place; tiles before begin and end;
   // the sequence's span.
   int* found = scratch + 2 * kWarps;
@@ -190,8 +220,8 @@ __device__ __forceinline__ RowOf row_of(const AttendArgs& a, int kvh, int r) {
 // `first` (nt tiles) and writes its rows, which start at row0 of its kv head.
 // Parts are added in run order.
 template <typename T, int kRows, int D, int kThreads>
-__device__ void join_parts(const AttendArgs& a, const Line& line, const Rows& w, int b, int kvh, int row0, int rows, int first,
-                           int nt, bool idle, int tid) {
+__device__ void join_parts(const AttendArgs& a, const Line& line, const Rows& w, int b, int kvh, int row0,
+                           int rows, int first, int nt, bool idle, int tid) {
   constexpr size_t kPart = kPartFloats<kRows, D>;
   const int p0 = line.run_of(first), n = line.run_of(first + nt - 1) - p0 + 1;
   // Every part but the first is the one its run begins with.
@@ -457,8 +487,8 @@ template <typename T, int kRows, int D, int kTile, int kGap, int kColumns, int k
 cudaError_t launch_join_as(const AttendArgs& a, int runs, int row_blocks, int block_rows, cudaStream_t s) {
   const dim3 grid(std::min(a.c.batch * a.c.kv_heads, runs) * row_blocks,
                   kRows == 128 ? D / kColumns : std::min(block_rows, a.nodes * a.group));
-  return launch_chained(join_kernel<T, kRows, D, kTile, kGap, kColumns, kGroup, kThreads>, grid, dim3(kThreads), 0, 1, s,
-                        a, row_blocks, block_rows, runs);
+  return launch_chained(join_kernel<T, kRows, D, kTile, kGap, kColumns, kGroup, kThreads>, grid, dim3(kThreads), 0, 1,
+                        s, a, row_blocks, block_rows, runs);
 }
 
 // Parts of an item where the lengths are alike: its share of the runs, or its

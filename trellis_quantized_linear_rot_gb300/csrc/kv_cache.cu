@@ -96,9 +96,10 @@ cudaError_t launch_kv_write(const CacheView& c, void* k, void* v, const void* k_
                             int64_t node, int64_t head, int nodes, cudaStream_t s) {
   const int64_t total = static_cast<int64_t>(c.batch) * nodes * c.kv_heads * (c.head_dim / 8);
   const int64_t blocks = (total + kThreads - 1) / kThreads;
-  return launch_chained(kv_write_kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0,
-                        1, s, c, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v),
-                        static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new), seq, node, head, nodes);
+  const dim3 grid(static_cast<unsigned>(blocks < 65536 ? blocks : 65536));
+  return launch_chained(kv_write_kernel, grid, dim3(kThreads), 0, 1, s, c, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v),
+                        static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new), seq, node, head,
+                        nodes);
 }
 
 cudaError_t launch_kv_keep(const CacheView& c, void* k, void* v, const int32_t* path, const int32_t* counts,

@@ -165,7 +165,8 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.partials_at);
   a.num_sms = sms;
   a.join_later = 0;
-  return launched(launch_tree_attention(a, cache->dtype, device, static_cast<cudaStream_t>(stream)), "tree attention launch");
+  return launched(launch_tree_attention(a, cache->dtype, device, static_cast<cudaStream_t>(stream)),
+                  "tree attention launch");
 }
 
 size_t tf_verify_draft_workspace_bytes(int batch, int nodes) {

@@ -153,7 +153,8 @@ AttendWorkspace attend_workspace(int nodes, int heads, int kv_heads, int head_di
   const size_t wide = std::max<size_t>(num_sms, nodes) * 2;
   AttendWorkspace w;
   w.partials_at = (2 * places * sizeof(int) + 255) & ~static_cast<size_t>(255);
-  w.bytes = w.partials_at + 2 * (rows <= kFewRows ? places * 16 : std::max(blocks, wide) * 64) * (head_dim + 2) * sizeof(float);
+  const size_t part_rows = rows <= kFewRows ? places * 16 : std::max(blocks, wide) * 64;
+  w.bytes = w.partials_at + 2 * part_rows * (head_dim + 2) * sizeof(float);
   return w;
 }
 

@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
               const float ep = isnan(s.zp[c]) ? 0.f : p.e(s.zp[c]);
               const float eq = isnan(s.zq[c]) || q.top == -INFINITY ? 0.f : q.e(s.zq[c]);
               const float qt = __fmul_rn(eq, static_cast<float>(q1));
-              const double rt = refused ? static_cast<double>(s.rest(ep, eq)) : static_cast<double>(__fmul_rn(ep, s.rest.cp));
+              const double rt =
+                  refused ? static_cast<double>(s.rest(ep, eq)) : static_cast<double>(__fmul_rn(ep, s.rest.cp));
               if (static_cast<double>(s.u[c]) * static_cast<double>(qt) * left < rt * kHalfUnit) {
                 s.verdict = c;
               } else {
