@@ -50,7 +50,8 @@ class Sim:
         self.k_full, self.k_empty = [Barrier(1) for _ in range(n)], [Barrier(1) for _ in range(n)]
         self.v_full, self.v_empty = [Barrier(1) for _ in range(n)], [Barrier(1) for _ in range(n)]
         self.q_full, self.q_empty = Barrier(1), Barrier(2)
-        self.s_full, self.p_half, self.p_full, self.pv_done = ([Barrier(1), Barrier(1)] for _ in range(4))
+        self.s_full, self.p_half, self.p_three, self.p_full, self.pv_done = (
+            [Barrier(1), Barrier(1)] for _ in range(5))
         self.k, self.v = [None] * STAGES, [None] * STAGES   # tile whose data a stage holds
         self.q, self.k_issued = None, 0
         self.scores = [None, None]
@@ -107,6 +108,7 @@ class Sim:
                 self.queues[s] += todo
                 yield self.v_full[self.number(j)], self.phase(j)
                 yield self.p_half[s], n & 1
+                yield self.p_three[s], n & 1
                 yield self.p_full[s], n & 1
                 if self.v[j % STAGES] != j:
                     raise Fault("sums of tile %d from %s" % (j, self.v[j % STAGES]))
@@ -127,6 +129,8 @@ class Sim:
                 if self.scores[s] != j or self.v[j % STAGES] != j:
                     raise Fault("weights of tile %d from %s, %s" % (j, self.scores[s], self.v[j % STAGES]))
                 self.p_half[s].arrive()
+                yield None
+                self.p_three[s].arrive()
                 yield None
                 self.p_full[s].arrive()
                 n += 1

@@ -151,7 +151,7 @@ def test_attention_long_context_is_split_and_joined(n):
     Case("fp16", [7000, 3], n, 1, 5, 64, 16, seed=6).check([tree("tree", n, rng), tree("star", n, rng)])
 
 
-@pytest.mark.parametrize("b,n", [(300, 1), (129, 6), (700, 2)])
+@pytest.mark.parametrize("b,n", [(300, 1), (129, 6), (700, 2), (32, 1), (33, 12), (100, 2), (400, 12)])
 def test_attention_large_batches(b, n):
     """More sequences than a block scans at once, lengths of all kinds."""
     rng = np.random.default_rng(b)
