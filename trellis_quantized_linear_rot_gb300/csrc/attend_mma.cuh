@@ -11,7 +11,7 @@
 // different rows.
 //
 // 32 tokens of 8 x 5 heads of 128 over up to 8,192 slots: 115 us for 684 MB,
-// 5.9 TB/s, 0.87 of a copy's rate. One token over 300 slots: 9.1 us, all of it
+// 5.9 TB/s, 0.87 of a copy's rate. One token over 300 slots: 8.7 us, all of it
 // latency (lengths, page numbers, keys, the join, one after the other).
 //
 // Softmax in units of log 2: p = 2^(s - m), s = (q . k) scale log2(e).

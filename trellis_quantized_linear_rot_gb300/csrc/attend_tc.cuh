@@ -9,9 +9,9 @@
 //
 // One block an SM, a run of tiles for each team of blocks, one block for each
 // block of rows: whole nodes with at most 128 rows (attend_work.cuh). An
-// item's key tiles go alternately to two streams, each with its own scores, weights,
-// sums and running maximum in Tensor Memory and registers, so that one
-// stream's products run while the other's exponentials do:
+// item's key tiles go alternately to two streams, each with its own scores,
+// weights, sums and running maximum in Tensor Memory and registers, so that
+// one stream's products run while the other's exponentials do:
 //   warp 0        copies of keys and values, a box for each page or part of
 //                 one, three tiles in flight
 //   warps 1, 2    products of stream 0 and 1: S = Q K^T into Tensor Memory;
@@ -28,12 +28,12 @@
 // parts: 53.7 us for 52.2). All waits are bounded.
 //
 // Measured, 8 kv heads of 128: 16 trees of 16 nodes x 6 heads over up to 4,096
-// slots 46.2 us (179 MB, 3.9 TB/s); one tree of 64 x 5 over 50,001 slots 76.9
-// us (65.6 GFLOP, 0.85 PFLOP/s, tensor pipe 47% active). A
-// stream's tile goes round in 3,700 cycles: 1,800 of weights, the products'
-// 1,000 and as much again waiting for the other stream's products and for
-// barriers. Two groups of 128 threads for a stream, half a row each, took
-// longer (93 us): instructions issued, not registers, bound the weights.
+// slots 45.4 us (179 MB, 3.9 TB/s); one tree of 64 x 5 over 50,001 slots 76.1
+// us (65.6 GFLOP, 0.86 PFLOP/s, tensor pipe 47% active). A stream's tile goes
+// round in 4,000 cycles: 1,750 of weights (380 the maximum, 1,030 exponentials
+// and packing), the rest the products and what they wait for the other
+// stream's. Two groups of 128 threads for a stream, half a row each, took
+// longer (93 us).
 #pragma once
 
 #include "attend_mma.cuh"

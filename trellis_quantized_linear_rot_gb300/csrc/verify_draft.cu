@@ -19,9 +19,9 @@
 // cluster takes a sequence and walks down its tree, so that only the rows on
 // the accepted path are read.
 //
-// 8 chains of 8 rows of 129,280 in bf16 with a draft: 43 us (2 blocks a row;
+// 8 chains of 8 rows of 129,280 in bf16 with a draft: 42 us (2 blocks a row;
 // 1.3 instructions a cycle, waits for loads and for the cluster in between).
-// 32 trees of 16 rows in fp32: 70 us, 79 MB of 265 read.
+// 32 trees of 16 rows in fp32: 65 us, 78 MB of 265 read.
 #include <cooperative_groups.h>
 
 #include <type_traits>
