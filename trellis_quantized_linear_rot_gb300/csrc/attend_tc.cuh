@@ -120,37 +120,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) 
       : "memory");
 }
 
-// 2^x for two x of at most 8 in multiply-adds: 2^n of the nearest whole n, by
-// its exponent bits, times a polynomial of degree 5 in the rest f, |f| <= 1/2
-// (fitted for the least largest relative error, 1.6e-7 with the coefficients
-// in fp32: as near as ex2.approx). 0 below -127, NaN for NaN.
-__device__ __forceinline__ float2 exp2_by_fma(float2 x) {
-  constexpr float kWhole = 12582912.f;   // 1.5 * 2^23: added, it leaves n in the low bits
-  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));   // -127
-  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
-  const float2 t = add2(x, float2{kWhole, kWhole}), n = add2(t, float2{-kWhole, -kWhole});
-  const float2 f = fma2(n, float2{-1.f, -1.f}, x);
-  float2 p = fma2(f, float2{0.0013276472454890609f, 0.0013276472454890609f},
-                  float2{0.009675540961325169f, 0.009675540961325169f});
-  p = fma2(p, f, float2{0.05550713092088699f, 0.05550713092088699f});
-  p = fma2(p, f, float2{0.24022120237350464f, 0.24022120237350464f});
-  p = fma2(p, f, float2{0.6931469440460205f, 0.6931469440460205f});
-  p = fma2(p, f, float2{1.0000001192092896f, 1.0000001192092896f});
-  const uint32_t one = 0x3F800000u;
-  return mul2(p, float2{__uint_as_float((__float_as_uint(t.x) << 23) + one),
-                        __uint_as_float((__float_as_uint(t.y) << 23) + one)});
-}
-
-// One pair of weights in kFmaEvery is made by multiply-adds, so that the
-// exponential units hold the two streams up less where they come at once. us
-// with none, one in 16, 8 and 4: 16 trees of 16 nodes over 4,096 slots 49.4,
-// 48.0, 47.0, 47.2; 19 of 25 over up to 6,000 112.7, 110.8, 110.1, 110.7; one
-// of 64 over 50,001 79.0, 76.9, 78.5, 83.7 (instructions issued bound it).
-// With D = 64 the products are half as long, and none is best: 77.5, 78.6,
-// 81.4, 87.3.
-template <int D>
-constexpr int kFmaEvery = D == 128 ? 8 : 1 << 30;
-
 // One row of a tile, by its thread: from the scores (128 columns at `scores`)
 // to the weights over them, with the running maximum m and sum l. The sums
 // (D columns at `sums`) are rescaled where the maximum has risen by more than
@@ -162,10 +131,13 @@ template <typename T, int D, bool kCut>
 __device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, const uint32_t (&vis)[4], bool begun,
                                       uint32_t half, uint32_t three, float* m_row, float* l_row) {
   // The scores are read twice, in parts: all 128 of them and what is made of
-  // them do not fit a thread's registers.
+  // them do not fit a thread's registers. The loops are not unrolled further:
+  // the four roles' instructions together pass the cache for them (with all
+  // four parts unrolled a tree of 64 nodes over 50,001 slots took 76.1 us for
+  // 74.4, 16 trees of 16 over 4,096 45.7 for 44.6; with none 76.8 and 44.4).
   float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   auto word_of = [&](int c) { return c < 2 ? (c == 0 ? vis[0] : vis[1]) : (c == 2 ? vis[2] : vis[3]); };
-#pragma unroll(kCut ? 1 : 4)
+#pragma unroll(kCut ? 1 : 2)
   for (int c = 0; c < 4; ++c) {
     float v[32];
     tmem_ld32(scores + c * 32, v);
@@ -199,7 +171,7 @@ __device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, 
   if (rise) m = fmaxf(m, top);
   const float low = m == -INFINITY ? 0.f : -m;
   float2 sum[4] = {};
-#pragma unroll(kCut ? 1 : 4)
+#pragma unroll(kCut ? 1 : 2)
   for (int c = 0; c < 4; ++c) {
     float v[32];
     tmem_ld32(scores + c * 32, v);
@@ -208,12 +180,8 @@ __device__ __forceinline__ void weigh(uint32_t scores, uint32_t sums, float sc, 
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float2 x = fma2(float2{v[2 * i], v[2 * i + 1]}, float2{sc, sc}, float2{low, low});
-      if (!kCut && i % kFmaEvery<D> == kFmaEvery<D> - 1) {
-        x = exp2_by_fma(x);
-      } else {
-        x.x = exp2_approx(x.x);
-        x.y = exp2_approx(x.y);
-      }
+      x.x = exp2_approx(x.x);
+      x.y = exp2_approx(x.y);
       if (kCut) {
         if (!(word >> (2 * i) & 1)) x.x = 0.f;
         if (!(word >> (2 * i + 1) & 1)) x.y = 0.f;
