@@ -28,8 +28,8 @@
 // parts: 53.7 us for 52.2). All waits are bounded.
 //
 // Measured, 8 kv heads of 128: 16 trees of 16 nodes x 6 heads over up to 4,096
-// slots 45.4 us (179 MB, 3.9 TB/s); one tree of 64 x 5 over 50,001 slots 76.1
-// us (65.6 GFLOP, 0.86 PFLOP/s, tensor pipe 47% active). A stream's tile goes
+// slots 44.2 us (179 MB, 4.0 TB/s); one tree of 64 x 5 over 50,001 slots 74.4
+// us (65.6 GFLOP, 0.88 PFLOP/s, tensor pipe 50% active). A stream's tile goes
 // round in 4,000 cycles: 1,750 of weights (380 the maximum, 1,030 exponentials
 // and packing), the rest the products and what they wait for the other
 // stream's. Two groups of 128 threads for a stream, half a row each, took
