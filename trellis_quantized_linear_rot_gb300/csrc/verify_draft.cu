@@ -320,7 +320,12 @@ __device__ void arrive(const VerifyArgs& a, const Results& r, Shared& s, int b) 
 template <typename T, bool kWalk>
 __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ Shared s;
+  // A block's shared memory may be written by the others only once it runs:
+  // every block says so here, and hears it of all below, while the kernel
+  // before this one still ends.
+  cluster_arrive();
   chain();
+  cluster_wait();
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank(), id = blockIdx.x / ranks;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
