@@ -140,8 +140,8 @@ tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int
                           int nodes, int vocab, int32_t* counts, int32_t* path, int32_t* out_tokens,
                           float* logprobs, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace tf_verify_draft needs, 0 for sizes it refuses. The pages
- * have no counterpart. */
+/* Bytes of workspace tf_verify_draft needs for these sizes and any smaller
+ * ones, 0 for sizes it refuses. The pages have no counterpart. */
 size_t tf_verify_draft_workspace_bytes(int batch, int nodes);
 
 /*

@@ -690,6 +690,29 @@ def test_verify_same_bits_every_time_on_streams_and_in_a_graph(b, n, v, with_dra
     tf.tf_device_error()
 
 
+def test_verify_one_workspace_for_the_largest_and_all_smaller_sizes():
+    """A program that makes its workspace once, for its largest batch of
+    trees, verifies whatever part of it there is in a step."""
+    sizes = [(32, 16), (8, 16), (1, 24), (16, 9), (152, 1), (17, 9), (1, 1), (32, 16), (9, 16)]
+    ws = tf.tf_verify_draft_workspace(152, 24)
+    rng = np.random.default_rng(2)
+    for b, n in sizes:
+        x, _, g = logits_like(b, n, 500, "bf16", b + n)
+        par = i32([tree("tree", n, rng) for _ in range(b)])
+        tok = x.float().argmax(-1).int().roll(1, 1).contiguous()
+        us = torch.rand((b, n), device="cuda", generator=g)
+        want = tf.tf_verify_draft(x, tok, par, us, workspace=tf.tf_verify_draft_workspace(b, n))
+        got = tf.tf_verify_draft(x, tok, par, us, workspace=ws)
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), (b, n)
+    assert not ws.any()   # ready for the next call
+    # No smaller size needs more than a larger one.
+    need = [[tf.lib().tf_verify_draft_workspace_bytes(b, n) for n in (1, 2, 7, 16, 31, 128)]
+            for b in (1, 2, 8, 32, 151, 152, 153, 4000)]
+    assert all(x <= y for row in need for x, y in zip(row, row[1:]))
+    assert all(x <= y for r0, r1 in zip(need, need[1:]) for x, y in zip(r0, r1))
+    tf.tf_device_error()
+
+
 # -------------------------------------------------------- refusals, empties
 def test_empty_batches_launch_nothing():
     k = torch.zeros((2, 16, 1, 64), dtype=torch.float16, device="cuda")

@@ -24,6 +24,7 @@
 // 32 trees of 16 rows in fp32: 65 us, 78 MB of 265 read.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "spec.cuh"
@@ -703,8 +704,12 @@ cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+// Only calls that do not walk use it, with at most num_sms rows, and so at most
+// as many sequences. What any of them within these sizes needs, so that a
+// workspace made for the largest batch, which may walk, serves the smaller ones.
 size_t verify_workspace_bytes(int batch, int nodes, int num_sms) {
-  return walks(batch, nodes, num_sms) ? 256 : (3 * static_cast<size_t>(batch) * nodes + batch + 1) * sizeof(int);
+  const int64_t rows = std::min<int64_t>(static_cast<int64_t>(batch) * nodes, num_sms);
+  return static_cast<size_t>(3 * rows + std::min(batch, num_sms) + 1) * sizeof(int);
 }
 
 cudaError_t launch_verify_draft(const VerifyArgs& a, int dtype, cudaStream_t s) {
