@@ -124,7 +124,9 @@ size_t tf_tree_attention_workspace_bytes(int batch, int nodes, int heads, int kv
  * logits, draft_logits: [batch][nodes][vocab] of one dtype (TF_F32, TF_F16 or
  *   TF_BF16) with the given strides, last dimension contiguous; vocab <= 2^24.
  * tokens, u_accept, u_sample: [batch][nodes] (tokens[b][0], u_accept[b][0]
- *   unused); u in [0, 1), others are clamped. parents as in tf_tree_attention.
+ *   unused), u in [0, 1). Other values are clamped, u_sample to the last token
+ *   of its sum, u_accept to 1 (which refuses a child unless r[t] * 2^31 is
+ *   above q[t] * S); a NaN counts as 0. parents as in tf_tree_attention.
  * Written, each [batch][nodes] unless said: counts [batch] = kept nodes (0
  *   for a sequence whose node 0 is absent); path: the kept nodes, first node
  *   0, then -1; out_tokens: the accepted tokens and the sampled one (-1 where

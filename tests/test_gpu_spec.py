@@ -621,6 +621,37 @@ def test_verify_equal_distributions_and_a_refusal_without_a_rest():
     assert c.tolist() == [1, 1] and o[:, 0].tolist() == want[2][:, 0].tolist()
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_verify_clamps_the_numbers_that_accept(dtype):
+    """A child whose token has no weight in the target (5), one that the target
+    finds 24 times likelier than the draft (7), or an ordinary one (9, 1.2
+    times). u_accept outside [0, 1] counts as the nearer end, a NaN as 0."""
+    v = 64
+    x = torch.zeros((1, 4, v), device="cuda")
+    d = torch.zeros((1, 4, v), device="cuda")
+    x[..., 5], d[..., 5] = -float("inf"), 3.0
+    x[..., 7], d[..., 7] = 2.0, -1.0
+    x, d = x.to(DT[dtype]), d.to(DT[dtype])
+    us = torch.full((1, 4), 0.5, device="cuda")
+
+    def first(child_token, u):
+        tok, ua = i32([[0, child_token, 0, 0]]), torch.full((1, 4), u, device="cuda")
+        return [t.tolist() for t in tf.tf_verify_draft(x, tok, i32([[-1, 0, -2, -2]]), us, draft_logits=d, u_accept=ua)]
+
+    nan, inf = float("nan"), float("inf")
+    for low in (-0.0, -1e-30, -0.5, -7.0, -inf, nan):
+        got = first(5, low)
+        assert got[0] == [1] and got[2][0][0] != 5, low   # a weight of 0 is never accepted
+        for t in (7, 9):
+            got = first(t, low)
+            assert got[0] == [2] and got[1][0][:2] == [0, 1] and got[2][0][0] == t == first(t, 0.0)[2][0][0], low
+    for high in (1.0, 1.5, 40.0, inf):
+        assert first(5, high)[0] == [1] and first(7, high)[0] == [2], high
+        for t in (5, 7, 9):
+            assert first(t, high) == first(t, 1.0), (t, high)
+    tf.tf_device_error()
+
+
 def test_verify_parent_out_of_order_is_recorded():
     x, _, _ = logits_like(1, 3, 50, "fp32", 8)
     tok = x[:, 0].argmax(-1).int()[:, None].expand(1, 3).contiguous()

@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     if (tid < a.nodes) {
       parent = a.parents[b * a.stride_parents + tid];
       drafted = a.tokens[row0 + tid];
-      if (draft) u_child = a.u_accept[row0 + tid];
+      // in [0, 1], a NaN as 0: a child of no weight in p must not be accepted
+      if (draft) u_child = fminf(fmaxf(a.u_accept[row0 + tid], 0.f), 1.f);
     }
 
     // This warp's vectors of each row.
