@@ -661,6 +661,24 @@ def test_verify_parent_out_of_order_is_recorded():
     assert e.value.status == tf.TF_ERR_INDEX and p.tolist()[0][:2] == [0, 2]
 
 
+def test_verify_parent_out_of_order_is_recorded_in_large_batches():
+    """The same where a batch has more rows than the GPU has SMs and is walked
+    down, so that the malformed node is never come to."""
+    b = 200
+    x, _, _ = logits_like(1, 3, 50, "fp32", 8)
+    x = x.expand(b, 3, 50).contiguous()
+    tok = x[:, 0].argmax(-1).int()[:, None].expand(b, 3).contiguous()
+    good = [[-1, 0, 0]] * b
+    tf.tf_verify_draft(x, tok, i32(good), None, temperature=0.0)
+    tf.tf_device_error()
+    for at, par, kept in ((0, [-1, 1, 0], [0, 2]), (b - 1, [-1, -2, 2], [0]), (77, [0, 0, 0], [])):
+        c, p, _, _ = tf.tf_verify_draft(x, tok, i32(good[:at] + [par] + good[at + 1:]), None, temperature=0.0)
+        with pytest.raises(tf.TFError) as e:
+            tf.tf_device_error()
+        assert e.value.status == tf.TF_ERR_INDEX
+        assert p[at].tolist() == kept + [-1] * (3 - len(kept)) and c[at] == len(kept)
+
+
 @pytest.mark.parametrize("with_draft", [False, True])
 def test_verify_emits_tokens_with_the_targets_probabilities(with_draft):
     """The point of it all: over many sequences the first emitted token has

@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
     float z_child = 0.f, zq_child = 0.f;
     if (tid < a.nodes) {
       if (parent >= tid) {
-        if (tid == node) record_index_error(a.err);
+        // each row's own, or in a walk, which never comes to such a node, all at its start
+        if (kWalk ? node == 0 : tid == node) record_index_error(a.err);
         parent = -2;
       }
       child = parent == node && tid > node && drafted >= 0 && drafted < a.vocab;
