@@ -762,6 +762,46 @@ def test_verify_one_workspace_for_the_largest_and_all_smaller_sizes():
     tf.tf_device_error()
 
 
+def test_a_graph_of_a_stream_that_is_not_the_current_one_has_its_own_workspaces():
+    """A side stream is captured while another stream is the current one: the
+    graph must not hold the workspaces that the binding keeps for the side
+    stream, which a larger call replaces."""
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    rng = np.random.default_rng(4)
+    c = Case("bf16", [3000, 40], 3, 2, 4, 64, 16, seed=3)
+    par = i32([tree("tree", 3, rng)] * 2)
+    x, _, g = logits_like(2, 3, 1000, "bf16", 6)
+    tok, us = x.float().argmax(-1).int(), torch.rand((2, 3), device="cuda", generator=g)
+    big = Case("bf16", [900], 100, 2, 4, 128, 64, seed=4)
+    big_par = i32([tree("tree", 100, rng)])
+
+    def calls():
+        return [*tf.tf_tree_attention(c.q, c.k, c.v, c.table, c.lengths, par, stream=side),
+                *tf.tf_verify_draft(x, tok, par, us, stream=side)]
+
+    torch.cuda.synchronize()
+    want = calls()   # the side stream's workspaces are made here
+    torch.cuda.synchronize()
+    kept = {k: w[0] for k, w in tf.spec._workspaces.items() if k[2] == side.cuda_stream}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        graph.capture_begin(capture_error_mode="relaxed")
+        with torch.cuda.stream(other):
+            got = calls()
+        graph.capture_end()
+    assert kept == {k: w[0] for k, w in tf.spec._workspaces.items() if k[2] == side.cuda_stream} and len(kept) == 2
+    tf.tf_tree_attention(big.q, big.k, big.v, big.table, big.lengths, big_par, stream=side)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for t in got:
+            t.fill_(3)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    tf.tf_device_error()
+
+
 # -------------------------------------------------------- refusals, empties
 def test_empty_batches_launch_nothing():
     k = torch.zeros((2, 16, 1, 64), dtype=torch.float16, device="cuda")

@@ -142,12 +142,22 @@ def _cache(k, v, page_table, lengths, layers=False):
     return packed, batch
 
 
+def _captured(stream):
+    """Whether the stream the call runs on is being captured, which is not
+    always what the current one is."""
+    if stream is None:
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with torch.cuda.stream(stream):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def _workspace(name, nbytes, device, handle, stream):
-    """The workspace the binding keeps for the stream. While a graph is being
-    captured each call gets its own (its zeroing is captured too), since a
-    kept one could outlive the graph's memory."""
+    """The workspace the binding keeps for the stream. While the stream is
+    captured into a graph each call gets its own (its zeroing is captured
+    too): a kept one may be dropped for a larger one, and the graph would go
+    on using its memory."""
     ws = _workspaces.get((name, device.index, handle))
-    if ws is not None and ws[1] >= nbytes and not torch._C._cuda_isCurrentStreamCapturing():
+    if ws is not None and ws[1] >= nbytes and not _captured(stream):
         return ws
     with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device):
         t = torch.zeros(max(nbytes, 1), dtype=torch.uint8, device=device)
