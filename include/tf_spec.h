@@ -81,7 +81,8 @@ tf_status tf_kv_write(const tf_kv_cache* cache, const void* k_new, const void* v
  *   of kv_heads; head h reads kv head h / (heads / kv_heads).
  * parents: [batch][nodes], rows stride_parents apart (0: one tree for all).
  * out: [batch][nodes][heads][head_dim] contiguous; lse: [batch][nodes][heads].
- * head_dim 64, 128 or 256; cache->layers must be 1.
+ * head_dim 64, 128 or 256; cache->layers must be 1. scale * log2(e) must be
+ *   finite in fp32 (TF_ERR_SHAPE).
  * workspace: device memory, 256-byte aligned, at least
  *   tf_tree_attention_workspace_bytes(...) bytes, zeroed before its first use;
  *   each call leaves it ready for the next. Calls that share a workspace must

@@ -98,6 +98,13 @@ def test_attention_refusals(lib):
     assert f(-1, 1, 8, 8, 64) == f(1, 129, 8, 8, 64) == f(1, 1, 9, 8, 64) == f(1, 1, 8, 8, 96) == 0
 
 
+def test_attention_refuses_a_scale_that_fp32_cannot_hold(lib):
+    for scale in (1e39, -1e39, 1e300, 3.4e38, -2.4e38):   # the last two times log2(e) = 1.44
+        assert attend(lib, cache(), scale=scale) == tf.TF_ERR_SHAPE, scale
+    for scale in (2.3e38, -2.3e38, 0.0, 1e-45, -1e-300):
+        assert attend(lib, cache(), scale=scale) != tf.TF_ERR_SHAPE, scale
+
+
 def test_keep_refusals(lib):
     assert keep(lib, None) == tf.TF_ERR_NULL
     assert keep(lib, cache(), n=0) == keep(lib, cache(), n=200) == tf.TF_ERR_SHAPE

@@ -58,6 +58,9 @@ struct AttendArgs {
   int join_later;   // the parts are joined by a launch of their own
 };
 
+// Scores are scaled by scale * kLog2e, in fp32.
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Blocks of an attention launch for each SM.
 constexpr int kBlocksPerSm = 2;
 

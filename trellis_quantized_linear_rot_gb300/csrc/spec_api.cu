@@ -1,7 +1,9 @@
 // C ABI of the operators declared in tf_spec.h: argument checks, then a launch
 // on the caller's stream.
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
+#include <limits>
 
 #include "spec.h"
 
@@ -14,6 +16,11 @@ constexpr int64_t kMaxRows = int64_t{1} << 24;  // batch * nodes * heads of one 
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool eights(int64_t a, int64_t b, int64_t c) { return ((a | b | c) & 7) == 0; }
+
+// Whether the factor of a score is a number in fp32 (false for NaN).
+bool fp32_scale(double scale) {
+  return std::fabs(scale) <= std::numeric_limits<float>::max() && std::isfinite(static_cast<float>(scale) * kLog2e);
+}
 
 // The checks of a cache that need no device; *view and the device's state on TF_OK.
 tf_status check_cache(const tf_kv_cache* c, int nodes) {
@@ -124,7 +131,7 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
   if (s != TF_OK) return s;
   const int d = cache->head_dim;
   if (cache->layers != 1 || heads < 1 || heads % cache->kv_heads || (d != 64 && d != 128 && d != 256) ||
-      q_stride_seq < 0 || q_stride_node < 0 || q_stride_head < 0 || stride_parents < 0 || !std::isfinite(scale) ||
+      q_stride_seq < 0 || q_stride_node < 0 || q_stride_head < 0 || stride_parents < 0 || !fp32_scale(scale) ||
       static_cast<int64_t>(cache->batch) * nodes * heads > kMaxRows)
     return TF_ERR_SHAPE;
   // The kernels number the tiles (of at least 32 slots, and up to two places more) of all kv heads in 31 bits.
