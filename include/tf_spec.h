@@ -8,7 +8,8 @@
  *
  * Conventions are those of tf_exl3.h: device pointers owned by the caller,
  * asynchronous calls on `stream`, arguments checked before any launch, no
- * call traps. Strides are in elements. Index arrays are int32.
+ * call traps. Strides are in elements. Index arrays are int32. What a call
+ * writes must overlap nothing that it reads (the cache of tf_kv_keep aside).
  *
  * A sequence's tree has `nodes` nodes (at most TF_MAX_NODES). Node 0 is the
  * last accepted token; the others are drafted. parents[j] is the parent of
@@ -153,9 +154,10 @@ size_t tf_verify_draft_workspace_bytes(int batch, int nodes);
  *   new_lengths[b] = lengths[b] + counts[b].
  * path: [batch][nodes], strictly rising and below nodes over its first
  * counts[b] entries (a path of tf_verify_draft); it is followed as far as it
- * is, and the rest recorded as TF_ERR_INDEX. new_lengths must not be
- * cache->lengths (TF_ERR_POINTER): every block of the launch reads those. An
- * idle sequence keeps its length. The pages have no counterpart.
+ * is, and the rest recorded as TF_ERR_INDEX. new_lengths must not overlap
+ * cache->lengths, cache->page_table, path or counts (TF_ERR_POINTER): every
+ * block of the launch reads those. An idle sequence keeps its length. The
+ * pages have no counterpart.
  */
 tf_status tf_kv_keep(const tf_kv_cache* cache, const int32_t* path, const int32_t* counts, int nodes,
                      int32_t* new_lengths, void* stream);

@@ -115,6 +115,23 @@ def test_keep_refusals(lib):
     assert keep(lib, cache(batch=0), path=NUL) == tf.TF_OK
 
 
+def test_keep_refuses_new_lengths_over_what_its_blocks_read(lib):
+    """Every block of a sequence reads its length, count, path and pages, and
+    one of them writes the new length."""
+    c = cache(page_table=0x30000, lengths=0x40000)     # 2 sequences, 4 pages each
+    call = lambda new: keep(lib, c, path=0x50000, counts=0x60000, new=new)  # noqa: E731
+    for begin, size in ((0x30000, 2 * 4 * 4), (0x40000, 2 * 4), (0x50000, 2 * 3 * 4), (0x60000, 2 * 4)):
+        for new in (begin - 4, begin, begin + size - 4):
+            assert call(new) == tf.TF_ERR_POINTER, hex(new)
+    wide = cache(page_table=0x30000, lengths=0x40000, stride_table=100)
+    assert keep(lib, wide, path=0x50000, counts=0x60000, new=0x30000 + 103 * 4) == tf.TF_ERR_POINTER
+    import torch
+    if not torch.cuda.is_available():
+        for begin, size in ((0x30000, 2 * 4 * 4), (0x40000, 2 * 4), (0x50000, 2 * 3 * 4), (0x60000, 2 * 4)):
+            for new in (begin - 8, begin + size):
+                assert call(new) == tf.TF_ERR_CUDA, hex(new)   # past the checks
+
+
 def test_verify_refusals(lib):
     def v(logits=P, dt=tf.TF_F32, st=(400, 100), draft=P, dst=(400, 100), tok=P, par=P, sp=4, ua=P, us=P, t=1.0, b=2,
           n=4, vocab=100, counts=P, path=P, out=P, lp=P, ws=P, nb=1 << 40):

@@ -1,7 +1,6 @@
 // C ABI of the operators declared in tf_spec.h: argument checks, then a launch
 // on the caller's stream.
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 #include <limits>
 
@@ -16,6 +15,12 @@ constexpr int64_t kMaxRows = int64_t{1} << 24;  // batch * nodes * heads of one 
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool eights(int64_t a, int64_t b, int64_t c) { return ((a | b | c) & 7) == 0; }
+
+// Whether two arrays of 32-bit numbers share any.
+bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uint64_t>(nb) * 4 && y < x + static_cast<uint64_t>(na) * 4;
+}
 
 // Whether the factor of a score is a number in fp32 (false for NaN).
 bool fp32_scale(double scale) {
@@ -101,8 +106,12 @@ tf_status tf_kv_keep(const tf_kv_cache* cache, const int32_t* path, const int32_
   s = check_cache_pointers(cache);
   if (s == TF_ERR_NULL || !path || !counts || !new_lengths) return TF_ERR_NULL;
   if (s != TF_OK || !aligned(path, 4) || !aligned(counts, 4) || !aligned(new_lengths, 4)) return TF_ERR_ALIGN;
-  const intptr_t apart = reinterpret_cast<intptr_t>(new_lengths) - reinterpret_cast<intptr_t>(cache->lengths);
-  if (std::llabs(apart) < static_cast<int64_t>(cache->batch) * 4) return TF_ERR_POINTER;
+  // One block of a sequence writes its new length while others still read these.
+  const int64_t batch = cache->batch;
+  if (overlap(new_lengths, batch, cache->lengths, batch) || overlap(new_lengths, batch, counts, batch) ||
+      overlap(new_lengths, batch, path, batch * nodes) ||
+      overlap(new_lengths, batch, cache->page_table, (batch - 1) * cache->stride_table + cache->table_width))
+    return TF_ERR_POINTER;
   int device, sms, *err;
   s = current_device_state(&device, &sms, &err);
   if (s == TF_OK)
