@@ -96,7 +96,9 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
                             double scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace tf_tree_attention needs for these sizes on the current
- * device, 0 for sizes it refuses. The pages have no counterpart. */
+ * device, 0 for sizes it refuses. Smaller sizes need no more, but for
+ * kv_heads: fewer of them have more rows each, and one has the most. The
+ * pages have no counterpart. */
 size_t tf_tree_attention_workspace_bytes(int batch, int nodes, int heads, int kv_heads, int head_dim);
 
 /*

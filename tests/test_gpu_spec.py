@@ -349,6 +349,22 @@ def test_attention_one_workspace_for_many_sizes_in_turn():
         c.check(t.tolist())
 
 
+def test_attention_workspace_for_the_largest_sizes_serves_fewer_kv_heads():
+    need = tf.lib().tf_tree_attention_workspace_bytes
+    rng = np.random.default_rng(3)
+    for heads, kv, n, d in ((8, 8, 4, 64), (16, 8, 16, 128), (24, 6, 9, 128)):
+        ws = tf.tf_tree_attention_workspace(2, n, heads, kv, d)
+        smaller = [need(2, m, h, k, e) for m in (1, n) for h in (heads // 2, heads) for k in range(1, kv + 1)
+                   for e in (64, d) if h % k == 0]
+        assert max(smaller) <= ws.numel()
+        for k in (1, 2, kv):
+            c = Case("bf16", [700, 90], n, k, heads // k, d, 16, seed=k)
+            par = [tree("tree", n, rng)] * 2
+            got = tf.tf_tree_attention(c.q, c.k, c.v, c.table, c.lengths, i32(par), workspace=ws)
+            c.check(par, out=got[0], lse=got[1])
+    assert tf.tf_tree_attention_workspace(2, 4, 8, 3, 64).numel() == 1   # refused sizes
+
+
 def test_attention_bad_indices_are_skipped_and_recorded():
     c = Case("fp16", [100, 100], 4, 1, 2, 64, 16, seed=13)
     par = i32([[-1, 0, 1, 2]] * 2)

@@ -197,7 +197,10 @@ def tf_kv_write(k_new, v_new, k_cache, v_cache, page_table, lengths, stream=None
 
 def tf_tree_attention_workspace(batch, nodes, heads, kv_heads, head_dim, device="cuda"):
     """A zeroed workspace for tf_tree_attention calls of up to these sizes."""
-    n = (_lib or _load()).tf_tree_attention_workspace_bytes(batch, nodes, heads, kv_heads, head_dim)
+    need = (_lib or _load()).tf_tree_attention_workspace_bytes
+    n = need(batch, nodes, heads, kv_heads, head_dim)
+    if n:   # fewer kv heads have more rows each, and need more
+        n = need(batch, nodes, heads, 1, head_dim)
     return torch.zeros(max(n, 1), dtype=torch.uint8, device=device)
 
 
