@@ -514,6 +514,45 @@ def test_verify_walks(dtype, v, temperature, with_draft):
     verify_and_check(x, tok.int(), par, us, temperature, d if with_draft else None, ua)
 
 
+@pytest.mark.parametrize("dtype,off", [("fp32", 0), ("fp32", 1), ("bf16", 3), ("fp16", 0)])
+@pytest.mark.parametrize("b,n", [(10, 20), (32, 9), (60, 5), (200, 3)])   # 8, 4, 2 blocks a sequence, and 1
+@pytest.mark.parametrize("mode", ["greedy", "sampled", "draft"])
+def test_verify_large_batches_walk_down_their_trees(dtype, off, b, n, mode):
+    """More rows than SMs: a cluster walks down a sequence's tree, from node to
+    node with refusals on the way. Against the definition, and bit for bit
+    against the same sequences a few at a time, which are not walked. Padded
+    and idle sequences among them; rows that begin off a 16-byte boundary."""
+    assert b * n > torch.cuda.get_device_properties(0).multi_processor_count
+    v, rng = 2003, np.random.default_rng(b)
+    x, d, g = logits_like(b, n, v + 8, dtype, b + n, spread=1.0)
+    x, d = x[:, :, off:off + v], d[:, :, off:off + v]
+    par = [tree(("chain", "tree", "star", "padded")[i % 4], n, rng) for i in range(b)]
+    for i in range(7, b, 10):
+        par[i] = [-2] + par[i][1:]
+    up = torch.tensor(par, device="cuda").clamp(min=0)
+    if mode == "draft":    # drawn from the parent's draft row
+        rows = torch.gather(d.float(), 1, up[:, :, None].expand(b, n, v)) / 0.8
+        u = torch.rand(rows.shape, device="cuda", generator=g).clamp(1e-9, 1 - 1e-6)
+        tok = (rows - torch.log(-torch.log(u))).argmax(-1)
+    else:                  # one of the parent's two best
+        best = torch.gather(torch.topk(x.float(), 2, dim=-1).indices, 1, up[:, :, None].expand(b, n, 2))
+        tok = torch.gather(best, 2, torch.randint(0, 2, (b, n, 1), device="cuda", generator=g))[..., 0]
+    tok = tok.int()
+    us, ua = (torch.rand((b, n), device="cuda", generator=g) for _ in range(2))
+    t = 0.0 if mode == "greedy" else 0.8
+    dr = d if mode == "draft" else None
+    got = verify_and_check(x, tok, par, us, t, dr, ua if mode == "draft" else None)
+    assert int(got[0].max()) >= 2 and int(got[0].min()) == 0   # some went down, some are idle
+    few = 100 // n
+    for i in range(0, b, few):
+        at = slice(i, i + few)
+        part = tf.tf_verify_draft(x[at], tok[at], i32(par[at]), us[at], temperature=t,
+                                  draft_logits=None if dr is None else dr[at],
+                                  u_accept=ua[at] if mode == "draft" else None)
+        assert all(torch.equal(p, q[at]) for p, q in zip(part, got)), i
+    tf.tf_device_error()
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
 @pytest.mark.parametrize("temperature", [0.6, 0.8, 1.0, 1.3])
 @pytest.mark.parametrize("v", [257, 129280])
