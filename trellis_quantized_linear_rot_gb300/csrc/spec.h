@@ -13,8 +13,9 @@ namespace tfx {
 constexpr int kErrWait = 1;   // device error bits: a bounded wait gave up,
 constexpr int kErrIndex = 2;  // an index outside its array was skipped
 
-// Division of numbers below 2^31 by a divisor known on the host: two
-// instructions on the device instead of about twenty.
+// Division of numbers below 2^31 by a divisor known on the host, by Granlund
+// and Montgomery's multiplier and shift: two instructions on the device
+// instead of about twenty.
 struct FastDiv {
   uint32_t mul = 0, shift = 0;
   FastDiv() = default;

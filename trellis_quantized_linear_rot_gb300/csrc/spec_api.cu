@@ -143,7 +143,9 @@ tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_s
       q_stride_seq < 0 || q_stride_node < 0 || q_stride_head < 0 || stride_parents < 0 || !fp32_scale(scale) ||
       static_cast<int64_t>(cache->batch) * nodes * heads > kMaxRows)
     return TF_ERR_SHAPE;
-  // The kernels number the tiles (of at least 32 slots, and up to two places more) of all kv heads in 31 bits.
+  // The kernels number the places of all items in 31 bits. With mma.sync an item has a place for each tile
+  // of 32 slots at least, and one more; on tcgen05 one for each tile of 128 and four more, which is no more
+  // than counted here from 65 slots on, and 5 for each of kMaxRows items at most below.
   const int64_t tiles = (static_cast<int64_t>(cache->table_width) * cache->page_size + 31) / 32 + 2;
   if (static_cast<double>(tiles) * cache->kv_heads * cache->batch > 2147483647.0)
     return TF_ERR_SHAPE;

@@ -10,8 +10,8 @@
 // a part of the vocabulary, with one exchange through distributed shared
 // memory for the maximum, one for the sum and one for each refusal's rest; the
 // row is read from memory once and again from the L1 cache or L2. What bounds
-// a row is the arithmetic of exp (about 15 instructions an element and pass)
-// and the latency of the exchanges.
+// a row is latency: passes and meetings of the cluster one after the other, in
+// a block whose 16 warps issue 1.3 of 4 instructions a cycle.
 //
 // With no more rows than SMs, every row is taken at once by a cluster of its
 // own, in the time of one row, and the block that completes a sequence's last
@@ -19,9 +19,9 @@
 // cluster takes a sequence and walks down its tree, so that only the rows on
 // the accepted path are read.
 //
-// 8 chains of 8 rows of 129,280 in bf16 with a draft: 42 us (2 blocks a row;
-// 1.3 instructions a cycle, waits for loads and for the cluster in between).
-// 32 trees of 16 rows in fp32: 65 us, 78 MB of 265 read.
+// 8 chains of 8 rows of 129,280 in bf16 with a draft: 42 us (2 blocks a row).
+// 32 trees of 16 rows in fp32: 65 us, 78 MB of 265 read; at temperature 0,
+// with its pass for the lowest index, 71 (one row 10.2 and 10.3).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -686,8 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_draft_kernel(const __grid_
 // (vocabulary 129,280): fp32 without a draft 8 x 8 rows 21 and 30, 32 x 4 34
 // and 44, 32 x 16 117 and 69; bf16 with a draft, chains 8 x 8 43 and 91, 16 x 8
 // 72 and 98, 8 x 16 73 and 181, trees 8 x 8 50 and 61, 16 x 8 128 and 66, 32 x
-// 16 179 and 104. (Trees ask more children a node and end sooner; which it is
-// only the device knows.)
+// 16 179 and 104. So at 512 rows the walk wins, and at 128 it depends: chains
+// and rows without a draft are faster together, by up to 2.5 times, and trees
+// with a draft walked, by up to 2. (Those ask more children a node and end
+// sooner; which it is only the device knows, and the rule does without.)
 bool walks(int batch, int nodes, int num_sms) { return static_cast<int64_t>(batch) * nodes > num_sms; }
 
 template <typename T>
