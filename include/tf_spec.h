@@ -106,9 +106,10 @@ size_t tf_tree_attention_workspace_bytes(int batch, int nodes, int heads, int kv
  * that follows them. Row (b, j) of `logits` is the target's prediction after
  * node j. From node 0 the call goes down the tree while a child is accepted,
  * then samples one more token at the node it ended on.
- * Probabilities: z = fp32(logit) * fp32(1 / temperature) (a NaN counts as
- * -inf), e = exp(z - max z) in fp32, w = round(2^30 e), P = sum w: whole
- * numbers, so that no order of summation changes a token.
+ * Probabilities: z = fp32(logit) * fp32(1 / temperature) (the factor must be
+ * finite and above 0, else TF_ERR_SHAPE; a NaN z counts as -inf), e =
+ * exp(z - max z) in fp32, w = round(2^30 e), P = sum w: whole numbers, so that
+ * no order of summation changes a token.
  *   temperature 0: the next token is the largest logit's, lowest index first
  *     (probabilities as for temperature 1; u_sample, draft_logits unused).
  *   without draft_logits: the token at a node is the least i with

@@ -152,6 +152,16 @@ def test_verify_refusals(lib):
     assert f(-1, 4) == f(1, 0) == f(1, 129) == 0
 
 
+def test_verify_refuses_a_temperature_whose_reciprocal_fp32_cannot_hold(lib):
+    def v(t):
+        return lib.tf_verify_draft(P, tf.TF_F32, 400, 100, None, 0, 0, P, P, 4, None, P, t, 2, 4, 100, P, P, P, P, P,
+                                   1 << 40, S)
+    for t in (1e-39, 1e-300, 1e46, 1e300):     # infinite, or 0, which makes an infinite logit a NaN
+        assert v(t) == tf.TF_ERR_SHAPE, t
+    for t in (0.0, 3e-39, 1.0, 1e38, 1e44):
+        assert v(t) != tf.TF_ERR_SHAPE, t
+
+
 def test_without_gpu_valid_calls_fail_cleanly(lib):
     import torch
     if torch.cuda.is_available():

@@ -203,7 +203,8 @@ tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int
   if (batch < 0 || batch > 65535 || nodes < 1 || nodes > TF_MAX_NODES || vocab < 1 || vocab > kMaxVocab ||
       stride_seq < 0 || stride_node < 0 || draft_stride_seq < 0 || draft_stride_node < 0 || stride_parents < 0 ||
       !(temperature >= 0.0) || !std::isfinite(temperature) ||
-      (temperature > 0.0 && !std::isfinite(static_cast<float>(1.0 / temperature))))
+      (temperature > 0.0 &&
+       !(1.0 / temperature <= std::numeric_limits<float>::max() && static_cast<float>(1.0 / temperature) > 0.f)))
     return TF_ERR_SHAPE;
   if (dtype != TF_F16 && dtype != TF_F32 && dtype != TF_BF16) return TF_ERR_DTYPE;
   if (batch == 0) return TF_OK;
