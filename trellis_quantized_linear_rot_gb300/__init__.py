@@ -1,8 +1,9 @@
 """GB300 (sm_103a) trellis-quantized projection for decode rows.
 
 A thin Python binding over the C ABI of libtf_exl3.so (include/tf_exl3.h;
-include/tf_spec.h for the operators on drafted tokens, in spec.py), with the
-same names. It only marshals arguments: every step of the
+include/tf_spec.h for the operators on drafted tokens, in spec.py;
+include/tf_qcache.h for head norms, positions and the quantised cache, in
+qcache.py), with the same names. It only marshals arguments: every step of the
 computation runs in the library's CUDA kernels. PyTorch provides device
 memory and streams. There is no CPU fallback: a missing library raises.
 
@@ -14,7 +15,10 @@ import ctypes
 import os
 
 from . import build as _build
+from . import qcache as _qcache
 from . import spec as _spec
+from .qcache import (tf_kvq_attention, tf_kvq_attention_workspace, tf_kvq_cache, tf_kvq_keep,  # noqa: F401
+                     tf_kvq_read, tf_kvq_write, tf_qk_norm_rope)
 from .spec import (TF_MAX_NODES, tf_kv_keep, tf_kv_write, tf_tree_attention,  # noqa: F401
                    tf_tree_attention_workspace, tf_verify_draft, tf_verify_draft_workspace)
 
@@ -43,6 +47,7 @@ SIGNATURES = {
     "tf_device_error": (_I, [_VP]),
     "tf_selftest_stranded_wait": (_I, [_VP]),
     **_spec.SIGNATURES,
+    **_qcache.SIGNATURES,
 }
 
 _lib = None

@@ -4,6 +4,7 @@
 #include <cstring>
 #include <limits>
 
+#include "checks.h"
 #include "spec.h"
 
 using namespace tfx;
@@ -11,21 +12,6 @@ using namespace tfx;
 namespace {
 
 constexpr int kMaxVocab = 1 << 24;
-constexpr int64_t kMaxRows = int64_t{1} << 24;  // batch * nodes * heads of one call
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool eights(int64_t a, int64_t b, int64_t c) { return ((a | b | c) & 7) == 0; }
-
-// Whether two arrays of 32-bit numbers share any.
-bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + static_cast<uint64_t>(nb) * 4 && y < x + static_cast<uint64_t>(na) * 4;
-}
-
-// Whether the factor of a score is a number in fp32 (false for NaN).
-bool fp32_scale(double scale) {
-  return std::fabs(scale) <= std::numeric_limits<float>::max() && std::isfinite(static_cast<float>(scale) * kLog2e);
-}
 
 // The checks of a cache that need no device; *view and the device's state on TF_OK.
 tf_status check_cache(const tf_kv_cache* c, int nodes) {
@@ -70,8 +56,6 @@ CacheView view_of(const tf_kv_cache* c, int* err) {
   v.err = err;
   return v;
 }
-
-tf_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TF_OK : record_cuda_error(e, what); }
 
 }  // namespace
 
