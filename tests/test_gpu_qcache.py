@@ -428,7 +428,7 @@ def test_attention_page_sizes(page, n):
 
 @pytest.mark.parametrize("n", [1, 3, 64, 128])
 @pytest.mark.parametrize("lens", [[0], [1], [2, 127], [128, 126], [129, 63, 64, 65], [1000, 0, 5, 31, 32, 33]])
-@pytest.mark.parametrize("bits,d", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("bits,d", [(4, 128), (8, 64), (8, 128)])
 def test_attention_lengths(n, lens, bits, d):
     rng = np.random.default_rng(len(lens))
     Case(bits, "bf16", lens, n, 2, 2, d, 32, seed=n).check([tree("tree", n, rng) for _ in lens])

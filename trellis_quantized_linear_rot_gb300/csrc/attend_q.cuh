@@ -19,9 +19,10 @@
 // * The order of dimensions in a product is free, if q is in the same one, so
 //   each lane takes the words as they lie in a row, and the order of the keys
 //   is that of the lanes that need them for the second product.
-// * The four warps take different keys of a tile, each with a running maximum,
-//   sum and ring of asynchronous copies of its own: they meet at an item's
-//   ends only.
+// * Four warps take different keys of a tile, each with a running maximum and
+//   sum of its own: they meet at an item's ends only. A fifth warp looks pages
+//   up and copies: what a tile costs besides its arithmetic (with the four
+//   warps' own copies a quarter of all instructions) is spent once for them.
 //
 // Weights. p = 2^(s - m), s = (q . c) ks scale log2(e); O = sum of w c with w
 // = p vs 2^-E rounded to fp16. m is raised when a score passes it by 8, the
@@ -38,47 +39,43 @@ namespace tfx {
 
 template <int kBits, int D, int kCols>   // kCols: groups of 8 rows of a block
 struct QShape {
-  static constexpr int kThreads = 128;
+  static constexpr int kThreads = 160;                // four warps of arithmetic, one of copies
   static constexpr int kRows = 8 * kCols;
   static constexpr int kRowBytes = D * kBits / 8;
   static constexpr int kTile = kRowBytes <= 64 ? 128 : 64;
   static constexpr int kGap = 1;
   static constexpr int kKeys = kTile / 4;             // of a warp
-  static constexpr int kBlocks = D == 256 ? 2 : 3;   // an SM
+  static constexpr int kBlocks = D == 256 || (D == 128 && kCols == 2) ? 2 : 3;   // an SM
   static constexpr int kStages = kRowBytes <= 32 ? 4 : 3;
-  static constexpr int kHalf = kKeys * kRowBytes;     // a warp's keys or values of a tile
-  static constexpr int kWarpBytes = 2 * kHalf;
-  static constexpr int kStageBytes = 4 * kWarpBytes;
+  static constexpr int kHalf = kTile * kRowBytes;     // keys or values of a tile
+  static constexpr int kStageBytes = 2 * kHalf;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kNodes = TF_MAX_NODES;
-  // Codes, rows of q, factors, parents; then the tree's masks.
+  // Codes, keys before values; rows of q; factors.
   static constexpr int kQAt = kStages * kStageBytes;
   static constexpr int kScalesAt = kQAt + kStages * kQBytes;
-  static constexpr int kParentsAt = kScalesAt + kStages * kTile * 4;
-  static constexpr int kSmem = kParentsAt + kStages * kNodes * 4;
+  static constexpr int kSmem = kScalesAt + kStages * kTile * 4;
   // The warps' sums are joined in a stage that is done with, kJoinCols columns at a time.
   static constexpr int kJoinFit = kStageBytes / (4 * kRows * 4);
   static constexpr int kJoinCols = kJoinFit < D ? kJoinFit : D;
 };
 
-// A row's 16-byte chunk c of key k (of a warp's) in shared memory, so that the
-// lanes that read at once meet different banks: in the first product lanes (g,
-// t) read a quarter of key (g / 2) 4 + g % 2, in the second an eighth of key 4t.
-template <int kRowBytes>
-__device__ __forceinline__ int key_chunk(int k, int c) {
-  constexpr int kChunks = kRowBytes / 16;
-  const int at = k * kChunks + c;
-  if (kRowBytes == 32) return at ^ (k & 4);
-  if (kRowBytes >= 128) return at ^ ((k & 1) * 4);
-  return at;
+// The keys of a 16-key part that lane (g, t) has. In the first product rows g
+// and g + 8 of A are keys of_row(g) and of_row(g) ^ 2, in the second the pairs
+// of k 2t and 2t + 8 are keys of_pair(t, 0 .. 3). Rows lie one after the other
+// in shared memory, and this order keeps the lanes that read at once on
+// different banks: parts of 8 and 16 bytes of rows of 64 bytes twofold in the
+// second product, of longer rows fourfold, none otherwise.
+__device__ __forceinline__ int of_pair(int t, int z) { return 4 * t + (z ^ (t >> 1 | (t & 1) << 1)); }
+__device__ __forceinline__ int of_row(int g) { return of_pair(g >> 1, g & 1); }
+
+// A run of bytes, by one lane: both addresses and the size multiples of 16.
+__device__ __forceinline__ void copy_run(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
-template <int kRowBytes>
-__device__ __forceinline__ int value_chunk(int k, int c) {
-  constexpr int kChunks = kRowBytes / 16;
-  const int at = k * kChunks + c, t = k / 4 & 3;
-  if (kRowBytes == 256) return at ^ ((t & 1) | (t & 2) * 2);
-  return at ^ (t * 2);
-}
+
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -91,7 +88,8 @@ template <int kBits, bool kUpper>
 __device__ __forceinline__ uint32_t whole2(uint32_t w) {
   constexpr uint32_t kMask = kBits == 8 ? 0x00FF00FFu : kUpper ? 0x00F000F0u : 0x000F000Fu;
   constexpr uint32_t kFrom = kBits == 8 || kUpper ? 0x64806480u : 0x64086408u;   // 1024 + 128, 1024 + 8
-  const uint32_t x = (w & kMask) | 0x64006400u;
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "n"(kMask), "r"(0x64006400u));   // (w & mask) | 1024
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&kFrom));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
@@ -105,13 +103,17 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[4], const unsigned char
   w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
 }
 
+// A maximum before any score: every finite one is far above it, so that the
+// first weights do not fit and the maximum rises, and -inf is far below it.
+constexpr float kNoMax = -3.0e38f;
+
 // 2^e for a whole e from -126 to 127.
 __device__ __forceinline__ float power2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 // The exponent of a positive finite number, -127 for subnormal ones and 0.
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>(__float_as_uint(x) >> 23 & 255) - 127; }
 
 template <typename T, int kBits, int D, int kCols>
-__global__ void __launch_bounds__(128, QShape<kBits, D, kCols>::kBlocks)
+__global__ void __launch_bounds__(160, QShape<kBits, D, kCols>::kBlocks)
 kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
   using S = QShape<kBits, D, kCols>;
   constexpr int kTile = S::kTile, kStages = S::kStages, kKeys = S::kKeys, kRB = S::kRowBytes, kRows = S::kRows;
@@ -121,111 +123,188 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
   const AttendArgs& a = args.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ TreeMasks<S::kNodes> masks;
-  __shared__ int scratch[2 * 4 + 6];
-  __shared__ uint32_t gone[4][kStages + 1];   // a warp's keys of a tile whose page is outside the pool
+  __shared__ int scratch[2 * 5 + 6];
+  __shared__ uint32_t gone[kStages][kTile / 32];   // keys whose page is outside the pool
   __shared__ float wm[4][kRows], wl[4][kRows];
-  __shared__ int last_here;
+  __shared__ int last_here[2], given_up;
+  __shared__ unsigned long long full[kStages], empty[kStages];   // a tile has landed; the four warps are done with it
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
   const int rows_all = a.nodes * a.group;
   const int row_blocks = (rows_all + kRows - 1) / kRows, team = blockIdx.x / row_blocks;
   const Rows mine{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
   const int row0 = mine.rb * kRows;
 
+  if (tid == 0) {
+    given_up = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&full[i]), args.box ? 1 : 33);
+      mbar_init(smem_u32(&empty[i]), 4);
+    }
+    fence_barrier_init();
+  }
   chain();
   Line line;
-  Cursor look;   // next tile whose pages are looked up
-  const int n_tiles = find_run<kTile, S::kGap, S::kThreads>(a, gridDim.x / row_blocks, team, scratch, &line, &look);
+  Cursor cur;   // tile computed next
+  const int n_tiles = find_run<kTile, S::kGap, S::kThreads>(a, gridDim.x / row_blocks, team, scratch, &line, &cur);
   if (n_tiles == 0) return;
-  Cursor cur = look, load = look;   // tiles computed and copied next
   const uint8_t* kp = static_cast<const uint8_t*>(a.k);
   const uint8_t* vp = static_cast<const uint8_t*>(a.v);
 
-  // A lane has a key of its warp's: its page is asked for one tile before its
-  // places are made of it (-1: not there), those one tile before the copies.
-  struct Pending {
-    int page, row, kvh;
-    bool exists;
-  };
-  struct Places {
-    int64_t codes, factors;
-  };
-  auto look_up = [&](const Cursor& c) -> Pending {
-    const int slot = c.t * kTile + warp * kKeys + lane, p = a.c.by_page(slot);
-    const bool exists = lane < kKeys && slot < c.span.slots;
-    return {exists ? a.c.page_table[c.b * a.c.stride_table + p] : 0, slot - p * a.c.page_size, c.item, exists};
-  };
-  auto settle = [&](const Pending& x, int i) -> Places {
-    const bool outside = x.exists && static_cast<unsigned>(x.page) >= static_cast<unsigned>(a.c.pages);
-    const uint32_t none = __ballot_sync(~0u, outside);
-    if (lane == 0) gone[warp][i % (kStages + 1)] = none;
-    if (none && outside) record_index_error(a.c.err);
-    if (!x.exists || outside) return {-1, 0};
-    return {x.page * a.c.stride_page + x.row * a.c.stride_token + x.kvh * a.c.stride_head,
-            x.page * args.scale_page + x.row * args.scale_token + x.kvh * args.scale_head};
-  };
-  // Copies of q and of the parents for the item of tile i, by all warps.
-  auto issue_rows = [&](const Cursor& c, int i) {
-    const uint32_t dst = smem_u32(smem + S::kQAt) + (i % kStages) * S::kQBytes;
-    constexpr int kChunks = D / 8;
-    for (int id = tid; id < kRows * kChunks; id += 128) {
-      const int r = id / kChunks, ch = id % kChunks;
-      const bool real = row0 + r < rows_all;
-      const RowOf ro = row_of(a, c.item, real ? row0 + r : 0);
-      copy16(dst + r * D * 2 + ((ch ^ (r & 7)) << 4),
-             static_cast<const T*>(a.q) + c.b * a.q_seq + ro.node * a.q_node + ro.head * a.q_head + ch * 8, real);
-    }
-    if (tid < a.nodes)
-      copy4(smem_u32(smem + S::kParentsAt) + ((i % kStages) * S::kNodes + tid) * 4, a.parents + c.b * a.stride_parents + tid);
-  };
-  // Copies of this warp's keys of tile i of the run.
-  auto issue = [&](const Places& at, int i) {
-    const int st = i % kStages;
-    const uint32_t dst = smem_u32(smem) + st * S::kStageBytes + warp * S::kWarpBytes;
-    constexpr int kChunks = kRB / 16;
-#pragma unroll
-    for (int n = 0; n < kKeys * kChunks / 32; ++n) {
-      const int id = n * 32 + lane, key = id / kChunks, ch = id % kChunks;
-      const int64_t o = __shfl_sync(~0u, at.codes, key);
-      const int64_t from = o < 0 ? 0 : o + ch * 16;
-      copy16(dst + key_chunk<kRB>(key, ch) * 16, kp + from, o >= 0);
-      copy16(dst + S::kHalf + value_chunk<kRB>(key, ch) * 16, vp + from, o >= 0);
-    }
-    if (lane < kKeys)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem + S::kScalesAt) +
-                                                                        (st * kTile + warp * kKeys + lane) * 4),
-                   "l"(args.scales + at.factors), "r"(at.codes < 0 ? 0 : 4)
-                   : "memory");
-  };
-
-  // The first kStages - 1 tiles, the places of the one after them.
-  Places next;
-  Pending ahead;
-  {
-    Pending first[kStages];
-    issue_rows(cur, 0);
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-      if (i < n_tiles) {
-        first[i] = look_up(look);
-        advance<kTile, S::kGap>(a, &look);
+  __syncthreads();   // the barriers are there
+  if (warp == 4) {
+    // A tile's keys are runs of args.box slots of a page, whose codes and
+    // factors lie together: a lane has a run's place, and each run is copied in
+    // three pieces. Where they don't lie together (box 0) a lane has a key in
+    // each 32, and all lanes copy 16 bytes at a time. A tile's pages are asked
+    // for while the tile before it is waited for.
+    const int rows = min(kRows, rows_all - row0);
+    bool any_gone = false;
+    for (int i = lane; i < kStages * kTile / 32; i += 32) gone[0][i] = 0;
+    __syncwarp();
+    Cursor c = cur;
+    int st = 0, phase = 1, i = 0;   // phase: of the stage's last use by the other warps
+    // Runs (from first_run on) of a tile whose page is outside the pool: rare, but
+    // from then on every tile says which of its keys are gone.
+    auto note_gone = [&](uint32_t outside, int box, int first_run, bool mine_too) {
+      any_gone = true;
+      if (mine_too) record_index_error(a.c.err);
+      for (int word = first_run * box / 32; word < min((first_run + 32) * box, kTile) / 32; ++word) {
+        uint32_t bits = 0;
+        for (int z = 0; z < 32; ++z) bits |= (outside >> ((word * 32 + z) / box - first_run) & 1u) << z;
+        if (lane == 0) gone[st][word] = bits;
       }
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < n_tiles) {
-        if (i > 0 && load.t == 0) issue_rows(load, i);
-        issue(settle(first[i], i), i);
-        advance<kTile, S::kGap>(a, &load);
+      __syncwarp();
+    };
+    auto stage_free = [&]() {
+      return i < kStages || __all_sync(~0u, mbar_wait(smem_u32(&empty[st]), phase, &given_up));
+    };
+    auto pages_of = [&](const Cursor& x) { return a.c.page_table + x.b * a.c.stride_table; };
+    if (args.box) {
+      const int box = args.box, here = lane < kTile / box ? lane * box : 1 << 30;   // (no slot comes near that)
+      const uint32_t bytes = box * kRB;
+      const int32_t* pages = pages_of(c);
+      const uint8_t* k_head = kp + c.item * a.c.stride_head;
+      const uint32_t* s_head = args.scales + c.item * args.scale_head;
+      const int64_t to_values = vp - kp;
+      int page = 0, row = -1;   // of the lane's run of tile i; row -1: it is not there
+      auto look_up = [&]() {
+        const int slot = c.t * kTile + here;
+        row = -1;
+        if (slot < c.span.slots) {
+          const int p = a.c.by_page(slot);
+          page = pages[p];
+          row = slot - p * a.c.page_size;
+        }
+      };
+      look_up();
+#pragma unroll 1
+      for (; i < n_tiles; ++i) {
+        const bool with_rows = i == 0 || c.t == 0;
+        const int b = c.b, item = c.item, my_page = page, my_row = row;
+        const uint8_t* k_at = k_head;
+        const uint32_t* s_at = s_head;
+        if (i + 1 < n_tiles) {
+          if (++c.t == c.nt) {   // the next item
+            c.t = c.nt - 1;
+            advance<kTile, S::kGap>(a, &c);
+            pages = pages_of(c);
+            k_head = kp + c.item * a.c.stride_head;
+            s_head = args.scales + c.item * args.scale_head;
+          }
+          look_up();
+        }
+        const bool real = my_row >= 0 && static_cast<uint32_t>(my_page) < static_cast<uint32_t>(a.c.pages);
+        const uint32_t there = __ballot_sync(~0u, real), outside = __ballot_sync(~0u, my_row >= 0 && !real);
+        if (!stage_free()) break;   // (no copy of the tile is begun)
+        if (any_gone || outside) note_gone(outside, box, 0, my_row >= 0 && !real);
+        const uint32_t bar = smem_u32(&full[st]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * (2 * bytes + box * 4) + (with_rows ? rows * D * 2 : 0));
+        __syncwarp();
+        k_at += static_cast<uint64_t>(static_cast<uint32_t>(my_page)) * a.c.stride_page + my_row * kRB;
+        s_at += static_cast<uint64_t>(static_cast<uint32_t>(my_page)) * args.scale_page + my_row;
+        // What does not exist keeps an earlier tile's bytes: whatever they are, it gets no weight.
+#pragma unroll 1
+        for (uint32_t left = there; left; left &= left - 1) {
+          const int run = __ffs(left) - 1;
+          const uint64_t from = __shfl_sync(~0u, reinterpret_cast<uint64_t>(k_at), run);
+          const uint64_t with = __shfl_sync(~0u, reinterpret_cast<uint64_t>(s_at), run);
+          if (elect_one()) {
+            const uint32_t keys = smem_u32(smem) + st * S::kStageBytes + run * bytes;
+            copy_run(keys, reinterpret_cast<const void*>(from), bytes, bar);
+            copy_run(keys + S::kHalf, reinterpret_cast<const void*>(from + to_values), bytes, bar);
+            copy_run(smem_u32(smem + S::kScalesAt) + (st * kTile + run * box) * 4, reinterpret_cast<const void*>(with),
+                     box * 4, bar);
+          }
+          __syncwarp();
+        }
+        if (with_rows && lane < rows) {
+          const RowOf ro = row_of(a, item, row0 + lane);
+          copy_run(smem_u32(smem + S::kQAt) + st * S::kQBytes + lane * D * 2,
+                   static_cast<const T*>(a.q) + b * a.q_seq + ro.node * a.q_node + ro.head * a.q_head, D * 2, bar);
+        }
+        if (++st == kStages) st = 0, phase ^= 1;
       }
-      copies_commit();
+    } else {
+      constexpr int kChunks = kRB / 16, kRowChunks = D / 8;
+#pragma unroll 1
+      for (; i < n_tiles; ++i) {
+        const int32_t* pages = pages_of(c);
+        int page[kTile / 32], row[kTile / 32];
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k) {
+          const int slot = c.t * kTile + k * 32 + lane, p = a.c.by_page(slot);
+          const bool exists = slot < c.span.slots;
+          page[k] = exists ? pages[p] : 0;
+          row[k] = exists ? slot - p * a.c.page_size : -1;
+        }
+        if (!stage_free()) break;
+        const uint32_t bar = smem_u32(&full[st]), keys = smem_u32(smem) + st * S::kStageBytes;
+        if (i == 0 || c.t == 0)
+          for (int id = lane; id < rows * kRowChunks; id += 32) {
+            const RowOf ro = row_of(a, c.item, row0 + id / kRowChunks);
+            copy16(smem_u32(smem + S::kQAt) + st * S::kQBytes + id * 16,
+                   static_cast<const T*>(a.q) + c.b * a.q_seq + ro.node * a.q_node + ro.head * a.q_head +
+                       id % kRowChunks * 8,
+                   true);
+          }
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k) {
+          const bool real = row[k] >= 0 && static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(a.c.pages);
+          const uint32_t outside = __ballot_sync(~0u, row[k] >= 0 && !real);
+          if (any_gone || outside) note_gone(outside, 1, k * 32, row[k] >= 0 && !real);
+          const int64_t at = real ? page[k] * a.c.stride_page + row[k] * a.c.stride_token + c.item * a.c.stride_head : -1;
+#pragma unroll
+          for (int n = 0; n < kChunks; ++n) {
+            const int id = n * 32 + lane;
+            const int64_t from = __shfl_sync(~0u, at, id / kChunks);
+            if (from >= 0) {
+              copy16(keys + k * 32 * kRB + id * 16, kp + from + id % kChunks * 16, true);
+              copy16(keys + S::kHalf + k * 32 * kRB + id * 16, vp + from + id % kChunks * 16, true);
+            }
+          }
+          if (real)
+            copy4(smem_u32(smem + S::kScalesAt) + (st * kTile + k * 32 + lane) * 4,
+                  args.scales + page[k] * args.scale_page + row[k] * args.scale_token + c.item * args.scale_head);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        if (lane == 0) mbar_arrive(bar);   // for gone[], which no copy writes
+        advance<kTile, S::kGap>(a, &c);
+        if (++st == kStages) st = 0, phase ^= 1;
+      }
     }
-    next = {-1, 0};
-    if (kStages - 1 < n_tiles) next = settle(first[kStages - 1], kStages - 1);
-    ahead = {0, 0, 0, false};
-    if (kStages < n_tiles) {
-      ahead = look_up(look);
-      advance<kTile, S::kGap>(a, &look);
+    // Every copy has landed before the others are through, unless a wait gave up: then here.
+    if (given_up) {
+      int again = 0;
+      for (int x = 0; x < kStages; ++x) {
+        mbar_wait(smem_u32(&full[x]), 0, &again);
+        mbar_wait(smem_u32(&full[x]), 1, &again);
+      }
+      if (lane == 0) atomicOr(a.c.err, kErrWait);
     }
+    return;
   }
+  // The four warps of arithmetic meet here.
+  auto meet = [] { asm volatile("barrier.sync 1, 128;" ::: "memory"); };
 
   uint32_t qf[kCols][kSteps][2];
   float f[kCols][2];                          // of rows 2t, 2t + 1: the scores' factor
@@ -233,48 +312,43 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
   float m[kCols][2], l[kCols][2];
   int e[kCols][2];
   int node[kCols][2];
+  float to16[kCols][2];                       // 2^-E
+  struct Part {   // an item that other runs have parts of
+    int b, item, first, nt;
+    bool idle;
+  } parts[2];
+  int n_parts = 0;
   bool fresh = true;
-  int masks_of = -1;
+  int masks_of = cur.b;
+  masks.build(a.parents + cur.b * a.stride_parents, a.nodes, a.c.err, meet);   // while the first tile is on its way
 
+  int st = 0, phase = 0;
 #pragma unroll 1
   for (int i = 0; i < n_tiles; ++i) {
-    copies_wait<kStages - 2>();
+    mbar_wait(smem_u32(&full[st]), phase, &given_up);
     __syncwarp();
-    if (i + kStages - 1 < n_tiles) {
-      if (load.t == 0) issue_rows(load, i + kStages - 1);
-      issue(next, i + kStages - 1);
-      advance<kTile, S::kGap>(a, &load);
-    }
-    copies_commit();
-    if (i + kStages < n_tiles) next = settle(ahead, i + kStages);
-    if (i + kStages + 1 < n_tiles) {
-      ahead = look_up(look);
-      advance<kTile, S::kGap>(a, &look);
-    }
-    const int st = i % kStages;
 
     if (fresh) {   // a new item: its rows of q, its masks
-      __syncthreads();   // all warps' copies of q have landed
       const unsigned char* q8 = smem + S::kQAt + st * S::kQBytes;
 #pragma unroll
       for (int n = 0; n < kCols; ++n) {
         const int r = n * 8 + g;
-        // Four (8 bits) or eight elements of row r that a word of codes has.
-        auto elements = [&](int word, float (&x)[8]) {
-          constexpr int kPer = 32 / kBits;
-          const int first = word * kPer, ch = first / 8;
-          const T* p = reinterpret_cast<const T*>(q8 + r * D * 2 + ((ch ^ (r & 7)) << 4)) + first % 8;
-#pragma unroll
-          for (int y = 0; y < kPer; ++y) x[y] = to_f32(p[y]);
+        // The elements of row r that this lane's words of codes have, eight or
+        // (8 bits) four of them a word, in 16-byte pieces.
+        constexpr int kPieces = D / 32;
+        auto piece_of = [&](int i) {   // of the row's D / 8
+          if (kBits == 8) return kRB == 64 ? t * 2 + i : t * 2 + i / 2 * 8 + i % 2;
+          return kRB == 32 ? t * 2 + i : t * 4 + i / 4 * 16 + i % 4;
         };
-        auto word_of = [&](int w) { return kRB == 32 ? 2 * t + w : 4 * (t + w / 4 * 4) + w % 4; };
+        uint4 raw[kPieces];
         uint32_t top = 0;
 #pragma unroll
-        for (int w = 0; w < kSteps / kWordSteps; ++w) {
+        for (int i = 0; i < kPieces; ++i) {
+          raw[i] = row0 + r < rows_all ? reinterpret_cast<const uint4*>(q8)[r * (D / 8) + piece_of(i)] : uint4{0, 0, 0, 0};
           float x[8];
-          elements(word_of(w), x);
+          unpack8<T>(raw[i], x);
 #pragma unroll
-          for (int y = 0; y < 32 / kBits; ++y) top = max(top, __float_as_uint(x[y]) & 0x7FFFFFFFu);
+          for (int y = 0; y < 8; ++y) top = max(top, __float_as_uint(x[y]) & 0x7FFFFFFFu);
         }
         top = max(top, __shfl_xor_sync(~0u, top, 1));
         top = max(top, __shfl_xor_sync(~0u, top, 2));
@@ -283,17 +357,20 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
         const float by = power2(shift);
         auto pair = [&](float x, float y, float upper) { return pack2(__half(), x * by * upper, y * by * upper); };
 #pragma unroll
-        for (int w = 0; w < kSteps / kWordSteps; ++w) {
+        for (int i = 0; i < kPieces; ++i) {
           float x[8];
-          elements(word_of(w), x);
+          unpack8<T>(raw[i], x);
           if constexpr (kBits == 4) {
-            qf[n][2 * w][0] = pair(x[0], x[4], 1.f);
-            qf[n][2 * w][1] = pair(x[2], x[6], 1.f);
-            qf[n][2 * w + 1][0] = pair(x[1], x[5], 0.0625f);   // codes in the upper nibble are 16 times as large
-            qf[n][2 * w + 1][1] = pair(x[3], x[7], 0.0625f);
+            qf[n][2 * i][0] = pair(x[0], x[4], 1.f);
+            qf[n][2 * i][1] = pair(x[2], x[6], 1.f);
+            qf[n][2 * i + 1][0] = pair(x[1], x[5], 0.0625f);   // codes in the upper nibble are 16 times as large
+            qf[n][2 * i + 1][1] = pair(x[3], x[7], 0.0625f);
           } else {
-            qf[n][w][0] = pair(x[0], x[2], 1.f);
-            qf[n][w][1] = pair(x[1], x[3], 1.f);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              qf[n][2 * i + y][0] = pair(x[4 * y], x[4 * y + 2], 1.f);
+              qf[n][2 * i + y][1] = pair(x[4 * y + 1], x[4 * y + 3], 1.f);
+            }
           }
         }
         const float back = a.scale * kLog2e * power2(-shift);
@@ -302,35 +379,34 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
           f[n][x] = __shfl_sync(~0u, back, (2 * t + x) * 4);
           const int row = row0 + n * 8 + 2 * t + x;
           node[n][x] = row < rows_all ? row / a.group : -1;
-          m[n][x] = -INFINITY, l[n][x] = 0.f, e[n][x] = -120;
+          m[n][x] = kNoMax, l[n][x] = 0.f, e[n][x] = -120, to16[n][x] = power2(120);
         }
       }
 #pragma unroll
       for (int d = 0; d < kSteps; ++d)
         for (int n = 0; n < kCols; ++n)
           for (int x = 0; x < 4; ++x) o[d][n][x] = 0.f;
-      if (cur.b != masks_of) {
+      if (cur.b != masks_of) {   // (everybody is through with the item before: they met at its end)
         masks_of = cur.b;
-        masks.build(reinterpret_cast<const int*>(smem + S::kParentsAt) + st * S::kNodes, a.nodes, a.c.err);
+        masks.build(a.parents + cur.b * a.stride_parents, a.nodes, a.c.err, meet);
       }
-      __syncthreads();   // q's place and the parents' may be written again
       fresh = false;
     }
 
     const int slot0 = cur.t * kTile + warp * kKeys;
     if (slot0 < cur.span.slots) {
-      const unsigned char* kt = smem + st * S::kStageBytes + warp * S::kWarpBytes;
+      const unsigned char* kt = smem + st * S::kStageBytes + warp * kKeys * kRB;
       const unsigned char* vt = kt + S::kHalf;
       const uint32_t* sc = reinterpret_cast<const uint32_t*>(smem + S::kScalesAt) + st * kTile + warp * kKeys;
-      const uint32_t missing = gone[warp][i % (kStages + 1)];
+      const uint32_t missing = kKeys == 32 ? gone[st][warp] : gone[st][warp / 2] >> (warp % 2 * 16) & 0xFFFFu;
       const bool tail = slot0 + kKeys > cur.span.context || missing;
-      // This lane's keys of a part: key0 and key0 + 2 (rows g and g + 8 of A).
-      const int key0 = g / 2 * 4 + g % 2;
+      // This lane's keys of a part: key0 and key0 ^ 2 (rows g and g + 8 of A).
+      const int key0 = of_row(g);
       float s[kTiles16][kCols][4];
       uint32_t factors[kTiles16][2];
 #pragma unroll
       for (int u = 0; u < kTiles16; ++u) {
-        factors[u][0] = sc[u * 16 + key0], factors[u][1] = sc[u * 16 + key0 + 2];
+        factors[u][0] = sc[u * 16 + key0], factors[u][1] = sc[u * 16 + (key0 ^ 2)];
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
           for (int x = 0; x < 4; ++x) s[u][n][x] = 0.f;
@@ -338,13 +414,9 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll
         for (int w0 = 0; w0 < kSteps / kWordSteps; w0 += kLoad) {
           uint32_t ka[kLoad], kb[kLoad];
-          if (kRB == 32) {   // half a chunk
-            load_words(ka, kt + key_chunk<kRB>(u * 16 + key0, t / 2) * 16 + t % 2 * 8);
-            load_words(kb, kt + key_chunk<kRB>(u * 16 + key0 + 2, t / 2) * 16 + t % 2 * 8);
-          } else {
-            load_words(ka, kt + key_chunk<kRB>(u * 16 + key0, t + w0) * 16);
-            load_words(kb, kt + key_chunk<kRB>(u * 16 + key0 + 2, t + w0) * 16);
-          }
+          const int quarter = kRB == 32 ? t * 8 : (t + w0) * 16;
+          load_words(ka, kt + (u * 16 + key0) * kRB + quarter);
+          load_words(kb, kt + (u * 16 + (key0 ^ 2)) * kRB + quarter);
 #pragma unroll
           for (int w = 0; w < kLoad; ++w) {
             const uint32_t xa = ka[w] >> 8, xb = kb[w] >> 8;
@@ -361,96 +433,101 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
           }
         }
       }
-      bool rise = false;
-      float high[kCols][2];
-#pragma unroll
-      for (int n = 0; n < kCols; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) high[n][x] = -INFINITY;
+      // Scores in units of log 2; -inf for a key that is not seen.
 #pragma unroll
       for (int u = 0; u < kTiles16; ++u)
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            s[u][n][x] = s[u][n][x] * f[n][x & 1] * key_scale(factors[u][x >> 1]);
-            if (tail) {
-              const int key = u * 16 + key0 + (x >> 1) * 2, slot = slot0 + key, j = slot - cur.span.context;
+          for (int x = 0; x < 4; ++x) s[u][n][x] = s[u][n][x] * f[n][x & 1] * key_scale(factors[u][x >> 1]);
+      if (tail) {
+#pragma unroll
+        for (int u = 0; u < kTiles16; ++u)
+#pragma unroll
+          for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = u * 16 + (key0 ^ (x & 2)), slot = slot0 + key, j = slot - cur.span.context;
               const int i_row = node[n][x & 1];
               bool sees = slot < cur.span.slots && i_row >= 0 && !(missing >> key & 1);
               if (sees && j >= 0) sees = masks.sees(i_row, j);
               if (!sees) s[u][n][x] = -INFINITY;
             }
-            high[n][x & 1] = fmaxf(high[n][x & 1], s[u][n][x]);
-          }
-#pragma unroll
-      for (int n = 0; n < kCols; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) rise |= high[n][x] > m[n][x] + 8.f || (m[n][x] == -INFINITY && high[n][x] > -INFINITY);
-      rise = __any_sync(~0u, rise);
-      // What a risen maximum takes from the sums: 2^down; the least E may be then.
-      float down[kCols][2];
-      int least[kCols][2];
-#pragma unroll
-      for (int n = 0; n < kCols; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) down[n][x] = 0.f, least[n][x] = e[n][x];
-      if (rise) {
-#pragma unroll
-        for (int n = 0; n < kCols; ++n)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float top = high[n][x];
-            for (int z = 4; z < 32; z *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, z));
-            if (!(top > m[n][x])) continue;   // a maximum of the whole warp: the lanes of a row agree
-            down[n][x] = m[n][x] - top;
-            least[n][x] = max(-120, e[n][x] + static_cast<int>(floorf(fmaxf(down[n][x], -250.f))));
-            l[n][x] *= exp2_approx(down[n][x]);
-            m[n][x] = top;
-          }
       }
-      // p, then the weights p vs over the scores.
-      float most[kCols][2] = {}, base[kCols][2];
-#pragma unroll
-      for (int n = 0; n < kCols; ++n)
-        for (int x = 0; x < 2; ++x) base[n][x] = m[n][x] == -INFINITY ? 0.f : m[n][x];
-#pragma unroll
-      for (int u = 0; u < kTiles16; ++u)
-#pragma unroll
-        for (int n = 0; n < kCols; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float p = exp2_approx(s[u][n][x] - base[n][x & 1]);
-            float w = p * value_scale(factors[u][x >> 1]);
-            if (tail && s[u][n][x] == -INFINITY) w = 0.f;   // a key that is not seen, whatever its factor
-            l[n][x & 1] += p;
-            s[u][n][x] = w;
-            most[n][x & 1] = fmaxf(most[n][x & 1], w);
-          }
-      bool over = rise;
+      // p = 2^(s - m) and the weights p vs 2^-E. Where a row's maximum or its
+      // E has to rise they are worked out again: at an item's first tile, and
+      // seldom after it.
+      float w[kTiles16][kCols][4], sum[kCols][2];
+      bool over = false;
 #pragma unroll
       for (int n = 0; n < kCols; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) over |= most[n][x] * power2(-e[n][x]) > 0x1p15f;
+        for (int x = 0; x < 2; ++x) {
+          float all = sum[n][x] = 0.f;
+#pragma unroll
+          for (int u = 0; u < kTiles16; ++u)
+#pragma unroll
+            for (int y = x; y < 4; y += 2) {
+              const float p = exp2_approx(s[u][n][y] - m[n][x]);
+              sum[n][x] += p;
+              w[u][n][y] = p * (value_scale(factors[u][y >> 1]) * to16[n][x]);
+              all += fabsf(w[u][n][y]);
+            }
+          over |= sum[n][x] > 0x1p9f || all > 0x1p15f;   // (NaN stays NaN)
+        }
       if (__any_sync(~0u, over)) {
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float top = most[n][x];
-            for (int z = 4; z < 32; z *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, z));
-            const int to = min(126, max(least[n][x], exponent_of(top) + 1));
-            const float by = exp2_approx(down[n][x] + static_cast<float>(e[n][x] - to));
+            float high = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kTiles16; ++u) high = fmaxf(high, fmaxf(s[u][n][x], s[u][n][x + 2]));
+            for (int z = 4; z < 32; z *= 2) high = fmaxf(high, __shfl_xor_sync(~0u, high, z));
+            // What the maximum takes from the sums, 2^down, and the least E may be then.
+            float down = 0.f;
+            int least = e[n][x];
+            if (high > m[n][x]) {
+              down = m[n][x] - high;
+              least = max(-120, least + static_cast<int>(floorf(fmaxf(down, -250.f))));
+              l[n][x] *= exp2_approx(down);
+              m[n][x] = high;
+            }
+            float most = 0.f;
+            sum[n][x] = 0.f;
+#pragma unroll
+            for (int u = 0; u < kTiles16; ++u)
+#pragma unroll
+              for (int y = x; y < 4; y += 2) {
+                const float p = exp2_approx(s[u][n][y] - m[n][x]);
+                sum[n][x] += p;
+                w[u][n][y] = p * value_scale(factors[u][y >> 1]);
+                most = fmaxf(most, fabsf(w[u][n][y]));
+              }
+            for (int z = 4; z < 32; z *= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, z));
+            const int to = min(126, max(least, exponent_of(most) + 1));
+            const float by = exp2_approx(down + static_cast<float>(e[n][x] - to));
             e[n][x] = to;
+            to16[n][x] = power2(-to);
+#pragma unroll
+            for (int u = 0; u < kTiles16; ++u) w[u][n][x] *= to16[n][x], w[u][n][x + 2] *= to16[n][x];
 #pragma unroll
             for (int d = 0; d < kSteps; ++d) o[d][n][x] *= by, o[d][n][x + 2] *= by;
           }
       }
-      float to16[kCols][2];
 #pragma unroll
       for (int n = 0; n < kCols; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) to16[n][x] = power2(-e[n][x]);
+        for (int x = 0; x < 2; ++x) l[n][x] += sum[n][x];
+      if (tail) {   // no weight for a key that is not seen, whatever its factor
+#pragma unroll
+        for (int u = 0; u < kTiles16; ++u)
+#pragma unroll
+          for (int n = 0; n < kCols; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (s[u][n][x] == -INFINITY) w[u][n][x] = 0.f;
+      }
 #pragma unroll
       for (int u = 0; u < kTiles16; ++u) {
         uint32_t b[kCols][2];
@@ -458,23 +535,20 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
         for (int n = 0; n < kCols; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            b[n][x] = transpose8(pack2(__half(), s[u][n][2 * x] * to16[n][0], s[u][n][2 * x + 1] * to16[n][1]));
-        // An eighth of the rows of keys 4t .. 4t + 3.
+            b[n][x] = transpose8(pack2(__half(), w[u][n][2 * x], w[u][n][2 * x + 1]));
+        // An eighth of the rows of the lane's four keys.
         constexpr int kBytes = kRB / 8, kLoad = kBytes >= 16 ? 4 : kBytes / 4;
 #pragma unroll
         for (int w0 = 0; w0 < kBytes / 4; w0 += kLoad) {
           uint32_t v[4][kLoad];
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int at = g * kBytes + w0 * 4;
-            load_words(v[z], vt + value_chunk<kRB>(u * 16 + 4 * t + z, at / 16) * 16 + at % 16);
-          }
+          for (int z = 0; z < 4; ++z) load_words(v[z], vt + (u * 16 + of_pair(t, z)) * kRB + g * kBytes + w0 * 4);
 #pragma unroll
-          for (int w = 0; w < kLoad; ++w)
+          for (int i_w = 0; i_w < kLoad; ++i_w)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const uint32_t pick = half ? 0x7632u : 0x5410u;
-              const uint32_t x = __byte_perm(v[0][w], v[1][w], pick), y = __byte_perm(v[2][w], v[3][w], pick);
+              const uint32_t x = __byte_perm(v[0][i_w], v[1][i_w], pick), y = __byte_perm(v[2][i_w], v[3][i_w], pick);
               if constexpr (kBits == 4) {
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
@@ -482,13 +556,13 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
                   const uint32_t c[4] = {whole2<4, false>(xs), whole2<4, true>(xs), whole2<4, false>(ys), whole2<4, true>(ys)};
 #pragma unroll
                   for (int n = 0; n < kCols; ++n)
-                    mma16816<__half>(o[(w0 + w) * 4 + half * 2 + z][n], c, b[n][0], b[n][1]);
+                    mma16816<__half>(o[(w0 + i_w) * 4 + half * 2 + z][n], c, b[n][0], b[n][1]);
                 }
               } else {
                 const uint32_t c[4] = {whole2<8, false>(x), whole2<8, false>(x >> 8), whole2<8, false>(y),
                                        whole2<8, false>(y >> 8)};
 #pragma unroll
-                for (int n = 0; n < kCols; ++n) mma16816<__half>(o[(w0 + w) * 2 + half][n], c, b[n][0], b[n][1]);
+                for (int n = 0; n < kCols; ++n) mma16816<__half>(o[(w0 + i_w) * 2 + half][n], c, b[n][0], b[n][1]);
               }
             }
         }
@@ -506,9 +580,10 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           for (int z = 4; z < 32; z *= 2) l[n][x] += __shfl_xor_sync(~0u, l[n][x], z);
+          if (m[n][x] <= kNoMax) m[n][x] = -INFINITY;
           if (g == 0) wm[warp][n * 8 + 2 * t + x] = m[n][x], wl[warp][n * 8 + 2 * t + x] = l[n][x];
         }
-      __syncthreads();   // and everyone is done with tile i
+      meet();   // and everyone is done with tile i
       float* sums = reinterpret_cast<float*>(smem + st * S::kStageBytes);
       float by[kCols][2];   // from this warp's units to the item's
 #pragma unroll
@@ -525,7 +600,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
       constexpr float kOdd = kBits == 4 ? 0.0625f : 1.f;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += S::kJoinCols) {
-        if (c0) __syncthreads();
+        if (c0) meet();
 #pragma unroll
         for (int d = 0; d < kSteps; d += 2) {
           const int col = g * (D / 8) + d * 2 - c0;
@@ -540,7 +615,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
                   float4{o[d][n][x] * z, o[d][n][x + 2] * zo, o[d + 1][n][x] * z, o[d + 1][n][x + 2] * zo};
             }
         }
-        __syncthreads();
+        meet();
         for (int id = tid; id < rows * kFours; id += 128) {
           const int r = id / kFours, four = id - r * kFours, col = c0 + four * 4;
           float4 y = {0.f, 0.f, 0.f, 0.f};
@@ -570,21 +645,35 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
           }
         }
       }
-      if (!whole && !a.join_later) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          last_here = arrives_last(a, line, mine, cur.first, cur.nt);
-          __threadfence();
-        }
-        __syncthreads();
-        if (last_here)
-          join_parts<T, kRows, D, 128>(a, line, mine, cur.b, cur.item, row0, rows, cur.first, cur.nt, idle, tid);
+      if (!whole && !a.join_later) {   // at most twice: of the run's first and of its last item
+        parts[n_parts].b = cur.b, parts[n_parts].item = cur.item;
+        parts[n_parts].first = cur.first, parts[n_parts].nt = cur.nt;
+        parts[n_parts].idle = idle;
+        ++n_parts;
       }
       fresh = true;
-      __syncthreads();   // the masks and the stage may be written again
+      fence_proxy_async_shared();
+      meet();   // the masks and the stage may be written again
     }
+    __syncwarp();
+    if (lane == 0 && i + kStages < n_tiles) mbar_arrive(smem_u32(&empty[st]));
+    if (++st == kStages) st = 0, phase ^= 1;
     advance<kTile, S::kGap>(a, &cur);
+  }
+  // Parts are counted when the run is through: counting takes a fence and a
+  // round trip to memory, 2 us that each of the two would hold the run up for.
+  if (n_parts > 0) {
+    meet();
+    if (tid == 0) {
+      __threadfence();
+      for (int x = 0; x < 2; ++x) last_here[x] = x < n_parts && arrives_last(a, line, mine, parts[x].first, parts[x].nt);
+      __threadfence();
+    }
+    meet();
+    for (int x = 0; x < 2; ++x)
+      if (last_here[x])
+        join_parts<T, kRows, D, 128>(a, line, mine, parts[x].b, parts[x].item, row0, min(kRows, rows_all - row0),
+                                     parts[x].first, parts[x].nt, parts[x].idle, tid);
   }
 }
 

@@ -90,9 +90,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ void fence_proxy_async_shared() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // Columns of this thread's Tensor Memory lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t column, float (&v)[32]) {

@@ -112,6 +112,10 @@ __device__ __forceinline__ bool group_all(int bar_id, int nthreads, bool pred) {
 __device__ __forceinline__ void fence_proxy_async_global() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
+// The same for shared memory.
+__device__ __forceinline__ void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 
 // A load with acquire semantics at GPU scope.
 __device__ __forceinline__ int ld_acquire_gpu(const int* p) {

@@ -39,6 +39,7 @@ struct QAttendArgs {
   AttendArgs a;
   int64_t scale_page, scale_token, scale_head;
   const uint32_t* scales;
+  int box;   // slots of a page that lie together and are copied at once, 0 where none do
 };
 
 cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, int dtype, int weight_dtype, int head_dim, cudaStream_t s);

@@ -222,6 +222,7 @@ tf_status tf_kvq_attention(const tf_kvq_cache* cache, const void* q, int dtype, 
   x.scale_token = view.scale_token;
   x.scale_head = view.scale_head;
   x.scales = view.scales;
+  x.box = 0;
   AttendArgs& a = x.a;
   a.c = view.c;
   a.k = cache->k;

@@ -1,6 +1,7 @@
 // Launch of the attention of a drafted token tree over a quantised paged cache
 // (tf_kvq_attention).
 #include <algorithm>
+#include <numeric>
 
 #include "attend_q.cuh"
 
@@ -12,10 +13,20 @@ constexpr int kMaxDevices = 64;
 // Blocks of a launch with `blocks` places: whole teams of row_blocks, one at least.
 int team_blocks(int blocks, int row_blocks) { return std::max(1, blocks / row_blocks) * row_blocks; }
 
+// Slots that are copied at once: the most that divide both a page and a tile, where their rows lie one after the other, and their factors too, at
+// multiples of 16 bytes; 0 where they don't.
+int run_of_slots(const QAttendArgs& x, int tile, int row_bytes) {
+  const CacheView& c = x.a.c;
+  const int box = std::gcd(c.page_size, tile);
+  const bool together = c.stride_token == row_bytes && x.scale_token == 1 && ((x.scale_page | x.scale_head) & 3) == 0 &&
+                        (reinterpret_cast<uintptr_t>(x.scales) & 15) == 0;
+  return together && box >= 4 ? box : 0;
+}
+
 // Parts of an item above which a launch of its own joins them.
 constexpr int kManyParts = 6;
 // Blocks an SM of any of the kernels, at most.
-constexpr int kMostBlocks = 3;
+constexpr int kMostBlocks = 4;
 
 template <typename T, int kBits, int D, int kCols>
 cudaError_t launch(QAttendArgs x, int device, cudaStream_t s) {
@@ -31,6 +42,7 @@ cudaError_t launch(QAttendArgs x, int device, cudaStream_t s) {
   const int row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
   const int blocks = team_blocks(S::kBlocks * a.num_sms, row_blocks);
   a.join_later = parts_of(a, blocks / row_blocks, S::kTile) > kManyParts;
+  x.box = run_of_slots(x, S::kTile, S::kRowBytes);
   const cudaError_t launched =
       launch_chained(kvq_attention_kernel<T, kBits, D, kCols>, dim3(blocks), dim3(S::kThreads), S::kSmem, 1, s, x);
   if (launched != cudaSuccess || !a.join_later) return launched;

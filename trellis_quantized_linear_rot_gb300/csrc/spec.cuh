@@ -102,7 +102,8 @@ __device__ __forceinline__ int64_t slot_offset(const CacheView& c, int b, int64_
 
 // The ancestors of up to kNodes nodes as bit masks: sees(i, j) when row i sees
 // node j (itself or an ancestor, none absent). Built in log2(nodes) rounds of
-// pointer doubling, by all threads of a block of at least kNodes.
+// pointer doubling, by at least kNodes threads that meet in sync(): all of a
+// block's, or its first.
 template <int kNodes>
 struct TreeMasks {
   static constexpr int kWords = (kNodes + 31) / 32;
@@ -112,6 +113,10 @@ struct TreeMasks {
   __device__ __forceinline__ bool sees(int i, int j) const { return anc[i][j >> 5] >> (j & 31) & 1; }
 
   __device__ __forceinline__ void build(const int32_t* parents, int nodes, int* err) {
+    build(parents, nodes, err, [] { __syncthreads(); });
+  }
+  template <typename Sync>
+  __device__ __forceinline__ void build(const int32_t* parents, int nodes, int* err, Sync&& sync) {
     const int j = threadIdx.x;
     if (j < nodes) {
       int p = parents[j];
@@ -123,7 +128,7 @@ struct TreeMasks {
       if (p >= -1) anc[j][j >> 5] = 1u << (j & 31);
       up[j] = p >= 0 ? p : -1;
     }
-    __syncthreads();
+    sync();
     for (int span = 1; span < nodes; span *= 2) {
       uint32_t m[kWords] = {};
       int next = -1;
@@ -132,12 +137,12 @@ struct TreeMasks {
         for (int w = 0; w < kWords; ++w) m[w] = anc[p][w];
         next = up[p];
       }
-      __syncthreads();
+      sync();
       if (j < nodes) {
         for (int w = 0; w < kWords; ++w) anc[j][w] |= m[w];
         up[j] = next;
       }
-      __syncthreads();
+      sync();
     }
   }
 };
