@@ -54,8 +54,8 @@ enum {
  *     number of ones that i and j have in common
  * rounded once to the dtype. The last step leaves q.k as it is and spreads
  * large elements over the head before they are quantised.
- * A negative position marks a row that is not there: it is neither read nor
- * written. keys may be NULL (queries alone).
+ * A negative position marks a row that is not there: what it holds has no
+ * influence, and nothing is written. keys may be NULL (queries alone).
  * dtype: TF_F16 or TF_BF16; weight_dtype: also TF_F32. positions: [batch]
  * [nodes], rows stride_positions apart (0: one for all). inv_freq: fp64
  * [rotary/2]. rotary: a multiple of 16 up to head_dim, 0 for no rotation

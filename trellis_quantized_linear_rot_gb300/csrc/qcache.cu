@@ -1,8 +1,14 @@
 // Rows of the quantised cache: written (tf_kvq_write), read back
-// (tf_kvq_read), moved (tf_kvq_keep). head_dim / 8 lanes have a row of one
-// head, 8 elements each, keys and values side by side, so that one lane writes
-// both factors as one word. What bounds them is the launch for a few tokens
-// and memory for many.
+// (tf_kvq_read), moved (tf_kvq_keep).
+//
+// head_dim / 8 lanes have a token's or slot's rows of kAtOnce heads, 8 elements
+// of a row each, keys and values side by side, so that one lane writes both
+// factors as one word. A page is looked up once for those heads (a look-up for
+// each row was most of the instructions: a batch of 16 contexts of up to 4,096
+// slots read in 66 us), and their rows are in flight together. What bounds
+// them is the launch for a few tokens and memory for many.
+#include <algorithm>
+
 #include "qcache.cuh"
 
 namespace tfx {
@@ -19,23 +25,44 @@ constexpr int kThreads = 256;
 // across one, in two additions instead of a division. Factors whose
 // reciprocal leaves fp32's normal range are divided by.
 template <int kBits>
+__device__ __noinline__ uint64_t quantise8_by_division(float4 a, float4 b, float s) {
+  constexpr float kMost = kBits == 4 ? 7.f : 127.f;
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint64_t out = 0;
+#pragma unroll 1
+  for (int i = 7; i >= 0; --i)
+    out = out << kBits | static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(__fdiv_rn(x[i], s), -kMost), kMost)) +
+                                               (1 << (kBits - 1)));
+  return out;
+}
+template <int kBits>
 __device__ __forceinline__ uint64_t quantise8(const float (&x)[8], uint32_t top, uint16_t* factor) {
   constexpr float kMost = kBits == 4 ? 7.f : 127.f;
-  constexpr int kBias = kBits == 4 ? 8 : 128;
-  uint64_t out = 0;
-  const bool finite = top < 0x7F800000u;
+  constexpr uint64_t kNone = kBits == 4 ? 0x88888888ull : 0x8080808080808080ull;
   const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), kMost));
   const float s = __bfloat162float(s16);
-  *factor = finite ? __bfloat16_as_ushort(s16) : static_cast<uint16_t>(0x7FC0);
-  const bool none = !finite || s == 0.f, plain = s >= 0x1p-100f && s <= 0x1p100f;
+  *factor = __bfloat16_as_ushort(s16);
+  if (top >= 0x7F800000u) {   // not finite
+    *factor = 0x7FC0;
+    return kNone;
+  }
+  if (s == 0.f) return kNone;
+  if (s < 0x1p-100f || s > 0x1p100f)
+    return quantise8_by_division<kBits>(float4{x[0], x[1], x[2], x[3]}, float4{x[4], x[5], x[6], x[7]}, s);
   const float inv = __fdiv_rn(1.f, s);
+  // 1536 + t, rounded to a multiple of 2^-13; then to a whole number by the
+  // addition of 1.5 * 2^23 + bias, whose lowest bits are the code.
+  constexpr float kWhole = 12582912.f + (kBits == 4 ? 8.f : 128.f);
+  uint32_t lo = 0, hi = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = plain ? __fadd_rn(__fadd_rn(__fmul_rn(x[i], inv), 1536.f), -1536.f) : __fdiv_rn(x[i], s);
-    const int c = none ? 0 : __float2int_rn(fminf(fmaxf(t, -kMost), kMost));
-    out |= static_cast<uint64_t>(static_cast<uint32_t>(c + kBias)) << (i * kBits);
+    const float t = __fadd_rn(__fadd_rn(__fmul_rn(x[i], inv), 1536.f), -1536.f);
+    const uint32_t c = __float_as_uint(__fadd_rn(fminf(fmaxf(t, -kMost), kMost), kWhole)) & ((1u << kBits) - 1);
+    if (kBits == 4) lo |= c << (4 * i);
+    else if (i < 4) lo |= c << (8 * i);
+    else hi |= c << (8 * (i - 4));
   }
-  return out;
+  return lo | static_cast<uint64_t>(hi) << 32;
 }
 
 template <int kLanes>
@@ -48,52 +75,74 @@ __device__ __forceinline__ uint32_t row_top(const float (&x)[8]) {
   return top;
 }
 
-// Whole warps run through the loop together, so that the rows' lanes can meet.
+constexpr int kAtOnce = 4;
+
+// The units of a call: kAtOnce heads of one of a sequence's `tokens` tokens.
+struct Units {
+  uint32_t count;   // below 2^31, so that a step past the end does not wrap
+  int chunks;
+  FastDiv by_chunks, by_tokens;
+  Units(int batch, int tokens, int heads)
+      : chunks((heads + kAtOnce - 1) / kAtOnce), by_chunks(static_cast<uint32_t>(chunks)),
+        by_tokens(static_cast<uint32_t>(tokens)) {
+    count = static_cast<uint32_t>(batch) * tokens * chunks;
+  }
+};
+
+// Whole warps run through the loops together, so that a row's lanes can meet.
 template <typename T, int kBits, int D>
 __global__ void __launch_bounds__(kThreads)
 kvq_write_kernel(const __grid_constant__ QView q, const __grid_constant__ RowsIn k_new,
-                 const __grid_constant__ RowsIn v_new, const int32_t* counts, int nodes) {
-  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
+                 const __grid_constant__ RowsIn v_new, const int32_t* counts, int nodes, Units units) {
+  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
   chain();
   const int lane = threadIdx.x % kLanes;
-  const int64_t rows = static_cast<int64_t>(q.c.batch) * nodes * q.c.kv_heads;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t id = r0 + threadIdx.x / kLanes;
-    const int64_t token = id / q.c.kv_heads;
-    const int h = static_cast<int>(id - token * q.c.kv_heads);
-    const int b = static_cast<int>(token / nodes), i = static_cast<int>(token - static_cast<int64_t>(b) * nodes);
-    bool real = id < rows;
-    Place at = {0, 0};
-    if (real) {
-      const int len = q.c.lengths[b];
-      int n = counts ? counts[b] : nodes;
-      if (n < 0 || n > nodes) {
-        record_index_error(q.c.err);
-        n = n < 0 ? 0 : nodes;
+  for (uint32_t u0 = blockIdx.x * kGroups; u0 < units.count; u0 += gridDim.x * kGroups) {
+    const uint32_t unit = u0 + threadIdx.x / kLanes;
+    const bool in = unit < units.count;
+    const int token = in ? units.by_chunks(unit) : 0, h0 = in ? (unit - token * units.chunks) * kAtOnce : 0;
+    const int b = units.by_tokens(token), i = token - b * nodes;
+    const T* k_row = static_cast<const T*>(k_new.at) + b * k_new.seq + i * k_new.node + lane * 8;
+    const T* v_row = static_cast<const T*>(v_new.at) + b * v_new.seq + i * v_new.node + lane * 8;
+    int n = counts ? counts[b] : nodes;
+    if (n < 0 || n > nodes) {
+      if (in) record_index_error(q.c.err);
+      n = n < 0 ? 0 : nodes;
+    }
+    uint4 kw[kAtOnce], vw[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      kw[u] = vw[u] = uint4{0, 0, 0, 0};
+      if (in && i < n && h0 + u < q.c.kv_heads) {
+        kw[u] = *reinterpret_cast<const uint4*>(k_row + (h0 + u) * k_new.head);
+        vw[u] = *reinterpret_cast<const uint4*>(v_row + (h0 + u) * v_new.head);
       }
-      real = len >= 0 && i < n && place_of(q.c, b, static_cast<int64_t>(len) + i, &at);
     }
-    auto row = [&](const RowsIn& r) {
-      return *reinterpret_cast<const uint4*>(static_cast<const T*>(r.at) + b * r.seq + i * r.node + h * r.head + lane * 8);
-    };
-    float x[8] = {}, y[8] = {};
-    if (real) {
-      unpack8<T>(row(k_new), x);
-      unpack8<T>(row(v_new), y);
+    const int len = q.c.lengths[b];
+    Place at = {0, 0};
+    const bool real = in && len >= 0 && i < n && place_of(q.c, b, static_cast<int64_t>(len) + i, &at);
+    uint8_t* k_to = q.k + codes_at(q.c, at) + lane * kBits;
+    uint8_t* v_to = q.v + codes_at(q.c, at) + lane * kBits;
+    uint32_t* s_to = q.scales + scales_at(q, at);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      float x[8], y[8];
+      unpack8<T>(kw[u], x);
+      unpack8<T>(vw[u], y);
+      uint16_t ks, vs;
+      const uint64_t kc = quantise8<kBits>(x, row_top<kLanes>(x), &ks);
+      const uint64_t vc = quantise8<kBits>(y, row_top<kLanes>(y), &vs);
+      if (!real || h0 + u >= q.c.kv_heads) continue;
+      const int64_t dst = (h0 + u) * q.c.stride_head;
+      if (kBits == 4) {
+        *reinterpret_cast<uint32_t*>(k_to + dst) = static_cast<uint32_t>(kc);
+        *reinterpret_cast<uint32_t*>(v_to + dst) = static_cast<uint32_t>(vc);
+      } else {
+        *reinterpret_cast<uint64_t*>(k_to + dst) = kc;
+        *reinterpret_cast<uint64_t*>(v_to + dst) = vc;
+      }
+      if (lane == 0) s_to[(h0 + u) * q.scale_head] = ks | static_cast<uint32_t>(vs) << 16;
     }
-    uint16_t ks, vs;
-    const uint64_t kc = quantise8<kBits>(x, row_top<kLanes>(x), &ks);
-    const uint64_t vc = quantise8<kBits>(y, row_top<kLanes>(y), &vs);
-    if (!real) continue;
-    const int64_t dst = codes_at(q.c, at) + h * q.c.stride_head + lane * kBits;
-    if (kBits == 4) {
-      *reinterpret_cast<uint32_t*>(q.k + dst) = static_cast<uint32_t>(kc);
-      *reinterpret_cast<uint32_t*>(q.v + dst) = static_cast<uint32_t>(vc);
-    } else {
-      *reinterpret_cast<uint64_t*>(q.k + dst) = kc;
-      *reinterpret_cast<uint64_t*>(q.v + dst) = vc;
-    }
-    if (lane == 0) q.scales[scales_at(q, at) + h * q.scale_head] = ks | static_cast<uint32_t>(vs) << 16;
   }
 }
 
@@ -109,16 +158,13 @@ __device__ __forceinline__ uint4 values8(uint64_t codes, float s) {
 template <typename T, int kBits, int D>
 __global__ void __launch_bounds__(kThreads)
 kvq_read_kernel(const __grid_constant__ QView q, const int32_t* starts, T* k_out, T* v_out, int64_t seq, int64_t slot,
-                int64_t head, int slots) {
-  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
+                int64_t head, int slots, Units units) {
+  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
   chain();
   const int lane = threadIdx.x % kLanes;
-  const int64_t rows = static_cast<int64_t>(q.c.batch) * slots * q.c.kv_heads;
-  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kLanes; id < rows;
-       id += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t token = id / q.c.kv_heads;
-    const int h = static_cast<int>(id - token * q.c.kv_heads);
-    const int b = static_cast<int>(token / slots), i = static_cast<int>(token - static_cast<int64_t>(b) * slots);
+  for (uint32_t unit = blockIdx.x * kGroups + threadIdx.x / kLanes; unit < units.count; unit += gridDim.x * kGroups) {
+    const int id = units.by_chunks(unit), h0 = (unit - id * units.chunks) * kAtOnce;
+    const int b = units.by_tokens(id), i = id - b * slots;
     const int start = starts ? starts[b] : 0;
     if (start < 0) {
       record_index_error(q.c.err);
@@ -127,19 +173,47 @@ kvq_read_kernel(const __grid_constant__ QView q, const int32_t* starts, T* k_out
     const int64_t s = static_cast<int64_t>(start) + i;
     Place at;
     if (s >= q.c.lengths[b] || !place_of(q.c, b, s, &at)) continue;
-    const int64_t src = codes_at(q.c, at) + h * q.c.stride_head + lane * kBits;
-    const uint32_t w = q.scales[scales_at(q, at) + h * q.scale_head];
-    uint64_t kc, vc;
-    if (kBits == 4) {
-      kc = *reinterpret_cast<const uint32_t*>(q.k + src);
-      vc = *reinterpret_cast<const uint32_t*>(q.v + src);
-    } else {
-      kc = *reinterpret_cast<const uint64_t*>(q.k + src);
-      vc = *reinterpret_cast<const uint64_t*>(q.v + src);
+    const uint8_t* k_from = q.k + codes_at(q.c, at) + lane * kBits;
+    const uint8_t* v_from = q.v + codes_at(q.c, at) + lane * kBits;
+    const uint32_t* s_from = q.scales + scales_at(q, at);
+    T* k_to = k_out + b * seq + i * slot + lane * 8;
+    T* v_to = v_out + b * seq + i * slot + lane * 8;
+    uint64_t kc[kAtOnce], vc[kAtOnce];
+    uint32_t w[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (h0 + u >= q.c.kv_heads) break;
+      const int64_t src = (h0 + u) * q.c.stride_head;
+      w[u] = s_from[(h0 + u) * q.scale_head];
+      if (kBits == 4) {
+        kc[u] = *reinterpret_cast<const uint32_t*>(k_from + src);
+        vc[u] = *reinterpret_cast<const uint32_t*>(v_from + src);
+      } else {
+        kc[u] = *reinterpret_cast<const uint64_t*>(k_from + src);
+        vc[u] = *reinterpret_cast<const uint64_t*>(v_from + src);
+      }
     }
-    const int64_t dst = b * seq + i * slot + h * head + lane * 8;
-    *reinterpret_cast<uint4*>(k_out + dst) = values8<T, kBits>(kc, key_scale(w));
-    *reinterpret_cast<uint4*>(v_out + dst) = values8<T, kBits>(vc, value_scale(w));
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (h0 + u >= q.c.kv_heads) break;
+      *reinterpret_cast<uint4*>(k_to + (h0 + u) * head) = values8<T, kBits>(kc[u], key_scale(w[u]));
+      *reinterpret_cast<uint4*>(v_to + (h0 + u) * head) = values8<T, kBits>(vc[u], value_scale(w[u]));
+    }
+  }
+}
+
+constexpr int kAhead = 8;
+
+template <typename W, typename From, typename To>
+__device__ __forceinline__ void move_along(int n, const Place* from, From&& source, To&& target) {
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    W w[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i0 + u < n && from[i0 + u].page >= 0) w[u] = *source(i0 + u);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i0 + u < n && from[i0 + u].page >= 0) *target(i0 + u) = w[u];
   }
 }
 
@@ -147,7 +221,8 @@ kvq_read_kernel(const __grid_constant__ QView q, const int32_t* starts, T* k_out
 // 16-byte chunk of codes, or one word of factors, along the whole path. The
 // path rises: entry k goes from slot path[k] >= k to slot k, so that no later
 // source is written by an earlier move, and kAhead moves are loaded before
-// the first of them is stored.
+// the first of them is stored (32 paths of 16 in 32 layers, 8 bits, 9.4 us one
+// by one).
 __global__ void __launch_bounds__(kThreads)
 kvq_keep_kernel(const __grid_constant__ QView q, const int32_t* path, const int32_t* counts, int nodes,
                 int32_t* new_lengths) {
@@ -160,34 +235,28 @@ kvq_keep_kernel(const __grid_constant__ QView q, const int32_t* path, const int3
     if (blockIdx.x == 0 && layer == 0 && threadIdx.x == 0) new_lengths[b] = len;
     return;
   }
-  if (threadIdx.x == 0) {
-    int n = counts[b];
-    if (n < 0 || n > nodes) {
-      record_index_error(q.c.err);
-      n = n < 0 ? 0 : nodes;
-    }
-    int last = -1, i = 0;
-    for (; i < n; ++i) {
-      const int p = path[b * nodes + i];
-      if (p <= last || p >= nodes) {
-        record_index_error(q.c.err);
-        break;
-      }
-      last = p;
-    }
-    kept = i;
-    if (blockIdx.x == 0 && layer == 0) new_lengths[b] = len + i;
+  int n = counts[b];
+  if (n < 0 || n > nodes) {
+    if (threadIdx.x == 0) record_index_error(q.c.err);
+    n = n < 0 ? 0 : nodes;
+  }
+  if (threadIdx.x == 0) kept = n;
+  __syncthreads();
+  const int entry = threadIdx.x, p = entry < n ? path[b * nodes + entry] : 0;
+  if (entry < n && (p >= nodes || p <= (entry ? path[b * nodes + entry - 1] : -1))) {
+    record_index_error(q.c.err);
+    atomicMin(&kept, entry);   // the path is followed up to here
   }
   __syncthreads();
-  const int n = kept;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int p = path[b * nodes + i];
+  n = kept;
+  if (blockIdx.x == 0 && layer == 0 && entry == 0) new_lengths[b] = len + n;
+  if (entry < n) {
     Place x = {-1, 0}, y = {-1, 0};
-    if (p == i || !place_of(q.c, b, static_cast<int64_t>(len) + p, &x) ||
-        !place_of(q.c, b, static_cast<int64_t>(len) + i, &y))
+    if (p == entry || !place_of(q.c, b, static_cast<int64_t>(len) + p, &x) ||
+        !place_of(q.c, b, static_cast<int64_t>(len) + entry, &y))
       x.page = -1;
-    from[i] = x;
-    to[i] = y;
+    from[entry] = x;
+    to[entry] = y;
   }
   __syncthreads();
   const int chunks = q.c.head_dim * q.bits / 128, units = q.c.kv_heads * (2 * chunks + 1);
@@ -196,37 +265,33 @@ kvq_keep_kernel(const __grid_constant__ QView q, const int32_t* path, const int3
     if (rest < 2 * chunks) {
       uint8_t* base = (rest < chunks ? q.k : q.v) + layer * q.c.stride_layer + h * q.c.stride_head +
                       (rest < chunks ? rest : rest - chunks) * 16;
-      for (int i = 0; i < n; ++i)
-        if (from[i].page >= 0)
-          *reinterpret_cast<uint4*>(base + codes_at(q.c, to[i])) =
-              *reinterpret_cast<const uint4*>(base + codes_at(q.c, from[i]));
+      move_along<uint4>(n, from, [&](int i) { return reinterpret_cast<uint4*>(base + codes_at(q.c, from[i])); },
+                        [&](int i) { return reinterpret_cast<uint4*>(base + codes_at(q.c, to[i])); });
     } else {
       uint32_t* base = q.scales + layer * q.scale_layer + h * q.scale_head;
-      for (int i = 0; i < n; ++i)
-        if (from[i].page >= 0) base[scales_at(q, to[i])] = base[scales_at(q, from[i])];
+      move_along<uint32_t>(n, from, [&](int i) { return base + scales_at(q, from[i]); },
+                           [&](int i) { return base + scales_at(q, to[i]); });
     }
   }
 }
 
-// One launch of a kernel that goes through `rows` rows.
+// One launch of a kernel that goes through the units.
 template <typename... P, typename... A>
-cudaError_t launch_rows(void (*kernel)(P...), int64_t rows, int head_dim, cudaStream_t s, A&&... args) {
-  const int64_t per = kThreads / (head_dim / 8), blocks = (rows + per - 1) / per;
-  return launch_chained(kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0, 1, s,
-                        static_cast<A&&>(args)...);
+cudaError_t launch_units(void (*kernel)(P...), const Units& units, int head_dim, cudaStream_t s, A&&... args) {
+  const int per = kThreads / (head_dim / 8), blocks = static_cast<int>((units.count - 1) / per) + 1;
+  return launch_chained(kernel, dim3(std::min(blocks, 32768)), dim3(kThreads), 0, 1, s, static_cast<A&&>(args)..., units);
 }
 
 template <typename T, int kBits, int D>
 struct Kernels {
   static cudaError_t write(const QView& q, const RowsIn& k, const RowsIn& v, const int32_t* counts, int nodes,
                            cudaStream_t s) {
-    return launch_rows(kvq_write_kernel<T, kBits, D>, static_cast<int64_t>(q.c.batch) * nodes * q.c.kv_heads, D, s, q, k,
-                       v, counts, nodes);
+    return launch_units(kvq_write_kernel<T, kBits, D>, Units(q.c.batch, nodes, q.c.kv_heads), D, s, q, k, v, counts, nodes);
   }
   static cudaError_t read(const QView& q, const int32_t* starts, void* k, void* v, int64_t seq, int64_t slot,
                           int64_t head, int slots, cudaStream_t s) {
-    return launch_rows(kvq_read_kernel<T, kBits, D>, static_cast<int64_t>(q.c.batch) * slots * q.c.kv_heads, D, s, q,
-                       starts, static_cast<T*>(k), static_cast<T*>(v), seq, slot, head, slots);
+    return launch_units(kvq_read_kernel<T, kBits, D>, Units(q.c.batch, slots, q.c.kv_heads), D, s, q, starts,
+                        static_cast<T*>(k), static_cast<T*>(v), seq, slot, head, slots);
   }
 };
 

@@ -1,12 +1,17 @@
 // Norms of queries and keys for each head, the rotation by their positions
 // and the Hadamard rotation over the head, in one pass (tf_qk_norm_rope).
 //
-// head_dim / 8 lanes have a row, 8 elements each, in registers from the load
-// to the store: the mean square is summed over the lanes by shuffles, the
-// other half of a pair comes from the lane rotary / 16 away, and the Hadamard
-// rotation is log2(head_dim) additions an element. A block takes heads of one
-// token, whose cosines and sines it works out once for all of them. Reading
-// and writing each row once is what bounds it; for few tokens the launch.
+// head_dim / 16 lanes have a row, in registers from the load to the store: a
+// lane the c-th 8 elements of each half of the head. So the pair of an element
+// (half a head away where the whole head is rotated) is the same lane's, and
+// the Hadamard rotation leaves the lane for log2(head_dim) - 4 of its steps. A
+// block takes several tokens (as many as its threads can work out the cosines
+// and sines of at once), whose rows follow one another; the next row is asked
+// for before this one is worked on. Reading and writing each row once is what
+// bounds it, and close to that the instructions, so two elements are worked on
+// by one wherever they can be. For few tokens the launch.
+#include <algorithm>
+
 #include "qcache.cuh"
 
 namespace tfx {
@@ -15,117 +20,210 @@ namespace {
 constexpr int kThreads = 256;
 constexpr double kTurn = 0.15915494309189533577;   // 1 / (2 pi)
 
-template <typename W>
-__device__ __forceinline__ void load_weight(const void* weight, int at, float (&w)[8]) {
+// Eight elements as four pairs.
+template <typename T>
+__device__ __forceinline__ void pairs_of(const uint4& w, float2 (&x)[4]) {
+  float f[8];
+  unpack8<T>(w, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = weight ? to_f32(static_cast<const W*>(weight)[at + i]) : 1.f;
+  for (int i = 0; i < 4; ++i) x[i] = float2{f[2 * i], f[2 * i + 1]};
 }
+template <typename W>
+__device__ __forceinline__ void load_weight(const void* weight, int at, float2 (&w)[4]) {
+  if (!weight) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = float2{1.f, 1.f};
+    return;
+  }
+  // (a weight is aligned to its type only)
+  const W* p = static_cast<const W*>(weight) + at;
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    if constexpr (sizeof(W) == 4) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      w[0] = float2{a.x, a.y}, w[1] = float2{a.z, a.w}, w[2] = float2{b.x, b.y}, w[3] = float2{b.z, b.w};
+    } else {
+      pairs_of<W>(*reinterpret_cast<const uint4*>(p), w);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) w[i] = float2{to_f32(p[2 * i]), to_f32(p[2 * i + 1])};
+  }
+}
+__device__ __forceinline__ float2 twice(float x) { return float2{x, x}; }
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return fma2(b, twice(-1.f), a); }
 
 template <typename T, typename W, int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int splits) {
-  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
-  __shared__ float2 turn[D / 2];   // cosine and sine of pair i
+__global__ void __launch_bounds__(kThreads)
+qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int tokens, int per_block, int splits, FastDiv by_nodes,
+                    FastDiv by_rows) {
+  constexpr int kLanes = D / 16, kRows = kThreads / kLanes, kHalf = D / 2;
+  __shared__ __align__(16) float cosines[kThreads], sines[kThreads];   // of pair i of token k at k * half + i
+  __shared__ int positions[kThreads];
   chain();
-  const int64_t token = blockIdx.x / splits;
-  const int split = static_cast<int>(blockIdx.x - token * splits);
-  const int b = static_cast<int>(token / a.nodes), node = static_cast<int>(token - static_cast<int64_t>(b) * a.nodes);
-  const int pos = a.positions[b * a.stride_positions + node];
-  if (pos < 0) return;
+  const int split = blockIdx.x % splits, token0 = static_cast<int>(blockIdx.x / splits) * per_block;
+  const int here = min(per_block, tokens - token0);   // tokens of this block
   const int half = a.rotary / 2;
-  for (int i = threadIdx.x; i < half; i += kThreads) {
+  const int lane = threadIdx.x % kLanes, e = lane * 8, all = a.q.heads + a.k.heads, rows = here * all;
+  struct Row {
+    const tf_head_rows* kind;
+    int k, b, node, head;   // k: its token's number in the block
+  };
+  auto row_of = [&](int r) -> Row {
+    r = min(r, rows - 1);
+    const int k = by_rows(r), h = r - k * all, token = token0 + k, b = by_nodes(token);
+    const bool key = h >= a.q.heads;
+    return {key ? &a.k : &a.q, k, b, token - b * a.nodes, key ? h - a.q.heads : h};
+  };
+  auto load = [&](const Row& r, uint4 (&raw)[2]) {
+    const T* from = static_cast<const T*>(r.kind->x) + r.b * r.kind->x_seq + r.node * r.kind->x_node +
+                    r.head * r.kind->x_head + e;
+    raw[0] = *reinterpret_cast<const uint4*>(from);
+    raw[1] = *reinterpret_cast<const uint4*>(from + kHalf);
+  };
+  const int first = split * kRows, step = splits * kRows, mine = threadIdx.x / kLanes;
+  Row next_row = row_of(first + mine);
+  uint4 next[2];
+  load(next_row, next);
+  for (int i = threadIdx.x; i < here * half; i += kThreads) {
+    const int k = i / half, token = token0 + k, b = by_nodes(token);
+    const int pos = a.positions[b * a.stride_positions + token - b * a.nodes];
     // The angle in turns; whole turns are dropped in fp64.
-    const double t = pos * a.inv_freq[i] * kTurn;
+    const double t = pos * a.inv_freq[i - k * half] * kTurn;
     float s, c;
     sincospif(static_cast<float>(2.0 * (t - rint(t))), &s, &c);
-    turn[i] = float2{c, s};
+    cosines[i] = c;
+    sines[i] = s;
+  }
+  if (threadIdx.x < here) {
+    const int token = token0 + threadIdx.x, b = by_nodes(token);
+    positions[threadIdx.x] = a.positions[b * a.stride_positions + token - b * a.nodes];
   }
   __syncthreads();
-  const int lane = threadIdx.x % kLanes, e = lane * 8;
-  const bool interleaved = a.flags & TF_QK_INTERLEAVED;
-  const int all = a.q.heads + a.k.heads;
+  const bool interleaved = a.flags & TF_QK_INTERLEAVED, hadamard = a.flags & TF_QK_HADAMARD;
   // Whole warps run through the loop together, so that lanes can meet.
-  for (int r0 = split * kRows; r0 < all; r0 += splits * kRows) {
-    const int r = min(r0 + static_cast<int>(threadIdx.x) / kLanes, all - 1);
-    const bool key = r >= a.q.heads;
-    const tf_head_rows& rows = key ? a.k : a.q;
-    const int h = key ? r - a.q.heads : r;
-    float x[8], w[8];
-    unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(rows.x) + b * rows.x_seq + node * rows.x_node +
-                                               h * rows.x_head + e),
-               x);
-    load_weight<W>(rows.weight, e, w);
+#pragma unroll 1
+  for (int r0 = first; r0 < rows; r0 += step) {
+    const Row row = next_row;
+    // x[0][..] are elements e .. e + 7, x[1][..] those half a head on.
+    float2 x[2][4], w[2][4];
+    pairs_of<T>(next[0], x[0]);
+    pairs_of<T>(next[1], x[1]);
+    if (r0 + step < rows) {
+      next_row = row_of(r0 + step + mine);
+      load(next_row, next);
+    }
+    load_weight<W>(row.kind->weight, e, w[0]);
+    load_weight<W>(row.kind->weight, e + kHalf, w[1]);
+    float f = 1.f;
     if (!(a.flags & TF_QK_NO_NORM)) {
-      float sum = 0.f;
+      float2 both = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
+      for (int i = 0; i < 8; ++i) both = fma2(x[i / 4][i % 4], x[i / 4][i % 4], both);
+      float sum = both.x + both.y;
 #pragma unroll
       for (int o = 1; o < kLanes; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
-      const float f = rsqrtf(sum * (1.f / D) + a.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= f;
+      f = rsqrtf(sum * (1.f / D) + a.eps);
     }
+    if (hadamard) f *= D == 64 ? 0.125f : D == 128 ? 0.0883883476f : 0.0625f;   // 1 / sqrt(D)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= w[i];
+    for (int i = 0; i < 8; ++i) x[i / 4][i % 4] = mul2(mul2(x[i / 4][i % 4], twice(f)), w[i / 4][i % 4]);
+    const float* cs = cosines + row.k * half;
+    const float* sn = sines + row.k * half;
     if (half > 0 && interleaved) {
 #pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        if (e + i < a.rotary) {
-          const float2 t = turn[(e + i) / 2];
-          const float u = x[i], v = x[i + 1];
-          x[i] = u * t.x - v * t.y;
-          x[i + 1] = v * t.x + u * t.y;
-        }
-    } else if (half > 0) {
-      const bool first = e < half, turned = e < a.rotary;
-      const int other = !turned ? lane : first ? lane + half / 8 : lane - half / 8;
-      const int base = static_cast<int>(threadIdx.x % 32) - lane;
-#pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = __shfl_sync(~0u, x[i], base + other);
-        if (turned) {
-          const float2 t = turn[first ? e + i : e + i - half];
-          x[i] = x[i] * t.x + (first ? -v : v) * t.y;
+        const int d = e + i / 4 * kHalf + i % 4 * 2;
+        if (d < a.rotary) {
+          const float2 v = x[i / 4][i % 4];
+          const float c = cs[d / 2], s = sn[d / 2];
+          x[i / 4][i % 4] = float2{v.x * c - v.y * s, v.y * c + v.x * s};
         }
       }
+    } else if (a.rotary == D) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 c = *reinterpret_cast<const float2*>(cs + e + 2 * i), s = *reinterpret_cast<const float2*>(sn + e + 2 * i);
+        const float2 u = x[0][i], v = x[1][i];
+        x[0][i] = minus(mul2(u, c), mul2(v, s));
+        x[1][i] = fma2(v, c, mul2(u, s));
+      }
+    } else if (half > 0) {
+      // The pairs of a piece of 8 elements lie half / 8 pieces away, in either
+      // half of another lane.
+      float2 y[2][4];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int piece = lane + p * kLanes, d = piece * 8;
+        const bool turned = d < a.rotary, low = d < half;
+        const int other = !turned ? piece : low ? piece + half / 8 : piece - half / 8;
+        const int from = static_cast<int>(threadIdx.x % 32) - lane + other % kLanes;
+        const int at = turned ? (low ? d : d - half) : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 z[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            z[k] = float2{__shfl_sync(~0u, x[k][i].x, from), __shfl_sync(~0u, x[k][i].y, from)};
+          const float2 v = other < kLanes ? z[0] : z[1];
+          const float2 c = *reinterpret_cast<const float2*>(cs + at + 2 * i), s = *reinterpret_cast<const float2*>(sn + at + 2 * i);
+          y[p][i] = x[p][i];
+          if (turned) y[p][i] = fma2(mul2(v, s), twice(low ? -1.f : 1.f), mul2(x[p][i], c));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i / 4][i % 4] = y[i / 4][i % 4];
     }
-    if (a.flags & TF_QK_HADAMARD) {
+    if (hadamard) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {   // neighbours
+        const float2 v = x[i / 4][i % 4];
+        x[i / 4][i % 4] = float2{v.x + v.y, v.x - v.y};
+      }
 #pragma unroll
       for (int o = 1; o < 8; o *= 2)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (!(i & o)) {
-            const float u = x[i], v = x[i + o];
-            x[i] = u + v;
-            x[i + o] = u - v;
+            const int j = i + o;
+            const float2 u = x[i / 4][i % 4], v = x[j / 4][j % 4];
+            x[i / 4][i % 4] = add2(u, v);
+            x[j / 4][j % 4] = minus(u, v);
           }
 #pragma unroll
-      for (int o = 1; o < kLanes; o *= 2)
+      for (int o = 1; o < kLanes; o *= 2) {
+        const float2 sign = twice(lane & o ? -1.f : 1.f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float v = __shfl_xor_sync(~0u, x[i], o);
-          x[i] = lane & o ? v - x[i] : x[i] + v;
+          const float2 v = x[i / 4][i % 4];
+          x[i / 4][i % 4] = fma2(v, sign, float2{__shfl_xor_sync(~0u, v.x, o), __shfl_xor_sync(~0u, v.y, o)});
         }
-      constexpr float f = D == 64 ? 0.125f : D == 128 ? 0.0883883476f : 0.0625f;   // 1 / sqrt(D)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= f;
+      }
     }
-    if (r0 + static_cast<int>(threadIdx.x) / kLanes < all)
-      *reinterpret_cast<uint4*>(static_cast<T*>(rows.y) + b * rows.y_seq + node * rows.y_node + h * rows.y_head + e) =
-          pack8<T>(x);
+    if (r0 + mine < rows && positions[row.k] >= 0) {
+      T* to = static_cast<T*>(row.kind->y) + row.b * row.kind->y_seq + row.node * row.kind->y_node +
+              row.head * row.kind->y_head + e;
+      *reinterpret_cast<uint4*>(to) = pack8<T>(*reinterpret_cast<const float(*)[8]>(x[0]));
+      *reinterpret_cast<uint4*>(to + kHalf) = pack8<T>(*reinterpret_cast<const float(*)[8]>(x[1]));
+    }
   }
 }
 
 template <typename T, typename W>
 cudaError_t launch(const NormRopeArgs& a, int head_dim, cudaStream_t s) {
-  const int per = kThreads / (head_dim / 8), all = a.q.heads + a.k.heads;
-  const int64_t tokens = static_cast<int64_t>(a.batch) * a.nodes;
-  // Few tokens: a block for each kThreads / lanes heads; many: one a token.
-  const int splits = tokens < 4 * a.num_sms ? (all + per - 1) / per : 1;
-  const dim3 grid(static_cast<unsigned>(tokens * splits));
+  const int rows = kThreads / (head_dim / 16), all = a.q.heads + a.k.heads, tokens = a.batch * a.nodes;
+  // Few tokens: a block for each `rows` heads of one. Many: as many tokens a
+  // block as its threads can have the angles of, but every SM some blocks.
+  const int splits = tokens < 4 * a.num_sms ? (all + rows - 1) / rows : 1;
+  const int per_block = std::max(1, std::min(kThreads / std::max(a.rotary / 2, 32), tokens / (8 * a.num_sms)));
+  const dim3 grid(static_cast<unsigned>((tokens + per_block - 1) / per_block * splits));
+  const FastDiv by_nodes(static_cast<uint32_t>(a.nodes)), by_rows(static_cast<uint32_t>(all));
+  auto with = [&](auto kernel) {
+    return launch_chained(kernel, grid, dim3(kThreads), 0, 1, s, a, tokens, per_block, splits, by_nodes, by_rows);
+  };
   switch (head_dim) {
-    case 64: return launch_chained(qk_norm_rope_kernel<T, W, 64>, grid, dim3(kThreads), 0, 1, s, a, splits);
-    case 128: return launch_chained(qk_norm_rope_kernel<T, W, 128>, grid, dim3(kThreads), 0, 1, s, a, splits);
-    default: return launch_chained(qk_norm_rope_kernel<T, W, 256>, grid, dim3(kThreads), 0, 1, s, a, splits);
+    case 64: return with(qk_norm_rope_kernel<T, W, 64>);
+    case 128: return with(qk_norm_rope_kernel<T, W, 128>);
+    default: return with(qk_norm_rope_kernel<T, W, 256>);
   }
 }
 
