@@ -37,26 +37,34 @@
 
 namespace tfx {
 
-template <int kBits, int D, int kCols>   // kCols: groups of 8 rows of a block
+// kCols: groups of 8 rows of a block. The narrow form has four warps of
+// arithmetic and q in registers, two or three blocks an SM; the wide one, for
+// more rows, eight warps (one block an SM, of which they take the registers),
+// q in shared memory in the order of its fragments, and 16 keys at a time.
+template <int kBits, int D, int kCols>
 struct QShape {
-  static constexpr int kThreads = 160;                // four warps of arithmetic, one of copies
+  static constexpr bool kWide = D == 256 ? kCols == 2 : kCols == 4;
+  static constexpr int kWarps = kWide ? 8 : 4;          // of arithmetic
+  static constexpr int kArith = 32 * kWarps;
+  static constexpr int kThreads = kWide ? 384 : 160;    // and a warp (wide: a group of four, for its registers) of copies
   static constexpr int kRows = 8 * kCols;
   static constexpr int kRowBytes = D * kBits / 8;
-  static constexpr int kTile = kRowBytes <= 64 ? 128 : 64;
+  static constexpr int kKeys = kRowBytes <= 64 ? 32 : 16;   // of a warp
+  static constexpr int kTile = kKeys * kWarps;
   static constexpr int kGap = 1;
-  static constexpr int kKeys = kTile / 4;             // of a warp
-  static constexpr int kBlocks = D == 256 || (D == 128 && kCols == 2) ? 2 : 3;   // an SM
-  static constexpr int kStages = kRowBytes <= 32 ? 4 : 3;
+  static constexpr int kBlocks = kWide ? 1 : D == 256 || (D == 128 && kCols == 2) ? 2 : 3;   // an SM
+  static constexpr int kStages = kRowBytes <= 32 ? 4 : kWide && kRowBytes == 256 ? 2 : 3;
   static constexpr int kHalf = kTile * kRowBytes;     // keys or values of a tile
   static constexpr int kStageBytes = 2 * kHalf;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kNodes = TF_MAX_NODES;
-  // Codes, keys before values; rows of q; factors.
+  // Codes, keys before values; rows of q; factors; q's fragments.
   static constexpr int kQAt = kStages * kStageBytes;
   static constexpr int kScalesAt = kQAt + kStages * kQBytes;
-  static constexpr int kSmem = kScalesAt + kStages * kTile * 4;
+  static constexpr int kFragsAt = kScalesAt + kStages * kTile * 4;
+  static constexpr int kSmem = kFragsAt + (kWide ? kQBytes : 0);
   // The warps' sums are joined in a stage that is done with, kJoinCols columns at a time.
-  static constexpr int kJoinFit = kStageBytes / (4 * kRows * 4);
+  static constexpr int kJoinFit = kStageBytes / (kWarps * kRows * 4);
   static constexpr int kJoinCols = kJoinFit < D ? kJoinFit : D;
 };
 
@@ -113,21 +121,24 @@ __device__ __forceinline__ float power2(int e) { return __uint_as_float(static_c
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>(__float_as_uint(x) >> 23 & 255) - 127; }
 
 template <typename T, int kBits, int D, int kCols>
-__global__ void __launch_bounds__(160, QShape<kBits, D, kCols>::kBlocks)
+__global__ void __launch_bounds__(QShape<kBits, D, kCols>::kThreads, QShape<kBits, D, kCols>::kBlocks)
 kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
   using S = QShape<kBits, D, kCols>;
   constexpr int kTile = S::kTile, kStages = S::kStages, kKeys = S::kKeys, kRB = S::kRowBytes, kRows = S::kRows;
-  constexpr int kTiles16 = kKeys / 16;        // 16-key parts of a warp's keys
+  constexpr bool kWide = S::kWide;
+  constexpr int kWarps = S::kWarps, kArith = S::kArith;
+  constexpr int kTiles16 = kWide ? 1 : kKeys / 16;   // 16-key parts of a warp's keys, worked on together
   constexpr int kSteps = D / 16;              // of the first product; 16-row parts of the second
   constexpr int kWordSteps = kBits == 4 ? 2 : 1;   // steps a word of codes is good for
   const AttendArgs& a = args.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ TreeMasks<S::kNodes> masks;
-  __shared__ int scratch[2 * 5 + 6];
+  __shared__ int scratch[2 * (S::kThreads / 32) + 6];
   __shared__ uint32_t gone[kStages][kTile / 32];   // keys whose page is outside the pool
-  __shared__ float wm[4][kRows], wl[4][kRows];
+  __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
+  __shared__ __align__(8) float row_factor[kWide ? kRows : 2];   // of the item's scores
   __shared__ int last_here[2], given_up;
-  __shared__ unsigned long long full[kStages], empty[kStages];   // a tile has landed; the four warps are done with it
+  __shared__ unsigned long long full[kStages], empty[kStages];   // a tile has landed; all warps are done with it
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
   const int rows_all = a.nodes * a.group;
   const int row_blocks = (rows_all + kRows - 1) / kRows, team = blockIdx.x / row_blocks;
@@ -138,7 +149,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
     given_up = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&full[i]), args.box ? 1 : 33);
-      mbar_init(smem_u32(&empty[i]), 4);
+      mbar_init(smem_u32(&empty[i]), kWarps);
     }
     fence_barrier_init();
   }
@@ -151,7 +162,11 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
   const uint8_t* vp = static_cast<const uint8_t*>(a.v);
 
   __syncthreads();   // the barriers are there
-  if (warp == 4) {
+  // Wide: the registers of 384 threads, 168 each, are shared out anew: 56 for
+  // copies, twice 224 for arithmetic.
+  if (warp >= kWarps) {
+    if constexpr (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp > kWarps) return;
     // A tile's keys are runs of args.box slots of a page, whose codes and
     // factors lie together: a lane has a run's place, and each run is copied in
     // three pieces. Where they don't lie together (box 0) a lane has a key in
@@ -237,7 +252,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
           }
           __syncwarp();
         }
-        if (with_rows && lane < rows) {
+        if (with_rows && lane < rows) {   // 32 rows at most
           const RowOf ro = row_of(a, item, row0 + lane);
           copy_run(smem_u32(smem + S::kQAt) + st * S::kQBytes + lane * D * 2,
                    static_cast<const T*>(a.q) + b * a.q_seq + ro.node * a.q_node + ro.head * a.q_head, D * 2, bar);
@@ -249,14 +264,14 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll 1
       for (; i < n_tiles; ++i) {
         const int32_t* pages = pages_of(c);
-        int page[kTile / 32], row[kTile / 32];
-#pragma unroll
-        for (int k = 0; k < kTile / 32; ++k) {
+        struct Look {
+          int page, row;   // row -1: not there
+        };
+        auto look = [&](int k) -> Look {
           const int slot = c.t * kTile + k * 32 + lane, p = a.c.by_page(slot);
-          const bool exists = slot < c.span.slots;
-          page[k] = exists ? pages[p] : 0;
-          row[k] = exists ? slot - p * a.c.page_size : -1;
-        }
+          return slot < c.span.slots ? Look{pages[p], slot - p * a.c.page_size} : Look{0, -1};
+        };
+        Look next = look(0);
         if (!stage_free()) break;
         const uint32_t bar = smem_u32(&full[st]), keys = smem_u32(smem) + st * S::kStageBytes;
         if (i == 0 || c.t == 0)
@@ -267,24 +282,27 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
                        id % kRowChunks * 8,
                    true);
           }
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kTile / 32; ++k) {
-          const bool real = row[k] >= 0 && static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(a.c.pages);
-          const uint32_t outside = __ballot_sync(~0u, row[k] >= 0 && !real);
-          if (any_gone || outside) note_gone(outside, 1, k * 32, row[k] >= 0 && !real);
-          const int64_t at = real ? page[k] * a.c.stride_page + row[k] * a.c.stride_token + c.item * a.c.stride_head : -1;
-#pragma unroll
+          const Look x = next;
+          if (k + 1 < kTile / 32) next = look(k + 1);
+          const bool real = x.row >= 0 && static_cast<uint32_t>(x.page) < static_cast<uint32_t>(a.c.pages);
+          const uint32_t outside = __ballot_sync(~0u, x.row >= 0 && !real);
+          if (any_gone || outside) note_gone(outside, 1, k * 32, x.row >= 0 && !real);
+          const int64_t at = real ? x.page * a.c.stride_page + x.row * a.c.stride_token + c.item * a.c.stride_head : -1;
+          const uint32_t into = keys + (k * 32 * kChunks + lane) * 16;
+#pragma unroll 4
           for (int n = 0; n < kChunks; ++n) {
             const int id = n * 32 + lane;
             const int64_t from = __shfl_sync(~0u, at, id / kChunks);
             if (from >= 0) {
-              copy16(keys + k * 32 * kRB + id * 16, kp + from + id % kChunks * 16, true);
-              copy16(keys + S::kHalf + k * 32 * kRB + id * 16, vp + from + id % kChunks * 16, true);
+              copy16(into + n * 512, kp + from + id % kChunks * 16, true);
+              copy16(into + n * 512 + S::kHalf, vp + from + id % kChunks * 16, true);
             }
           }
           if (real)
             copy4(smem_u32(smem + S::kScalesAt) + (st * kTile + k * 32 + lane) * 4,
-                  args.scales + page[k] * args.scale_page + row[k] * args.scale_token + c.item * args.scale_head);
+                  args.scales + x.page * args.scale_page + x.row * args.scale_token + c.item * args.scale_head);
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         if (lane == 0) mbar_arrive(bar);   // for gone[], which no copy writes
@@ -303,16 +321,16 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
     }
     return;
   }
-  // The four warps of arithmetic meet here.
-  auto meet = [] { asm volatile("barrier.sync 1, 128;" ::: "memory"); };
+  if constexpr (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  // The warps of arithmetic meet here.
+  auto meet = [] { asm volatile("barrier.sync 1, %0;" ::"n"(kArith) : "memory"); };
 
-  uint32_t qf[kCols][kSteps][2];
-  float f[kCols][2];                          // of rows 2t, 2t + 1: the scores' factor
+  uint32_t qf[kWide ? 1 : kCols][kWide ? 1 : kSteps][2];
+  uint2* frags = reinterpret_cast<uint2*>(smem + S::kFragsAt) + lane;   // of group n and step k at (n kSteps + k) 32
+  float f[kWide ? 1 : kCols][2];              // of rows 2t, 2t + 1: the scores' factor
   float o[kSteps][kCols][4];
   float m[kCols][2], l[kCols][2];
   int e[kCols][2];
-  int node[kCols][2];
-  float to16[kCols][2];                       // 2^-E
   struct Part {   // an item that other runs have parts of
     int b, item, first, nt;
     bool idle;
@@ -331,7 +349,9 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
     if (fresh) {   // a new item: its rows of q, its masks
       const unsigned char* q8 = smem + S::kQAt + st * S::kQBytes;
 #pragma unroll
-      for (int n = 0; n < kCols; ++n) {
+      for (int n0 = 0; n0 < (kWide ? 1 : kCols); ++n0) {
+        const int n = kWide ? warp : n0;   // wide: a group a warp
+        if (kWide && n >= kCols) break;
         const int r = n * 8 + g;
         // The elements of row r that this lane's words of codes have, eight or
         // (8 bits) four of them a word, in 16-byte pieces.
@@ -360,28 +380,31 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
         for (int i = 0; i < kPieces; ++i) {
           float x[8];
           unpack8<T>(raw[i], x);
+          auto keep = [&](int step, uint32_t b0, uint32_t b1) {
+            if (kWide) frags[(n * kSteps + step) * 32] = uint2{b0, b1};
+            else qf[kWide ? 0 : n0][kWide ? 0 : step][0] = b0, qf[kWide ? 0 : n0][kWide ? 0 : step][1] = b1;
+          };
           if constexpr (kBits == 4) {
-            qf[n][2 * i][0] = pair(x[0], x[4], 1.f);
-            qf[n][2 * i][1] = pair(x[2], x[6], 1.f);
-            qf[n][2 * i + 1][0] = pair(x[1], x[5], 0.0625f);   // codes in the upper nibble are 16 times as large
-            qf[n][2 * i + 1][1] = pair(x[3], x[7], 0.0625f);
+            keep(2 * i, pair(x[0], x[4], 1.f), pair(x[2], x[6], 1.f));
+            keep(2 * i + 1, pair(x[1], x[5], 0.0625f), pair(x[3], x[7], 0.0625f));   // upper codes are 16 times as large
           } else {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              qf[n][2 * i + y][0] = pair(x[4 * y], x[4 * y + 2], 1.f);
-              qf[n][2 * i + y][1] = pair(x[4 * y + 1], x[4 * y + 3], 1.f);
-            }
+            for (int y = 0; y < 2; ++y)
+              keep(2 * i + y, pair(x[4 * y], x[4 * y + 2], 1.f), pair(x[4 * y + 1], x[4 * y + 3], 1.f));
           }
         }
         const float back = a.scale * kLog2e * power2(-shift);
+        if (kWide) {
+          if (t == 0) row_factor[r] = back;
+        } else {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          f[n][x] = __shfl_sync(~0u, back, (2 * t + x) * 4);
-          const int row = row0 + n * 8 + 2 * t + x;
-          node[n][x] = row < rows_all ? row / a.group : -1;
-          m[n][x] = kNoMax, l[n][x] = 0.f, e[n][x] = -120, to16[n][x] = power2(120);
+          for (int x = 0; x < 2; ++x) f[kWide ? 0 : n0][x] = __shfl_sync(~0u, back, (2 * t + x) * 4);
         }
       }
+#pragma unroll
+      for (int n = 0; n < kCols; ++n)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) m[n][x] = kNoMax, l[n][x] = 0.f, e[n][x] = -120;
 #pragma unroll
       for (int d = 0; d < kSteps; ++d)
         for (int n = 0; n < kCols; ++n)
@@ -390,6 +413,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
         masks_of = cur.b;
         masks.build(a.parents + cur.b * a.stride_parents, a.nodes, a.c.err, meet);
       }
+      if (kWide) meet();   // q is there
       fresh = false;
     }
 
@@ -402,11 +426,17 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
       const bool tail = slot0 + kKeys > cur.span.context || missing;
       // This lane's keys of a part: key0 and key0 ^ 2 (rows g and g + 8 of A).
       const int key0 = of_row(g);
+#pragma unroll 1
+      for (int part0 = 0; part0 < kKeys; part0 += 16 * kTiles16, kt += 16 * kTiles16 * kRB, vt += 16 * kTiles16 * kRB) {
+      if (kWide && slot0 + part0 >= cur.span.slots) break;
+      auto q_of = [&](int n, int step) {
+        return kWide ? frags[(n * kSteps + step) * 32] : uint2{qf[kWide ? 0 : n][kWide ? 0 : step][0], qf[kWide ? 0 : n][kWide ? 0 : step][1]};
+      };
       float s[kTiles16][kCols][4];
       uint32_t factors[kTiles16][2];
 #pragma unroll
       for (int u = 0; u < kTiles16; ++u) {
-        factors[u][0] = sc[u * 16 + key0], factors[u][1] = sc[u * 16 + (key0 ^ 2)];
+        factors[u][0] = sc[part0 + u * 16 + key0], factors[u][1] = sc[part0 + u * 16 + (key0 ^ 2)];
 #pragma unroll
         for (int n = 0; n < kCols; ++n)
           for (int x = 0; x < 4; ++x) s[u][n][x] = 0.f;
@@ -424,22 +454,31 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
             const uint32_t lo[4] = {whole2<kBits, false>(ka[w]), whole2<kBits, false>(kb[w]), whole2<kBits, false>(xa),
                                     whole2<kBits, false>(xb)};
 #pragma unroll
-            for (int n = 0; n < kCols; ++n) mma16816<__half>(s[u][n], lo, qf[n][step][0], qf[n][step][1]);
+            for (int n = 0; n < kCols; ++n) {
+              const uint2 b = q_of(n, step);
+              mma16816<__half>(s[u][n], lo, b.x, b.y);
+            }
             if constexpr (kBits == 4) {
               const uint32_t hi[4] = {whole2<4, true>(ka[w]), whole2<4, true>(kb[w]), whole2<4, true>(xa), whole2<4, true>(xb)};
 #pragma unroll
-              for (int n = 0; n < kCols; ++n) mma16816<__half>(s[u][n], hi, qf[n][step + 1][0], qf[n][step + 1][1]);
+              for (int n = 0; n < kCols; ++n) {
+                const uint2 b = q_of(n, step + 1);
+                mma16816<__half>(s[u][n], hi, b.x, b.y);
+              }
             }
           }
         }
       }
       // Scores in units of log 2; -inf for a key that is not seen.
 #pragma unroll
-      for (int u = 0; u < kTiles16; ++u)
+      for (int n = 0; n < kCols; ++n) {
+        const float2 by = kWide ? *reinterpret_cast<const float2*>(row_factor + (n * 8 + 2 * t) % (kWide ? kRows : 2))
+                                : float2{f[kWide ? 0 : n][0], f[kWide ? 0 : n][1]};
 #pragma unroll
-        for (int n = 0; n < kCols; ++n)
+        for (int u = 0; u < kTiles16; ++u)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[u][n][x] = s[u][n][x] * f[n][x & 1] * key_scale(factors[u][x >> 1]);
+          for (int x = 0; x < 4; ++x) s[u][n][x] = s[u][n][x] * (x & 1 ? by.y : by.x) * key_scale(factors[u][x >> 1]);
+      }
       if (tail) {
 #pragma unroll
         for (int u = 0; u < kTiles16; ++u)
@@ -447,8 +486,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
           for (int n = 0; n < kCols; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int key = u * 16 + (key0 ^ (x & 2)), slot = slot0 + key, j = slot - cur.span.context;
-              const int i_row = node[n][x & 1];
+              const int key = part0 + u * 16 + (key0 ^ (x & 2)), slot = slot0 + key, j = slot - cur.span.context;
+              const int row = row0 + n * 8 + 2 * t + (x & 1), i_row = row < rows_all ? row / a.group : -1;
               bool sees = slot < cur.span.slots && i_row >= 0 && !(missing >> key & 1);
               if (sees && j >= 0) sees = masks.sees(i_row, j);
               if (!sees) s[u][n][x] = -INFINITY;
@@ -463,6 +502,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
       for (int n = 0; n < kCols; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+          const float to16 = power2(-e[n][x]);   // 2^-E
           float all = sum[n][x] = 0.f;
 #pragma unroll
           for (int u = 0; u < kTiles16; ++u)
@@ -470,7 +510,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
             for (int y = x; y < 4; y += 2) {
               const float p = exp2_approx(s[u][n][y] - m[n][x]);
               sum[n][x] += p;
-              w[u][n][y] = p * (value_scale(factors[u][y >> 1]) * to16[n][x]);
+              w[u][n][y] = p * (value_scale(factors[u][y >> 1]) * to16);
               all += fabsf(w[u][n][y]);
             }
           over |= sum[n][x] > 0x1p9f || all > 0x1p15f;   // (NaN stays NaN)
@@ -508,9 +548,9 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
             const int to = min(126, max(least, exponent_of(most) + 1));
             const float by = exp2_approx(down + static_cast<float>(e[n][x] - to));
             e[n][x] = to;
-            to16[n][x] = power2(-to);
+            const float to16 = power2(-to);
 #pragma unroll
-            for (int u = 0; u < kTiles16; ++u) w[u][n][x] *= to16[n][x], w[u][n][x + 2] *= to16[n][x];
+            for (int u = 0; u < kTiles16; ++u) w[u][n][x] *= to16, w[u][n][x + 2] *= to16;
 #pragma unroll
             for (int d = 0; d < kSteps; ++d) o[d][n][x] *= by, o[d][n][x + 2] *= by;
           }
@@ -567,6 +607,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
             }
         }
       }
+      }
     }
 
     const bool item_ends = cur.t + 1 == cur.nt;
@@ -591,7 +632,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int r = n * 8 + 2 * t + x;
-          const float top = fmaxf(fmaxf(wm[0][r], wm[1][r]), fmaxf(wm[2][r], wm[3][r]));
+          float top = wm[0][r];
+          for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wm[w][r]);
           by[n][x] = exp2_approx(m[n][x] - (top == -INFINITY ? 0.f : top) + static_cast<float>(e[n][x]));
         }
       // A lane's columns are D / 8 in a row; groups of four are rotated by the
@@ -616,20 +658,21 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
             }
         }
         meet();
-        for (int id = tid; id < rows * kFours; id += 128) {
+        for (int id = tid; id < rows * kFours; id += kArith) {
           const int r = id / kFours, four = id - r * kFours, col = c0 + four * 4;
           float4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = 0; w < kWarps; ++w) {
             const float4 z = *reinterpret_cast<const float4*>(sums + (w * kRows + r) * S::kJoinCols +
                                                               (four + r / 2) % kFours * 4);
             y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
           }
-          const float top = fmaxf(fmaxf(wm[0][r], wm[1][r]), fmaxf(wm[2][r], wm[3][r]));
+          float top = wm[0][r];
+          for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wm[w][r]);
           const float low = top == -INFINITY ? 0.f : top;
           float sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) sum += wl[w][r] * exp2_approx(wm[w][r] - low);
+          for (int w = 0; w < kWarps; ++w) sum += wl[w][r] * exp2_approx(wm[w][r] - low);
           if (whole) {
             const RowOf ro = row_of(a, cur.item, row0 + r);
             const bool present = !idle && masks.sees(ro.node, ro.node);
@@ -672,7 +715,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
     meet();
     for (int x = 0; x < 2; ++x)
       if (last_here[x])
-        join_parts<T, kRows, D, 128>(a, line, mine, parts[x].b, parts[x].item, row0, min(kRows, rows_all - row0),
+        join_parts<T, kRows, D, kArith>(a, line, mine, parts[x].b, parts[x].item, row0, min(kRows, rows_all - row0),
                                      parts[x].first, parts[x].nt, parts[x].idle, tid);
   }
 }

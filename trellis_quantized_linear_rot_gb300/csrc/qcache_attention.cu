@@ -20,7 +20,7 @@ int run_of_slots(const QAttendArgs& x, int tile, int row_bytes) {
   const int box = std::gcd(c.page_size, tile);
   const bool together = c.stride_token == row_bytes && x.scale_token == 1 && ((x.scale_page | x.scale_head) & 3) == 0 &&
                         (reinterpret_cast<uintptr_t>(x.scales) & 15) == 0;
-  return together && box >= 4 ? box : 0;
+  return together && box >= std::max(4, tile / 32) ? box : 0;   // a lane has a run
 }
 
 // Parts of an item above which a launch of its own joins them.
@@ -51,11 +51,15 @@ cudaError_t launch(QAttendArgs x, int device, cudaStream_t s) {
 
 template <typename T, int kBits>
 cudaError_t by_dim(const QAttendArgs& x, int device, cudaStream_t s) {
-  const bool few = x.a.nodes * x.a.group <= 8;
+  const int rows = x.a.nodes * x.a.group;
   switch (x.a.c.head_dim) {
-    case 64: return few ? launch<T, kBits, 64, 1>(x, device, s) : launch<T, kBits, 64, 2>(x, device, s);
-    case 128: return few ? launch<T, kBits, 128, 1>(x, device, s) : launch<T, kBits, 128, 2>(x, device, s);
-    default: return launch<T, kBits, 256, 1>(x, device, s);
+    case 64:
+      return rows <= 8 ? launch<T, kBits, 64, 1>(x, device, s)
+             : rows <= 16 ? launch<T, kBits, 64, 2>(x, device, s) : launch<T, kBits, 64, 4>(x, device, s);
+    case 128:
+      return rows <= 8 ? launch<T, kBits, 128, 1>(x, device, s)
+             : rows <= 16 ? launch<T, kBits, 128, 2>(x, device, s) : launch<T, kBits, 128, 4>(x, device, s);
+    default: return rows <= 8 ? launch<T, kBits, 256, 1>(x, device, s) : launch<T, kBits, 256, 2>(x, device, s);
   }
 }
 
@@ -63,7 +67,8 @@ cudaError_t by_dim(const QAttendArgs& x, int device, cudaStream_t s) {
 
 // A counter for each part (their number and place depend on the device alone;
 // a launch with more blocks of rows than places has one run, and nothing to
-// join), then two parts for each block of the launch, of 16 rows at most.
+// join), then two parts for each block of the launch: 16 rows, or 32
+// where a block has an SM to itself.
 AttendWorkspace kvq_attend_workspace(int nodes, int heads, int kv_heads, int head_dim, int num_sms) {
   const int64_t rows = static_cast<int64_t>(nodes) * (heads / kv_heads);
   const size_t places = static_cast<size_t>(kMostBlocks) * num_sms;
