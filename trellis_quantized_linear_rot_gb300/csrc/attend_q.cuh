@@ -27,7 +27,7 @@
 // Weights. p = 2^(s - m), s = (q . c) ks scale log2(e); O = sum of w c with w
 // = p vs 2^-E rounded to fp16. m is raised when a score passes it by 8, the
 // row's E when a weight would pass 2^15, so that most tiles need no exchange
-// between lanes; E is about the largest p vs so far, so that factors of any
+// between lanes; 2^E is about 2^-8 of the largest p vs so far, so that factors of any
 // size and range lose nothing. q is scaled by a power of two into fp16's range
 // (exact but for elements 2^-39 below the row's largest).
 #pragma once
@@ -545,7 +545,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
                 most = fmaxf(most, fabsf(w[u][n][y]));
               }
             for (int z = 4; z < 32; z *= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, z));
-            const int to = min(126, max(least, exponent_of(most) + 1));
+            const int to = min(126, max(least, exponent_of(most) - 7));   // the largest weight is below 2^8
             const float by = exp2_approx(down + static_cast<float>(e[n][x] - to));
             e[n][x] = to;
             const float to16 = power2(-to);

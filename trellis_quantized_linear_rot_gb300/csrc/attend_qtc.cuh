@@ -1,0 +1,649 @@
+// Attention over a cache in 4 bits with tcgen05: more than 16 rows a kv head.
+//
+// The tiles, streams, rows and joins are those of attend_tc.cuh: blocks of up
+// to 128 rows, tiles of 128 keys that go alternately to two streams, scores
+// and weights in Tensor Memory. What is different is how a tile gets there:
+//   warp 0        copies of codes and factors, three tiles in flight
+//   warps 1, 2    products of stream 0 and 1
+//   warps 4-7, 8-11  weights of stream 0 and 1, one thread a row
+//   warps 12-15   one thread a key: codes to fp16 in the products' layout, keys
+//                 and values, and q at an item's begin
+//
+// A code has 3 bits and a sign and a factor 8 bits, so c s is exact in fp16's
+// 11, as long as it stays in range: factors go in relative to the largest of
+// their 32 keys, whose exponents ek and ev the weights' threads put back. What
+// is below 2^-18 of the largest of the 32 loses bits. q is scaled into fp16's
+// range by a power of two a row. Elements are in the order in which they come
+// out of a word (0, 4, 1, 5, 2, 6, 3, 7), in q too, and in the sums until
+// they are written.
+//
+// Weights are p 2^(ev - E), E of a row rising like its maximum, so that
+// values of any size weigh what they should; sums of weights are of p itself.
+// The largest weight of a row is bounded (largest p times largest factor of 32
+// keys), not known; what is bounded is 2^8 when E is set, so that what lies
+// 2^-22 below it still has its bits.
+// A value row whose factor is not finite is 0 here, and its weight NaN for the
+// rows that see it.
+#pragma once
+
+#include "attend_q.cuh"
+#include "attend_tc.cuh"
+
+namespace tfx {
+
+constexpr int kQtcStages = 3;   // of codes
+enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcStages, kXQFull = kCEmpty + kQtcStages, kXQEmpty, kXKFull, kXKEmpty = kXKFull + 2,
+                  kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2, kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2,
+                  kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2, kXPvDone = kXPThree + 2, kXBarriers = kXPvDone + 2 };
+
+struct QtcShared {
+  unsigned long long bars[kXBarriers];
+  float row_max[2][128], row_sum[2][128];   // of the streams, at an item's end
+  int row_exp[2][128];
+  float row_factor[2][128];                 // of a stream's tile: scale log2(e) over the power that q was scaled by
+  int ek[2][4], ev[2][4];                   // exponents of each 32 keys of a stream's tile
+  uint32_t there[2][4], spoilt[2][4];       // keys that exist; keys whose value row is not finite
+  int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
+  int scratch[2 * (512 / 32) + 6];
+  uint32_t tmem;
+  int abort;
+};
+
+template <int D>
+struct QtcShape {
+  static constexpr int kThreads = 512;
+  static constexpr int kTile = 128, kGap = 4;
+  static constexpr int kParts = D / 64;                  // 64-column parts of a tile
+  static constexpr int kPartBytes = kTile * 128;
+  static constexpr int kTileBytes = kParts * kPartBytes;
+  static constexpr int kRowBytes = D / 2;                // of codes
+  static constexpr int kHalf = kTile * kRowBytes;
+  static constexpr int kStageBytes = 2 * kHalf + kTile * 4;   // codes of keys and values, factors
+  static constexpr int kKeysAt = kTileBytes, kValuesAt = kKeysAt + 2 * kTileBytes, kCodesAt = kValuesAt + 2 * kTileBytes;
+  static constexpr int kShared = kCodesAt + kQtcStages * kStageBytes;
+  static constexpr int kSmem = kShared + static_cast<int>(sizeof(QtcShared));
+  static_assert(kSmem <= 232448, "a block has 227 KB");
+  static constexpr int kScores = 0, kSums = 256, kColumns = 512;
+};
+
+struct QtcArgs {
+  QAttendArgs q;
+  int block_nodes;   // whole nodes of a row block
+};
+
+// One row of a tile, by its thread, as weigh() of attend_tc.cuh, with a factor
+// for the scores and one for the weights of each 32 keys. sc > 0 or 0.
+template <int D, bool kCut>
+__device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, float sc, const int* ek, const int* ev,
+                                        const uint32_t (&vis)[4], const uint32_t (&spoilt)[4], bool begun, uint32_t half,
+                                        uint32_t three, float* m_row, float* l_row, int* e_row) {
+  auto word_of = [](const uint32_t (&w)[4], int c) { return c < 2 ? (c == 0 ? w[0] : w[1]) : (c == 2 ? w[2] : w[3]); };
+  auto score_by = [&](int c) { return sc * power2(ek[c] - 8); };
+  float top = -INFINITY, need = -INFINITY;   // the largest score, the largest weight with its values' size
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    tmem_ld32(scores + c * 32, v);
+    const uint32_t word = kCut ? word_of(vis, c) : 0;
+    float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      if (kCut) {
+        if (!(word >> i & 1)) v[i] = -INFINITY;
+        if (!(word >> (i + 1) & 1)) v[i + 1] = -INFINITY;
+      }
+      hi[i / 2 % 4] = fmaxf(hi[i / 2 % 4], fmaxf(v[i], v[i + 1]));
+    }
+    float high = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+    high = high == -INFINITY ? -INFINITY : high * score_by(c);
+    top = fmaxf(top, high);
+    need = fmaxf(need, high + static_cast<float>(ev[c]));
+  }
+  float m = *m_row, l = *l_row;
+  int e = *e_row;
+  const bool rise = top > m + 8.f;
+  const float to = rise ? top : m;
+  const bool grow = need - to > static_cast<float>(e) + 15.f;   // a weight might pass fp16's range
+  if (__any_sync(~0u, rise || grow)) {
+    const float down = m - to;   // 0, or below
+    int to_e = e;
+    if (rise) to_e = max(-200, e + static_cast<int>(floorf(fmaxf(down, -400.f))));
+    if (rise || grow) to_e = max(to_e, static_cast<int>(ceilf(fmaxf(need - to, -190.f))) - 8);
+    l *= exp2_approx(down);
+    if (begun) {
+      const float f = exp2_approx(down + static_cast<float>(e - to_e));
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        float o[16];
+        uint32_t w[16];
+        tmem_ld16(sums + c * 16, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+        tmem_st16(sums + c * 16, w);
+      }
+    }
+    m = to;
+    e = to_e;
+  }
+  float2 sum[4] = {};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    float v[32];
+    tmem_ld32(scores + c * 32, v);
+    const uint32_t word = kCut ? word_of(vis, c) : 0, nans = kCut ? word_of(spoilt, c) : 0;
+    const float by = score_by(c), size = power2(max(-126, min(126, ev[c] - e)));
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float2 x = fma2(float2{v[2 * i], v[2 * i + 1]}, float2{by, by}, float2{-m, -m});
+      x.x = exp2_approx(x.x);
+      x.y = exp2_approx(x.y);
+      if (kCut) {
+        if (!(word >> (2 * i) & 1)) x.x = 0.f;
+        if (!(word >> (2 * i + 1) & 1)) x.y = 0.f;
+      }
+      sum[i % 4] = add2(sum[i % 4], x);
+      x = mul2(x, float2{size, size});
+      if (kCut) {
+        if (word & nans & (1u << (2 * i))) x.x = __uint_as_float(0x7FC00000u);
+        if (word & nans & (1u << (2 * i + 1))) x.y = __uint_as_float(0x7FC00000u);
+      }
+      w[i] = pack2(__half(), x.x, x.y);
+    }
+    tmem_st16(scores + c * 16, w);   // over scores already read
+    if (c == 1 || c == 2) {
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(c == 1 ? half : three);
+    }
+  }
+  const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+  *m_row = m;
+  *l_row = l + (both.x + both.y);
+  *e_row = e;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_constant__ QtcArgs args) {
+  using S = QtcShape<D>;
+  constexpr int kTile = S::kTile, kRB = S::kRowBytes;
+  const AttendArgs& a = args.q.a;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  QtcShared& sh = *reinterpret_cast<QtcShared*>(smem + S::kShared);
+  volatile int* abort_flag = &sh.abort;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
+  const int team = blockIdx.x / row_blocks;
+  const Rows own{static_cast<int>(blockIdx.x) - team * row_blocks, row_blocks};
+  const int node0 = own.rb * args.block_nodes;
+  const int rows = min(args.block_nodes, a.nodes - node0) * a.group;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t q_at = base, k_at = base + S::kKeysAt, v_at = base + S::kValuesAt;
+  auto bar = [&](int i) { return smem_u32(&sh.bars[i]); };
+  if (base & 1023) {   // the swizzled tiles need it; there is no static shared memory before them
+    if (tid == 0) atomicOr(a.c.err, kErrWait);
+    chain();
+    return;
+  }
+  if (tid == 0) {
+    sh.abort = 0;
+    for (int i = 0; i < kQtcStages; ++i) {
+      mbar_init(bar(kCFull + i), args.q.box ? 1 : 32);
+      mbar_init(bar(kCEmpty + i), 4);
+    }
+    mbar_init(bar(kXQFull), 4);
+    mbar_init(bar(kXQEmpty), 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kXKFull + i), 4);
+      mbar_init(bar(kXKEmpty + i), 1);
+      mbar_init(bar(kXVFull + i), 4);
+      mbar_init(bar(kXVEmpty + i), 1);
+      mbar_init(bar(kXSFull + i), 1);
+      mbar_init(bar(kXPFull + i), 128);
+      mbar_init(bar(kXPHalf + i), 128);
+      mbar_init(bar(kXPThree + i), 128);
+      mbar_init(bar(kXPvDone + i), 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem), S::kColumns);
+    tmem_relinquish();
+  }
+  chain();
+  Line line;
+  Cursor cur;
+  const int n_tiles = find_run<kTile, S::kGap, S::kThreads>(a, gridDim.x / row_blocks, team, sh.scratch, &line, &cur);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  // The registers of 512 threads, 128 each, are shared out anew: 72, 168, 168, 104.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (n_tiles == 0 || warp == 3) {
+      // nothing to do
+    } else if (warp == 0) {
+      // -------------------------------------------------------------- copies
+      const int box = args.q.box ? args.q.box : 1;
+      constexpr int kMost = 4;   // runs of a lane
+      int st = 0, phase = 1;
+      bool ok = true;
+      int page[kMost], row[kMost];
+      auto look_up = [&]() {
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+          const int run = k * 32 + lane, slot = cur.t * kTile + run * box, p = a.c.by_page(slot);
+          const bool exists = run * box < kTile && slot < cur.span.slots;
+          page[k] = exists ? a.c.page_table[cur.b * a.c.stride_table + p] : -1;
+          row[k] = slot - p * a.c.page_size;
+        }
+      };
+      look_up();
+#pragma unroll 1
+      for (int j = 0; j < n_tiles; ++j) {
+        int64_t at[kMost], with[kMost];
+        uint32_t there[kMost];
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+          // (a page outside the pool is recorded and left out by the threads of its keys)
+          const bool real = static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(a.c.pages);
+          there[k] = __ballot_sync(~0u, real);
+          at[k] = real ? page[k] * a.c.stride_page + row[k] * a.c.stride_token + cur.item * a.c.stride_head : -1;
+          with[k] = real ? page[k] * args.q.scale_page + row[k] * args.q.scale_token + cur.item * args.q.scale_head : 0;
+        }
+        if (j + 1 < n_tiles) {
+          advance<kTile, S::kGap>(a, &cur);
+          look_up();
+        }
+        if (j >= kQtcStages) ok = __all_sync(~0u, mbar_wait(bar(kCEmpty + st), phase, abort_flag));
+        if (!ok) break;
+        const uint32_t codes = base + S::kCodesAt + st * S::kStageBytes, factors = codes + 2 * S::kHalf;
+        const uint32_t full = bar(kCFull + st);
+        const uint8_t* kp = static_cast<const uint8_t*>(a.k);
+        const uint8_t* vp = static_cast<const uint8_t*>(a.v);
+        if (args.q.box) {   // 4 slots at least: no lane has a second run
+          const uint32_t bytes = box * kRB;
+          if (lane == 0) mbar_arrive_expect_tx(full, __popc(there[0]) * (2 * bytes + box * 4));
+          __syncwarp();
+#pragma unroll 1
+          for (uint32_t left = there[0]; left; left &= left - 1) {
+            const int run = __ffs(left) - 1;
+            const int64_t from = __shfl_sync(~0u, at[0], run), s_from = __shfl_sync(~0u, with[0], run);
+            if (elect_one()) {
+              copy_run(codes + run * bytes, kp + from, bytes, full);
+              copy_run(codes + S::kHalf + run * bytes, vp + from, bytes, full);
+              copy_run(factors + run * box * 4, args.q.scales + s_from, box * 4, full);
+            }
+            __syncwarp();
+          }
+        } else {
+          constexpr int kChunks = kRB / 16;
+#pragma unroll
+          for (int k = 0; k < kMost; ++k) {
+#pragma unroll
+            for (int n = 0; n < kChunks; ++n) {
+              const int id = n * 32 + lane;
+              const int64_t from = __shfl_sync(~0u, at[k], id / kChunks);
+              if (from >= 0) {
+                copy16(codes + (k * 32 * kChunks + id) * 16, kp + from + id % kChunks * 16, true);
+                copy16(codes + S::kHalf + (k * 32 * kChunks + id) * 16, vp + from + id % kChunks * 16, true);
+              }
+            }
+            if (at[k] >= 0) copy4(factors + (k * 32 + lane) * 4, args.q.scales + with[k]);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+        }
+        if (++st == kQtcStages) st = 0, phase ^= 1;
+      }
+      if (*abort_flag) {   // given up somewhere: the copies in flight still have to land
+        int again = 0;
+        for (int x = 0; x < kQtcStages; ++x) {
+          mbar_wait(bar(kCFull + x), 0, &again);
+          mbar_wait(bar(kCFull + x), 1, &again);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ products
+      const int s = warp - 1;
+      const uint32_t scores = tmem + S::kScores + s * 128, sums = tmem + S::kSums + s * D;
+      constexpr uint32_t kScoreDesc = idesc_of<__half>(128, false), kSumDesc = idesc_of<__half>(D, true);
+      const uint32_t k_tile = k_at + s * S::kTileBytes, v_tile = v_at + s * S::kTileBytes;
+      int n = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int ja = 0, n_items = 0; ja < n_tiles && ok; ++n_items) {   // the items of the run, tiles ja .. jb - 1
+        const int jb = ja + min(n_tiles - ja, cur.nt - cur.t), j0 = ja + ((ja ^ s) & 1);
+        ok = __all_sync(~0u, mbar_wait(bar(kXQFull), n_items & 1, abort_flag));
+        // a stream without a tile of the item does not hold q up
+        if (ok && j0 >= jb && jb < n_tiles && elect_one()) mbar_arrive(bar(kXQEmpty));
+        __syncwarp();
+#pragma unroll 1
+        for (int j = j0; j < jb && ok; j += 2) {
+          ok = mbar_wait(bar(kXKFull + s), n & 1, abort_flag);
+          // the weights lie over the scores until their product is done
+          if (ok && n > 0) ok = mbar_wait(bar(kXPvDone + s), (n - 1) & 1, abort_flag);
+          if (!__all_sync(~0u, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k / 4) * S::kPartBytes + (k % 4) * 32;
+              mma_ss(scores, smem_desc_sw128(q_at + off, 1024), smem_desc_sw128(k_tile + off, 1024), kScoreDesc, k > 0);
+            }
+            mma_commit(bar(kXSFull + s));
+            // only what someone will wait for, so that nothing arrives after the end
+            if (j + 2 < n_tiles) mma_commit(bar(kXKEmpty + s));
+            if (j + 2 >= jb && jb < n_tiles) mma_commit(bar(kXQEmpty));
+          }
+          __syncwarp();
+          ok = mbar_wait(bar(kXVFull + s), n & 1, abort_flag) && mbar_wait(bar(kXPHalf + s), n & 1, abort_flag);
+          if (!__all_sync(~0u, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          auto add_up = [&](int k) {
+            mma_ts(sums, scores + k * 8, desc_by_keys(v_tile + k * 2048, S::kPartBytes), kSumDesc, j > j0 || k > 0);
+          };
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k) add_up(k);
+          }
+          __syncwarp();
+          ok = __all_sync(~0u, mbar_wait(bar(kXPThree + s), n & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = kTile / 32; k < kTile / 64 * 3; ++k) add_up(k);
+          }
+          __syncwarp();
+          ok = __all_sync(~0u, mbar_wait(bar(kXPFull + s), n & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = kTile / 64 * 3; k < kTile / 16; ++k) add_up(k);
+            mma_commit(bar(kXPvDone + s));
+            if (j + 2 < n_tiles) mma_commit(bar(kXVEmpty + s));
+          }
+          __syncwarp();
+          ++n;
+        }
+        cur.t += jb - ja - 1;
+        advance<kTile, S::kGap>(a, &cur);
+        ja = jb;
+      }
+      if (!ok && n > 0) {   // given up: the products in flight still have to end
+        volatile int never = 0;
+        mbar_wait(bar(kXPvDone + s), (n - 1) & 1, &never);
+      }
+    }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    // ------------------------------------------------------- codes to fp16
+    const int key = tid - 384, quarter = warp - 12;   // a thread's key of a tile, and row of q
+    // 16-byte chunk c of row r of a tile in the products' layout.
+    auto place = [&](int at, int r, int c) {
+      return reinterpret_cast<uint4*>(smem + at + (c / 8) * S::kPartBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4));
+    };
+    // Codes of this thread's row times the factor s16, which is exact.
+    auto unpack_row = [&](const unsigned char* codes, int to, __half s16) {
+      const __half2 by = __half2half2(s16), by16 = __hmul2(by, __float2half2_rn(0.0625f));
+#pragma unroll
+      for (int it = 0; it < kRB / 16; ++it) {
+        // (this order keeps eight threads on different banks, reading and writing)
+        const int chunk = kRB == 64 ? (it + (key >> 1)) & 3 : (it + (key >> 2)) & 1;
+        const uint4 w4 = *reinterpret_cast<const uint4*>(codes + key * kRB + chunk * 16);
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = w[i] >> 8;
+          const uint32_t c[4] = {whole2<4, false>(w[i]), whole2<4, true>(w[i]), whole2<4, false>(x), whole2<4, true>(x)};
+          uint32_t y[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&c[z]), z & 1 ? by16 : by);
+            y[z] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          *place(to, key, chunk * 4 + i) = uint4{y[0], y[1], y[2], y[3]};
+        }
+      }
+    };
+    int st = 0, phase = 0, n_items = 0;
+    bool ok = true;
+    float row_factor = 0.f;   // of row `key` of the item
+    // The page of this thread's key, asked for a tile ahead: -1 where there is
+    // no such key (a -1 in the table becomes -2).
+    auto outside_is = [](int page) { return page == -1 ? -2 : page; };
+    auto page_of = [&](const Cursor& c) {
+      const int slot = c.t * kTile + key;
+      return slot < c.span.slots ? outside_is(a.c.page_table[c.b * a.c.stride_table + a.c.by_page(slot)]) : -1;
+    };
+    int next_page = n_tiles > 0 ? page_of(cur) : -1;
+#pragma unroll 1
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      const int s = j & 1, use = j >> 1;   // the stream, and how many of its tiles came before
+      const int page = next_page;
+      Cursor after = cur;
+      if (j + 1 < n_tiles) {
+        advance<kTile, S::kGap>(a, &after);
+        next_page = page_of(after);
+      }
+      if (j == 0 || cur.t == 0) {   // q of a new item
+        if (n_items > 0) ok = __all_sync(~0u, mbar_wait(bar(kXQEmpty), (n_items - 1) & 1, abort_flag));
+        if (!ok) break;
+        ++n_items;
+        uint4 raw[D / 8];
+        uint32_t top = 0;
+        const int node = key / a.group;
+        const T* from = static_cast<const T*>(a.q) + cur.b * a.q_seq + (node0 + node) * a.q_node +
+                        (cur.item * a.group + key - node * a.group) * a.q_head;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) raw[c] = key < rows ? reinterpret_cast<const uint4*>(from)[c] : uint4{0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          float x[8];
+          unpack8<T>(raw[c], x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        }
+        const int shift = top == 0 || top >= 0x7F800000u ? 0 : min(14 - exponent_of(__uint_as_float(top)), 126);
+        const float by = power2(shift);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          float x[8];
+          unpack8<T>(raw[c], x);
+          *place(0, key, c) = uint4{pack2(__half(), x[0] * by, x[4] * by), pack2(__half(), x[1] * by, x[5] * by),
+                                    pack2(__half(), x[2] * by, x[6] * by), pack2(__half(), x[3] * by, x[7] * by)};
+        }
+        row_factor = a.scale * kLog2e * power2(-shift);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kXQFull));
+      }
+      ok = __all_sync(~0u, mbar_wait(bar(kCFull + st), phase, abort_flag));
+      if (ok && use > 0) ok = __all_sync(~0u, mbar_wait(bar(kXKEmpty + s), (use - 1) & 1, abort_flag));
+      if (!ok) break;
+      const unsigned char* codes = smem + S::kCodesAt + st * S::kStageBytes;
+      const bool real = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
+      if (page != -1 && !real) record_index_error(a.c.err);
+      const uint32_t factors = real ? reinterpret_cast<const uint32_t*>(codes + 2 * S::kHalf)[key] : 0;
+      const float ks = key_scale(factors), vs = value_scale(factors);
+      const bool k_fine = (factors & 0x7F80u) != 0x7F80u, v_fine = (factors & 0x7F800000u) != 0x7F800000u;
+      const int ek = __reduce_max_sync(~0u, k_fine && ks != 0.f ? max(exponent_of(fabsf(ks)), -100) : -100);
+      const int ev = __reduce_max_sync(~0u, v_fine && vs != 0.f ? max(exponent_of(fabsf(vs)), -100) : -100);
+      const uint32_t there = __ballot_sync(~0u, real), spoilt = __ballot_sync(~0u, !v_fine);
+      unpack_row(codes, S::kKeysAt + s * S::kTileBytes, __float2half_rn(ks * power2(8 - ek)));
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kXKFull + s));
+      if (use > 0) ok = __all_sync(~0u, mbar_wait(bar(kXVEmpty + s), (use - 1) & 1, abort_flag));
+      if (!ok) break;
+      // (the weights of the stream's tile before are made: nobody reads its words any
+      // more. An item's factors go with its tiles too: the products that q was
+      // needed for may be done long before its weights are)
+      sh.row_factor[s][key] = row_factor;
+      if (lane == 0) {
+        sh.ek[s][quarter] = ek, sh.ev[s][quarter] = ev;
+        sh.there[s][quarter] = there, sh.spoilt[s][quarter] = spoilt;
+      }
+      unpack_row(codes + S::kHalf, S::kValuesAt + s * S::kTileBytes, __float2half_rn(v_fine ? vs * power2(8 - ev) : 0.f));
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kXVFull + s));
+        if (j + kQtcStages < n_tiles) mbar_arrive(bar(kCEmpty + st));
+      }
+      cur = after;
+      if (++st == kQtcStages) st = 0, phase ^= 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // --------------------------------------------------------------- weights
+    const int s = (warp - 4) / 4, row = (warp % 4) * 32 + lane, both = tid - 128;
+    const uint32_t mine = static_cast<uint32_t>((warp % 4) * 32) << 16;   // this warp's Tensor Memory lanes
+    const uint32_t scores = tmem + mine + S::kScores + s * 128, sums = tmem + mine + S::kSums + s * D;
+    const int row_node = row / a.group;
+    const int node = row < rows ? node0 + row_node : -1;
+    int n = 0, seen_b = -1;
+    Seen seen = {};
+#pragma unroll 1
+    for (int ja = 0; ja < n_tiles;) {   // the items of the run, tiles ja .. jb - 1 of it
+      const int jb = ja + min(n_tiles - ja, cur.nt - cur.t);
+      const int kvh = cur.item;
+      if (cur.b != seen_b) {   // the tree is its sequence's: another item of it has it still
+        seen_b = cur.b;
+        if (both < a.nodes) {
+          int p = a.parents[cur.b * a.stride_parents + both];
+          if (p >= both) {
+            record_index_error(a.c.err);
+            p = -2;
+          }
+          sh.up[both] = p < -2 ? -2 : p;
+        }
+        if (!group_all(3, 256, !*abort_flag)) break;
+        seen = node >= 0 ? seen_by(sh.up, node) : Seen{};
+      }
+      float m = kNoMax, l = 0.f;
+      int e = -200;
+      bool used = false;
+#pragma unroll 1
+      for (int j = ja + ((ja ^ s) & 1); j < jb; j += 2) {
+        const int slot0 = (cur.t + j - ja) * kTile;
+        mbar_wait(bar(kXSFull + s), n & 1, abort_flag);
+        // (held until this tile's product; makes the tile's words and the rows' factors visible)
+        mbar_wait(bar(kXVFull + s), n & 1, abort_flag);
+        __syncwarp();
+        tc_fence_after();
+        const float sc = sh.row_factor[s][row];
+        uint32_t vis[4], spoilt[4], all = ~0u, none = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          vis[w] = sh.there[s][w], spoilt[w] = sh.spoilt[s][w];
+          all &= vis[w];
+          none |= spoilt[w];
+        }
+        if (slot0 + kTile <= cur.span.context && all == ~0u && none == 0) {
+          weigh_q<D, false>(scores, sums, sc, sh.ek[s], sh.ev[s], vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
+                            &l, &e);
+        } else {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int off = slot0 + w * 32 - cur.span.context;   // tree node of the word's first key
+            uint32_t word = ~0u;
+            if (off > -32) {
+              word = off >= 0 ? __funnelshift_r(seen_word(seen, off >> 5), seen_word(seen, (off >> 5) + 1), off & 31)
+                              : (seen.w[0] << -off) | ((1u << -off) - 1);
+            }
+            vis[w] = node >= 0 ? word & vis[w] : 0u;
+          }
+          weigh_q<D, true>(scores, sums, sc, sh.ek[s], sh.ev[s], vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
+                           &l, &e);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kXPFull + s));
+        used = true;
+        ++n;
+      }
+      {
+        // The streams' sums together; each group takes half of the columns.
+        if (used) mbar_wait(bar(kXPvDone + s), (n - 1) & 1, abort_flag);
+        __syncwarp();
+        sh.row_max[s][row] = used && m > kNoMax ? m : -INFINITY;
+        sh.row_sum[s][row] = used ? l : 0.f;
+        sh.row_exp[s][row] = e;
+        tc_fence_before();
+        if (!group_all(3, 256, !*abort_flag)) break;
+        tc_fence_after();
+        const float m0 = sh.row_max[0][row], m1 = sh.row_max[1][row], top = fmaxf(m0, m1);
+        const float low = top == -INFINITY ? 0.f : top;
+        const float sum = exp2_approx(m0 - low) * sh.row_sum[0][row] + exp2_approx(m1 - low) * sh.row_sum[1][row];
+        const float f0 = exp2_approx(m0 - low + static_cast<float>(sh.row_exp[0][row] - 8));
+        const float f1 = exp2_approx(m1 - low + static_cast<float>(sh.row_exp[1][row] - 8));
+        // A stream without a tile of this item has nothing in its columns.
+        const bool has0 = jb - ja > 1 || (ja & 1) == 0, has1 = jb - ja > 1 || (ja & 1) == 1;
+        const bool whole = cur.t == 0 && cur.nt == jb - ja;
+        const bool idle = cur.span.context < 0;
+        const bool present = node >= 0 && !idle && sh.up[node] >= -1;
+        const bool empty = !present || sum == 0.f;
+        const float inv = whole ? (empty ? 0.f : 1.f / sum) : 1.f;
+        const size_t out_at = node >= 0 ? (static_cast<size_t>(cur.b) * a.nodes + node) * a.heads + kvh * a.group +
+                                              row - row_node * a.group : 0;
+        T* out = static_cast<T*>(a.out) + out_at * D;
+        float* part = a.partials + part_index(line, own, team, cur.first) * kPartFloats<128, D>;
+#pragma unroll 1
+        for (int c = s * (D / 2); c < (s + 1) * (D / 2); c += 16) {
+          float x[16] = {}, y[16] = {};
+          if (has0) tmem_ld16(tmem + mine + S::kSums + c, x);
+          if (has1) tmem_ld16(tmem + mine + S::kSums + D + c, y);
+          float z[16];   // in the order of the head again
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int from = (i & 8) + (i & 4 ? 2 * (i & 3) + 1 : 2 * (i & 3));
+            z[i] = (f0 * x[from] + f1 * y[from]) * inv;
+          }
+          if (node < 0) continue;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+              *reinterpret_cast<uint4*>(out + c + i) =
+                  empty ? uint4{0, 0, 0, 0}
+                        : uint4{pack2(T(), z[i], z[i + 1]), pack2(T(), z[i + 2], z[i + 3]), pack2(T(), z[i + 4], z[i + 5]),
+                                pack2(T(), z[i + 6], z[i + 7])};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(part + (c + i) * 128 + row, z[i]);
+          }
+        }
+        tc_fence_before();
+        if (node >= 0 && s == 0) {
+          if (whole) {
+            a.lse[out_at] = empty ? -INFINITY : (top + log2f(sum)) * kLn2;
+          } else {
+            part[128 * D + row] = top;
+            part[128 * D + 128 + row] = sum;
+          }
+        }
+        // Sums, parents and maxima have been read.
+        if (!group_all(3, 256, true)) break;
+      }
+      cur.t += jb - ja - 1;
+      advance<kTile, S::kGap>(a, &cur);
+      ja = jb;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, S::kColumns);
+  if (tid == 0 && sh.abort) atomicOr(a.c.err, kErrWait);
+}
+
+}  // namespace tfx

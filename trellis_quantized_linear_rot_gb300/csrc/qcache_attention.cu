@@ -3,7 +3,7 @@
 #include <algorithm>
 #include <numeric>
 
-#include "attend_q.cuh"
+#include "attend_qtc.cuh"
 
 namespace tfx {
 namespace {
@@ -49,9 +49,36 @@ cudaError_t launch(QAttendArgs x, int device, cudaStream_t s) {
   return launch_join<T, S::kRows, D, S::kTile, S::kGap>(a, blocks / row_blocks, row_blocks, S::kRows, s);
 }
 
+// More than kManyRows rows of 4 bits a kv head.
+template <typename T, int D>
+cudaError_t launch_tc(QAttendArgs x, int device, cudaStream_t s) {
+  using S = QtcShape<D>;
+  AttendArgs& a = x.a;
+  static PerDeviceOnce<kMaxDevices> once;
+  const int e = once.run(device, cudaErrorInvalidDevice, [] {
+    return static_cast<int>(
+        cudaFuncSetAttribute(kvq_attention_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem));
+  });
+  if (e != cudaSuccess) return static_cast<cudaError_t>(e);
+  x.box = run_of_slots(x, S::kTile, S::kRowBytes);
+  const QtcArgs args = {x, std::min(S::kTile / a.group, a.nodes)};
+  const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
+  const int blocks = team_blocks(a.num_sms, row_blocks);
+  const cudaError_t launched =
+      launch_chained(kvq_attention_tc_kernel<T, D>, dim3(blocks), dim3(S::kThreads), S::kSmem, 1, s, args);
+  // No item has a second tile to be cut off.
+  if (launched != cudaSuccess || static_cast<int64_t>(a.c.table_width) * a.c.page_size <= S::kTile) return launched;
+  return launch_join<T, 128, D, S::kTile, S::kGap>(a, blocks / row_blocks, row_blocks, args.block_nodes * a.group, s);
+}
+
+constexpr int kManyRows = 16;
+
 template <typename T, int kBits>
 cudaError_t by_dim(const QAttendArgs& x, int device, cudaStream_t s) {
   const int rows = x.a.nodes * x.a.group;
+  if constexpr (kBits == 4)
+    if (rows > kManyRows && x.a.group <= 128 && x.a.scale >= 0.f && x.a.c.head_dim != 256)
+      return x.a.c.head_dim == 64 ? launch_tc<T, 64>(x, device, s) : launch_tc<T, 128>(x, device, s);
   switch (x.a.c.head_dim) {
     case 64:
       return rows <= 8 ? launch<T, kBits, 64, 1>(x, device, s)
@@ -74,7 +101,10 @@ AttendWorkspace kvq_attend_workspace(int nodes, int heads, int kv_heads, int hea
   const size_t places = static_cast<size_t>(kMostBlocks) * num_sms;
   AttendWorkspace w;
   w.partials_at = (2 * places * sizeof(int) + 255) & ~static_cast<size_t>(255);
-  w.bytes = w.partials_at + 2 * std::max<size_t>(places, (rows + 7) / 8) * 16 * (head_dim + 2) * sizeof(float);
+  size_t part_rows = std::max<size_t>(places, (rows + 7) / 8) * 16;
+  // Blocks of rows of the tcgen05 kernel hold whole nodes, of 128 rows at most.
+  if (rows > kManyRows) part_rows = std::max(part_rows, std::max<size_t>(num_sms, nodes) * 128);
+  w.bytes = w.partials_at + 2 * part_rows * (head_dim + 2) * sizeof(float);
   return w;
 }
 
