@@ -6,8 +6,8 @@
 //   warp 0        copies of codes and factors, three tiles in flight
 //   warps 1, 2    products of stream 0 and 1
 //   warps 4-7, 8-11  weights of stream 0 and 1, one thread a row
-//   warps 12-15   one thread a key: codes to fp16 in the products' layout, keys
-//                 and values, and q at an item's begin
+//   warps 12-15, 16-19  codes of stream 0 and 1 to fp16 in the products' layout,
+//                 keys and values, one thread a key, and q at an item's begin
 //
 // A code has 3 bits and a sign and a factor 8 bits, so c s is exact in fp16's
 // 11, as long as it stays in range: factors go in relative to the largest of
@@ -31,8 +31,10 @@
 
 namespace tfx {
 
-constexpr int kQtcStages = 3;   // of codes
-enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcStages, kXQFull = kCEmpty + kQtcStages, kXQEmpty, kXKFull, kXKEmpty = kXKFull + 2,
+// Codes of tile j lie in stage j % 3 and are stream j % 2's; their barriers are
+// number j % 6, so that whoever waits on one waits for each of its phases.
+constexpr int kQtcStages = 3, kQtcSlots = 6;
+enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcSlots, kXQFull = kCEmpty + kQtcSlots, kXQEmpty, kXKFull, kXKEmpty = kXKFull + 2,
                   kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2, kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2,
                   kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2, kXPvDone = kXPThree + 2, kXBarriers = kXPvDone + 2 };
 
@@ -44,14 +46,14 @@ struct QtcShared {
   int ek[2][4], ev[2][4];                   // exponents of each 32 keys of a stream's tile
   uint32_t there[2][4], spoilt[2][4];       // keys that exist; keys whose value row is not finite
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
-  int scratch[2 * (512 / 32) + 6];
+  int scratch[2 * (640 / 32) + 6];
   uint32_t tmem;
   int abort;
 };
 
 template <int D>
 struct QtcShape {
-  static constexpr int kThreads = 512;
+  static constexpr int kThreads = 640;
   static constexpr int kTile = 128, kGap = 4;
   static constexpr int kParts = D / 64;                  // 64-column parts of a tile
   static constexpr int kPartBytes = kTile * 128;
@@ -164,7 +166,7 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, float sc
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_constant__ QtcArgs args) {
+__global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_constant__ QtcArgs args) {
   using S = QtcShape<D>;
   constexpr int kTile = S::kTile, kRB = S::kRowBytes;
   const AttendArgs& a = args.q.a;
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
   }
   if (tid == 0) {
     sh.abort = 0;
-    for (int i = 0; i < kQtcStages; ++i) {
+    for (int i = 0; i < kQtcSlots; ++i) {
       mbar_init(bar(kCFull + i), args.q.box ? 1 : 32);
       mbar_init(bar(kCEmpty + i), 4);
     }
@@ -219,16 +221,15 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  // The registers of 512 threads, 128 each, are shared out anew: 72, 168, 168, 104.
+  // The registers of 640 threads, 96 each, are shared out anew: the first four
+  // warps keep theirs, 32 go from a thread of the last eight to one of weights.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (n_tiles == 0 || warp == 3) {
       // nothing to do
     } else if (warp == 0) {
       // -------------------------------------------------------------- copies
       const int box = args.q.box ? args.q.box : 1;
       constexpr int kMost = 4;   // runs of a lane
-      int st = 0, phase = 1;
       bool ok = true;
       int page[kMost], row[kMost];
       auto look_up = [&]() {
@@ -257,10 +258,12 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
           advance<kTile, S::kGap>(a, &cur);
           look_up();
         }
-        if (j >= kQtcStages) ok = __all_sync(~0u, mbar_wait(bar(kCEmpty + st), phase, abort_flag));
+        const int st = j % kQtcStages, before = j - kQtcStages;   // the tile before in its stage
+        if (before >= 0)
+          ok = __all_sync(~0u, mbar_wait(bar(kCEmpty + before % kQtcSlots), (before / kQtcSlots) & 1, abort_flag));
         if (!ok) break;
         const uint32_t codes = base + S::kCodesAt + st * S::kStageBytes, factors = codes + 2 * S::kHalf;
-        const uint32_t full = bar(kCFull + st);
+        const uint32_t full = bar(kCFull + j % kQtcSlots);
         const uint8_t* kp = static_cast<const uint8_t*>(a.k);
         const uint8_t* vp = static_cast<const uint8_t*>(a.v);
         if (args.q.box) {   // 4 slots at least: no lane has a second run
@@ -295,11 +298,10 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
         }
-        if (++st == kQtcStages) st = 0, phase ^= 1;
       }
       if (*abort_flag) {   // given up somewhere: the copies in flight still have to land
         int again = 0;
-        for (int x = 0; x < kQtcStages; ++x) {
+        for (int x = 0; x < kQtcSlots; ++x) {
           mbar_wait(bar(kCFull + x), 0, &again);
           mbar_wait(bar(kCFull + x), 1, &again);
         }
@@ -385,9 +387,9 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
       }
     }
   } else if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ------------------------------------------------------- codes to fp16
-    const int key = tid - 384, quarter = warp - 12;   // a thread's key of a tile, and row of q
+    const int s = (warp - 12) / 4, key = (tid - 384) % 128, quarter = (warp - 12) % 4;   // a thread's key of a tile, and row of q
     // 16-byte chunk c of row r of a tile in the products' layout.
     auto place = [&](int at, int r, int c) {
       return reinterpret_cast<uint4*>(smem + at + (c / 8) * S::kPartBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4));
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
         }
       }
     };
-    int st = 0, phase = 0, n_items = 0;
+    int n_items = 0;
     bool ok = true;
     float row_factor = 0.f;   // of row `key` of the item
     // The page of this thread's key, asked for a tile ahead: -1 where there is
@@ -425,49 +427,62 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
       const int slot = c.t * kTile + key;
       return slot < c.span.slots ? outside_is(a.c.page_table[c.b * a.c.stride_table + a.c.by_page(slot)]) : -1;
     };
-    int next_page = n_tiles > 0 ? page_of(cur) : -1;
+    // q of an item: its rows' factors for both streams, q itself by the one
+    // that has the item's first tile.
+    auto new_item = [&](const Cursor& c, bool first) {
+      // (both wait for every item's, so that neither passes over a phase)
+      if (n_items > 0) ok = __all_sync(~0u, mbar_wait(bar(kXQEmpty), (n_items - 1) & 1, abort_flag));
+      ++n_items;
+      if (!ok) return;
+      const int node = key / a.group;
+      const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + c.b * a.q_seq + (node0 + node) * a.q_node +
+                                                         (c.item * a.group + key - node * a.group) * a.q_head);
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        float x[8];
+        unpack8<T>(key < rows ? from[i] : uint4{0, 0, 0, 0}, x);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) top = max(top, __float_as_uint(x[y]) & 0x7FFFFFFFu);
+      }
+      const int shift = top == 0 || top >= 0x7F800000u ? 0 : min(14 - exponent_of(__uint_as_float(top)), 126);
+      const float by = power2(shift);
+      row_factor = a.scale * kLog2e * power2(-shift);
+      if (!first) return;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        float x[8];
+        unpack8<T>(key < rows ? from[i] : uint4{0, 0, 0, 0}, x);
+        *place(0, key, i) = uint4{pack2(__half(), x[0] * by, x[4] * by), pack2(__half(), x[1] * by, x[5] * by),
+                                  pack2(__half(), x[2] * by, x[6] * by), pack2(__half(), x[3] * by, x[7] * by)};
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kXQFull));
+    };
+    int next_page = -1;
 #pragma unroll 1
     for (int j = 0; j < n_tiles && ok; ++j) {
-      const int s = j & 1, use = j >> 1;   // the stream, and how many of its tiles came before
+      const bool first = j == 0 || cur.t == 0;
+      if ((j & 1) != s) {   // the other stream's
+        if (first) new_item(cur, false);
+        advance<kTile, S::kGap>(a, &cur);
+        if (j == 0 && n_tiles > 1) next_page = page_of(cur);
+        continue;
+      }
+      if (j == 0) next_page = page_of(cur);
+      const int use = j >> 1;   // the stream's tiles before
+      if (first) new_item(cur, true);
+      if (!ok) break;
       const int page = next_page;
       Cursor after = cur;
-      if (j + 1 < n_tiles) {
+      if (j + 2 < n_tiles) {
+        advance<kTile, S::kGap>(a, &after);
         advance<kTile, S::kGap>(a, &after);
         next_page = page_of(after);
       }
-      if (j == 0 || cur.t == 0) {   // q of a new item
-        if (n_items > 0) ok = __all_sync(~0u, mbar_wait(bar(kXQEmpty), (n_items - 1) & 1, abort_flag));
-        if (!ok) break;
-        ++n_items;
-        uint4 raw[D / 8];
-        uint32_t top = 0;
-        const int node = key / a.group;
-        const T* from = static_cast<const T*>(a.q) + cur.b * a.q_seq + (node0 + node) * a.q_node +
-                        (cur.item * a.group + key - node * a.group) * a.q_head;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) raw[c] = key < rows ? reinterpret_cast<const uint4*>(from)[c] : uint4{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          float x[8];
-          unpack8<T>(raw[c], x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-        }
-        const int shift = top == 0 || top >= 0x7F800000u ? 0 : min(14 - exponent_of(__uint_as_float(top)), 126);
-        const float by = power2(shift);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          float x[8];
-          unpack8<T>(raw[c], x);
-          *place(0, key, c) = uint4{pack2(__half(), x[0] * by, x[4] * by), pack2(__half(), x[1] * by, x[5] * by),
-                                    pack2(__half(), x[2] * by, x[6] * by), pack2(__half(), x[3] * by, x[7] * by)};
-        }
-        row_factor = a.scale * kLog2e * power2(-shift);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kXQFull));
-      }
-      ok = __all_sync(~0u, mbar_wait(bar(kCFull + st), phase, abort_flag));
+      const int st = j % kQtcStages, slot_j = j % kQtcSlots;
+      ok = __all_sync(~0u, mbar_wait(bar(kCFull + slot_j), (j / kQtcSlots) & 1, abort_flag));
       if (ok && use > 0) ok = __all_sync(~0u, mbar_wait(bar(kXKEmpty + s), (use - 1) & 1, abort_flag));
       if (!ok) break;
       const unsigned char* codes = smem + S::kCodesAt + st * S::kStageBytes;
@@ -498,13 +513,12 @@ __global__ void __launch_bounds__(512, 1) kvq_attention_tc_kernel(const __grid_c
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(kXVFull + s));
-        if (j + kQtcStages < n_tiles) mbar_arrive(bar(kCEmpty + st));
+        if (j + kQtcStages < n_tiles) mbar_arrive(bar(kCEmpty + slot_j));
       }
-      cur = after;
-      if (++st == kQtcStages) st = 0, phase ^= 1;
+      advance<kTile, S::kGap>(a, &cur);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     // --------------------------------------------------------------- weights
     const int s = (warp - 4) / 4, row = (warp % 4) * 32 + lane, both = tid - 128;
     const uint32_t mine = static_cast<uint32_t>((warp % 4) * 32) << 16;   // this warp's Tensor Memory lanes
