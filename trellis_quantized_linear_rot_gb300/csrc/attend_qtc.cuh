@@ -36,15 +36,20 @@ namespace tfx {
 constexpr int kQtcStages = 3, kQtcSlots = 6;
 enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcSlots, kXQFull = kCEmpty + kQtcSlots, kXQEmpty, kXKFull, kXKEmpty = kXKFull + 2,
                   kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2, kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2,
-                  kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2, kXPvDone = kXPThree + 2, kXBarriers = kXPvDone + 2 };
+                  kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2, kXPvDone = kXPThree + 2, kXWords = kXPvDone + 2,
+                  kXBarriers = kXWords + 4 };
 
 struct QtcShared {
   unsigned long long bars[kXBarriers];
   float row_max[2][128], row_sum[2][128];   // of the streams, at an item's end
   int row_exp[2][128];
-  float row_factor[2][128];                 // of a stream's tile: scale log2(e) over the power that q was scaled by
-  int ek[2][4], ev[2][4];                   // exponents of each 32 keys of a stream's tile
-  uint32_t there[2][4], spoilt[2][4];       // keys that exist; keys whose value row is not finite
+  // What the weights need to know of a stream's tile, in places by turns: the
+  // place is written with the tile's keys, while the tile before is weighed.
+  struct Words {
+    float row_factor[128];                  // scale log2(e) over the power that q was scaled by
+    int ek[4], ev[4];                       // exponents of each 32 keys
+    uint32_t there[4], spoilt[4];           // keys that exist; keys whose value row is not finite
+  } words[2][2];
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
   int scratch[2 * (640 / 32) + 6];
   uint32_t tmem;
@@ -205,6 +210,8 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       mbar_init(bar(kXPHalf + i), 128);
       mbar_init(bar(kXPThree + i), 128);
       mbar_init(bar(kXPvDone + i), 1);
+      mbar_init(bar(kXWords + i), 4);
+      mbar_init(bar(kXWords + 2 + i), 4);
     }
     fence_barrier_init();
   }
@@ -228,75 +235,99 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       // nothing to do
     } else if (warp == 0) {
       // -------------------------------------------------------------- copies
-      const int box = args.q.box ? args.q.box : 1;
-      constexpr int kMost = 4;   // runs of a lane
-      bool ok = true;
-      int page[kMost], row[kMost];
-      auto look_up = [&]() {
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-          const int run = k * 32 + lane, slot = cur.t * kTile + run * box, p = a.c.by_page(slot);
-          const bool exists = run * box < kTile && slot < cur.span.slots;
-          page[k] = exists ? a.c.page_table[cur.b * a.c.stride_table + p] : -1;
-          row[k] = slot - p * a.c.page_size;
-        }
+      // (a page outside the pool is recorded and left out by the threads of its keys)
+      const uint8_t* kp = static_cast<const uint8_t*>(a.k);
+      const uint8_t* vp = static_cast<const uint8_t*>(a.v);
+      auto stage_free = [&](int j) {
+        const int before = j - kQtcStages;   // the tile before in its stage
+        return before < 0 || __all_sync(~0u, mbar_wait(bar(kCEmpty + before % kQtcSlots), (before / kQtcSlots) & 1, abort_flag));
       };
-      look_up();
+      auto codes_of = [&](int j) { return base + S::kCodesAt + j % kQtcStages * S::kStageBytes; };
+      if (args.q.box) {   // 4 slots at least: a lane has a run
+        const int box = args.q.box, here = lane < kTile / box ? lane * box : 1 << 30;   // (no slot comes near that)
+        const uint32_t bytes = box * kRB;
+        const int32_t* pages = a.c.page_table + cur.b * a.c.stride_table;
+        const uint8_t* k_head = kp + cur.item * a.c.stride_head;
+        const uint32_t* s_head = args.q.scales + cur.item * args.q.scale_head;
+        int page = -1, row = 0;
+        auto look_up = [&]() {
+          const int slot = cur.t * kTile + here;
+          page = -1;
+          if (slot < cur.span.slots) {
+            const int p = a.c.by_page(slot);
+            page = pages[p];
+            row = slot - p * a.c.page_size;
+          }
+        };
+        look_up();
 #pragma unroll 1
-      for (int j = 0; j < n_tiles; ++j) {
-        int64_t at[kMost], with[kMost];
-        uint32_t there[kMost];
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-          // (a page outside the pool is recorded and left out by the threads of its keys)
-          const bool real = static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(a.c.pages);
-          there[k] = __ballot_sync(~0u, real);
-          at[k] = real ? page[k] * a.c.stride_page + row[k] * a.c.stride_token + cur.item * a.c.stride_head : -1;
-          with[k] = real ? page[k] * args.q.scale_page + row[k] * args.q.scale_token + cur.item * args.q.scale_head : 0;
-        }
-        if (j + 1 < n_tiles) {
-          advance<kTile, S::kGap>(a, &cur);
-          look_up();
-        }
-        const int st = j % kQtcStages, before = j - kQtcStages;   // the tile before in its stage
-        if (before >= 0)
-          ok = __all_sync(~0u, mbar_wait(bar(kCEmpty + before % kQtcSlots), (before / kQtcSlots) & 1, abort_flag));
-        if (!ok) break;
-        const uint32_t codes = base + S::kCodesAt + st * S::kStageBytes, factors = codes + 2 * S::kHalf;
-        const uint32_t full = bar(kCFull + j % kQtcSlots);
-        const uint8_t* kp = static_cast<const uint8_t*>(a.k);
-        const uint8_t* vp = static_cast<const uint8_t*>(a.v);
-        if (args.q.box) {   // 4 slots at least: no lane has a second run
-          const uint32_t bytes = box * kRB;
-          if (lane == 0) mbar_arrive_expect_tx(full, __popc(there[0]) * (2 * bytes + box * 4));
+        for (int j = 0; j < n_tiles; ++j) {
+          const bool real = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
+          const uint8_t* k_at = k_head + static_cast<uint64_t>(static_cast<uint32_t>(page)) * a.c.stride_page + row * kRB;
+          const uint32_t* s_at = s_head + static_cast<uint64_t>(static_cast<uint32_t>(page)) * args.q.scale_page + row;
+          const uint32_t there = __ballot_sync(~0u, real);
+          if (j + 1 < n_tiles) {
+            if (++cur.t == cur.nt) {   // the next item
+              cur.t = cur.nt - 1;
+              advance<kTile, S::kGap>(a, &cur);
+              pages = a.c.page_table + cur.b * a.c.stride_table;
+              k_head = kp + cur.item * a.c.stride_head;
+              s_head = args.q.scales + cur.item * args.q.scale_head;
+            }
+            look_up();
+          }
+          if (!stage_free(j)) break;
+          const uint32_t full = bar(kCFull + j % kQtcSlots), codes = codes_of(j);
+          if (lane == 0) mbar_arrive_expect_tx(full, __popc(there) * (2 * bytes + box * 4));
           __syncwarp();
 #pragma unroll 1
-          for (uint32_t left = there[0]; left; left &= left - 1) {
+          for (uint32_t left = there; left; left &= left - 1) {
             const int run = __ffs(left) - 1;
-            const int64_t from = __shfl_sync(~0u, at[0], run), s_from = __shfl_sync(~0u, with[0], run);
+            const uint64_t from = __shfl_sync(~0u, reinterpret_cast<uint64_t>(k_at), run);
+            const uint64_t with = __shfl_sync(~0u, reinterpret_cast<uint64_t>(s_at), run);
             if (elect_one()) {
-              copy_run(codes + run * bytes, kp + from, bytes, full);
-              copy_run(codes + S::kHalf + run * bytes, vp + from, bytes, full);
-              copy_run(factors + run * box * 4, args.q.scales + s_from, box * 4, full);
+              copy_run(codes + run * bytes, reinterpret_cast<const void*>(from), bytes, full);
+              copy_run(codes + S::kHalf + run * bytes, reinterpret_cast<const void*>(from + (vp - kp)), bytes, full);
+              copy_run(codes + 2 * S::kHalf + run * box * 4, reinterpret_cast<const void*>(with), box * 4, full);
             }
             __syncwarp();
           }
-        } else {
-          constexpr int kChunks = kRB / 16;
-#pragma unroll
-          for (int k = 0; k < kMost; ++k) {
+        }
+      } else {   // a lane has a key of each 32
+        constexpr int kChunks = kRB / 16;
+#pragma unroll 1
+        for (int j = 0; j < n_tiles; ++j) {
+          const int32_t* pages = a.c.page_table + cur.b * a.c.stride_table;
+          auto look = [&](int k, int* row) {
+            const int slot = cur.t * kTile + k * 32 + lane, p = a.c.by_page(slot);
+            *row = slot - p * a.c.page_size;
+            return slot < cur.span.slots ? pages[p] : -1;
+          };
+          int next_row, next_page = look(0, &next_row);
+          if (!stage_free(j)) break;
+          const uint32_t full = bar(kCFull + j % kQtcSlots), codes = codes_of(j);
+#pragma unroll 1
+          for (int k = 0; k < kTile / 32; ++k) {
+            const int page = next_page, row = next_row;
+            if (k + 1 < kTile / 32) next_page = look(k + 1, &next_row);
+            const bool real = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
+            const int64_t at = real ? page * a.c.stride_page + row * a.c.stride_token + cur.item * a.c.stride_head : -1;
+            const uint32_t into = codes + (k * 32 * kChunks + lane) * 16;
 #pragma unroll
             for (int n = 0; n < kChunks; ++n) {
               const int id = n * 32 + lane;
-              const int64_t from = __shfl_sync(~0u, at[k], id / kChunks);
+              const int64_t from = __shfl_sync(~0u, at, id / kChunks);
               if (from >= 0) {
-                copy16(codes + (k * 32 * kChunks + id) * 16, kp + from + id % kChunks * 16, true);
-                copy16(codes + S::kHalf + (k * 32 * kChunks + id) * 16, vp + from + id % kChunks * 16, true);
+                copy16(into + n * 512, kp + from + id % kChunks * 16, true);
+                copy16(into + n * 512 + S::kHalf, vp + from + id % kChunks * 16, true);
               }
             }
-            if (at[k] >= 0) copy4(factors + (k * 32 + lane) * 4, args.q.scales + with[k]);
+            if (real)
+              copy4(codes + 2 * S::kHalf + (k * 32 + lane) * 4,
+                    args.q.scales + page * args.q.scale_page + row * args.q.scale_token + cur.item * args.q.scale_head);
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+          advance<kTile, S::kGap>(a, &cur);
         }
       }
       if (*abort_flag) {   // given up somewhere: the copies in flight still have to land
@@ -494,20 +525,22 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       const int ek = __reduce_max_sync(~0u, k_fine && ks != 0.f ? max(exponent_of(fabsf(ks)), -100) : -100);
       const int ev = __reduce_max_sync(~0u, v_fine && vs != 0.f ? max(exponent_of(fabsf(vs)), -100) : -100);
       const uint32_t there = __ballot_sync(~0u, real), spoilt = __ballot_sync(~0u, !v_fine);
+      // (the scores of the stream's tile before are made, which came after the
+      // weights of the one before that: nobody reads this place any more)
+      QtcShared::Words& words = sh.words[s][use & 1];
+      words.row_factor[key] = row_factor;
+      if (lane == 0) {
+        words.ek[quarter] = ek, words.ev[quarter] = ev;
+        words.there[quarter] = there, words.spoilt[quarter] = spoilt;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kXWords + 2 * s + (use & 1)));
       unpack_row(codes, S::kKeysAt + s * S::kTileBytes, __float2half_rn(ks * power2(8 - ek)));
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kXKFull + s));
       if (use > 0) ok = __all_sync(~0u, mbar_wait(bar(kXVEmpty + s), (use - 1) & 1, abort_flag));
       if (!ok) break;
-      // (the weights of the stream's tile before are made: nobody reads its words any
-      // more. An item's factors go with its tiles too: the products that q was
-      // needed for may be done long before its weights are)
-      sh.row_factor[s][key] = row_factor;
-      if (lane == 0) {
-        sh.ek[s][quarter] = ek, sh.ev[s][quarter] = ev;
-        sh.there[s][quarter] = there, sh.spoilt[s][quarter] = spoilt;
-      }
       unpack_row(codes + S::kHalf, S::kValuesAt + s * S::kTileBytes, __float2half_rn(v_fine ? vs * power2(8 - ev) : 0.f));
       fence_proxy_async_shared();
       __syncwarp();
@@ -551,20 +584,20 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       for (int j = ja + ((ja ^ s) & 1); j < jb; j += 2) {
         const int slot0 = (cur.t + j - ja) * kTile;
         mbar_wait(bar(kXSFull + s), n & 1, abort_flag);
-        // (held until this tile's product; makes the tile's words and the rows' factors visible)
-        mbar_wait(bar(kXVFull + s), n & 1, abort_flag);
+        mbar_wait(bar(kXWords + 2 * s + (n & 1)), (n >> 1) & 1, abort_flag);
         __syncwarp();
         tc_fence_after();
-        const float sc = sh.row_factor[s][row];
+        const QtcShared::Words& words = sh.words[s][n & 1];
+        const float sc = words.row_factor[row];
         uint32_t vis[4], spoilt[4], all = ~0u, none = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          vis[w] = sh.there[s][w], spoilt[w] = sh.spoilt[s][w];
+          vis[w] = words.there[w], spoilt[w] = words.spoilt[w];
           all &= vis[w];
           none |= spoilt[w];
         }
         if (slot0 + kTile <= cur.span.context && all == ~0u && none == 0) {
-          weigh_q<D, false>(scores, sums, sc, sh.ek[s], sh.ev[s], vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
+          weigh_q<D, false>(scores, sums, sc, words.ek, words.ev, vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
                             &l, &e);
         } else {
 #pragma unroll
@@ -577,7 +610,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
             }
             vis[w] = node >= 0 ? word & vis[w] : 0u;
           }
-          weigh_q<D, true>(scores, sums, sc, sh.ek[s], sh.ev[s], vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
+          weigh_q<D, true>(scores, sums, sc, words.ek, words.ev, vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
                            &l, &e);
         }
         tmem_wait_st();
