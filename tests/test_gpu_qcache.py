@@ -296,6 +296,31 @@ def test_write_is_the_definition_and_touches_nothing_else(bits, dtype, n, kh, d,
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_write_factors_of_every_16_bit_number(bits, dtype):
+    """A row for each finite magnitude that the type has as its largest, with
+    parts of it in the others: ties, and what is next to them."""
+    tops = torch.arange(0, 1 << 15, dtype=torch.int16, device="cuda").view(DT[dtype])
+    tops = tops[torch.isfinite(tops)]
+    n, most = len(tops), 7 if bits == 4 else 127
+    share = torch.linspace(-1, 1, 64, device="cuda", dtype=torch.float64)
+    share[:30] = (torch.arange(30, device="cuda") - 14.5) / most     # near ties
+    share[0] = -1.0
+    for parts in (share, share.clamp(-1, 1)):     # (the first go past the largest, some to infinity)
+        x = (tops.double()[:, None] * parts).to(DT[dtype])
+        x[:, 63] = tops
+        k, v, s = tf.tf_kvq_cache(-(-n // 64), 64, 1, 64, bits)
+        table = torch.arange(k.shape[0], device="cuda", dtype=torch.int32)[None]
+        rows = x.view(1, n, 1, 64)
+        tf.tf_kvq_write(rows, rows.flip(1).contiguous(), k, v, s, table, i32([0]))
+        tf.tf_device_error()
+        for y, codes, at in ((x, k, 0), (x.flip(0), v, 1)):
+            whole, factor = qo.quantise(f64(y), bits)
+            assert np.array_equal(f64(s).reshape(-1, 2)[:n, at], factor, equal_nan=True)
+            assert np.array_equal(codes.cpu().numpy().reshape(-1, codes.shape[-1])[:n], qo.pack(whole, bits))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("kh,d,page,layout", [(8, 128, 16, "hnd"), (3, 64, 7, "nhd"), (2, 256, 32, "both")])
 def test_read_gives_the_values_and_leaves_the_rest(bits, dtype, kh, d, page, layout):
     lens = [0, 145, -1, 31, 200]

@@ -224,9 +224,10 @@ def test_oracle_pins(bits):
 
 def test_a_quotient_is_no_tie_by_less_than_the_kernel_can_tell():
     """x of 11 bits, s of 8: x / s below 128 is exactly halfway between whole
-    numbers or at least 2^-12 away from it, and x times the rounded 1 / s
-    (fp32), rounded to a multiple of 2^-13, rounds to the same whole number as
-    the quotient does: over all mantissas, in the order of the kernel's steps."""
+    numbers or at least 2^-12 away from it, and x times 1 / s (fp32, off by a
+    unit in its last place either way), rounded to a multiple of 2^-13, rounds
+    to the same whole number as the quotient does: over all mantissas, in the
+    order of the kernel's steps."""
     f = np.float32
     big = f(1536.0)
     mant_x = np.arange(1024, 2048, dtype=np.int64)
@@ -239,5 +240,22 @@ def test_a_quotient_is_no_tie_by_less_than_the_kernel_can_tell():
             x, s = (mant_x * 2.0 ** e)[use], float(mant_s)
             off = np.abs(q[use] - np.floor(q[use]) - 0.5)
             assert np.all((off == 0) | (off >= 2.0 ** -12))
-            t = (x.astype(f) * (f(1) / f(s)) + big) - big
-            assert np.array_equal(np.rint(t), np.rint(x / s)), (mant_s, e)
+            inv = f(1) / f(s)
+            for r in (inv, np.nextafter(inv, f(0)), np.nextafter(inv, f(1))):
+                t = (x.astype(f) * r + big) - big
+                assert np.array_equal(np.rint(t), np.rint(x / s)), (mant_s, e)
+
+
+def test_a_factor_is_its_quotient_in_every_bit():
+    """top * RN(1 / m), corrected once by fma(-m, q, top), is RN(top / m) for
+    every mantissa of a 16-bit number (fma by exact arithmetic in fp64: the
+    products have at most 35 bits)."""
+    f = np.float32
+    top = np.arange(1024, 2048, dtype=np.float64)
+    for m in (7.0, 127.0):
+        inv = f(1) / f(m)
+        q = (top.astype(f) * inv).astype(f)
+        rest = (top - m * q.astype(np.float64)).astype(f)
+        got = (rest.astype(np.float64) * np.float64(inv) + q.astype(np.float64)).astype(f)
+        assert np.array_equal(got, (top / m).astype(f))
+        assert np.array_equal(got, (top.astype(f) / f(m)))

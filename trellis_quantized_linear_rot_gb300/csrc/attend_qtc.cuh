@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
     // Codes of this thread's row times the factor s16, which is exact.
     auto unpack_row = [&](const unsigned char* codes, int to, __half s16) {
       const __half2 by = __half2half2(s16), by16 = __hmul2(by, __float2half2_rn(0.0625f));
-#pragma unroll
+#pragma unroll 1
       for (int it = 0; it < kRB / 16; ++it) {
         // (this order keeps eight threads on different banks, reading and writing)
         const int chunk = kRB == 64 ? (it + (key >> 1)) & 3 : (it + (key >> 2)) & 1;

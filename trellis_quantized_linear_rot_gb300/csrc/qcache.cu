@@ -8,6 +8,7 @@
 // slots read in 66 us), and their rows are in flight together. What bounds
 // them is the launch for a few tokens and memory for many.
 #include <algorithm>
+#include <type_traits>
 
 #include "qcache.cuh"
 
@@ -16,14 +17,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Codes of eight elements of a row whose largest magnitude has the bits `top`
-// (as fp32), and the row's factor. The definition is round(x / s), to the
-// nearest, ties to even. x has at most 11 significant bits and s 8, so that a
-// quotient below 128 that is no tie is at least 2^-12 from one; x times the
-// rounded 1 / s is off by 2^-16 at most. Rounding it to a multiple of 2^-13
-// first (the addition of 1.5 * 2^10) makes a tie exact and moves nothing else
-// across one, in two additions instead of a division. Factors whose
-// reciprocal leaves fp32's normal range are divided by.
+// Codes of eight elements of a row whose largest magnitude is `top` (finite),
+// and the row's factor. The definition is round(x / s), to the nearest, ties to
+// even. x has at most 11 significant bits and s 8, so that a quotient below 128
+// that is no tie is at least 2^-12 from one; x times 1 / s, which may be off by
+// a unit in its last place, is off by 2^-15 at most. Rounding it to a multiple
+// of 2^-13 first (the addition of 1.5 * 2^10) makes a tie exact and moves
+// nothing else across one, in two additions instead of a division. s is off
+// by 2^-9 of itself at most, so that no quotient rounds to more than 7 or 127.
+// Rows whose factor is not in the middle of fp32's range are divided.
 template <int kBits>
 __device__ __noinline__ uint64_t quantise8_by_division(float4 a, float4 b, float s) {
   constexpr float kMost = kBits == 4 ? 7.f : 127.f;
@@ -35,44 +37,77 @@ __device__ __noinline__ uint64_t quantise8_by_division(float4 a, float4 b, float
                                                (1 << (kBits - 1)));
   return out;
 }
+// bf16(top / m) in every bit: the quotient of a number by a small constant is
+// its product with the rounded reciprocal, corrected once by what is left.
 template <int kBits>
-__device__ __forceinline__ uint64_t quantise8(const float (&x)[8], uint32_t top, uint16_t* factor) {
-  constexpr float kMost = kBits == 4 ? 7.f : 127.f;
-  constexpr uint64_t kNone = kBits == 4 ? 0x88888888ull : 0x8080808080808080ull;
-  const __nv_bfloat16 s16 = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), kMost));
-  const float s = __bfloat162float(s16);
-  *factor = __bfloat16_as_ushort(s16);
-  if (top >= 0x7F800000u) {   // not finite
-    *factor = 0x7FC0;
-    return kNone;
-  }
-  if (s == 0.f) return kNone;
+__device__ __noinline__ float factor_by_division(float top) {
+  return __bfloat162float(__float2bfloat16_rn(__fdiv_rn(top, kBits == 4 ? 7.f : 127.f)));
+}
+template <int kBits>
+__device__ __forceinline__ float factor_of(float top) {
+  constexpr float kMost = kBits == 4 ? 7.f : 127.f, kInv = 1.f / kMost;
+  if (top < 0x1p-90f || top > 0x1p90f) return factor_by_division<kBits>(top);
+  const float q = __fmul_rn(top, kInv), s = __fmaf_rn(__fmaf_rn(-kMost, q, top), kInv, q);
+  return __bfloat162float(__float2bfloat16_rn(s));
+}
+// Whole numbers below 2^22 as the lowest bits of their fp32 sum with this.
+constexpr float kWhole = 12582912.f;   // 1.5 * 2^23
+
+template <int kBits>
+__device__ __forceinline__ uint64_t quantise8(const float (&x)[8], float s) {
+  if (s == 0.f) return kBits == 4 ? 0x88888888ull : 0x8080808080808080ull;
   if (s < 0x1p-100f || s > 0x1p100f)
     return quantise8_by_division<kBits>(float4{x[0], x[1], x[2], x[3]}, float4{x[4], x[5], x[6], x[7]}, s);
-  const float inv = __fdiv_rn(1.f, s);
-  // 1536 + t, rounded to a multiple of 2^-13; then to a whole number by the
-  // addition of 1.5 * 2^23 + bias, whose lowest bits are the code.
-  constexpr float kWhole = 12582912.f + (kBits == 4 ? 8.f : 128.f);
-  uint32_t lo = 0, hi = 0;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  float2 t[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __fadd_rn(__fadd_rn(__fmul_rn(x[i], inv), 1536.f), -1536.f);
-    const uint32_t c = __float_as_uint(__fadd_rn(fminf(fmaxf(t, -kMost), kMost), kWhole)) & ((1u << kBits) - 1);
-    if (kBits == 4) lo |= c << (4 * i);
-    else if (i < 4) lo |= c << (8 * i);
-    else hi |= c << (8 * (i - 4));
+  for (int i = 0; i < 4; ++i) {   // two whole numbers each
+    t[i] = mul2(float2{x[2 * i], x[2 * i + 1]}, float2{inv, inv});
+    t[i] = add2(add2(t[i], float2{1536.f, 1536.f}), float2{-1536.f, -1536.f});
+    t[i] = add2(add2(t[i], float2{kWhole, kWhole}), float2{-kWhole, -kWhole});
   }
-  return lo | static_cast<uint64_t>(hi) << 32;
+  // Several of them as one whole number of 16 bits, exactly, with the bias.
+  uint32_t w[4];
+  if (kBits == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = __fmaf_rn(16.f, t[2 * i].y, t[2 * i].x), b = __fmaf_rn(16.f, t[2 * i + 1].y, t[2 * i + 1].x);
+      w[i] = __float_as_uint(__fmaf_rn(256.f, b, a) + (kWhole + 0x8888));
+    }
+    return __byte_perm(w[0], w[1], 0x5410);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(__fmaf_rn(256.f, t[i].y, t[i].x) + (kWhole + 0x8080));
+  return __byte_perm(w[0], w[1], 0x5410) | static_cast<uint64_t>(__byte_perm(w[2], w[3], 0x5410)) << 32;
 }
 
+// The largest magnitude of a row of 16-bit elements, as the element's bits
+// (which order magnitudes, infinity and NaN last), for all its lanes.
 template <int kLanes>
-__device__ __forceinline__ uint32_t row_top(const float (&x)[8]) {
-  uint32_t top = 0;
+__device__ __forceinline__ uint32_t row_top(const uint4& w) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  uint32_t top = __vmaxu2(__vmaxu2(w.x & kAbs, w.y & kAbs), __vmaxu2(w.z & kAbs, w.w & kAbs));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int o = 1; o < kLanes; o *= 2) top = max(top, __shfl_xor_sync(~0u, top, o));
-  return top;
+  for (int o = 1; o < kLanes; o *= 2) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+  return max(top & 0xFFFFu, top >> 16);
+}
+
+// Eight elements of a row: codes, and the factor's bits.
+template <typename T, int kBits, int kLanes>
+__device__ __forceinline__ uint64_t quantise(const uint4& w, uint16_t* factor) {
+  constexpr uint32_t kInfinity = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+  const uint32_t bits = row_top<kLanes>(w);
+  if (bits >= kInfinity) {   // a row that is not finite
+    *factor = 0x7FC0;
+    return kBits == 4 ? 0x88888888ull : 0x8080808080808080ull;
+  }
+  const uint16_t b16 = static_cast<uint16_t>(bits);
+  const float s = factor_of<kBits>(to_f32(*reinterpret_cast<const T*>(&b16)));
+  float x[8];
+  unpack8<T>(w, x);
+  *factor = static_cast<uint16_t>(__float_as_uint(s) >> 16);
+  return quantise8<kBits>(x, s);
 }
 
 constexpr int kAtOnce = 4;
@@ -126,12 +161,8 @@ kvq_write_kernel(const __grid_constant__ QView q, const __grid_constant__ RowsIn
     uint32_t* s_to = q.scales + scales_at(q, at);
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      float x[8], y[8];
-      unpack8<T>(kw[u], x);
-      unpack8<T>(vw[u], y);
       uint16_t ks, vs;
-      const uint64_t kc = quantise8<kBits>(x, row_top<kLanes>(x), &ks);
-      const uint64_t vc = quantise8<kBits>(y, row_top<kLanes>(y), &vs);
+      const uint64_t kc = quantise<T, kBits, kLanes>(kw[u], &ks), vc = quantise<T, kBits, kLanes>(vw[u], &vs);
       if (!real || h0 + u >= q.c.kv_heads) continue;
       const int64_t dst = (h0 + u) * q.c.stride_head;
       if (kBits == 4) {
