@@ -195,7 +195,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
     };
     auto pages_of = [&](const Cursor& x) { return a.c.page_table + x.b * a.c.stride_table; };
     if (args.box) {
-      const int box = args.box, here = lane < kTile / box ? lane * box : 1 << 30;   // (no slot comes near that)
+      const int box = args.box;
+      const bool has_run = lane < kTile / box;
       const uint32_t bytes = box * kRB;
       const int32_t* pages = pages_of(c);
       const uint8_t* k_head = kp + c.item * a.c.stride_head;
@@ -203,9 +204,9 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
       const int64_t to_values = vp - kp;
       int page = 0, row = -1;   // of the lane's run of tile i; row -1: it is not there
       auto look_up = [&]() {
-        const int slot = c.t * kTile + here;
+        const int slot = c.t * kTile + lane * box;
         row = -1;
-        if (slot < c.span.slots) {
+        if (has_run && slot < c.span.slots) {
           const int p = a.c.by_page(slot);
           page = pages[p];
           row = slot - p * a.c.page_size;

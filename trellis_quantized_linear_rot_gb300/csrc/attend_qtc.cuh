@@ -32,9 +32,11 @@
 namespace tfx {
 
 // Codes of tile j lie in stage j % 3 and are stream j % 2's; their barriers are
-// number j % 6, so that whoever waits on one waits for each of its phases.
+// number j % 6, so that whoever waits on one waits for each of its phases. So
+// is the end of an item's q told to the group of warps that has the next item's
+// first tile, and writes its q, on a barrier of that group's own.
 constexpr int kQtcStages = 3, kQtcSlots = 6;
-enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcSlots, kXQFull = kCEmpty + kQtcSlots, kXQEmpty, kXKFull, kXKEmpty = kXKFull + 2,
+enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcSlots, kXQFull = kCEmpty + kQtcSlots, kXQEmpty, kXKFull = kXQEmpty + 2, kXKEmpty = kXKFull + 2,
                   kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2, kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2,
                   kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2, kXPvDone = kXPThree + 2, kXWords = kXPvDone + 2,
                   kXBarriers = kXWords + 4 };
@@ -199,8 +201,8 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       mbar_init(bar(kCEmpty + i), 4);
     }
     mbar_init(bar(kXQFull), 4);
-    mbar_init(bar(kXQEmpty), 2);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kXQEmpty + i), 2);
       mbar_init(bar(kXKFull + i), 4);
       mbar_init(bar(kXKEmpty + i), 1);
       mbar_init(bar(kXVFull + i), 4);
@@ -244,16 +246,17 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       };
       auto codes_of = [&](int j) { return base + S::kCodesAt + j % kQtcStages * S::kStageBytes; };
       if (args.q.box) {   // 4 slots at least: a lane has a run
-        const int box = args.q.box, here = lane < kTile / box ? lane * box : 1 << 30;   // (no slot comes near that)
+        const int box = args.q.box;
+        const bool has_run = lane < kTile / box;
         const uint32_t bytes = box * kRB;
         const int32_t* pages = a.c.page_table + cur.b * a.c.stride_table;
         const uint8_t* k_head = kp + cur.item * a.c.stride_head;
         const uint32_t* s_head = args.q.scales + cur.item * args.q.scale_head;
         int page = -1, row = 0;
         auto look_up = [&]() {
-          const int slot = cur.t * kTile + here;
+          const int slot = cur.t * kTile + lane * box;
           page = -1;
-          if (slot < cur.span.slots) {
+          if (has_run && slot < cur.span.slots) {
             const int p = a.c.by_page(slot);
             page = pages[p];
             row = slot - p * a.c.page_size;
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
         const int jb = ja + min(n_tiles - ja, cur.nt - cur.t), j0 = ja + ((ja ^ s) & 1);
         ok = __all_sync(~0u, mbar_wait(bar(kXQFull), n_items & 1, abort_flag));
         // a stream without a tile of the item does not hold q up
-        if (ok && j0 >= jb && jb < n_tiles && elect_one()) mbar_arrive(bar(kXQEmpty));
+        if (ok && j0 >= jb && jb < n_tiles && elect_one()) mbar_arrive(bar(kXQEmpty + (jb & 1)));
         __syncwarp();
 #pragma unroll 1
         for (int j = j0; j < jb && ok; j += 2) {
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
             mma_commit(bar(kXSFull + s));
             // only what someone will wait for, so that nothing arrives after the end
             if (j + 2 < n_tiles) mma_commit(bar(kXKEmpty + s));
-            if (j + 2 >= jb && jb < n_tiles) mma_commit(bar(kXQEmpty));
+            if (j + 2 >= jb && jb < n_tiles) mma_commit(bar(kXQEmpty + (jb & 1)));
           }
           __syncwarp();
           ok = mbar_wait(bar(kXVFull + s), n & 1, abort_flag) && mbar_wait(bar(kXPHalf + s), n & 1, abort_flag);
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
         }
       }
     };
-    int n_items = 0;
+    int n_ends = 0;   // of q that this group has waited for
     bool ok = true;
     float row_factor = 0.f;   // of row `key` of the item
     // The page of this thread's key, asked for a tile ahead: -1 where there is
@@ -460,10 +463,11 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
     };
     // q of an item: its rows' factors for both streams, q itself by the one
     // that has the item's first tile.
-    auto new_item = [&](const Cursor& c, bool first) {
-      // (both wait for every item's, so that neither passes over a phase)
-      if (n_items > 0) ok = __all_sync(~0u, mbar_wait(bar(kXQEmpty), (n_items - 1) & 1, abort_flag));
-      ++n_items;
+    auto new_item = [&](const Cursor& c, bool first, int cur_j) {
+      if (first && cur_j > 0) {
+        ok = __all_sync(~0u, mbar_wait(bar(kXQEmpty + s), n_ends & 1, abort_flag));
+        ++n_ends;
+      }
       if (!ok) return;
       const int node = key / a.group;
       const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + c.b * a.q_seq + (node0 + node) * a.q_node +
@@ -496,14 +500,14 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
     for (int j = 0; j < n_tiles && ok; ++j) {
       const bool first = j == 0 || cur.t == 0;
       if ((j & 1) != s) {   // the other stream's
-        if (first) new_item(cur, false);
+        if (first) new_item(cur, false, j);
         advance<kTile, S::kGap>(a, &cur);
         if (j == 0 && n_tiles > 1) next_page = page_of(cur);
         continue;
       }
       if (j == 0) next_page = page_of(cur);
       const int use = j >> 1;   // the stream's tiles before
-      if (first) new_item(cur, true);
+      if (first) new_item(cur, true, j);
       if (!ok) break;
       const int page = next_page;
       Cursor after = cur;
