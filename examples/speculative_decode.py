@@ -10,7 +10,11 @@ tree of one node is ordinary decoding, and both give the same tokens.
 The drafts come from a stand-in for a drafting model: the true continuation,
 spoilt here and there, with a wrong sibling beside each.
 
-    python examples/speculative_decode.py [--steps N]
+With --cache 4 or 8 queries and keys are normed and rotated by their positions
+(tf_qk_norm_rope), and the cache is held in that many bits (tf_kvq_write,
+tf_kvq_attention, tf_kvq_keep).
+
+    python examples/speculative_decode.py [--steps N] [--cache 4]
 """
 
 import argparse
@@ -46,7 +50,8 @@ class Projection:
 
 
 class Model:
-    def __init__(self, batch, capacity, seed=0):
+    def __init__(self, batch, capacity, seed=0, cache_bits=None):
+        self.cache_bits = cache_bits
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.embed = torch.randn((VOCAB, HIDDEN), device="cuda", generator=g).half()
         self.qkv = [Projection(HIDDEN, (HEADS + 2 * KV_HEADS) * DIM, 100 + 10 * i) for i in range(LAYERS)]
@@ -54,8 +59,12 @@ class Model:
         self.head = Projection(HIDDEN, VOCAB, 300)
         width = -(-capacity // PAGE)
         self.table = torch.randperm(batch * width, device="cuda", generator=g).to(torch.int32).view(batch, width)
-        shape = (LAYERS, batch * width, PAGE, KV_HEADS, DIM)
-        self.k, self.v = (torch.zeros(shape, dtype=torch.float16, device="cuda") for _ in range(2))
+        if cache_bits:
+            self.k, self.v, self.scales = tf.tf_kvq_cache(batch * width, PAGE, KV_HEADS, DIM, cache_bits, layers=LAYERS)
+            self.inv_freq = 10000.0 ** (-torch.arange(0, DIM, 2, dtype=torch.float64, device="cuda") / DIM)
+        else:
+            shape = (LAYERS, batch * width, PAGE, KV_HEADS, DIM)
+            self.k, self.v = (torch.zeros(shape, dtype=torch.float16, device="cuda") for _ in range(2))
 
     def logits(self, tokens, parents, lengths):
         """Logits after every node of a tree of tokens [batch, nodes]."""
@@ -64,11 +73,37 @@ class Model:
         for i in range(LAYERS):
             rows = self.qkv[i](x).view(b, n, HEADS + 2 * KV_HEADS, DIM)
             q, k, v = rows.split([HEADS, KV_HEADS, KV_HEADS], dim=2)
-            tf.tf_kv_write(k, v, self.k[i], self.v[i], self.table, lengths)
-            o, _ = tf.tf_tree_attention(q, self.k[i], self.v[i], self.table, lengths, parents)
+            o = self.attend(i, q, k, v, parents, lengths)
             x = x + self.out[i](o.view(b * n, HEADS * DIM))
             x = (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).half()
         return self.head(x, torch.float32).view(b, n, VOCAB)
+
+    def attend(self, i, q, k, v, parents, lengths):
+        """The tree's keys and values into layer i's cache, and its attention."""
+        if not self.cache_bits:
+            tf.tf_kv_write(k, v, self.k[i], self.v[i], self.table, lengths)
+            return tf.tf_tree_attention(q, self.k[i], self.v[i], self.table, lengths, parents)[0]
+        depth = torch.tensor(depths(q.shape[1]), dtype=torch.int32, device="cuda")
+        # (an idle sequence's length is negative, and with it its positions: nothing of it is written)
+        positions = torch.where(lengths[:, None] < 0, lengths[:, None], lengths[:, None] + depth)
+        q, k = tf.tf_qk_norm_rope(q, k, positions, self.inv_freq, hadamard=True)
+        cache = (self.k[i], self.v[i], self.scales[i], self.table, lengths)
+        tf.tf_kvq_write(k, v, *cache)
+        return tf.tf_kvq_attention(q, *cache, parents)[0]
+
+    def keep(self, lengths, path, counts):
+        """The accepted path kept in all layers; the new lengths."""
+        if not self.cache_bits:
+            return tf.tf_kv_keep(self.k, self.v, self.table, lengths, path, counts)
+        return tf.tf_kvq_keep(self.k, self.v, self.scales, self.table, lengths, path, counts)
+
+
+def depths(nodes):
+    """Steps from node 0 to each node of TREE, or of a tree of one node."""
+    out = []
+    for j in range(nodes):
+        out.append(0 if TREE[j] < 0 else out[TREE[j]] + 1)
+    return out
 
 
 def decode(model, first, count, parents, draft):
@@ -90,7 +125,7 @@ def decode(model, first, count, parents, draft):
         trees = torch.where(idle[:, None], torch.full_like(tree, -2), tree).contiguous()
         logits = model.logits(tokens, trees, here)
         counts, path, new, _ = tf.tf_verify_draft(logits, tokens, trees, None, temperature=0.0)
-        kept = tf.tf_kv_keep(model.k, model.v, model.table, here, path, counts)
+        kept = model.keep(here, path, counts)
         lengths = torch.where(idle, lengths, kept)
         at = done[:, None] + torch.arange(len(parents), device="cuda")
         fresh = torch.arange(len(parents), device="cuda") < counts[:, None]
@@ -121,19 +156,21 @@ def stand_in_drafts(truth, seed):
     return draft
 
 
-def run(count=40, batch=3):
+def run(count=40, batch=3, cache_bits=None):
     first = torch.arange(1, batch + 1, device="cuda")
     capacity = count + 2 * len(TREE)
     none = lambda done: torch.zeros((batch, 0), dtype=torch.int32, device="cuda")  # noqa: E731
-    plain, plain_steps = decode(Model(batch, capacity), first, count, [-1], none)
-    spec, steps = decode(Model(batch, capacity), first, count, TREE, stand_in_drafts(plain, 7))
+    plain, plain_steps = decode(Model(batch, capacity, cache_bits=cache_bits), first, count, [-1], none)
+    spec, steps = decode(Model(batch, capacity, cache_bits=cache_bits), first, count, TREE, stand_in_drafts(plain, 7))
     return plain, plain_steps, spec, steps
 
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=40, help="tokens to decode for each sequence")
-    plain, plain_steps, spec, steps = run(ap.parse_args().steps)
+    ap.add_argument("--cache", type=int, choices=(4, 8), help="bits of the cache (16 without this)")
+    args = ap.parse_args()
+    plain, plain_steps, spec, steps = run(args.steps, cache_bits=args.cache)
     print("one token a step: %d steps; a tree of %d nodes a step: %d steps" % (plain_steps, len(TREE), steps))
     print("the same tokens" if torch.equal(plain, spec) else "DIFFERENT TOKENS")
     print(spec[0].tolist())
