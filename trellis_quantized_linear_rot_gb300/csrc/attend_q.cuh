@@ -216,7 +216,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll 1
       for (; i < n_tiles; ++i) {
         const bool with_rows = i == 0 || c.t == 0;
-        const int b = c.b, item = c.item, my_page = page, my_row = row;
+        const int b = c.b, item = c.item, my_page = page, my_row = row, tile_slot = c.t * kTile;
         const uint8_t* k_at = k_head;
         const uint32_t* s_at = s_head;
         if (i + 1 < n_tiles) {
@@ -236,20 +236,20 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
         const uint32_t bar = smem_u32(&full[st]);
         if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * (2 * bytes + box * 4) + (with_rows ? rows * D * 2 : 0));
         __syncwarp();
-        k_at += static_cast<uint64_t>(static_cast<uint32_t>(my_page)) * a.c.stride_page + my_row * kRB;
-        s_at += static_cast<uint64_t>(static_cast<uint32_t>(my_page)) * args.scale_page + my_row;
         // What does not exist keeps an earlier tile's bytes: whatever they are, it gets no weight.
 #pragma unroll 1
         for (uint32_t left = there; left; left &= left - 1) {
           const int run = __ffs(left) - 1;
-          const uint64_t from = __shfl_sync(~0u, reinterpret_cast<uint64_t>(k_at), run);
-          const uint64_t with = __shfl_sync(~0u, reinterpret_cast<uint64_t>(s_at), run);
+          // (only the page comes from its lane, so that the rest is the warp's arithmetic)
+          const uint64_t of_run = static_cast<uint32_t>(__shfl_sync(~0u, my_page, run));
+          const int slot = tile_slot + run * box, row_of_run = slot - a.c.by_page(slot) * a.c.page_size;
+          const uint8_t* from = k_at + of_run * a.c.stride_page + row_of_run * kRB;
+          const uint32_t* with = s_at + of_run * args.scale_page + row_of_run;
           if (elect_one()) {
             const uint32_t keys = smem_u32(smem) + st * S::kStageBytes + run * bytes;
-            copy_run(keys, reinterpret_cast<const void*>(from), bytes, bar);
-            copy_run(keys + S::kHalf, reinterpret_cast<const void*>(from + to_values), bytes, bar);
-            copy_run(smem_u32(smem + S::kScalesAt) + (st * kTile + run * box) * 4, reinterpret_cast<const void*>(with),
-                     box * 4, bar);
+            copy_run(keys, from, bytes, bar);
+            copy_run(keys + S::kHalf, from + to_values, bytes, bar);
+            copy_run(smem_u32(smem + S::kScalesAt) + (st * kTile + run * box) * 4, with, box * 4, bar);
           }
           __syncwarp();
         }

@@ -23,8 +23,11 @@ int run_of_slots(const QAttendArgs& x, int tile, int row_bytes) {
   return together && box >= std::max(4, tile / 32) ? box : 0;   // a lane has a run
 }
 
-// Parts of an item above which a launch of its own joins them.
-constexpr int kManyParts = 6;
+// Parts of an item above which a launch of its own joins them. One token over
+// 300 slots (3 parts) 11.7 us with the launch, 13.8 with the block that comes
+// last; 16 tokens over up to 8,192 (3 parts) 35.9 and 37.5; 32 (1 part) 56.4
+// and 55.1, over up to 256 17.8 and 14.4.
+constexpr int kManyParts = 2;
 // Blocks an SM of any of the kernels, at most.
 constexpr int kMostBlocks = 4;
 
