@@ -1,4 +1,4 @@
-// Attention over a quantised cache with mma.sync, up to 8 or 16 rows a block.
+// Attention over a quantised cache with mma.sync, 8 to 32 rows a block.
 //
 // Reading the cache bounds it, at a quarter of the bytes of a 16-bit cache,
 // so that an element has about three instructions of a lane in the time its
@@ -30,6 +30,15 @@
 // between lanes; 2^E is about 2^-8 of the largest p vs so far, so that factors of any
 // size and range lose nothing. q is scaled by a power of two into fp16's range
 // (exact but for elements 2^-39 below the row's largest).
+//
+// Measured, heads of 128: 32 tokens x 5 heads a kv head x 8 over up to 8,192
+// slots in 4 bits 56.8 us (174 MB, 3.1 TB/s), in 8 bits 74.3 (342 MB, 4.6
+// TB/s), in 4 bits over up to 32,768 157 (693 MB, 4.4 TB/s). Issue slots are
+// 52% busy, the ALU 40%: half of a warp's 611 instructions for 32 keys are the
+// codes' conversion. Start and end are most of the 15.6 us over up to 256
+// slots. Pages of 16 slots 63.9, of 7 (no bulk copies) 76.8. The wide form: 16
+// trees of 16 x 6 heads over up to 4,096 slots in 8 bits 172 us, issue slots
+// 38% busy with two arithmetic warps a scheduler.
 #pragma once
 
 #include "attend_mma.cuh"

@@ -24,6 +24,13 @@
 // 2^-22 below it still has its bits.
 // A value row whose factor is not finite is 0 here, and its weight NaN for the
 // rows that see it.
+//
+// Measured: 16 trees of 16 nodes x 6 heads of 128 x 8 over up to 4,096 slots
+// 55.4 us (292 TFLOP/s; 45.8 with heads of 64), of 64 nodes 152 (434), one tree
+// of 64 x 5 over 50,001 slots 119 (552). Not memory (14% of its rate at 16
+// nodes) but the chain of a tile bounds it, codes, scores, weights, sums, and
+// the instructions of five roles: issue slots 54% busy, tensor pipe 25%.
+// Unrolled, the roles do not fit the instruction cache (61 us for 55).
 #pragma once
 
 #include "attend_q.cuh"
