@@ -52,8 +52,10 @@ enum {
  *     and sin, so that far positions lose nothing)
  *   y = u, or H u / sqrt(head_dim) with TF_QK_HADAMARD, H[i][j] = -1 to the
  *     number of ones that i and j have in common
- * rounded once to the dtype. The last step leaves q.k as it is and spreads
- * large elements over the head before they are quantised.
+ * rounded once to the dtype. Rows of any size are normed, those too whose
+ * squares fp32 does not hold; with eps 0 a row of zeros is NaN. The last step
+ * leaves q.k as it is and spreads large elements over the head before they
+ * are quantised.
  * A negative position marks a row that is not there: what it holds has no
  * influence, and nothing is written. keys may be NULL (queries alone).
  * dtype: TF_F16 or TF_BF16; weight_dtype: also TF_F32. positions: [batch]
@@ -113,8 +115,9 @@ tf_status tf_kvq_write(const tf_kvq_cache* cache, const void* k_new, int64_t k_s
  * tf_kvq_read -- the values of slots starts[b] + i, i < slots, below
  * lengths[b], each rounded once to the dtype: k_out, v_out: [batch][slots]
  * [kv_heads][head_dim] fp16 or bf16 with the given strides, last dimension
- * contiguous; 16-byte aligned, strides multiples of 8. Rows of other slots
- * are left as they were. starts: [batch], or NULL for 0. cache->layers must
+ * contiguous; 16-byte aligned, strides multiples of 8. c * s may be above a
+ * row's largest element by 2^-9 of it (s is rounded), and infinite in fp16 for
+ * elements next to its largest. Rows of other slots are left as they were. starts: [batch], or NULL for 0. cache->layers must
  * be 1. The pages have no counterpart.
  */
 tf_status tf_kvq_read(const tf_kvq_cache* cache, const int32_t* starts, void* k_out, void* v_out, int dtype,

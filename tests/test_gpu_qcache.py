@@ -199,6 +199,20 @@ def test_norm_rope_small_and_large_rows(scale):
     norm_check("bf16", 2, 9, 3, 1, 128, 64, False, True, scale=scale, seed=10, eps=0.0)
 
 
+@pytest.mark.parametrize("hadamard", [False, True])
+@pytest.mark.parametrize("power", [70, 120, -45, -80, -120])
+def test_norm_rope_rows_whose_squares_leave_fp32(power, hadamard):
+    norm_check("bf16", 2, 9, 3, 1, 128, 128, False, hadamard, scale=2.0 ** power, seed=11, eps=0.0)
+    if power > 0:
+        norm_check("bf16", 2, 9, 3, 1, 128, 128, False, hadamard, scale=2.0 ** power, seed=12)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_norm_rope_rows_of_all_sizes_beside_each_other(d):
+    powers = torch.tensor([0, 70, -50, 3, 120, -110, -7, 100], device="cuda").repeat(20)[:150]
+    norm_check("bf16", 2, 15, 3, 1, d, d, True, False, scale=torch.exp2(powers.float()).view(2, 15, 5, 1), seed=13, eps=0.0)
+
+
 def test_norm_rope_in_place_strided_and_one_position_for_all():
     q, k, pos, freq, wt, want = norm_check("bf16", 3, 17, 6, 2, 128, 128, False, True, seed=4)
     rows = q._base.clone()

@@ -16,6 +16,7 @@
 // its cosines in registers have a quarter fewer instructions, but fewer warps:
 // 34 to 39 us, and 300 tokens 7.4 to 9.3 for 6.4.
 #include <algorithm>
+#include <type_traits>
 
 #include "qcache.cuh"
 
@@ -121,13 +122,26 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int tokens, int per_
     load_weight<W>(row.kind->weight, e + kHalf, w[1]);
     float f = 1.f;
     if (!(a.flags & TF_QK_NO_NORM)) {
-      float2 both = {0.f, 0.f};
+      auto mean_square = [&]() {
+        float2 both = {0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) both = fma2(x[i / 4][i % 4], x[i / 4][i % 4], both);
-      float sum = both.x + both.y;
+        for (int i = 0; i < 8; ++i) both = fma2(x[i / 4][i % 4], x[i / 4][i % 4], both);
+        float sum = both.x + both.y;
 #pragma unroll
-      for (int o = 1; o < kLanes; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
-      f = rsqrtf(sum * (1.f / D) + a.eps);
+        for (int o = 1; o < kLanes; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
+        return sum * (1.f / D);
+      };
+      float square = mean_square() + a.eps;
+      // Squares of large or small bf16 numbers pass fp32's range where the
+      // numbers don't: such rows are scaled by a power of two first.
+      if (std::is_same<T, __nv_bfloat16>::value &&
+          __any_sync(~0u, square >= 0x1p120f || square < 0x1p-80f)) {
+        const float by = square >= 0x1p120f ? 0x1p-90f : square < 0x1p-80f ? 0x1p90f : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i / 4][i % 4] = mul2(x[i / 4][i % 4], twice(by));
+        square = mean_square() + a.eps * by * by;
+      }
+      f = rsqrtf(square);
     }
     if (hadamard) f *= D == 64 ? 0.125f : D == 128 ? 0.0883883476f : 0.0625f;   // 1 / sqrt(D)
 #pragma unroll
