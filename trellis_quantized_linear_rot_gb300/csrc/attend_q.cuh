@@ -32,7 +32,7 @@
 // (exact but for elements 2^-39 below the row's largest).
 //
 // Measured, heads of 128: 32 tokens x 5 heads a kv head x 8 over up to 8,192
-// slots in 4 bits 56.8 us (174 MB, 3.1 TB/s), in 8 bits 74.3 (342 MB, 4.6
+// slots in 4 bits 55.5 us (174 MB, 3.1 TB/s), in 8 bits 74.3 (342 MB, 4.6
 // TB/s), in 4 bits over up to 32,768 157 (693 MB, 4.4 TB/s). Issue slots are
 // 52% busy, the ALU 40%: half of a warp's 611 instructions for 32 keys are the
 // codes' conversion. Start and end are most of the 15.6 us over up to 256

@@ -23,11 +23,15 @@ int run_of_slots(const QAttendArgs& x, int tile, int row_bytes) {
   return together && box >= std::max(4, tile / 32) ? box : 0;   // a lane has a run
 }
 
-// Parts of an item above which a launch of its own joins them. One token over
-// 300 slots (3 parts) 11.7 us with the launch, 13.8 with the block that comes
-// last; 16 tokens over up to 8,192 (3 parts) 35.9 and 37.5; 32 (1 part) 56.4
-// and 55.1, over up to 256 17.8 and 14.4.
-constexpr int kManyParts = 2;
+// Parts of an item above which a launch of its own joins them, where a run may
+// have kLongRun tiles and where it can't. 16 tokens over up to 8,192 slots (3
+// parts) 35.9 us with the launch, 37.5 with the block that comes last; 32 (1
+// part) 56.4 and 55.1, over up to 256 17.8 and 14.4. With short runs a call
+// outside a graph is bound by the host, for which a second launch is 2 us: one
+// token over 300 slots (3 parts) 14.8 with it and 12.6 without, call after
+// call, 6 chains of 5 over up to 1,500 (4 parts) 16.1 and 14.3 (in a graph 11.8
+// and 13.8, 15.8 and 16.4).
+constexpr int kManyParts = 2, kManyPartsOfShort = 6, kLongRun = 4;
 // Blocks an SM of any of the kernels, at most.
 constexpr int kMostBlocks = 4;
 
@@ -44,7 +48,9 @@ cudaError_t launch(QAttendArgs x, int device, cudaStream_t s) {
   if (e != cudaSuccess) return static_cast<cudaError_t>(e);
   const int row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
   const int blocks = team_blocks(S::kBlocks * a.num_sms, row_blocks);
-  a.join_later = parts_of(a, blocks / row_blocks, S::kTile) > kManyParts;
+  const int64_t runs = blocks / row_blocks, tiles = (static_cast<int64_t>(a.c.table_width) * a.c.page_size + S::kTile - 1) / S::kTile;
+  const bool long_runs = tiles * a.c.batch * a.c.kv_heads >= kLongRun * runs;
+  a.join_later = parts_of(a, runs, S::kTile) > (long_runs ? kManyParts : kManyPartsOfShort);
   x.box = run_of_slots(x, S::kTile, S::kRowBytes);
   const cudaError_t launched =
       launch_chained(kvq_attention_kernel<T, kBits, D, kCols>, dim3(blocks), dim3(S::kThreads), S::kSmem, 1, s, x);

@@ -10,9 +10,9 @@
 // for before this one is worked on. Reading and writing each row once is what
 // bounds it, and close to that the instructions, so two elements are worked on
 // by one wherever they can be. For few tokens the launch.
-// Measured: 4,096 tokens of 48 + 8 heads of 128 in bf16 37.4 us with the
-// Hadamard rotation, 29.1 without (117 MB: 3.1 and 4.0 TB/s), issue slots 61%
-// busy; 1 token of 40 + 8 heads 2.9 us. Lanes that stay with a token and have
+// Measured: 4,096 tokens of 48 + 8 heads of 128 in bf16 37.7 us with the
+// Hadamard rotation, 29.4 without (117 MB: 3.1 and 4.0 TB/s), issue slots 61%
+// busy; 1 token of 40 + 8 heads 3.0 us. Lanes that stay with a token and have
 // its cosines in registers have a quarter fewer instructions, but fewer warps:
 // 34 to 39 us, and 300 tokens 7.4 to 9.3 for 6.4.
 #include <algorithm>
