@@ -535,6 +535,43 @@ def test_attention_a_siblings_bad_row_stays_its_own(n, group, d, bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 2, 5])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_large_values_beside_a_bad_sibling(bits, d, group, bad):
+    """Tree nodes that see the context and themselves, after a context of small
+    values: their own are 2^20 times as large, one of them is bad. With q = 0
+    all weights are alike, so a row is the mean of the values it sees. More
+    items than runs, so that the nodes come after a run's first tile."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    b, kh, n, ctx, page = 70, 8, 5, 200, 16
+    per = -(-(ctx + n) // page)
+    k, v, s = tf.tf_kvq_cache(b * per, page, kh, d, bits)
+    table = torch.arange(b * per, dtype=torch.int32, device="cuda").view(b, per)
+    zero, lens = i32([0] * b), i32([ctx] * b)
+    rows = lambda m, size: (size * torch.randn((b, m, kh, d), device="cuda", generator=g)).to(torch.bfloat16)  # noqa: E731
+    tf.tf_kvq_write(rows(ctx, 1.0), rows(ctx, 2.0 ** -10), k, v, s, table, zero)
+    own = rows(n, 2.0 ** 10)
+    own[:, 2, :, 3] = bad
+    tf.tf_kvq_write(rows(n, 1.0), own, k, v, s, table, lens)
+    q = torch.zeros((b, n, kh * group, d), dtype=torch.bfloat16, device="cuda")
+    out, lse = tf.tf_kvq_attention(q, k, v, s, table, lens, i32([-1] * n))
+    values = tf.tf_kvq_read(k, v, s, table, i32([ctx + n] * b), slots=ctx + n, head_dim=d, dtype=torch.bfloat16)[1].double()
+    of_ctx, of_own = values[:, :ctx].sum(1, keepdim=True), values[:, ctx:]
+    want = ((of_ctx + of_own) / (ctx + 1)).repeat_interleave(group, 2)
+    mag = ((values[:, :ctx].abs().sum(1, keepdim=True) + of_own.abs()) / (ctx + 1)).repeat_interleave(group, 2)
+    # bf16 has 8 significant bits: steps of 2^-7 at 1, half of one is 2^-8. So
+    # values that were read back are off by 2^-8 and the result by 2^-8 again;
+    # weights, in fp16, by 2^-11; sums in fp32 by 2^-14 at most.
+    tol = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14) * mag + 2.0 ** -8 * want.abs() * (1 + 2.0 ** -7)
+    fine = [0, 1, 3, 4]
+    assert ((out.double() - want).abs() <= tol)[:, fine].all(), ((out.double() - want).abs() / tol)[:, fine].max()
+    assert torch.isnan(out[:, 2]).all()
+    assert (lse.double() - np.log(ctx + 1)).abs().max() <= 2.0 ** -18
+    tf.tf_device_error()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("n,group", [(1, 5), (4, 5), (40, 2)])
 def test_attention_factors_over_a_wide_range(bits, dtype, n, group):

@@ -523,7 +523,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
               w[u][n][y] = p * (value_scale(factors[u][y >> 1]) * to16);
               all += fabsf(w[u][n][y]);
             }
-          over |= sum[n][x] > 0x1p9f || all > 0x1p15f;   // (NaN stays NaN)
+          // (`all` is NaN with a bad value that the row may not see, too)
+          over |= sum[n][x] > 0x1p9f || !(all <= 0x1p15f);
         }
       if (__any_sync(~0u, over)) {
 #pragma unroll
