@@ -513,7 +513,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float to16 = power2(-e[n][x]);   // 2^-E
-          float all = sum[n][x] = 0.f;
+          float largest = sum[n][x] = 0.f;   // (a bad value that the row does not see, NaN here, is passed over)
 #pragma unroll
           for (int u = 0; u < kTiles16; ++u)
 #pragma unroll
@@ -521,10 +521,9 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
               const float p = exp2_approx(s[u][n][y] - m[n][x]);
               sum[n][x] += p;
               w[u][n][y] = p * (value_scale(factors[u][y >> 1]) * to16);
-              all += fabsf(w[u][n][y]);
+              largest = fmaxf(largest, fabsf(w[u][n][y]));
             }
-          // (`all` is NaN with a bad value that the row may not see, too)
-          over |= sum[n][x] > 0x1p9f || !(all <= 0x1p15f);
+          over |= sum[n][x] > 0x1p9f || largest > 0x1p15f;
         }
       if (__any_sync(~0u, over)) {
 #pragma unroll
