@@ -11,19 +11,20 @@
 //
 // A code has 3 bits and a sign and a factor 8 bits, so c s is exact in fp16's
 // 11, as long as it stays in range: factors go in relative to the largest of
-// their 32 keys, whose exponents ek and ev the weights' threads put back. What
-// is below 2^-18 of the largest of the 32 loses bits. q is scaled into fp16's
-// range by a power of two a row. Elements are in the order in which they come
-// out of a word (0, 4, 1, 5, 2, 6, 3, 7), in q too, and in the sums until
-// they are written.
+// their 32 keys, whose exponents ek and ev the weights' threads put back. That
+// is right where every row sees the 32 alike. Where they reach past the context
+// (rows see different nodes, and what an absent node's slot holds is anything),
+// or one of them is not finite, codes go in without factors, and a score and a
+// weight are multiplied by their key's own, in fp32: what a row does not see has
+// no part in its scores, maximum or exponent. q is scaled into fp16's range by a
+// power of two a row. Elements are in the order in which they come out of a word
+// (0, 4, 1, 5, 2, 6, 3, 7), in q too, and in the sums until they are written.
 //
 // Weights are p 2^(ev - E), E of a row rising like its maximum, so that
 // values of any size weigh what they should; sums of weights are of p itself.
 // The largest weight of a row is bounded (largest p times largest factor of 32
 // keys), not known; what is bounded is 2^8 when E is set, so that what lies
 // 2^-22 below it still has its bits.
-// A value row whose factor is not finite is 0 here, and its weight NaN for the
-// rows that see it.
 //
 // Measured: 16 trees of 16 nodes x 6 heads of 128 x 8 over up to 4,096 slots
 // 55.4 us (292 TFLOP/s; 45.8 with heads of 64), of 64 nodes 152 (434), one tree
@@ -56,8 +57,13 @@ struct QtcShared {
   // place is written with the tile's keys, while the tile before is weighed.
   struct Words {
     float row_factor[128];                  // scale log2(e) over the power that q was scaled by
+    // Of each key, where a tile's are not treated alike: what a score and a
+    // weight are multiplied by, and the least power of two (its exponent) that
+    // the latter is below.
+    alignas(16) float key_by[128], value_by[128], value_log[128];
     int ek[4], ev[4];                       // exponents of each 32 keys
-    uint32_t there[4], spoilt[4];           // keys that exist; keys whose value row is not finite
+    int apart[4];                           // whether their factors are not in the operands
+    uint32_t there[4];                      // keys that exist
   } words[2][2];
   int16_t up[TF_MAX_NODES];                 // parents: -1 for none, -2 for an absent node
   int scratch[2 * (640 / 32) + 6];
@@ -87,33 +93,55 @@ struct QtcArgs {
   int block_nodes;   // whole nodes of a row block
 };
 
+// The least exponent E: what is multiplied by 2^-E stays far from fp32's ends.
+constexpr int kLeastExp = -100;
+
 // One row of a tile, by its thread, as weigh() of attend_tc.cuh, with a factor
-// for the scores and one for the weights of each 32 keys. sc > 0 or 0.
-template <int D, bool kCut>
-__device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, float sc, const int* ek, const int* ev,
-                                        const uint32_t (&vis)[4], const uint32_t (&spoilt)[4], bool begun, uint32_t half,
-                                        uint32_t three, float* m_row, float* l_row, int* e_row) {
-  auto word_of = [](const uint32_t (&w)[4], int c) { return c < 2 ? (c == 0 ? w[0] : w[1]) : (c == 2 ? w[2] : w[3]); };
-  auto score_by = [&](int c) { return sc * power2(ek[c] - 8); };
+// for the scores and one for the weights of each 32 keys, or (kEach) of each
+// key, with the keys that the row sees in vis. sc: the row's factor, not below 0.
+template <int D, bool kEach>
+__device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, const QtcShared::Words& words, float sc,
+                                        const uint32_t (&vis)[4], bool begun, uint32_t half, uint32_t three,
+                                        float* m_row, float* l_row, int* e_row) {
+  auto word_of = [&](int c) { return c < 2 ? (c == 0 ? vis[0] : vis[1]) : (c == 2 ? vis[2] : vis[3]); };
+  auto score_by = [&](int c) { return sc * power2(words.ek[c] - 8); };
+  auto pairs_at = [&](const float* of, int key, float2 (&x)[2]) {   // of four keys
+    const float4 y = *reinterpret_cast<const float4*>(of + key);
+    x[0] = float2{y.x, y.y}, x[1] = float2{y.z, y.w};
+  };
   float top = -INFINITY, need = -INFINITY;   // the largest score, the largest weight with its values' size
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float v[32];
     tmem_ld32(scores + c * 32, v);
-    const uint32_t word = kCut ? word_of(vis, c) : 0;
     float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if constexpr (kEach) {
+      const uint32_t word = word_of(c);
+      float2 large = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      if (kCut) {
-        if (!(word >> i & 1)) v[i] = -INFINITY;
-        if (!(word >> (i + 1) & 1)) v[i + 1] = -INFINITY;
+      for (int i = 0; i < 32; i += 4) {
+        float2 by[2], size[2];
+        pairs_at(words.key_by, c * 32 + i, by);
+        pairs_at(words.value_log, c * 32 + i, size);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float2 x = mul2(float2{v[i + 2 * k], v[i + 2 * k + 1]}, mul2(by[k], float2{sc, sc}));
+          if (!(word >> (i + 2 * k) & 1)) x.x = -INFINITY;
+          if (!(word >> (i + 2 * k + 1) & 1)) x.y = -INFINITY;
+          hi[i / 4 % 2 * 2 + k] = fmaxf(hi[i / 4 % 2 * 2 + k], fmaxf(x.x, x.y));
+          const float2 weight = add2(x, size[k]);
+          large = float2{fmaxf(large.x, weight.x), fmaxf(large.y, weight.y)};
+        }
       }
-      hi[i / 2 % 4] = fmaxf(hi[i / 2 % 4], fmaxf(v[i], v[i + 1]));
+      top = fmaxf(top, fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])));
+      need = fmaxf(need, fmaxf(large.x, large.y));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) hi[i / 2 % 4] = fmaxf(hi[i / 2 % 4], fmaxf(v[i], v[i + 1]));
+      const float high = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) * score_by(c);
+      top = fmaxf(top, high);
+      need = fmaxf(need, high + static_cast<float>(words.ev[c]));
     }
-    float high = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
-    high = high == -INFINITY ? -INFINITY : high * score_by(c);
-    top = fmaxf(top, high);
-    need = fmaxf(need, high + static_cast<float>(ev[c]));
   }
   float m = *m_row, l = *l_row;
   int e = *e_row;
@@ -123,8 +151,8 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, float sc
   if (__any_sync(~0u, rise || grow)) {
     const float down = m - to;   // 0, or below
     int to_e = e;
-    if (rise) to_e = max(-200, e + static_cast<int>(floorf(fmaxf(down, -400.f))));
-    if (rise || grow) to_e = max(to_e, static_cast<int>(ceilf(fmaxf(need - to, -190.f))) - 8);
+    if (rise) to_e = max(kLeastExp, e + static_cast<int>(floorf(fmaxf(down, -400.f))));
+    if (rise || grow) to_e = min(126, max(to_e, static_cast<int>(ceilf(fmaxf(need - to, -190.f))) - 8));
     l *= exp2_approx(down);
     if (begun) {
       const float f = exp2_approx(down + static_cast<float>(e - to_e));
@@ -142,29 +170,41 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, float sc
     e = to_e;
   }
   float2 sum[4] = {};
+  const float to16 = power2(-e);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float v[32];
     tmem_ld32(scores + c * 32, v);
-    const uint32_t word = kCut ? word_of(vis, c) : 0, nans = kCut ? word_of(spoilt, c) : 0;
-    const float by = score_by(c), size = power2(max(-126, min(126, ev[c] - e)));
     uint32_t w[16];
+    if constexpr (kEach) {
+      const uint32_t word = word_of(c);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float2 x = fma2(float2{v[2 * i], v[2 * i + 1]}, float2{by, by}, float2{-m, -m});
-      x.x = exp2_approx(x.x);
-      x.y = exp2_approx(x.y);
-      if (kCut) {
-        if (!(word >> (2 * i) & 1)) x.x = 0.f;
-        if (!(word >> (2 * i + 1) & 1)) x.y = 0.f;
+      for (int i = 0; i < 32; i += 4) {
+        float2 by[2], values[2];
+        pairs_at(words.key_by, c * 32 + i, by);
+        pairs_at(words.value_by, c * 32 + i, values);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool sees_x = word >> (i + 2 * k) & 1, sees_y = word >> (i + 2 * k + 1) & 1;
+          float2 x = fma2(float2{v[i + 2 * k], v[i + 2 * k + 1]}, mul2(by[k], float2{sc, sc}), float2{-m, -m});
+          x.x = sees_x ? exp2_approx(x.x) : 0.f;
+          x.y = sees_y ? exp2_approx(x.y) : 0.f;
+          sum[i / 4 % 2 * 2 + k] = add2(sum[i / 4 % 2 * 2 + k], x);
+          x = mul2(mul2(x, values[k]), float2{to16, to16});   // (this order: the product is in range)
+          w[i / 2 + k] = pack2(__half(), sees_x ? x.x : 0.f, sees_y ? x.y : 0.f);   // whatever the factor
+        }
       }
-      sum[i % 4] = add2(sum[i % 4], x);
-      x = mul2(x, float2{size, size});
-      if (kCut) {
-        if (word & nans & (1u << (2 * i))) x.x = __uint_as_float(0x7FC00000u);
-        if (word & nans & (1u << (2 * i + 1))) x.y = __uint_as_float(0x7FC00000u);
+    } else {
+      const float by = score_by(c), size = power2(max(-126, min(126, words.ev[c] - e)));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float2 x = fma2(float2{v[2 * i], v[2 * i + 1]}, float2{by, by}, float2{-m, -m});
+        x.x = exp2_approx(x.x);
+        x.y = exp2_approx(x.y);
+        sum[i % 4] = add2(sum[i % 4], x);
+        x = mul2(x, float2{size, size});
+        w[i] = pack2(__half(), x.x, x.y);
       }
-      w[i] = pack2(__half(), x.x, x.y);
     }
     tmem_st16(scores + c * 16, w);   // over scores already read
     if (c == 1 || c == 2) {
@@ -532,27 +572,34 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       if (page != -1 && !real) record_index_error(a.c.err);
       const uint32_t factors = real ? reinterpret_cast<const uint32_t*>(codes + 2 * S::kHalf)[key] : 0;
       const float ks = key_scale(factors), vs = value_scale(factors);
-      const bool k_fine = (factors & 0x7F80u) != 0x7F80u, v_fine = (factors & 0x7F800000u) != 0x7F800000u;
-      const int ek = __reduce_max_sync(~0u, k_fine && ks != 0.f ? max(exponent_of(fabsf(ks)), -100) : -100);
-      const int ev = __reduce_max_sync(~0u, v_fine && vs != 0.f ? max(exponent_of(fabsf(vs)), -100) : -100);
-      const uint32_t there = __ballot_sync(~0u, real), spoilt = __ballot_sync(~0u, !v_fine);
+      const bool fine = (factors & 0x7F80u) != 0x7F80u && (factors & 0x7F800000u) != 0x7F800000u;
+      const int ek = __reduce_max_sync(~0u, ks != 0.f ? max(exponent_of(fabsf(ks)), -100) : -100);
+      const int ev = __reduce_max_sync(~0u, vs != 0.f ? max(exponent_of(fabsf(vs)), -100) : -100);
+      const uint32_t there = __ballot_sync(~0u, real);
+      // Rows may see different ones of the warp's 32 keys, or one is not finite.
+      const bool apart = cur.t * kTile + quarter * 32 + 32 > cur.span.context || !__all_sync(~0u, fine);
       // (the scores of the stream's tile before are made, which came after the
       // weights of the one before that: nobody reads this place any more)
       QtcShared::Words& words = sh.words[s][use & 1];
       words.row_factor[key] = row_factor;
+      // (operands are 2^8 times as large as values: codes of 7 at most are exact either way)
+      words.key_by[key] = apart ? ks * 0x1p-8f : power2(ek - 8);
+      words.value_by[key] = apart ? vs : power2(ev);
+      words.value_log[key] = !apart ? ev : vs == 0.f ? -1000.f : exponent_of(fabsf(vs)) + 1;
       if (lane == 0) {
         words.ek[quarter] = ek, words.ev[quarter] = ev;
-        words.there[quarter] = there, words.spoilt[quarter] = spoilt;
+        words.there[quarter] = there, words.apart[quarter] = apart;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kXWords + 2 * s + (use & 1)));
-      unpack_row(codes, S::kKeysAt + s * S::kTileBytes, __float2half_rn(ks * power2(8 - ek)));
+      unpack_row(codes, S::kKeysAt + s * S::kTileBytes, __float2half_rn(apart ? 256.f : ks * power2(8 - ek)));
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kXKFull + s));
       if (use > 0) ok = __all_sync(~0u, mbar_wait(bar(kXVEmpty + s), (use - 1) & 1, abort_flag));
       if (!ok) break;
-      unpack_row(codes + S::kHalf, S::kValuesAt + s * S::kTileBytes, __float2half_rn(v_fine ? vs * power2(8 - ev) : 0.f));
+      unpack_row(codes + S::kHalf, S::kValuesAt + s * S::kTileBytes,
+                 __float2half_rn(apart ? 256.f : vs * power2(8 - ev)));
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
@@ -589,7 +636,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
         seen = node >= 0 ? seen_by(sh.up, node) : Seen{};
       }
       float m = kNoMax, l = 0.f;
-      int e = -200;
+      int e = kLeastExp;
       bool used = false;
 #pragma unroll 1
       for (int j = ja + ((ja ^ s) & 1); j < jb; j += 2) {
@@ -600,16 +647,16 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
         tc_fence_after();
         const QtcShared::Words& words = sh.words[s][n & 1];
         const float sc = words.row_factor[row];
-        uint32_t vis[4], spoilt[4], all = ~0u, none = 0;
+        uint32_t vis[4], all = ~0u;
+        int apart = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          vis[w] = words.there[w], spoilt[w] = words.spoilt[w];
+          vis[w] = words.there[w];
           all &= vis[w];
-          none |= spoilt[w];
+          apart |= words.apart[w];
         }
-        if (slot0 + kTile <= cur.span.context && all == ~0u && none == 0) {
-          weigh_q<D, false>(scores, sums, sc, words.ek, words.ev, vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
-                            &l, &e);
+        if (all == ~0u && !apart) {   // a whole tile of the context
+          weigh_q<D, false>(scores, sums, words, sc, vis, used, bar(kXPHalf + s), bar(kXPThree + s), &m, &l, &e);
         } else {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -621,8 +668,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
             }
             vis[w] = node >= 0 ? word & vis[w] : 0u;
           }
-          weigh_q<D, true>(scores, sums, sc, words.ek, words.ev, vis, spoilt, used, bar(kXPHalf + s), bar(kXPThree + s), &m,
-                           &l, &e);
+          weigh_q<D, true>(scores, sums, words, sc, vis, used, bar(kXPHalf + s), bar(kXPThree + s), &m, &l, &e);
         }
         tmem_wait_st();
         tc_fence_before();
