@@ -128,11 +128,10 @@ tf_status tf_kvq_read(const tf_kvq_cache* cache, const int32_t* starts, void* k_
  * cache: the same arguments, masks, outputs and refusals. q and out are fp16
  * or bf16 (dtype). Codes go into the matrix products as they are; the factors
  * of keys multiply scores in fp32, those of values the weights, which are
- * rounded to 11 bits for the second product. Maxima, sums and accumulators
- * are fp32. With more than 16 rows a kv head over 4 bits (heads of 64 and
- * 128) a factor keeps its bits down to 2^-18 of the largest of its 32
- * neighbouring slots. workspace as there, of
- * tf_kvq_attention_workspace_bytes.
+ * rounded for the second product: to 11 bits, and to 2^-26 of the row's
+ * largest weight where they are smaller than 2^-15 of it. Weights exp(s - max
+ * s) below 2^-126 are 0. Maxima, sums and accumulators are fp32. workspace as
+ * there, of tf_kvq_attention_workspace_bytes.
  * The same inputs give the same bits. The pages have no counterpart.
  */
 tf_status tf_kvq_attention(const tf_kvq_cache* cache, const void* q, int dtype, int64_t q_stride_seq,

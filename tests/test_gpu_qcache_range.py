@@ -12,7 +12,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import trellis_quantized_linear_rot_gb300 as tf  # noqa: E402
-from test_gpu_qcache import Case, i32, tree  # noqa: E402
+from test_gpu_qcache import Case, f64, i32, tree  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -81,3 +81,83 @@ def test_a_pool_of_any_bits_under_absent_nodes(bits, d, n, group):
     c.s.view(torch.int16)[~used] = 0x3C00
     c.check([par] * 3, out=got[0], lse=got[1])
     tf.tf_device_error()
+
+
+def laid_out(bits, dtype, ctx, n, group, d, scores, sizes, q=1.0, seed=0):
+    """A chain whose slot s has the score scores[s] for every row (q is one
+    number, scale 1, codes 1 or -1), random values of factor sizes[s]."""
+    c = Case(bits, dtype, [ctx], n, 2, group, d, 16, seed=seed)
+    pg, rw = places(c, 0, list(range(ctx + n)))
+    c.q[...] = q
+    low, high = (0x77, 0x99) if bits == 4 else (127, 129)
+    sign = torch.tensor(scores, device="cuda")
+    c.k[pg, rw] = torch.where(sign < 0, low, high).to(torch.uint8)[:, None, None]
+    c.s[pg, rw, :, 0] = (sign.abs() / (d * q)).bfloat16()[:, None]
+    c.s[pg, rw, :, 1] = torch.as_tensor(sizes, device="cuda", dtype=torch.float32).bfloat16()[:, None]
+    return c
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("power", [24, 28, 40])
+def test_a_large_value_that_weighs_nothing(bits, d, n, group, dtype, power):
+    """Every seventh key of the context has a value 2^power as large as the
+    others, and a weight smaller still: p |v| of it is 2^-20 of theirs."""
+    ctx = 300
+    s = np.arange(ctx + n)
+    large = (s % 7 == 3) & (s < ctx)
+    scores = np.where(large, -(power + 20) * np.log(2.0), 0.25 * np.cos(s))
+    c = laid_out(bits, dtype, ctx, n, group, d, scores, np.where(large, 2.0 ** power, 1.0 / 8), seed=power)
+    c.check([tree("chain", n, None)], scale=1.0)
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("power", [19, 30, 60])
+def test_a_large_key_whose_score_is_nothing(bits, d, n, group, power):
+    """Every seventh key has a factor 2^power as large as the others, and codes
+    of 0 where q is not: its score is exactly 0."""
+    c = Case(bits, "bf16", [300, 20], n, 2, group, d, 16, seed=power)
+    par = tree("tree", n, np.random.default_rng(1)) if n > 3 else [-1, 0, 0]
+    c.q[..., 8:] = 0
+    zero = 0x88 if bits == 4 else 128
+    oracle_s = f64(c.s)
+    for i, ln in enumerate(c.lens):
+        pg, rw = places(c, i, list(range(3, ln + n, 7)))
+        c.k[pg, rw, :, : 8 * bits // 8] = zero
+        c.s[pg, rw, :, 0] = 2.0 ** power
+        oracle_s[pg.cpu().numpy(), rw.cpu().numpy(), :, 0] = 0.0
+    out, lse = c.attend(i32(par))
+    tf.tf_device_error()
+    # (the bound of a score grows with its key's factor; here the products are 0 whatever that is)
+    held, c.s = c.s, torch.tensor(oracle_s, device="cuda")
+    c.check([par] * 2, out=out, lse=lse)
+    c.s = held
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("dtype,size", [("fp16", 300.0), ("bf16", 300.0), ("bf16", 2.0 ** 60)])
+@pytest.mark.parametrize("lower", [30.0, 60.0, 100.0])
+def test_rows_of_zeros_before_large_values(bits, d, n, group, dtype, size, lower):
+    """Rows of zeros, and after them large values far below the maximum: the
+    weights of the largest scores are multiplied by nothing at all."""
+    ctx = 300
+    scores = np.where(np.arange(ctx + n) < 200, 0.0, -lower)
+    sizes = np.where(np.arange(ctx + n) < 200, 0.0, size)
+    c = laid_out(bits, dtype, ctx, n, group, d, scores, sizes, seed=3)
+    out, lse = c.attend(i32(tree("chain", n, None)), scale=1.0)
+    assert torch.isfinite(out).all()
+    if lower < 80.0:
+        c.check([tree("chain", n, None)], scale=1.0, out=out, lse=lse)
+    else:   # a weight below 2^-126 is 0 in fp32: nothing is left, or what it would have been
+        most = size * 2.0 ** (bits - 1) * 2.0 ** (-lower / np.log(2.0))
+        assert (out.double().abs() <= most + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("low,high", [(-40, 40), (-100, -20), (0, 25), (20, 90)])
+def test_values_over_many_powers_of_two(bits, d, n, group, low, high):
+    c = Case(bits, "bf16", [700, 131], n, 2, group, d, 16, seed=21)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    e = torch.randint(low, high + 1, c.s.shape[:3], device="cuda", generator=g).float()
+    c.s[..., 1] = (c.s[..., 1].float() * torch.exp2(e)).bfloat16()
+    c.check([tree("tree", n, np.random.default_rng(1)) if n > 3 else [-1, 0, 0]] * 2, scale=0.5)

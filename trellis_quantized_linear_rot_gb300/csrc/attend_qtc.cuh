@@ -12,19 +12,22 @@
 // A code has 3 bits and a sign and a factor 8 bits, so c s is exact in fp16's
 // 11, as long as it stays in range: factors go in relative to the largest of
 // their 32 keys, whose exponents ek and ev the weights' threads put back. That
-// is right where every row sees the 32 alike. Where they reach past the context
-// (rows see different nodes, and what an absent node's slot holds is anything),
-// or one of them is not finite, codes go in without factors, and a score and a
+// is right where every row sees the 32 alike, and they are of similar sizes.
+// Where they reach past the context (rows see different nodes, and what an
+// absent node's slot holds is anything), or their factors differ by more than
+// kKeySpread or kValueSpread, codes go in without factors, and a score and a
 // weight are multiplied by their key's own, in fp32: what a row does not see has
-// no part in its scores, maximum or exponent. q is scaled into fp16's range by a
-// power of two a row. Elements are in the order in which they come out of a word
+// no part in its scores, maximum or exponent, and what it sees is not rounded
+// for its neighbours' sake. q is scaled into fp16's range by a power of two a
+// row. Elements are in the order in which they come out of a word
 // (0, 4, 1, 5, 2, 6, 3, 7), in q too, and in the sums until they are written.
 //
 // Weights are p 2^(ev - E), E of a row rising like its maximum, so that
 // values of any size weigh what they should; sums of weights are of p itself.
 // The largest weight of a row is bounded (largest p times largest factor of 32
-// keys), not known; what is bounded is 2^8 when E is set, so that what lies
-// 2^-22 below it still has its bits.
+// keys, 2^6 too much at most; where keys are treated one by one their own); the
+// bound is 2^8 when E is set, so that fp16's last bit is 2^-26 of the largest
+// weight or less.
 //
 // Measured: 16 trees of 16 nodes x 6 heads of 128 x 8 over up to 4,096 slots
 // 55.4 us (292 TFLOP/s; 45.8 with heads of 64), of 64 nodes 152 (434), one tree
@@ -93,8 +96,17 @@ struct QtcArgs {
   int block_nodes;   // whole nodes of a row block
 };
 
-// The least exponent E: what is multiplied by 2^-E stays far from fp32's ends.
-constexpr int kLeastExp = -100;
+// Factors of 32 keys go into the operands where they differ by no more powers of
+// two than these. Of keys: c s 2^8 is a normal fp16 number down to 2^-18 of the
+// largest, and exact. Of values: what the weights' bound is too large by, which
+// their rounding to fp16 pays for.
+constexpr int kKeySpread = 18, kValueSpread = 6;
+// The least exponent E, of a factor that goes into an operand, and the largest of
+// a value that does: 2^(ev - E) is a number in fp32 then. Others are treated one
+// by one, where a weight is (p v) 2^-E.
+constexpr int kLeastExp = -100, kMostKeyExp = 100, kMostValueExp = 26;
+// In the place of the exponent of 0.
+constexpr int kNoExp = 1000;
 
 // One row of a tile, by its thread, as weigh() of attend_tc.cuh, with a factor
 // for the scores and one for the weights of each 32 keys, or (kEach) of each
@@ -195,7 +207,7 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, const Qt
         }
       }
     } else {
-      const float by = score_by(c), size = power2(max(-126, min(126, words.ev[c] - e)));
+      const float by = score_by(c), size = power2(max(-126, words.ev[c] - e));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float2 x = fma2(float2{v[2 * i], v[2 * i + 1]}, float2{by, by}, float2{-m, -m});
@@ -572,12 +584,18 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       if (page != -1 && !real) record_index_error(a.c.err);
       const uint32_t factors = real ? reinterpret_cast<const uint32_t*>(codes + 2 * S::kHalf)[key] : 0;
       const float ks = key_scale(factors), vs = value_scale(factors);
-      const bool fine = (factors & 0x7F80u) != 0x7F80u && (factors & 0x7F800000u) != 0x7F800000u;
-      const int ek = __reduce_max_sync(~0u, ks != 0.f ? max(exponent_of(fabsf(ks)), -100) : -100);
-      const int ev = __reduce_max_sync(~0u, vs != 0.f ? max(exponent_of(fabsf(vs)), -100) : -100);
       const uint32_t there = __ballot_sync(~0u, real);
-      // Rows may see different ones of the warp's 32 keys, or one is not finite.
-      const bool apart = cur.t * kTile + quarter * 32 + 32 > cur.span.context || !__all_sync(~0u, fine);
+      // Largest and least exponents of the warp's 32 keys (128 of what is not
+      // finite). A key of 0 is exact beside any other; a value of 0 is not
+      // beside others, whose weights may be less than its own by any power.
+      const int own_k = exponent_of(fabsf(ks)), own_v = vs != 0.f ? exponent_of(fabsf(vs)) : -kNoExp;
+      const int high_k = __reduce_max_sync(~0u, ks != 0.f ? own_k : -kNoExp);
+      const int low_k = __reduce_min_sync(~0u, ks != 0.f ? own_k : kNoExp);
+      const int high_v = __reduce_max_sync(~0u, own_v), low_v = __reduce_min_sync(~0u, own_v);
+      const int ek = max(high_k, kLeastExp), ev = max(high_v, kLeastExp);
+      const bool apart = cur.t * kTile + quarter * 32 + 32 > cur.span.context || high_k - low_k > kKeySpread ||
+                         low_k < kLeastExp || high_k > kMostKeyExp || high_v - low_v > kValueSpread ||
+                         (low_v < kLeastExp && high_v > -kNoExp) || high_v > kMostValueExp;
       // (the scores of the stream's tile before are made, which came after the
       // weights of the one before that: nobody reads this place any more)
       QtcShared::Words& words = sh.words[s][use & 1];
@@ -585,7 +603,7 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       // (operands are 2^8 times as large as values: codes of 7 at most are exact either way)
       words.key_by[key] = apart ? ks * 0x1p-8f : power2(ek - 8);
       words.value_by[key] = apart ? vs : power2(ev);
-      words.value_log[key] = !apart ? ev : vs == 0.f ? -1000.f : exponent_of(fabsf(vs)) + 1;
+      words.value_log[key] = apart ? own_v + 1 : ev;
       if (lane == 0) {
         words.ek[quarter] = ek, words.ev[quarter] = ev;
         words.there[quarter] = there, words.apart[quarter] = apart;
