@@ -161,3 +161,25 @@ def test_values_over_many_powers_of_two(bits, d, n, group, low, high):
     e = torch.randint(low, high + 1, c.s.shape[:3], device="cuda", generator=g).float()
     c.s[..., 1] = (c.s[..., 1].float() * torch.exp2(e)).bfloat16()
     c.check([tree("tree", n, np.random.default_rng(1)) if n > 3 else [-1, 0, 0]] * 2, scale=0.5)
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("dtype,size", [("fp16", 300.0), ("bf16", 300.0), ("bf16", 2.0 ** 60)])
+@pytest.mark.parametrize("lower", [30.0, 100.0])
+def test_rows_of_zeros_before_large_values_in_one_run(bits, d, n, group, dtype, size, lower):
+    """The same with more tiles than blocks, so that a block has rows of zeros first and large values in a later tile."""
+    ctx, b = 700, 160
+    c = Case(bits, dtype, [ctx] * b, n, 4, group, d, 16, seed=3)
+    first = (torch.arange(c.k.shape[1] * c.table.shape[1], device="cuda") < 400).view(c.table.shape[1], -1)
+    pages = c.table.long()
+    low, high = (0x77, 0x99) if bits == 4 else (127, 129)
+    c.q[...] = 1.0
+    c.k[pages] = torch.where(first, high, low).to(torch.uint8)[None, :, :, None, None]
+    c.s[pages, :, :, 0] = torch.where(first, 0.0, lower / d).bfloat16()[None, :, :, None]
+    c.s[pages, :, :, 1] = torch.where(first, 0.0, size).bfloat16()[None, :, :, None]
+    out, lse = c.attend(i32(tree("chain", n, None)), scale=1.0)
+    tf.tf_device_error()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    if lower < 80.0:
+        c.lens = c.lens[:1]
+        c.check([tree("chain", n, None)], scale=1.0, out=out[:1], lse=lse[:1])

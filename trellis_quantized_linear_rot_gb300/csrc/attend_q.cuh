@@ -520,7 +520,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
             for (int y = x; y < 4; y += 2) {
               const float p = exp2_approx(s[u][n][y] - m[n][x]);
               sum[n][x] += p;
-              w[u][n][y] = p * (value_scale(factors[u][y >> 1]) * to16);
+              w[u][n][y] = p * value_scale(factors[u][y >> 1]) * to16;   // (vs 2^-E alone may be infinite, p 0)
               largest = fmaxf(largest, fabsf(w[u][n][y]));
             }
           over |= sum[n][x] > 0x1p9f || largest > 0x1p15f;
