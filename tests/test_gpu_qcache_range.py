@@ -154,6 +154,16 @@ def test_rows_of_zeros_before_large_values(bits, d, n, group, dtype, size, lower
 
 
 @pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("power", [110, 120, 124])
+def test_large_queries_of_small_keys(bits, d, n, group, power):
+    """Queries of 2^power and keys that are smaller by as much: the scores are ordinary ones."""
+    c = Case(bits, "bf16", [300, 20], n, 2, group, d, 16, seed=power)
+    c.q = (c.q.float().clamp(-3, 3) * 2.0 ** power).bfloat16()
+    c.s[..., 0] = (c.s[..., 0].float() * 2.0 ** -power).bfloat16()
+    c.check([tree("tree", n, np.random.default_rng(1)) if n > 3 else [-1, 0, 0]] * 2)
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
 @pytest.mark.parametrize("low,high", [(-40, 40), (-100, -20), (0, 25), (20, 90)])
 def test_values_over_many_powers_of_two(bits, d, n, group, low, high):
     c = Case(bits, "bf16", [700, 131], n, 2, group, d, 16, seed=21)
