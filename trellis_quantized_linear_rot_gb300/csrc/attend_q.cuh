@@ -169,6 +169,7 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
   if (n_tiles == 0) return;
   const uint8_t* kp = static_cast<const uint8_t*>(a.k);
   const uint8_t* vp = static_cast<const uint8_t*>(a.v);
+  auto given_up_here = [&] { return *static_cast<volatile int*>(&given_up) != 0; };
 
   __syncthreads();   // the barriers are there
   // Wide: the registers of 384 threads, 168 each, are shared out anew: 56 for
@@ -320,13 +321,10 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
         if (++st == kStages) st = 0, phase ^= 1;
       }
     }
-    // Every copy has landed before the others are through, unless a wait gave up: then here.
-    if (given_up) {
-      int again = 0;
-      for (int x = 0; x < kStages; ++x) {
-        mbar_wait(smem_u32(&full[x]), 0, &again);
-        mbar_wait(smem_u32(&full[x]), 1, &again);
-      }
+    // Every copy has landed before the others are through, unless a wait gave
+    // up: then before this warp or the others leave, whichever see it.
+    if (given_up_here()) {
+      mbar_drain(smem_u32(&full[0]), kStages);
       if (lane == 0) atomicOr(a.c.err, kErrWait);
     }
     return;
@@ -728,6 +726,11 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
       if (last_here[x])
         join_parts<T, kRows, D, kArith>(a, line, mine, parts[x].b, parts[x].item, row0, min(kRows, rows_all - row0),
                                      parts[x].first, parts[x].nt, parts[x].idle, tid);
+  }
+  // (these warps have met since the last of their waits)
+  if (threadIdx.x == 0 && given_up_here()) {
+    mbar_drain(smem_u32(&full[0]), kStages);
+    atomicOr(a.c.err, kErrWait);
   }
 }
 

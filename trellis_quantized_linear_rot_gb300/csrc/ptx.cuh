@@ -82,6 +82,14 @@ __device__ __forceinline__ bool mbar_wait_sleepy(uint32_t bar, uint32_t parity, 
   }
 }
 
+// After a wait gave up: waits until what was begun on `count` barriers, one
+// after the other in memory, has ended, or the time limit has passed.
+__device__ __forceinline__ void mbar_drain(uint32_t bars, int count) {
+  int again = 0;
+#pragma unroll 1
+  for (int i = 0; i < 2 * count; ++i) mbar_wait(bars + i / 2 * 8, i & 1, &again);
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
