@@ -4,10 +4,11 @@ gives up sets a flag, waits that find it set give up too, and the block ends;
 before it does, somebody has to record the flag, and every copy that was begun
 has to have landed, or it lands in the shared memory of another block.
 
-The order of the end "apart": the copying warp leaves by itself and the warps of
-arithmetic do (mma.sync kernel over a quantised cache), so both look at the flag
-after their last wait. A control in which the copying warp alone looks, when its
-own last copy is begun, must be seen to fail.
+Two orders of the end. "apart": the copying warp leaves by itself and the warps
+of arithmetic do (mma.sync kernel over a quantised cache), so both look at the flag after their last
+wait. "together": all roles meet, then one looks (tcgen05 kernels). Controls in
+which the copying warp alone looks, when its own last copy is begun, must be
+seen to fail.
 """
 
 import random
@@ -129,13 +130,13 @@ CASES = [(n, late) for n in (1, 2, 3, 5, 8) for late in range(n)]
 
 
 @pytest.mark.parametrize("n,late", CASES)
-@pytest.mark.parametrize("end", ["apart"])
+@pytest.mark.parametrize("end", ["apart", "together"])
 def test_a_wait_that_gives_up_is_recorded_and_no_copy_outlives_the_block(n, late, end):
     for seed in range(200):
         Sim(n, late, seed, end, "all").run()
 
 
-@pytest.mark.parametrize("end", ["apart"])
+@pytest.mark.parametrize("end", ["apart", "together"])
 def test_a_look_by_the_copying_warp_alone_fails(end):
     faults = 0
     for n, late in CASES:

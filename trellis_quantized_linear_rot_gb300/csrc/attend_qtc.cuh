@@ -392,13 +392,6 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
           advance<kTile, S::kGap>(a, &cur);
         }
       }
-      if (*abort_flag) {   // given up somewhere: the copies in flight still have to land
-        int again = 0;
-        for (int x = 0; x < kQtcSlots; ++x) {
-          mbar_wait(bar(kCFull + x), 0, &again);
-          mbar_wait(bar(kCFull + x), 1, &again);
-        }
-      }
     } else {
       // ------------------------------------------------------------ products
       const int s = warp - 1;
@@ -765,7 +758,10 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, S::kColumns);
-  if (tid == 0 && sh.abort) atomicOr(a.c.err, kErrWait);
+  if (tid == 0 && *abort_flag) {   // given up somewhere: the copies in flight still have to land
+    mbar_drain(bar(kCFull), kQtcSlots);
+    atomicOr(a.c.err, kErrWait);
+  }
 }
 
 }  // namespace tfx

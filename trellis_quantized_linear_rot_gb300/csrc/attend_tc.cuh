@@ -394,13 +394,6 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         }
       }
     }
-    if (vs.j < n_tiles) {   // given up: the copies in flight still have to land
-      volatile int never = 0;
-      for (int j = max(0, ks.j - kStages); j < ks.j; ++j)
-        mbar_wait(bar(kKFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
-      for (int j = max(0, vs.j - kStages); j < vs.j; ++j)
-        mbar_wait(bar(kVFull + j % kTcSlots), (j / kTcSlots) & 1, &never);
-    }
   } else if (warp == 3) {
     // ----------------------------------------------------------- copies of q
     int n_items = 0;
@@ -421,10 +414,6 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
         ++n_items;
       }
       advance<kTile, S::kGap>(a, &cur);
-    }
-    if (!ok) {
-      volatile int never = 0;
-      mbar_wait(bar(kQFull), (n_items - 1) & 1, &never);
     }
   } else if (warp == 1 || warp == 2) {
     // -------------------------------------------------------------- products
@@ -694,7 +683,12 @@ tree_attention_tc_kernel(const __grid_constant__ TcMaps maps, const __grid_const
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, S::kColumns);
-  if (tid == 0 && sh.abort) atomicOr(a.c.err, kErrWait);
+  if (tid == 0 && *abort_flag) {   // given up somewhere: the copies in flight still have to land
+    mbar_drain(bar(kKFull), kTcSlots);
+    mbar_drain(bar(kVFull), kTcSlots);
+    mbar_drain(bar(kQFull), 1);
+    atomicOr(a.c.err, kErrWait);
+  }
 }
 
 }  // namespace tfx
