@@ -86,8 +86,10 @@ tf_status tf_kv_write(const tf_kv_cache* cache, const void* k_new, const void* v
  *   finite in fp32 (TF_ERR_SHAPE).
  * workspace: device memory, 256-byte aligned, at least
  *   tf_tree_attention_workspace_bytes(...) bytes, zeroed before its first use;
- *   each call leaves it ready for the next. Calls that share a workspace must
- *   be ordered by the caller. After TF_ERR_TIMEOUT it has to be zeroed again.
+ *   each call leaves it ready for the next call of this operator or of
+ *   tf_kvq_attention (another operator's workspace is another one). Calls that
+ *   share a workspace must be ordered by the caller. After TF_ERR_TIMEOUT it has
+ *   to be zeroed again.
  * The same inputs give the same bits. The pages have no counterpart.
  */
 tf_status tf_tree_attention(const tf_kv_cache* cache, const void* q, int64_t q_stride_seq,
@@ -141,7 +143,8 @@ size_t tf_tree_attention_workspace_bytes(int batch, int nodes, int heads, int kv
  *   0, then -1; out_tokens: the accepted tokens and the sampled one (-1 where
  *   no logit of its row is above -inf), then -1; logprobs fp32: their target
  *   log-probabilities at `temperature` (at 1 for temperature 0), then 0.
- * workspace as in tf_tree_attention, of tf_verify_draft_workspace_bytes.
+ * workspace as in tf_tree_attention, of tf_verify_draft_workspace_bytes, for
+ *   this operator alone.
  * The pages have no counterpart.
  */
 tf_status tf_verify_draft(const void* logits, int dtype, int64_t stride_seq, int64_t stride_node,

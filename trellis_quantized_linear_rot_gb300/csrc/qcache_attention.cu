@@ -32,13 +32,11 @@ int run_of_slots(const QAttendArgs& x, int tile, int row_bytes) {
 // call, 6 chains of 5 over up to 1,500 (4 parts) 16.1 and 14.3 (in a graph 11.8
 // and 13.8, 15.8 and 16.4).
 constexpr int kManyParts = 2, kManyPartsOfShort = 6, kLongRun = 4;
-// Blocks an SM of any of the kernels, at most.
-constexpr int kMostBlocks = 4;
 
 template <typename T, int kBits, int D, int kCols>
 cudaError_t launch(QAttendArgs x, int device, cudaStream_t s) {
   using S = QShape<kBits, D, kCols>;
-  static_assert(S::kBlocks <= kMostBlocks, "the workspace has room for these");
+  static_assert(S::kBlocks <= kMostBlocksPerSm, "the workspace has room for these");
   AttendArgs& a = x.a;
   static PerDeviceOnce<kMaxDevices> once;
   const int e = once.run(device, cudaErrorInvalidDevice, [] {
@@ -110,9 +108,9 @@ cudaError_t by_dim(const QAttendArgs& x, int device, cudaStream_t s) {
 // where a block has an SM to itself.
 AttendWorkspace kvq_attend_workspace(int nodes, int heads, int kv_heads, int head_dim, int num_sms) {
   const int64_t rows = static_cast<int64_t>(nodes) * (heads / kv_heads);
-  const size_t places = static_cast<size_t>(kMostBlocks) * num_sms;
+  const size_t places = static_cast<size_t>(kMostBlocksPerSm) * num_sms;
   AttendWorkspace w;
-  w.partials_at = (2 * places * sizeof(int) + 255) & ~static_cast<size_t>(255);
+  w.partials_at = attend_counter_bytes(num_sms);
   size_t part_rows = std::max<size_t>(places, (rows + 7) / 8) * 16;
   // Blocks of rows of the tcgen05 kernel hold whole nodes, of 128 rows at most.
   if (rows > kManyRows) part_rows = std::max(part_rows, std::max<size_t>(num_sms, nodes) * 128);

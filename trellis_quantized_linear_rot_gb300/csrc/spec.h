@@ -65,6 +65,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Blocks of an attention launch for each SM.
 constexpr int kBlocksPerSm = 2;
 
+// A workspace begins with counters for the most blocks that any attention
+// kernel launches, so that the parts of a call over a 16-bit cache never lie
+// where the counters of one over a quantised cache are.
+constexpr int kMostBlocksPerSm = 4;
+static_assert(kBlocksPerSm <= kMostBlocksPerSm, "counters for each block");
+inline size_t attend_counter_bytes(int num_sms) {
+  return (2 * static_cast<size_t>(kMostBlocksPerSm) * num_sms * sizeof(int) + 255) & ~static_cast<size_t>(255);
+}
+
 struct AttendWorkspace {
   size_t partials_at, bytes;
 };

@@ -155,7 +155,7 @@ AttendWorkspace attend_workspace(int nodes, int heads, int kv_heads, int head_di
   // Blocks of rows of the tcgen05 kernel hold whole nodes, half of 128 rows at least.
   const size_t wide = std::max<size_t>(num_sms, nodes) * 2;
   AttendWorkspace w;
-  w.partials_at = (2 * places * sizeof(int) + 255) & ~static_cast<size_t>(255);
+  w.partials_at = attend_counter_bytes(num_sms);
   const size_t part_rows = rows <= kFewRows ? places * 16 : std::max(blocks, wide) * 64;
   w.bytes = w.partials_at + 2 * part_rows * (head_dim + 2) * sizeof(float);
   return w;
