@@ -6,6 +6,7 @@ results."""
 import numpy as np
 import pytest
 
+import qcache_oracle as qo
 import spec_oracle as so
 
 torch = pytest.importorskip("torch")
@@ -193,3 +194,20 @@ def test_rows_of_zeros_before_large_values_in_one_run(bits, d, n, group, dtype, 
     if lower < 80.0:
         c.lens = c.lens[:1]
         c.check([tree("chain", n, None)], scale=1.0, out=out[:1], lse=lse[:1])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("power", [64, 90, 126])
+def test_norm_rope_small_elements_of_large_rows(d, power):
+    """One element of 2^power, the others from 2^-3 to 2^-115 of it: each keeps its bits, as far as bf16 has them."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn((2, 7, 3, d), device="cuda", generator=g).double().clamp(-1.9, 1.9)
+    x = x * torch.exp2(power - 3.0 - 112.0 * torch.rand(x.shape, device="cuda", generator=g).double())
+    x[..., 5] = 1.5 * 2.0 ** power
+    x = x.bfloat16()
+    pos = torch.zeros((2, 7), dtype=torch.int32, device="cuda")
+    got, _ = tf.tf_qk_norm_rope(x, None, pos, eps=0.0)
+    tf.tf_device_error()
+    want, mag = qo.norm_rope(f64(x), 1.0, np.zeros((2, 7)), [], 0.0, False, False)
+    off = np.abs(f64(got) - want)
+    assert np.all(off <= qo.norm_rope_bound(want, mag, "bf16", np.zeros((2, 7)), np.zeros(0), d))

@@ -133,10 +133,12 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int tokens, int per_
       };
       float square = mean_square() + a.eps;
       // Squares of large or small bf16 numbers pass fp32's range where the
-      // numbers don't: such rows are scaled by a power of two first.
+      // numbers don't: such rows are scaled by a power of two first (2^-70: the
+      // sum of 256 squares is below 2^128, and what is left of the row as a bf16
+      // number, 2^-126 of its root mean square and more, keeps 8 bits).
       if (std::is_same<T, __nv_bfloat16>::value &&
           __any_sync(~0u, square >= 0x1p120f || square < 0x1p-80f)) {
-        const float by = square >= 0x1p120f ? 0x1p-90f : square < 0x1p-80f ? 0x1p90f : 1.f;
+        const float by = square >= 0x1p120f ? 0x1p-70f : square < 0x1p-80f ? 0x1p90f : 1.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i / 4][i % 4] = mul2(x[i / 4][i % 4], twice(by));
         square = mean_square() + a.eps * by * by;
