@@ -211,3 +211,47 @@ def test_norm_rope_small_elements_of_large_rows(d, power):
     want, mag = qo.norm_rope(f64(x), 1.0, np.zeros((2, 7)), [], 0.0, False, False)
     off = np.abs(f64(got) - want)
     assert np.all(off <= qo.norm_rope_bound(want, mag, "bf16", np.zeros((2, 7)), np.zeros(0), d))
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("which", [0, 1])
+def test_factors_that_differ_in_some_places_only(bits, d, n, group, which):
+    """Tiles whose keys are alike beside tiles, and parts of tiles, whose are not; factors of either sign."""
+    c = Case(bits, "bf16", [900, 333], n, 2, group, d, 16, seed=31)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    c.s *= torch.where(torch.rand(c.s.shape, device="cuda", generator=g) < 0.5, -1.0, 1.0).bfloat16()
+    for i, ln in enumerate(c.lens):
+        pg, rw = places(c, i, [s for s in range(ln) if 150 <= s < 170 or s % 211 == 3])
+        c.s[pg, rw, :, which] *= 2.0 ** (-21 if which == 0 else 13)
+        pg, rw = places(c, i, list(range(200, 230)))
+        c.s[pg, rw, :, which] = 0.0
+    c.check([tree("tree", n, np.random.default_rng(1)) if n > 3 else [-1, 0, 0]] * 2)
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("page", [16, 7])
+def test_pages_outside_the_pool_are_left_out(bits, d, n, group, page):
+    """The other slots weigh what they would if those of the page were not there, whatever lies beside them."""
+    lens = [500, 40]
+    c = Case(bits, "bf16", lens, n, 2, group, d, page, seed=17)
+    par = tree("tree", n, np.random.default_rng(1)) if n > 3 else [-1, 0, 0]
+    table = c.table.clone()
+    bad = [[1, 2, 9, 30 // (page // 7)], [2]]
+    for i, pages in enumerate(bad):
+        for j, p in enumerate(pages):
+            table[i, p] = (c.k.shape[0], -1, 1 << 30, -(1 << 31))[j]
+    out, lse = tf.tf_kvq_attention(c.q, c.k, c.v, c.s, table, c.lengths, i32(par))
+    with pytest.raises(tf.TFError) as e:
+        tf.tf_device_error()
+    assert e.value.status == tf.TF_ERR_INDEX
+    kk, vv = (qo.unpack(x.cpu().numpy(), bits) for x in (c.k, c.v))
+    ss, qq = f64(c.s), f64(c.q)
+    for i, ln in enumerate(lens):
+        total = ln + n
+        pg, rw = so.slot_rows(c.table[i].cpu().numpy(), page, total)
+        seen = np.ones((n, total), dtype=bool)
+        seen[:, ln:] = so.seen_nodes(par)
+        seen[:, np.isin(np.arange(total) // page, bad[i])] = False
+        o, l, mag, err, top = qo.attend(qq[i], kk[pg, rw], ss[pg, rw, :, 0], vv[pg, rw], ss[pg, rw, :, 1], seen, d ** -0.5, bits)
+        tol_o, tol_l = qo.attend_bounds(o, l, mag, err, top, "bf16", total, bits)
+        assert np.all(np.abs(f64(lse[i]) - l) <= tol_l) and np.all(np.abs(f64(out[i]) - o) <= tol_o)
