@@ -117,8 +117,9 @@ tf_status tf_kvq_write(const tf_kvq_cache* cache, const void* k_new, int64_t k_s
  * [kv_heads][head_dim] fp16 or bf16 with the given strides, last dimension
  * contiguous; 16-byte aligned, strides multiples of 8. c * s may be above a
  * row's largest element by 2^-9 of it (s is rounded), and infinite in fp16 for
- * elements next to its largest. Rows of other slots are left as they were. starts: [batch], or NULL for 0. cache->layers must
- * be 1. The pages have no counterpart.
+ * elements next to its largest. Rows of other slots are left as they were.
+ * starts: [batch], or NULL for 0. cache->layers must be 1. The pages have no
+ * counterpart.
  */
 tf_status tf_kvq_read(const tf_kvq_cache* cache, const int32_t* starts, void* k_out, void* v_out, int dtype,
                       int64_t stride_seq, int64_t stride_slot, int64_t stride_head, int slots, void* stream);

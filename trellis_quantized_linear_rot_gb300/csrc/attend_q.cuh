@@ -25,20 +25,26 @@
 //   warps' own copies a quarter of all instructions) is spent once for them.
 //
 // Weights. p = 2^(s - m), s = (q . c) ks scale log2(e); O = sum of w c with w
-// = p vs 2^-E rounded to fp16. m is raised when a score passes it by 8, the
-// row's E when a weight would pass 2^15, so that most tiles need no exchange
-// between lanes; 2^E is about 2^-8 of the largest p vs so far, so that factors of any
-// size and range lose nothing. q is scaled by a power of two into fp16's range
-// (exact but for elements 2^-39 below the row's largest).
+// = p vs 2^-E rounded to fp16. m is raised when a lane's p add up to more than
+// 2^9, the row's E when a weight would pass 2^15, so that most tiles need no
+// exchange between lanes; 2^E is about 2^-8 of the largest p vs so far, so that
+// factors of any size and range lose nothing. Weights are rounded because the
+// matrix instruction takes 16 bits beside the codes' fp16 (two parts would be
+// twice the products): 2^-12 of a weight, and outputs are as far from the 64-bit
+// ones as the plain form's in bf16, 1.0 to 1.2 times as far in fp16. q is scaled
+// by a power of two into fp16's range: an element is off by 2^-39 of its row's
+// largest at most (2^-35 where it meets upper nibbles, for which it is divided
+// by 16), by nothing if it has bf16's 8 bits and is 2^-31 of it or more (2^-27).
 //
 // Measured, heads of 128: 32 tokens x 5 heads a kv head x 8 over up to 8,192
-// slots in 4 bits 55.5 us (174 MB, 3.1 TB/s), in 8 bits 74.3 (342 MB, 4.6
-// TB/s), in 4 bits over up to 32,768 157 (693 MB, 4.4 TB/s). Issue slots are
-// 52% busy, the ALU 40%: half of a warp's 611 instructions for 32 keys are the
-// codes' conversion. Start and end are most of the 15.6 us over up to 256
-// slots. Pages of 16 slots 63.9, of 7 (no bulk copies) 76.8. The wide form: 16
-// trees of 16 x 6 heads over up to 4,096 slots in 8 bits 172 us, issue slots
-// 38% busy with two arithmetic warps a scheduler.
+// slots in 4 bits 55.7 us (174 MB, 3.1 TB/s), in 8 bits 74.5 (342 MB, 4.6
+// TB/s), in 4 bits over up to 32,768 160 (693 MB, 4.3 TB/s). Issue slots are
+// 53% busy, the ALU 42%: half of a warp's 611 instructions for 32 keys are the
+// codes' conversion. Start and end are most of the 15.2 us over up to 256
+// slots. Pages of 16 slots 63.9, of 7 (no bulk copies) 75.5. With 16 rows a kv
+// head 91.5: five warps a block leave 168 registers a thread, and 204 bytes are
+// spilled. The wide form: 16 trees of 16 x 6 heads over up to 4,096 slots in 8
+// bits 172 us, issue slots 37% busy with two arithmetic warps a scheduler.
 #pragma once
 
 #include "attend_mma.cuh"
@@ -110,7 +116,9 @@ __device__ __forceinline__ uint32_t whole2(uint32_t w) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&kFrom));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-__device__ __forceinline__ void load_words(uint32_t (&w)[1], const unsigned char* p) { w[0] = *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ void load_words(uint32_t (&w)[1], const unsigned char* p) {
+  w[0] = *reinterpret_cast<const uint32_t*>(p);
+}
 __device__ __forceinline__ void load_words(uint32_t (&w)[2], const unsigned char* p) {
   const uint2 x = *reinterpret_cast<const uint2*>(p);
   w[0] = x.x, w[1] = x.y;
@@ -438,7 +446,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
       for (int part0 = 0; part0 < kKeys; part0 += 16 * kTiles16, kt += 16 * kTiles16 * kRB, vt += 16 * kTiles16 * kRB) {
       if (kWide && slot0 + part0 >= cur.span.slots) break;
       auto q_of = [&](int n, int step) {
-        return kWide ? frags[(n * kSteps + step) * 32] : uint2{qf[kWide ? 0 : n][kWide ? 0 : step][0], qf[kWide ? 0 : n][kWide ? 0 : step][1]};
+        return kWide ? frags[(n * kSteps + step) * 32]
+                     : uint2{qf[kWide ? 0 : n][kWide ? 0 : step][0], qf[kWide ? 0 : n][kWide ? 0 : step][1]};
       };
       float s[kTiles16][kCols][4];
       uint32_t factors[kTiles16][2];
@@ -467,7 +476,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
               mma16816<__half>(s[u][n], lo, b.x, b.y);
             }
             if constexpr (kBits == 4) {
-              const uint32_t hi[4] = {whole2<4, true>(ka[w]), whole2<4, true>(kb[w]), whole2<4, true>(xa), whole2<4, true>(xb)};
+              const uint32_t hi[4] = {whole2<4, true>(ka[w]), whole2<4, true>(kb[w]), whole2<4, true>(xa),
+                                      whole2<4, true>(xb)};
 #pragma unroll
               for (int n = 0; n < kCols; ++n) {
                 const uint2 b = q_of(n, step + 1);
@@ -602,7 +612,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                   const uint32_t xs = z ? x >> 8 : x, ys = z ? y >> 8 : y;
-                  const uint32_t c[4] = {whole2<4, false>(xs), whole2<4, true>(xs), whole2<4, false>(ys), whole2<4, true>(ys)};
+                  const uint32_t c[4] = {whole2<4, false>(xs), whole2<4, true>(xs), whole2<4, false>(ys),
+                                         whole2<4, true>(ys)};
 #pragma unroll
                   for (int n = 0; n < kCols; ++n)
                     mma16816<__half>(o[(w0 + i_w) * 4 + half * 2 + z][n], c, b[n][0], b[n][1]);

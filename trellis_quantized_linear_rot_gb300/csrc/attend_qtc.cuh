@@ -29,12 +29,17 @@
 // bound is 2^8 when E is set, so that fp16's last bit is 2^-26 of the largest
 // weight or less.
 //
+// Weights are rounded to fp16 for the second product, as values are in it: see
+// attend_q.cuh.
+//
 // Measured: 16 trees of 16 nodes x 6 heads of 128 x 8 over up to 4,096 slots
-// 55.4 us (292 TFLOP/s; 45.8 with heads of 64), of 64 nodes 152 (434), one tree
-// of 64 x 5 over 50,001 slots 119 (552). Not memory (14% of its rate at 16
-// nodes) but the chain of a tile bounds it, codes, scores, weights, sums, and
-// the instructions of five roles: issue slots 54% busy, tensor pipe 25%.
-// Unrolled, the roles do not fit the instruction cache (61 us for 55).
+// 56.0 us (289 TFLOP/s; 45.9 with heads of 64), of 64 nodes 153 (431), one tree
+// of 64 x 5 over 50,001 slots 117 (560). With values whose sizes differ by up to
+// 2^4 67, by up to 2^12, where every key is treated by itself, 73. Not memory
+// (14% of its rate at 16 nodes) but the chain of a tile bounds it, codes,
+// scores, weights, sums, and the instructions of five roles: issue slots 53%
+// busy, tensor pipe 24%. Unrolled, the roles do not fit the instruction cache
+// (61 us for 55).
 #pragma once
 
 #include "attend_q.cuh"
@@ -47,8 +52,8 @@ namespace tfx {
 // is the end of an item's q told to the group of warps that has the next item's
 // first tile, and writes its q, on a barrier of that group's own.
 constexpr int kQtcStages = 3, kQtcSlots = 6;
-enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcSlots, kXQFull = kCEmpty + kQtcSlots, kXQEmpty, kXKFull = kXQEmpty + 2, kXKEmpty = kXKFull + 2,
-                  kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2, kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2,
+enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcSlots, kXQFull = kCEmpty + kQtcSlots, kXQEmpty,
+                  kXKFull = kXQEmpty + 2, kXKEmpty = kXKFull + 2, kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2, kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2,
                   kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2, kXPvDone = kXPThree + 2, kXWords = kXPvDone + 2,
                   kXBarriers = kXWords + 4 };
 
@@ -301,7 +306,8 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       const uint8_t* vp = static_cast<const uint8_t*>(a.v);
       auto stage_free = [&](int j) {
         const int before = j - kQtcStages;   // the tile before in its stage
-        return before < 0 || __all_sync(~0u, mbar_wait(bar(kCEmpty + before % kQtcSlots), (before / kQtcSlots) & 1, abort_flag));
+        return before < 0 ||
+               __all_sync(~0u, mbar_wait(bar(kCEmpty + before % kQtcSlots), (before / kQtcSlots) & 1, abort_flag));
       };
       auto codes_of = [&](int j) { return base + S::kCodesAt + j % kQtcStages * S::kStageBytes; };
       if (args.q.box) {   // 4 slots at least: a lane has a run
@@ -475,7 +481,8 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     // ------------------------------------------------------- codes to fp16
-    const int s = (warp - 12) / 4, key = (tid - 384) % 128, quarter = (warp - 12) % 4;   // a thread's key of a tile, and row of q
+    // key: a thread's key of a tile, and row of q
+    const int s = (warp - 12) / 4, key = (tid - 384) % 128, quarter = (warp - 12) % 4;
     // 16-byte chunk c of row r of a tile in the products' layout.
     auto place = [&](int at, int r, int c) {
       return reinterpret_cast<uint4*>(smem + at + (c / 8) * S::kPartBytes + r * 128 + (((c % 8) ^ (r & 7)) << 4));
@@ -522,8 +529,9 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
       }
       if (!ok) return;
       const int node = key / a.group;
-      const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + c.b * a.q_seq + (node0 + node) * a.q_node +
-                                                         (c.item * a.group + key - node * a.group) * a.q_head);
+      const uint4* from =
+          reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + c.b * a.q_seq + (node0 + node) * a.q_node +
+                                         (c.item * a.group + key - node * a.group) * a.q_head);
       uint32_t top = 0;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {

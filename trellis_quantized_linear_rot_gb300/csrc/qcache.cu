@@ -43,7 +43,8 @@ __device__ __noinline__ uint64_t quantise8_by_division(float4 a, float4 b, float
   return out;
 }
 // bf16(top / m) in every bit: the quotient of a number by a small constant is
-// its product with the rounded reciprocal, corrected once by what is left.
+// its product with the rounded reciprocal, corrected once by what is left
+// (Markstein, Computation of elementary functions on the IBM RISC System/6000).
 template <int kBits>
 __device__ __noinline__ float factor_by_division(float top) {
   return __bfloat162float(__float2bfloat16_rn(__fdiv_rn(top, kBits == 4 ? 7.f : 127.f)));
@@ -322,7 +323,8 @@ template <typename T, int kBits, int D>
 struct Kernels {
   static cudaError_t write(const QView& q, const RowsIn& k, const RowsIn& v, const int32_t* counts, int nodes,
                            cudaStream_t s) {
-    return launch_units(kvq_write_kernel<T, kBits, D>, Units(q.c.batch, nodes, q.c.kv_heads), D, s, q, k, v, counts, nodes);
+    return launch_units(kvq_write_kernel<T, kBits, D>, Units(q.c.batch, nodes, q.c.kv_heads), D, s, q, k, v, counts,
+                        nodes);
   }
   static cudaError_t read(const QView& q, const int32_t* starts, void* k, void* v, int64_t seq, int64_t slot,
                           int64_t head, int slots, cudaStream_t s) {
@@ -334,7 +336,9 @@ struct Kernels {
 // f(Kernels<...>()) of the call's type, width and head size.
 template <typename T, int kBits, typename F>
 cudaError_t by_dim(int head_dim, F&& f) {
-  return head_dim == 64 ? f(Kernels<T, kBits, 64>()) : head_dim == 128 ? f(Kernels<T, kBits, 128>()) : f(Kernels<T, kBits, 256>());
+  return head_dim == 64    ? f(Kernels<T, kBits, 64>())
+         : head_dim == 128 ? f(Kernels<T, kBits, 128>())
+                           : f(Kernels<T, kBits, 256>());
 }
 template <typename F>
 cudaError_t by_kind(int dtype, int bits, int head_dim, F&& f) {

@@ -98,11 +98,13 @@ tf_status tf_qk_norm_rope(const tf_head_rows* queries, const tf_head_rows* keys,
       negative(q) || negative(k) || !(eps >= 0.0) || !(eps <= std::numeric_limits<float>::max()) ||
       (flags & ~(TF_QK_NO_NORM | TF_QK_INTERLEAVED | TF_QK_HADAMARD)) || too_many(batch, nodes, q.heads + k.heads))
     return TF_ERR_SHAPE;
-  if ((dtype != TF_F16 && dtype != TF_BF16) || (weight_dtype != TF_F16 && weight_dtype != TF_F32 && weight_dtype != TF_BF16))
+  if ((dtype != TF_F16 && dtype != TF_BF16) ||
+      (weight_dtype != TF_F16 && weight_dtype != TF_F32 && weight_dtype != TF_BF16))
     return TF_ERR_DTYPE;
   if (batch == 0 || nodes == 0) return TF_OK;
   if (!q.x || !q.y || (keys && (!k.x || !k.y)) || !positions || (rotary && !inv_freq)) return TF_ERR_NULL;
-  if (misaligned(q, weight_dtype) || misaligned(k, weight_dtype) || !aligned(positions, 4) || (rotary && !aligned(inv_freq, 8)))
+  if (misaligned(q, weight_dtype) || misaligned(k, weight_dtype) || !aligned(positions, 4) ||
+      (rotary && !aligned(inv_freq, 8)))
     return TF_ERR_ALIGN;
   int device, sms, *err;
   tf_status s = current_device_state(&device, &sms, &err);

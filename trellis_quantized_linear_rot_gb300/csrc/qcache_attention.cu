@@ -13,8 +13,9 @@ constexpr int kMaxDevices = 64;
 // Blocks of a launch with `blocks` places: whole teams of row_blocks, one at least.
 int team_blocks(int blocks, int row_blocks) { return std::max(1, blocks / row_blocks) * row_blocks; }
 
-// Slots that are copied at once: the most that divide both a page and a tile, where their rows lie one after the other, and their factors too, at
-// multiples of 16 bytes; 0 where they don't.
+// Slots that are copied at once: the most that divide both a page and a tile,
+// where their rows lie one after the other, and their factors too, at multiples
+// of 16 bytes; 0 where they don't.
 int run_of_slots(const QAttendArgs& x, int tile, int row_bytes) {
   const CacheView& c = x.a.c;
   const int box = std::gcd(c.page_size, tile);
@@ -46,7 +47,8 @@ cudaError_t launch(QAttendArgs x, int device, cudaStream_t s) {
   if (e != cudaSuccess) return static_cast<cudaError_t>(e);
   const int row_blocks = (a.nodes * a.group + S::kRows - 1) / S::kRows;
   const int blocks = team_blocks(S::kBlocks * a.num_sms, row_blocks);
-  const int64_t runs = blocks / row_blocks, tiles = (static_cast<int64_t>(a.c.table_width) * a.c.page_size + S::kTile - 1) / S::kTile;
+  const int64_t runs = blocks / row_blocks;
+  const int64_t tiles = (static_cast<int64_t>(a.c.table_width) * a.c.page_size + S::kTile - 1) / S::kTile;
   const bool long_runs = tiles * a.c.batch * a.c.kv_heads >= kLongRun * runs;
   a.join_later = parts_of(a, runs, S::kTile) > (long_runs ? kManyParts : kManyPartsOfShort);
   x.box = run_of_slots(x, S::kTile, S::kRowBytes);

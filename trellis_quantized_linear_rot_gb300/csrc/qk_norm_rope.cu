@@ -163,7 +163,8 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int tokens, int per_
     } else if (a.rotary == D) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 c = *reinterpret_cast<const float2*>(cs + e + 2 * i), s = *reinterpret_cast<const float2*>(sn + e + 2 * i);
+        const float2 c = *reinterpret_cast<const float2*>(cs + e + 2 * i);
+        const float2 s = *reinterpret_cast<const float2*>(sn + e + 2 * i);
         const float2 u = x[0][i], v = x[1][i];
         x[0][i] = minus(mul2(u, c), mul2(v, s));
         x[1][i] = fma2(v, c, mul2(u, s));
@@ -186,7 +187,8 @@ qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int tokens, int per_
           for (int k = 0; k < 2; ++k)
             z[k] = float2{__shfl_sync(~0u, x[k][i].x, from), __shfl_sync(~0u, x[k][i].y, from)};
           const float2 v = other < kLanes ? z[0] : z[1];
-          const float2 c = *reinterpret_cast<const float2*>(cs + at + 2 * i), s = *reinterpret_cast<const float2*>(sn + at + 2 * i);
+          const float2 c = *reinterpret_cast<const float2*>(cs + at + 2 * i);
+          const float2 s = *reinterpret_cast<const float2*>(sn + at + 2 * i);
           y[p][i] = x[p][i];
           if (turned) y[p][i] = fma2(mul2(v, s), twice(low ? -1.f : 1.f), mul2(x[p][i], c));
         }
