@@ -53,9 +53,9 @@ namespace tfx {
 // first tile, and writes its q, on a barrier of that group's own.
 constexpr int kQtcStages = 3, kQtcSlots = 6;
 enum QtcBarrier { kCFull, kCEmpty = kCFull + kQtcSlots, kXQFull = kCEmpty + kQtcSlots, kXQEmpty,
-                  kXKFull = kXQEmpty + 2, kXKEmpty = kXKFull + 2, kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2, kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2,
-                  kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2, kXPvDone = kXPThree + 2, kXWords = kXPvDone + 2,
-                  kXBarriers = kXWords + 4 };
+                  kXKFull = kXQEmpty + 2, kXKEmpty = kXKFull + 2, kXVFull = kXKEmpty + 2, kXVEmpty = kXVFull + 2,
+                  kXSFull = kXVEmpty + 2, kXPFull = kXSFull + 2, kXPHalf = kXPFull + 2, kXPThree = kXPHalf + 2,
+                  kXPvDone = kXPThree + 2, kXWords = kXPvDone + 2, kXBarriers = kXWords + 4 };
 
 struct QtcShared {
   unsigned long long bars[kXBarriers];
