@@ -255,3 +255,48 @@ def test_pages_outside_the_pool_are_left_out(bits, d, n, group, page):
         o, l, mag, err, top = qo.attend(qq[i], kk[pg, rw], ss[pg, rw, :, 0], vv[pg, rw], ss[pg, rw, :, 1], seen, d ** -0.5, bits)
         tol_o, tol_l = qo.attend_bounds(o, l, mag, err, top, "bf16", total, bits)
         assert np.all(np.abs(f64(lse[i]) - l) <= tol_l) and np.all(np.abs(f64(out[i]) - o) <= tol_o)
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("power", [10, 24, 28, 32, 40, 60, 100])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_of_any_size_find_the_largest(bits, d, n, group, power, sign):
+    """Scores of +-2^power, one of them an eighth above the others: its value is the result, far from fp32's
+    resolution at that size (from 10 on the others' weights are below 2^-100)."""
+    ctx, top = 500, 321
+    s = np.arange(ctx + n)
+    scores = 2.0 ** power * (0.5 + 0.25 * np.cos(s) ** 2) if sign > 0 else -(2.0 ** power) * (1.0 + 0.25 * np.cos(s) ** 2)
+    scores[top] = sign * 2.0 ** power * (1.0 if sign > 0 else 0.875)
+    c = laid_out(bits, "bf16", ctx, n, group, d, scores, np.full(ctx + n, 0.5), seed=power)
+    out, lse = c.attend(i32(tree("chain", n, None)), scale=1.0)
+    tf.tf_device_error()
+    pg, rw = places(c, 0, [top])
+    value = 0.5 * qo.unpack(c.v[pg, rw].cpu().numpy(), bits)[0]                       # [kh, d]
+    want = np.repeat(value, group, 0)[None]
+    # codes of up to 7 bits times a half are exact in bf16; the others weigh 2^-100 in all
+    assert np.array_equal(f64(out[0]), np.broadcast_to(want, (n, 2 * group, d)))
+    most = f64(c.s[pg, rw, :, 0])[0] * d * sign                                       # bf16 factors times d: exact
+    want_l = np.broadcast_to(np.repeat(most, group)[None], (n, 2 * group))
+    assert np.all(np.abs(f64(lse[0]) - want_l) <= (2 * d + 4) * 2.0 ** -24 * np.abs(want_l) * (1 + 2.0 ** (bits - 1)))
+
+
+@pytest.mark.parametrize("bits,d,n,group", FORMS)
+@pytest.mark.parametrize("power", [12, 34, 60])
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** -60, 2.0 ** 90])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_values_of_any_size_under_large_scores(bits, d, n, group, power, size, mixed):
+    """The value of the one key that weighs is the result, where scores are so large that a value's exponent is
+    less than their resolution; mixed: values beside it are larger or smaller by many powers."""
+    ctx, top = 500, 321
+    s = np.arange(ctx + n)
+    scores = 2.0 ** power * (0.5 + 0.25 * np.cos(s) ** 2)
+    scores[top] = 2.0 ** power
+    sizes = size * np.where(mixed & (s % 3 == 1), 2.0 ** -20, 1.0) * np.where(mixed & (s % 5 == 1), 2.0 ** 20, 1.0)
+    sizes[top] = size
+    c = laid_out(bits, "bf16", ctx, n, group, d, scores, sizes, seed=power)
+    out, lse = c.attend(i32(tree("chain", n, None)), scale=1.0)
+    tf.tf_device_error()
+    pg, rw = places(c, 0, [top])
+    value = size * qo.unpack(c.v[pg, rw].cpu().numpy(), bits)[0]
+    assert np.array_equal(f64(out[0]), np.broadcast_to(np.repeat(value, group, 0)[None], (n, 2 * group, d)))
+    assert torch.isfinite(lse).all()

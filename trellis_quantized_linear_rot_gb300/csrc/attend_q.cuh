@@ -495,8 +495,8 @@ kvq_attention_kernel(const __grid_constant__ QAttendArgs args) {
 #pragma unroll
         for (int u = 0; u < kTiles16; ++u)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)   // (factors first: a score may pass fp32's range without the key's)
-            s[u][n][x] *= (x & 1 ? by.y : by.x) * key_scale(factors[u][x >> 1]);
+          for (int x = 0; x < 4; ++x)   // (factors first: a score may pass fp32's range without the key's; rounded, as m is)
+            s[u][n][x] = __fmul_rn(s[u][n][x], (x & 1 ? by.y : by.x) * key_scale(factors[u][x >> 1]));
       }
       if (tail) {
 #pragma unroll

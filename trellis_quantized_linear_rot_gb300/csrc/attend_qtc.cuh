@@ -99,6 +99,7 @@ struct QtcShape {
 struct QtcArgs {
   QAttendArgs q;
   int block_nodes;   // whole nodes of a row block
+  float zero;        // 0: a product and this are rounded, where the compiler would fuse it with what is added next
 };
 
 // Factors of 32 keys go into the operands where they differ by no more powers of
@@ -116,17 +117,27 @@ constexpr int kNoExp = 1000;
 // One row of a tile, by its thread, as weigh() of attend_tc.cuh, with a factor
 // for the scores and one for the weights of each 32 keys, or (kEach) of each
 // key, with the keys that the row sees in vis. sc: the row's factor, not below 0.
+// Each key's scores are rounded before m, a rounded one, is subtracted, so that p
+// is 2^8 at most, and the weights' bound is kept relative to the scores'. Where a
+// warp's scores are large all tiles are treated so (not kEach: false then, and
+// nothing is done): at 2^30 an exact product passes m by up to 64, and its weight
+// fp16's range, and a value's exponent is lost beside a score. (All tiles always:
+// trees of 64 nodes 158.7 us.)
+constexpr float kLargeScore = 0x1p20f;
 template <int D, bool kEach>
-__device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, const QtcShared::Words& words, float sc,
-                                        const uint32_t (&vis)[4], bool begun, uint32_t half, uint32_t three,
-                                        float* m_row, float* l_row, int* e_row) {
+__device__ __forceinline__ bool weigh_q(uint32_t scores, uint32_t sums, const QtcShared::Words& words, float sc,
+                                        float zero, const uint32_t (&vis)[4], bool begun, uint32_t half,
+                                        uint32_t three, float* m_row, float* l_row, int* e_row) {
   auto word_of = [&](int c) { return c < 2 ? (c == 0 ? vis[0] : vis[1]) : (c == 2 ? vis[2] : vis[3]); };
   auto score_by = [&](int c) { return sc * power2(words.ek[c] - 8); };
   auto pairs_at = [&](const float* of, int key, float2 (&x)[2]) {   // of four keys
     const float4 y = *reinterpret_cast<const float4*>(of + key);
     x[0] = float2{y.x, y.y}, x[1] = float2{y.z, y.w};
   };
-  float top = -INFINITY, need = -INFINITY;   // the largest score, the largest weight with its values' size
+  auto product = [&](float x, float y, float2 by) { return fma2(float2{x, y}, by, float2{zero, zero}); };
+  // The largest score, and the largest weight with its values' size (kEach: were
+  // the largest score 0).
+  float top = -INFINITY, need = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     float v[32];
@@ -134,24 +145,35 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, const Qt
     float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if constexpr (kEach) {
       const uint32_t word = word_of(c);
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        float2 by[2];
+        pairs_at(words.key_by, c * 32 + i, by);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int n = i + 2 * k;
+          const float2 x = product(v[n], v[n + 1], mul2(by[k], float2{sc, sc}));
+          v[n] = word >> n & 1 ? x.x : -INFINITY;
+          v[n + 1] = word >> (n + 1) & 1 ? x.y : -INFINITY;
+          hi[n / 2 % 4] = fmaxf(hi[n / 2 % 4], fmaxf(v[n], v[n + 1]));
+        }
+      }
+      const float high = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+      const float base = high == -INFINITY ? 0.f : high;
       float2 large = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
-        float2 by[2], size[2];
-        pairs_at(words.key_by, c * 32 + i, by);
-        pairs_at(words.value_log, c * 32 + i, size);
+        float2 log[2];
+        pairs_at(words.value_log, c * 32 + i, log);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float2 x = mul2(float2{v[i + 2 * k], v[i + 2 * k + 1]}, mul2(by[k], float2{sc, sc}));
-          if (!(word >> (i + 2 * k) & 1)) x.x = -INFINITY;
-          if (!(word >> (i + 2 * k + 1) & 1)) x.y = -INFINITY;
-          hi[i / 4 % 2 * 2 + k] = fmaxf(hi[i / 4 % 2 * 2 + k], fmaxf(x.x, x.y));
-          const float2 weight = add2(x, size[k]);
+          const float2 weight = add2(add2(float2{v[i + 2 * k], v[i + 2 * k + 1]}, float2{-base, -base}), log[k]);
           large = float2{fmaxf(large.x, weight.x), fmaxf(large.y, weight.y)};
         }
       }
-      top = fmaxf(top, fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])));
-      need = fmaxf(need, fmaxf(large.x, large.y));
+      const float size = fmaxf(large.x, large.y);
+      need = high > top ? fmaxf(need + (top - high), size) : fmaxf(need, high - top + size);
+      top = fmaxf(top, high);
     } else {
 #pragma unroll
       for (int i = 0; i < 32; i += 2) hi[i / 2 % 4] = fmaxf(hi[i / 2 % 4], fmaxf(v[i], v[i + 1]));
@@ -164,12 +186,14 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, const Qt
   int e = *e_row;
   const bool rise = top > m + 8.f;
   const float to = rise ? top : m;
-  const bool grow = need - to > static_cast<float>(e) + 15.f;   // a weight might pass fp16's range
+  if (!kEach && __any_sync(~0u, !(fabsf(to) < kLargeScore))) return false;
+  need = kEach ? need + (top - to) : need - to;
+  const bool grow = need > static_cast<float>(e) + 15.f;   // a weight might pass fp16's range
   if (__any_sync(~0u, rise || grow)) {
     const float down = m - to;   // 0, or below
     int to_e = e;
     if (rise) to_e = max(kLeastExp, e + static_cast<int>(floorf(fmaxf(down, -400.f))));
-    if (rise || grow) to_e = min(126, max(to_e, static_cast<int>(ceilf(fmaxf(need - to, -190.f))) - 8));
+    if (rise || grow) to_e = min(126, max(to_e, static_cast<int>(ceilf(fmaxf(need, -190.f))) - 8));
     l *= exp2_approx(down);
     if (begun) {
       const float f = exp2_approx(down + static_cast<float>(e - to_e));
@@ -203,7 +227,7 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, const Qt
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const bool sees_x = word >> (i + 2 * k) & 1, sees_y = word >> (i + 2 * k + 1) & 1;
-          float2 x = fma2(float2{v[i + 2 * k], v[i + 2 * k + 1]}, mul2(by[k], float2{sc, sc}), float2{-m, -m});
+          float2 x = add2(product(v[i + 2 * k], v[i + 2 * k + 1], mul2(by[k], float2{sc, sc})), float2{-m, -m});
           x.x = sees_x ? exp2_approx(x.x) : 0.f;
           x.y = sees_y ? exp2_approx(x.y) : 0.f;
           sum[i / 4 % 2 * 2 + k] = add2(sum[i / 4 % 2 * 2 + k], x);
@@ -234,6 +258,7 @@ __device__ __forceinline__ void weigh_q(uint32_t scores, uint32_t sums, const Qt
   *m_row = m;
   *l_row = l + (both.x + both.y);
   *e_row = e;
+  return true;
 }
 
 template <typename T, int D>
@@ -674,9 +699,11 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
           all &= vis[w];
           apart |= words.apart[w];
         }
-        if (all == ~0u && !apart) {   // a whole tile of the context
-          weigh_q<D, false>(scores, sums, words, sc, vis, used, bar(kXPHalf + s), bar(kXPThree + s), &m, &l, &e);
-        } else {
+        bool done = false;
+        if (all == ~0u && !apart)   // a whole tile of the context
+          done = weigh_q<D, false>(scores, sums, words, sc, args.zero, vis, used, bar(kXPHalf + s), bar(kXPThree + s),
+                                   &m, &l, &e);
+        if (!done) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const int off = slot0 + w * 32 - cur.span.context;   // tree node of the word's first key
@@ -687,7 +714,8 @@ __global__ void __launch_bounds__(640, 1) kvq_attention_tc_kernel(const __grid_c
             }
             vis[w] = node >= 0 ? word & vis[w] : 0u;
           }
-          weigh_q<D, true>(scores, sums, words, sc, vis, used, bar(kXPHalf + s), bar(kXPThree + s), &m, &l, &e);
+          weigh_q<D, true>(scores, sums, words, sc, args.zero, vis, used, bar(kXPHalf + s), bar(kXPThree + s), &m, &l,
+                           &e);
         }
         tmem_wait_st();
         tc_fence_before();

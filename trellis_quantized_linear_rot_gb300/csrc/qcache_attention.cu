@@ -70,7 +70,7 @@ cudaError_t launch_tc(QAttendArgs x, int device, cudaStream_t s) {
   });
   if (e != cudaSuccess) return static_cast<cudaError_t>(e);
   x.box = run_of_slots(x, S::kTile, S::kRowBytes);
-  const QtcArgs args = {x, std::min(S::kTile / a.group, a.nodes)};
+  const QtcArgs args = {x, std::min(S::kTile / a.group, a.nodes), 0.f};
   const int row_blocks = (a.nodes + args.block_nodes - 1) / args.block_nodes;
   const int blocks = team_blocks(a.num_sms, row_blocks);
   const cudaError_t launched =
