@@ -131,9 +131,10 @@ tf_status tf_kvq_read(const tf_kvq_cache* cache, const int32_t* starts, void* k_
  * of keys multiply scores in fp32, those of values the weights, which are
  * rounded for the second product: to 11 bits, and to 2^-26 of the row's
  * largest weight where they are smaller than 2^-15 of it. Weights exp(s - max
- * s) below 2^-126 are 0. Maxima, sums and accumulators are fp32. workspace as
- * there, of tf_kvq_attention_workspace_bytes; the two operators may share one
- * that is large enough for both.
+ * s) below 2^-126 are 0. Maxima, sums and accumulators are fp32, and scores may
+ * have any size that fp32 holds. workspace as there, of
+ * tf_kvq_attention_workspace_bytes; the two operators may share one that is
+ * large enough for both.
  * The same inputs give the same bits. The pages have no counterpart.
  */
 tf_status tf_kvq_attention(const tf_kvq_cache* cache, const void* q, int dtype, int64_t q_stride_seq,

@@ -76,7 +76,9 @@ tf_status tf_kv_write(const tf_kv_cache* cache, const void* k_new, const void* v
  * and lse = -inf. What a row does not see has no influence on it, whatever
  * its bits (NaN and infinities among them).
  * The weights exp(s - max s) are rounded to the dtype for the second matrix
- * product; maxima, sums and accumulators are fp32.
+ * product; maxima, sums and accumulators are fp32. With more than 16 rows a kv
+ * head scores have to stay below 2^26 (fp16) or 2^30 (bf16) in magnitude: rows
+ * with larger ones may be NaN.
  * q: [batch][nodes][heads][head_dim] with the given strides, last dimension
  *   contiguous, 16-byte aligned, strides multiples of 8. heads is a multiple
  *   of kv_heads; head h reads kv head h / (heads / kv_heads).

@@ -33,7 +33,7 @@
 // attend_q.cuh.
 //
 // Measured: 16 trees of 16 nodes x 6 heads of 128 x 8 over up to 4,096 slots
-// 56.0 us (289 TFLOP/s; 45.9 with heads of 64), of 64 nodes 153 (431), one tree
+// 56.4 us (287 TFLOP/s; 45.9 with heads of 64), of 64 nodes 156 (423), one tree
 // of 64 x 5 over 50,001 slots 117 (560). With values whose sizes differ by up to
 // 2^4 67, by up to 2^12, where every key is treated by itself, 73. Not memory
 // (14% of its rate at 16 nodes) but the chain of a tile bounds it, codes,
@@ -122,7 +122,7 @@ constexpr int kNoExp = 1000;
 // warp's scores are large all tiles are treated so (not kEach: false then, and
 // nothing is done): at 2^30 an exact product passes m by up to 64, and its weight
 // fp16's range, and a value's exponent is lost beside a score. (All tiles always:
-// trees of 64 nodes 158.7 us.)
+// trees of 64 nodes 158.7 us for 156.)
 constexpr float kLargeScore = 0x1p20f;
 template <int D, bool kEach>
 __device__ __forceinline__ bool weigh_q(uint32_t scores, uint32_t sums, const QtcShared::Words& words, float sc,
