@@ -33,9 +33,9 @@
 // attend_q.cuh.
 //
 // Measured: 16 trees of 16 nodes x 6 heads of 128 x 8 over up to 4,096 slots
-// 56.4 us (287 TFLOP/s; 45.9 with heads of 64), of 64 nodes 156 (423), one tree
+// 56.1 us (289 TFLOP/s; 45.8 with heads of 64), of 64 nodes 156 (424), one tree
 // of 64 x 5 over 50,001 slots 117 (560). With values whose sizes differ by up to
-// 2^4 67, by up to 2^12, where every key is treated by itself, 73. Not memory
+// 2^4 69, by up to 2^12, where every key is treated by itself, 75. Not memory
 // (14% of its rate at 16 nodes) but the chain of a tile bounds it, codes,
 // scores, weights, sums, and the instructions of five roles: issue slots 53%
 // busy, tensor pipe 24%. Unrolled, the roles do not fit the instruction cache
@@ -135,11 +135,13 @@ __device__ __forceinline__ bool weigh_q(uint32_t scores, uint32_t sums, const Qt
     x[0] = float2{y.x, y.y}, x[1] = float2{y.z, y.w};
   };
   auto product = [&](float x, float y, float2 by) { return fma2(float2{x, y}, by, float2{zero, zero}); };
+  // Parts of 32 keys, up to the last that has some.
+  const int parts = !kEach || words.there[3] ? 4 : words.there[2] ? 3 : words.there[1] ? 2 : 1;
   // The largest score, and the largest weight with its values' size (kEach: were
   // the largest score 0).
   float top = -INFINITY, need = -INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < parts; ++c) {
     float v[32];
     tmem_ld32(scores + c * 32, v);
     float hi[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -210,10 +212,17 @@ __device__ __forceinline__ bool weigh_q(uint32_t scores, uint32_t sums, const Qt
     m = to;
     e = to_e;
   }
+  auto stored = [&](int c) {   // weights over scores already read
+    if (c == 1 || c == 2) {
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(c == 1 ? half : three);
+    }
+  };
   float2 sum[4] = {};
   const float to16 = power2(-e);
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < parts; ++c) {
     float v[32];
     tmem_ld32(scores + c * 32, v);
     uint32_t w[16];
@@ -247,12 +256,14 @@ __device__ __forceinline__ bool weigh_q(uint32_t scores, uint32_t sums, const Qt
         w[i] = pack2(__half(), x.x, x.y);
       }
     }
-    tmem_st16(scores + c * 16, w);   // over scores already read
-    if (c == 1 || c == 2) {
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(c == 1 ? half : three);
-    }
+    tmem_st16(scores + c * 16, w);
+    stored(c);
+  }
+#pragma unroll 1
+  for (int c = parts; c < 4; ++c) {
+    const uint32_t none[16] = {};
+    tmem_st16(scores + c * 16, none);
+    stored(c);
   }
   const float2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
   *m_row = m;
