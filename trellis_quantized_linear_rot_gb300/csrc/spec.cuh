@@ -40,7 +40,9 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Two fp32 operations in one instruction.
+// Two fp32 operations in one instruction. (A product and the sum it goes into are
+// fused by the assembler, whatever their modifiers say: where the product has to
+// be rounded first, it needs an addend of 0 that the compiler does not know.)
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
